@@ -6,8 +6,10 @@
  * quantizer (block-128 Walsh-Hadamard rotation, absmax scale, symmetric INT8
  * codes; FP8-e4m3 dynamic variant), W8A8 GEMMs whose epilogues fuse the
  * row x column scales, the bias and, for packed gate/up weights, the SwiGLU
- * product, and the runtime LoRA add.  Every step runs in hand-written CUDA
- * kernels on the caller's stream.
+ * product, and the runtime LoRA add.  For answering token by token it adds
+ * linears over 4-bit weights, a paged 8-bit cache of keys and values, and the
+ * attention that reads it.  Every step runs in hand-written CUDA kernels on
+ * the caller's stream.
  *
  * Conventions shared by every entry point:
  *  - Pointers are DEVICE pointers to memory the caller owns (clef_copy_sm
@@ -61,7 +63,9 @@ typedef enum clef_status {
     CLEF_ERR_INVALID_ARG = 1,   /* null/misaligned pointer, bad size or stride */
     CLEF_ERR_UNSUPPORTED = 2,   /* device is not sm_103, or a mode not built */
     CLEF_ERR_CUDA = 3,          /* a CUDA runtime call or launch failed */
-    CLEF_ERR_TIMEOUT = 4        /* a device-side wait exceeded its limit */
+    CLEF_ERR_TIMEOUT = 4,       /* a device-side wait exceeded its limit */
+    CLEF_ERR_BAD_PAGE = 5,      /* on the device: a page, sequence, length or row index out of range */
+    CLEF_ERR_NO_PAGES = 6       /* on the device: the pool has too few free pages; nothing was changed */
 } clef_status;
 
 typedef enum clef_act_mode {
@@ -365,6 +369,131 @@ int clef_lora_add_noalloc(const void *x, int64_t ldx, const void *A, const void 
  */
 int clef_gemm_workspace_bytes(int64_t *bytes);
 int clef_bind_workspace(void *stream, void *ws, int64_t bytes);
+
+/*
+ * ---- linears over 4-bit weights ----
+ *
+ * clef_quant_w4 -- packs bf16 weights w [N][K] (row pitch ldw elements) as
+ * 4-bit codes with a bf16 scale for each run of `group` (32, 64 or 128)
+ * weights of a row:
+ *   s = bf16(amax / 7);  c = clamp(rne(w / s), -8, 7)   (0 where s is 0)
+ * Packed row: K rounded up to K_pad, a multiple of 128; K_pad / 2 bytes.  Of
+ * each block of 128 weights, byte 16 t + 4 j (t, j in 0..3) starts the
+ * little-endian word of weights 32 j + 8 t .. + 7, whose nibble i < 4 holds
+ * weight 2 i and nibble i + 4 weight 2 i + 1, each as c + 8.  Weights past K
+ * are zeros.  qw: uint8 [N][K_pad / 2]; sw: bf16 [N][K_pad / group].
+ * Requirements: K % 8 == 0, ldw >= K, ldw % 8 == 0, N and K at most 2^24;
+ *   w, qw and sw 16-byte aligned.  N = 0 is a valid empty call.
+ *
+ * clef_w4_linear -- y[m][n] = bf16(sum_g sw[n][g] * (sum_{k in g} c[n][k] x[m][k]) + bias[n])
+ * with fp32 sums, for calls of few rows: weights are read once for every 16
+ * rows.  The order of a row's sum follows N and K alone, so its bits do not
+ * depend on M.  x: bf16 [M][K], pitch ldx; bias: bf16 [N] or NULL; y: bf16
+ * [M][N], pitch ldy (any: y and bias need 2-byte alignment only).
+ * Requirements: as above, M <= 2^19, ldx >= K, ldx % 8 == 0, ldy >= N.
+ */
+int clef_quant_w4(const void *w, int64_t N, int64_t K, int64_t ldw, int group, void *qw, void *sw, void *stream);
+int clef_w4_linear(const void *x, int64_t ldx, const void *qw, const void *sw, int group, const void *bias,
+                   int64_t M, int64_t N, int64_t K, void *y, int64_t ldy, void *stream);
+
+/*
+ * ---- the paged 8-bit cache ----
+ *
+ * A pool is `planes` planes (a layer's keys, then its values, layer by layer)
+ * of `pages` pages each; a page holds `page` tokens (16, 32, 64 or 128) of
+ * every key/value head: codes [pages][heads][page][dim], one byte each (kind
+ * 0: int8 in -127..127; 1: e4m3), dim 64, 128 or 256, and fp32 scales
+ * [pages][heads] >= 0; value = code * scale.  plane_bytes and plane_scales are
+ * the distances between planes in bytes and floats.  The calls of one layer
+ * take its key plane's address, the value plane following it.  A sequence is a
+ * row of table (int32 [seqs][width], pitch ldt) and a length in lens: its
+ * token i is at page table[i / page], place i % page.  Entries of a row past
+ * the sequence's pages are never read.  refs: int32 [pages], how many
+ * sequences hold a page (0: free).
+ *
+ * Indices and lengths live in device memory, so the host cannot check them:
+ * the kernels do, leave out what is out of range and record
+ * CLEF_ERR_BAD_PAGE (clef_poll_status).  Limits: 16,384 sequences, 2^20 pages a
+ * sequence, 2^24 pages.  Codes must be 16-byte aligned, integers 4-byte.
+ *
+ * clef_kv_append -- writes the newest tokens' keys and values.  lens holds
+ * the lengths with the new tokens; the rows of a sequence are its last ones:
+ * rows row_start[b] .. row_start[b + 1] - 1 of k and v (row_start: int32
+ * [seqs + 1]), or rows / seqs each where row_start is NULL.  k, v: bf16,
+ * token pitches ldk, ldv and head pitches ldk_head, ldv_head in elements.
+ * A page's scale grows with what it holds (top = 127 or 448):
+ *   s = max(s_old, fp32(amax / top)), s_old = 0 for a page without tokens;
+ *   where s grew, earlier codes become encode(value(code) * fp32(s_old / s));
+ *   new codes are encode(v * min(fp32(1 / s), FLT_MAX)), zeros where s = 0.
+ * The pages written must belong to one sequence each (clef_kv_reserve and
+ * clef_kv_fork see to it).
+ *
+ * clef_kv_gather -- k_out[r], v_out[r] = bf16(code * scale) of token pos[r]
+ * of sequence seq[r]; outputs bf16 [rows][heads * dim], pitches ldk, ldv;
+ * zeros where an index is out of range.
+ *
+ * clef_kv_attention -- softmax attention of queries over the cache, for query
+ * row i of sequence b (n rows) and head h reading key/value head h / (q_heads
+ * / heads):  o = sum_j softmax_j(scale * q . k_j) v_j over its tokens j <
+ * lens[b], with causal only j <= lens[b] - n + i (the queries are the last
+ * tokens).  Rows that see nothing are zeros.  q: bf16, pitches ldq (token) and
+ * ldq_head; rows and row_start as for append; out: bf16, pitches ldo,
+ * ldo_head; lse: fp32 [rows][q_heads], log of the sum of exponentials
+ * (-infinity for a row that sees nothing), or NULL.  Sums are fp32; the
+ * weights that multiply values are rounded to fp16.  A row's bits depend on
+ * its own sequence alone.  workspace: clef_kv_attention_workspace bytes with
+ * ragged = (row_start != NULL) and max_len = width * page, 16-byte aligned; its
+ * contents need no preparation and are not kept.
+ *
+ * clef_kv_reserve -- lens[b] += grow[b] for every sequence, with the pages
+ * that takes: the lowest free ones, in the order of the sequences.
+ * clef_kv_fork -- sequence dst[i], empty before, becomes a copy of src[i]:
+ * whole pages are shared (refs + 1), a part-filled last page is copied to the
+ * lowest free page.  scratch: int32 [2 n].
+ * Either changes nothing and records CLEF_ERR_NO_PAGES if the free pages do
+ * not suffice, CLEF_ERR_BAD_PAGE if an argument on the device is out of range.
+ * clef_kv_free -- the sequences list[0 .. n - 1] become empty; their pages'
+ * refs - 1.
+ * clef_kv_compact -- moves pages so that the L held ones are 0 .. L - 1 (the
+ * k-th lowest held page past L - 1 to the k-th lowest free page below), with
+ * every sequence's row written to table_out, refs to refs_out and L to *live
+ * (may be NULL).  table_out and refs_out may be table and refs.  scratch: int32
+ * [3 pages + 1].
+ * clef_kv_copy_pages -- page dst[i] = page src[i] in every plane; no target
+ * may also be a source or listed twice.
+ */
+int clef_kv_append(const void *k, int64_t ldk, int64_t ldk_head, const void *v, int64_t ldv, int64_t ldv_head,
+                   int64_t rows, const int32_t *row_start, int kind, void *codes, int64_t plane_bytes,
+                   float *scales, int64_t plane_scales, int64_t pages, int heads, int page, int dim,
+                   const int32_t *table, int64_t ldt, int64_t seqs, int64_t width, const int32_t *lens,
+                   void *stream);
+int clef_kv_gather(int kind, const void *codes, int64_t plane_bytes, const float *scales, int64_t plane_scales,
+                   int64_t pages, int heads, int page, int dim, const int32_t *table, int64_t ldt, int64_t seqs,
+                   int64_t width, const int32_t *seq, const int32_t *pos, int64_t rows, void *k_out, int64_t ldk,
+                   void *v_out, int64_t ldv, void *stream);
+int clef_kv_attention_workspace(int64_t rows, int ragged, int64_t seqs, int q_heads, int heads, int dim,
+                                int64_t max_len, int64_t *bytes);
+int clef_kv_attention(const void *q, int64_t ldq, int64_t ldq_head, int64_t rows, const int32_t *row_start,
+                      int q_heads, int kind, const void *codes, int64_t plane_bytes, const float *scales,
+                      int64_t plane_scales, int64_t pages, int heads, int page, int dim, const int32_t *table,
+                      int64_t ldt, int64_t seqs, int64_t width, const int32_t *lens, float scale, int causal,
+                      void *out, int64_t ldo, int64_t ldo_head, float *lse, void *workspace,
+                      int64_t workspace_bytes, void *stream);
+int clef_kv_reserve(int32_t *table, int64_t ldt, int64_t seqs, int64_t width, int32_t *lens, int32_t *refs,
+                    int64_t pages, int page, const int32_t *grow, void *stream);
+int clef_kv_fork(void *codes, int64_t plane_bytes, float *scales, int64_t plane_scales, int64_t planes,
+                 int64_t pages, int heads, int page, int dim, int32_t *table, int64_t ldt, int64_t seqs,
+                 int64_t width, int32_t *lens, int32_t *refs, const int32_t *src, const int32_t *dst, int64_t n,
+                 int32_t *scratch, void *stream);
+int clef_kv_free(int32_t *table, int64_t ldt, int64_t seqs, int64_t width, int32_t *lens, int32_t *refs,
+                 int64_t pages, int page, const int32_t *list, int64_t n, void *stream);
+int clef_kv_compact(void *codes, int64_t plane_bytes, float *scales, int64_t plane_scales, int64_t planes,
+                    int64_t pages, int heads, int page, int dim, const int32_t *table, int64_t ldt, int64_t seqs,
+                    int64_t width, const int32_t *lens, const int32_t *refs, int32_t *table_out, int64_t ldt_out,
+                    int32_t *refs_out, int32_t *live, int32_t *scratch, void *stream);
+int clef_kv_copy_pages(void *codes, int64_t plane_bytes, float *scales, int64_t plane_scales, int64_t planes,
+                       int64_t pages, int heads, int page, int dim, const int32_t *src, const int32_t *dst,
+                       int64_t n, void *stream);
 
 /*
  * clef_mma_peak -- dense tensor-core rate of this device for one instruction

@@ -26,11 +26,13 @@ __all__ = [
     "w8a8_gemm_s32", "w8a8_linear_lora", "w8a8_gateup_swiglu_lora",
     "poll_status", "set_wait_limit_ns", "set_quant_staging", "set_pdl", "ACT_MODES", "gemm_workspace_bytes",
     "bind_workspace", "mma_peak",
+    "quant_w4", "w4_linear", "kv_append", "kv_gather", "kv_attention", "kv_reserve", "kv_fork", "kv_free",
+    "kv_compact", "kv_copy_pages",
 ]
 
 ACT_MODES = {"int8_h128": 0, "fp8": 1, "fp8_h128": 2}
 _STATUS = {0: "CLEF_OK", 1: "CLEF_ERR_INVALID_ARG", 2: "CLEF_ERR_UNSUPPORTED", 3: "CLEF_ERR_CUDA",
-           4: "CLEF_ERR_TIMEOUT"}
+           4: "CLEF_ERR_TIMEOUT", 5: "CLEF_ERR_BAD_PAGE", 6: "CLEF_ERR_NO_PAGES"}
 
 _lock = threading.Lock()
 _lib = None
@@ -78,6 +80,22 @@ def library():
                 "clef_w8a8_gateup_swiglu_lora": [vp, vp, vp, vp, vp, i64, i64, i64, vp, i64, vp, vp, i64, vp,
                                                  i64, vp],
                 "clef_mma_peak": [i32, i64, vp],
+                "clef_quant_w4": [vp, i64, i64, i64, i32, vp, vp, vp],
+                "clef_w4_linear": [vp, i64, vp, vp, i32, vp, i64, i64, i64, vp, i64, vp],
+                "clef_kv_append": [vp, i64, i64, vp, i64, i64, i64, vp, i32, vp, i64, vp, i64, i64, i32, i32, i32,
+                                   vp, i64, i64, i64, vp, vp],
+                "clef_kv_gather": [i32, vp, i64, vp, i64, i64, i32, i32, i32, vp, i64, i64, i64, vp, vp, i64, vp, i64,
+                                   vp, i64, vp],
+                "clef_kv_attention_workspace": [i64, i32, i64, i32, i32, i32, i64, vp],
+                "clef_kv_attention": [vp, i64, i64, i64, vp, i32, i32, vp, i64, vp, i64, i64, i32, i32, i32, vp, i64,
+                                      i64, i64, vp, C.c_float, i32, vp, i64, i64, vp, vp, i64, vp],
+                "clef_kv_reserve": [vp, i64, i64, i64, vp, vp, i64, i32, vp, vp],
+                "clef_kv_fork": [vp, i64, vp, i64, i64, i64, i32, i32, i32, vp, i64, i64, i64, vp, vp, vp, vp, i64, vp,
+                                 vp],
+                "clef_kv_free": [vp, i64, i64, i64, vp, vp, i64, i32, vp, i64, vp],
+                "clef_kv_compact": [vp, i64, vp, i64, i64, i64, i32, i32, i32, vp, i64, i64, i64, vp, vp, vp, i64, vp,
+                                    vp, vp, vp],
+                "clef_kv_copy_pages": [vp, i64, vp, i64, i64, i64, i32, i32, i32, vp, vp, i64, vp],
                 "clef_set_sm_budget": [i32],
                 "clef_copy_sm": [vp, vp, i64, i32, vp],
                 "clef_poll_status": [],
@@ -536,3 +554,7 @@ def test_force_timeout(on) -> None:
     L.clef_test_force_timeout.argtypes = [C.c_int]
     L.clef_test_force_timeout.restype = None
     L.clef_test_force_timeout(int(on) if not isinstance(on, bool) else (1 if on else 0))
+
+
+from .decode import (kv_append, kv_attention, kv_compact, kv_copy_pages, kv_fork, kv_free, kv_gather, kv_reserve,  # noqa: E402
+                     quant_w4, w4_linear)

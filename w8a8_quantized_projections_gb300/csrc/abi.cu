@@ -657,6 +657,8 @@ const char *clef_status_string(int status) {
         case CLEF_ERR_UNSUPPORTED: return "CLEF_ERR_UNSUPPORTED";
         case CLEF_ERR_CUDA: return "CLEF_ERR_CUDA";
         case CLEF_ERR_TIMEOUT: return "CLEF_ERR_TIMEOUT";
+        case CLEF_ERR_BAD_PAGE: return "CLEF_ERR_BAD_PAGE";
+        case CLEF_ERR_NO_PAGES: return "CLEF_ERR_NO_PAGES";
         default: return "CLEF_ERR_UNKNOWN";
     }
 }

@@ -2,6 +2,7 @@
 // and the kernel translation units.  Not part of the public ABI.
 #pragma once
 
+#include <atomic>
 #include <cstdint>
 #include <utility>
 #include <cuda.h>
@@ -45,6 +46,24 @@ cudaError_t launch_kernel(void (*kern)(KArgs...), dim3 grid, dim3 block, size_t 
     cfg.numAttrs = n;
     return cudaLaunchKernelEx(&cfg, kern, std::forward<Args>(args)...);
 }
+
+// A kernel's shared-memory opt-in, made once for each device.
+class SmemOptIn {
+public:
+    cudaError_t set(const void *kern, size_t bytes) {
+        int dev = 0;
+        cudaError_t e = cudaGetDevice(&dev);
+        if (e != cudaSuccess) return e;
+        const uint64_t bit = (uint64_t)1 << (dev & 63);
+        if (dev < 64 && (done_.load(std::memory_order_relaxed) & bit)) return cudaSuccess;
+        e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+        if (e == cudaSuccess) done_.fetch_or(bit, std::memory_order_relaxed);
+        return e;
+    }
+
+private:
+    std::atomic<uint64_t> done_{0};
+};
 
 enum ActMode : int { kActInt8H128 = 0, kActFp8 = 1, kActFp8H128 = 2 };
 
