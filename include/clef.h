@@ -382,7 +382,7 @@ int clef_bind_workspace(void *stream, void *ws, int64_t bytes);
  * little-endian word of weights 32 j + 8 t .. + 7, whose nibble i < 4 holds
  * weight 2 i and nibble i + 4 weight 2 i + 1, each as c + 8.  Weights past K
  * are zeros.  qw: uint8 [N][K_pad / 2]; sw: bf16 [N][K_pad / group].
- * Requirements: K % 8 == 0, ldw >= K, ldw % 8 == 0, N and K at most 2^24;
+ * Requirements: K % 8 == 0, K <= 65536, ldw >= K, ldw % 8 == 0, N <= 2^24;
  *   w, qw and sw 16-byte aligned.  N = 0 is a valid empty call.
  *
  * clef_w4_linear -- y[m][n] = bf16(sum_g sw[n][g] * (sum_{k in g} c[n][k] x[m][k]) + bias[n])
@@ -413,7 +413,7 @@ int clef_w4_linear(const void *x, int64_t ldx, const void *qw, const void *sw, i
  *
  * Indices and lengths live in device memory, so the host cannot check them:
  * the kernels do, leave out what is out of range and record
- * CLEF_ERR_BAD_PAGE (clef_poll_status).  Limits: 16,384 sequences, 2^20 pages a
+ * CLEF_ERR_BAD_PAGE (clef_poll_status).  Limits: 4,096 sequences, 2^20 pages a
  * sequence, 2^24 pages.  Codes must be 16-byte aligned, integers 4-byte.
  *
  * clef_kv_append -- writes the newest tokens' keys and values.  lens holds

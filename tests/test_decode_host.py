@@ -35,7 +35,7 @@ def test_w4():
     assert L.clef_quant_w4(NUL, 0, 256, 256, 64, NUL, NUL, NUL) == 0
     lin = [P, 256, P, P, 128, NUL, 4, 64, 256, P, 64, NUL]
     refused(L.clef_w4_linear, lin, [(0, NUL), (0, ODD), (1, 248), (1, 260), (2, NUL), (2, ODD), (3, ODD), (4, 0), (4, 256),
-                                    (5, C.c_void_p(0x10001)), (6, -1), (6, FAR), (7, 0), (7, FAR), (8, 0), (8, 12),
+                                    (5, C.c_void_p(0x10001)), (6, -1), (6, FAR), (7, 0), (7, FAR), (8, 0), (8, 12), (8, 65544),
                                     (9, NUL), (9, C.c_void_p(0x10001)), (10, 63)])
     assert L.clef_w4_linear(NUL, 256, P, P, 128, NUL, 0, 64, 256, NUL, 64, NUL) == 0
 
@@ -46,7 +46,7 @@ LAYER_BAD = [(0, NUL), (0, ODD), (1, 4 * 2 * 16 * 64 - 16), (1, 4 * 2 * 16 * 64 
              (4, FAR), (5, 0), (5, 1025), (6, 8), (6, 48), (6, 256), (7, 32), (7, 96), (7, 512)]
 #       table ldt seqs width
 TABLE = [P, 3, 2, 3]
-TABLE_BAD = [(0, NUL), (0, ODD), (1, 2), (2, -1), (2, 16385), (3, -1), (3, 1 << 21)]
+TABLE_BAD = [(0, NUL), (0, ODD), (1, 2), (2, -1), (2, 4097), (3, -1), (3, 1 << 21)]
 
 
 def at(offset, bad):

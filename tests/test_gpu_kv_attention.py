@@ -25,7 +25,7 @@ def check(c, table, lens, q, start, got, lse, causal=True, scale=None):
     for b, x in enumerate(lens):
         r = slice(start[b], start[b + 1])
         o, ls, tol, tl = attention(q[r].astype(np.float64), c.values(table[b], x), scale, causal)
-        bad = np.abs(got[r] - o) > tol + bf16_ulp(o)
+        bad = ~(np.abs(got[r] - o) <= tol + bf16_ulp(o))
         assert not bad.any(), (b, x, int(bad.sum()), float((np.abs(got[r] - o) / (tol + bf16_ulp(o))).max()))
         none = np.isinf(ls)
         assert np.array_equal(none, np.isinf(lse[r])) and (lse[r][none] < 0).all() and not got[r][none].any()
@@ -73,6 +73,23 @@ def test_long(kind, len_, dim):
     q = bf16(rng.standard_normal((2, 4, dim)))
     got, lse = run(rng, c, table, lens, q)
     check(c, table, lens, q, np.arange(3), got, lse)
+
+
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("dim", [64, 128, 256])
+@pytest.mark.parametrize("n,len_,heads,group,page", [
+    (17, 17, 1, 1, 16), (128, 128, 2, 1, 32), (129, 200, 1, 1, 64), (257, 300, 1, 1, 128), (100, 700, 2, 5, 16),
+    (33, 1025, 1, 4, 64), (20, 2500, 2, 1, 128), (300, 1100, 1, 2, 32),
+])
+def test_many_rows(kind, dim, n, len_, heads, group, page):
+    """One and two row tiles, partly filled ones, one and more steps, sequences
+    cut along their tokens and joined; a second sequence beside the first."""
+    rng = np.random.default_rng(n + len_ + dim)
+    lens = [len_, max(n, len_ // 3)]
+    c, table, _ = filled_cache(rng, kind, lens, heads, page, dim)
+    q = bf16(rng.standard_normal((2 * n, heads * group, dim)) * 2)
+    got, lse = run(rng, c, table, lens, q)
+    check(c, table, lens, q, [0, n, 2 * n], got, lse)
 
 
 @pytest.mark.parametrize("kind", KINDS)
@@ -200,6 +217,26 @@ def test_out_of_range_is_reported(n):
         clef.kv_attention(q, codes, scales, dev_i32(table), dev_i32(lens), dev_i32(start))
         assert clef.poll_status() == 5
     assert clef.poll_status() == 0
+
+
+def test_waits_run_out():
+    """The test knob makes the tile kernel's products wait for what never comes:
+    the waits give up, the status says so, and the next call is right."""
+    rng = np.random.default_rng(18)
+    c, table, _ = filled_cache(rng, "int8", [300], 2, 64, 128)
+    codes, scales = c.device()
+    q = dev_bf16(rng.standard_normal((50, 4, 128)))
+    args = (q, codes, scales, dev_i32(table), dev_i32([300]))
+    ref = clef.kv_attention(*args)
+    clef.set_wait_limit_ns(2_000_000)
+    clef.test_force_timeout(True)
+    try:
+        clef.kv_attention(*args)
+        assert clef.poll_status() == 4
+    finally:
+        clef.test_force_timeout(False)
+        clef.set_wait_limit_ns(1_000_000_000)
+    assert torch.equal(clef.kv_attention(*args), ref) and clef.poll_status() == 0
 
 
 def test_refusals():

@@ -125,7 +125,7 @@ def test_exactly_enough_and_one_too_few():
 
 def test_many_sequences():
     """More sequences than a CTA has threads, and the most there may be."""
-    for seqs in (1025, 16384):
+    for seqs in (1025, 4096):
         rng = np.random.default_rng(seqs)
         pool = Pool(rng, seqs + 5, seqs, 2, planes=1)
         grow = rng.integers(0, 17, seqs)

@@ -136,10 +136,7 @@ int make_tmap(CUtensorMap *m, CUtensorMapDataType dt, const void *base, uint64_t
 
 // SMs a compute launch may fill: the device's, or the caller's budget
 // (clef_set_sm_budget) where that is fewer.
-int launch_sms(const DeviceState *d) {
-    const int b = g_sm_budget.load();
-    return (b > 0 && b < d->num_sms) ? b : d->num_sms;
-}
+int launch_sms(const DeviceState *d) { return internal_launch_sms(d->num_sms); }
 
 // The workspace bound to this device and stream, if any, which lets a launch
 // split tiles across CTA pairs (INT8 stream-K, the K parts of the FP8 linear
@@ -325,6 +322,16 @@ int internal_device(int *num_sms, unsigned int **status) {
     *num_sms = d->num_sms;
     *status = d->status;
     return CLEF_OK;
+}
+
+int internal_launch_sms(int num_sms) {
+    const int b = g_sm_budget.load();
+    return (b > 0 && b < num_sms) ? b : num_sms;
+}
+
+uint64_t internal_wait_limit(int *force_timeout) {
+    *force_timeout = g_force_timeout.load();
+    return g_wait_limit_ns.load();
 }
 
 int internal_lora_add(const void *x, int64_t ldx, const void *A, const void *B, int64_t M, int64_t K,

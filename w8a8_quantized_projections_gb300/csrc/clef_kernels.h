@@ -203,6 +203,10 @@ cudaError_t launch_swiglu_bf16(const uint16_t *y_gu, int64_t M, int64_t N, int64
 // set-up (SM count, status-word address), TMA tensor maps, and the calling
 // thread's last-error text.
 int internal_device(int *num_sms, unsigned int **status);
+// SMs that a compute launch may fill (the caller's budget), of the device's num_sms.
+int internal_launch_sms(int num_sms);
+// The time limit of device-side waits; *force_timeout: the test knob.
+uint64_t internal_wait_limit(int *force_timeout);
 // clef_lora_add's two launches (arguments already checked) with t at the
 // given dense [M][round_up(r, 64)] scratch: the same tile widths, wait limit
 // and test knob as the public call.

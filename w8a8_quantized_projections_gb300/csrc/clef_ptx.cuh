@@ -19,6 +19,7 @@ enum : unsigned int {
 enum WaitSite : unsigned int {
     kSiteTmaEmpty = 1, kSiteMmaFull = 2, kSiteMmaAccEmpty = 3, kSiteEpiAccFull = 4,
     kSiteConvRaw = 5, kSiteConvEmpty = 6, kSiteDrain = 7, kSiteQuantFull = 8,
+    kSiteKvLoad = 9, kSiteKvMma = 10, kSiteKvSoftmax = 11,
 };
 
 // The library-owned device status word lives in abi.cu; kernels receive its

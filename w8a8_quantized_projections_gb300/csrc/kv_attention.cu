@@ -15,14 +15,23 @@
 // sequence's own length alone, so the other sequences of a call do not change
 // a row's bits.
 //
+// Many rows are bound by the tensor cores and the exponentials:
+// kv_tile_kernel keeps 128 or 256 rows on chip and passes over the sequence's
+// tokens 128 at a time with tcgen05 products.
+//
 // Numbers.  Codes are widened to fp16, exactly (INT8 integers; e4m3 values are
 // multiples of 2^-9 up to 448).  A query row is scaled by a power of two to a
 // largest magnitude in [2^13, 2^14) and held in fp16: bf16 has fewer bits than
 // fp16, so only values under 2^-27 of the row's largest lose anything, less
-// than fp32 sums do.  Products are summed in fp32.  The softmax keeps two
-// running maxima: m of x for the sum of weights, and m2 of x + log2 vs for
-// the weights that multiply values, so the weights p * vs rounded to fp16 (11
-// bits against the output's 8) are at most 1 whatever the pages' scales are.
+// than fp32 sums do.  Products are summed in fp32.  The softmax's
+// reference is a running maximum m of x + log2 vs: the weights exp2(x + log2 vs
+// - m + 15) that multiply values, rounded to fp16 (11 bits against the output's
+// 8), are at most 2^15 whatever the pages' scales are, and only those under 2^-29
+// of the largest fall below fp16's normal numbers; the softmax's sum takes each
+// page's weights times 1 / vs.  A page whose value scale is zero counts with a
+// scale of 2^-60, small enough not to set the reference of the others, in the
+// sum, and with weights of zero.  (The value scales of a sequence are taken to lie
+// within 2^100 of one another.)
 #include <cstdint>
 
 #include <cuda_bf16.h>
@@ -41,22 +50,40 @@ namespace {
 constexpr int kWarps = 4;
 constexpr int kThreads = kWarps * 32;
 constexpr int kFewRows = 16;       // rows a key/value head up to which a sequence is split along its tokens
-constexpr int kMaxSplits = 64;
 constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLift = 15.0f;     // the largest weight of P is 2^kLift
 
 // Tokens of a split of a sequence of `len` tokens: short enough that one
-// sequence spreads over the SMs, long enough that the partial results (16 B
-// a value and split against 1 B a code) stay a small part of the traffic.
-__host__ __device__ inline int split_tokens(int len) {
-    if (len <= 2048) return 128;
-    if (len <= 8192) return 256;
-    if (len <= 32768) return 512;
-    const int t = (int)(((int64_t)len + kMaxSplits - 1) / kMaxSplits);
-    return (t + 511) / 512 * 512;
-}
+// sequence spreads over the SMs, long enough that the partial results (4 B
+// written and read a value and split, against 1 B a code) stay a small part of the traffic.
+__host__ __device__ inline int split_tokens(int len) { return len <= 1024 ? 128 : len <= 4096 ? 256 : len <= 16384 ? 512 : 1024; }
 __host__ __device__ inline int split_count(int len) {
     const int t = split_tokens(len);
-    return (int)(((int64_t)len + t - 1) / t);
+    return len / t + (len % t != 0);
+}
+constexpr int kMaxSplitTokens = 1024;
+
+// Rows that kv_tile_kernel keeps on chip at a time.
+__host__ __device__ constexpr int tile_rows(int dim) { return dim <= 128 ? 256 : 128; }
+
+// Splits of a sequence with more than kFewRows rows: while its row tiles leave
+// SMs idle (152 on this GPU; a fixed number, so that a row's bits do not follow
+// an SM budget), runs of at least 512 tokens, at most 16 of them.
+constexpr int kTileSlots = 152, kTileMaxSplits = 16;
+__host__ __device__ inline int tile_splits(int rows, int len, int heads, int dim) {
+    const int tiles = (rows + tile_rows(dim) - 1) / tile_rows(dim) * heads;
+    if (tiles < 1 || tiles > kTileSlots / 2) return 1;
+    const int steps = (len >> 7) + ((len & 127) != 0);       // of 128 tokens
+    int s = kTileSlots / tiles;
+    if (s > (steps + 3) / 4) s = (steps + 3) / 4;
+    if (s > kTileMaxSplits) s = kTileMaxSplits;
+    if (s <= 1) return 1;
+    const int per = (steps + s - 1) / s;      // equal splits, none of them empty
+    return (steps + per - 1) / per;
+}
+__host__ __device__ inline int tile_split_tokens(int len, int splits) {
+    const int steps = (len >> 7) + ((len & 127) != 0);
+    return (steps + splits - 1) / splits * 128;
 }
 
 struct AttnArgs {
@@ -70,10 +97,14 @@ struct AttnArgs {
     const int32_t *start;       // [seqs + 1] or null
     int rows, per_seq, group, q_heads, causal;
     float scale_log2;
-    float *part;                // [seqs * heads * row_cap][split_cap][dim] partial outputs
-    float *part_lse;            // [seqs * heads * row_cap][split_cap], base 2
-    int row_cap, split_cap;
+    // partial results of the sequences that are cut: each has part_units places
+    // of its own, place (head * rows + row) * splits + split
+    float *part;                // [seqs][part_units][dim]
+    float *part_lse;            // [seqs][part_units], base 2
+    int64_t part_units;
     unsigned int *status;
+    uint64_t wait_limit_ns;
+    int force_timeout;
 };
 
 __device__ __forceinline__ void query_rows(const AttnArgs &a, int b, int &row0, int &n) {
@@ -102,7 +133,7 @@ __device__ __forceinline__ float ex2(float x) {
 // 2^(a - b) for running maxima, 0 when a is -inf (b may be -inf then too)
 __device__ __forceinline__ float ex2_diff(float a, float b) { return a == -INFINITY ? 0.0f : ex2(a - b); }
 
-__device__ __forceinline__ void mma_f16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+__device__ __forceinline__ void mma_regs(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
     asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
         : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
@@ -153,7 +184,25 @@ template <int D>
 __host__ __device__ constexpr int step_tiles() { return D <= 128 ? 2 : 1; }
 
 template <int D, int NT>
-__host__ __device__ constexpr int split_smem_floats() { return kWarps * NT * 8 * (D + 3); }
+__host__ __device__ constexpr int split_smem_floats() { return kWarps * NT * 8 * (D + 2); }
+
+// What a CTA needs of an item before it can stream: made while the item before
+// is streamed, so that no item waits for it.
+template <int D, int NT>
+struct SplitPrep {
+    static constexpr int kRows = NT * 8;
+    static constexpr int kPitch = D + 4;        // fp16 elements: the lanes' 8-byte reads meet every bank once
+    static constexpr int kPages = kMaxSplitTokens / 16;
+    uint16_t q[kRows * kPitch];
+    float qs[kRows];
+    int end[kRows];                             // tokens a row sees
+    int page[kPages];
+    float ks[kPages], lv[kPages], inv[kPages];  // key scale; log2 of the value scale; its reciprocal (0: no weight)
+};
+
+struct SplitItem {
+    int b, row0, n, len, rows, head, split, splits, r0, rn, tok0, tok1;
+};
 
 // One item: a split of a sequence for one key/value head and NT * 8 of its
 // rows (row r = query i * G + head g).
@@ -167,21 +216,24 @@ __host__ __device__ constexpr int split_smem_floats() { return kWarps * NT * 8 *
 // two bytes 2 j and 2 j + 1 of its run are rows g and g + 8 of tile j.  P
 // leaves S^T's layout for that of the right-hand operand by an 8 x 8
 // transpose.  No data passes through shared memory but the queries.
+//
+// A warp's registers hold a step of keys and one of values; each is loaded
+// again, for the next step, as soon as its products are done.
+template <int D, int NT>
+__host__ __device__ constexpr int split_ctas() { return D * NT <= 64 ? 4 : D * NT <= 128 ? 3 : 2; }     // of an SM, by registers
+
 template <int KIND, int D, int NT>
-__global__ void __launch_bounds__(kThreads) kv_split_kernel(const AttnArgs a) {
+__global__ void __launch_bounds__(kThreads, split_ctas<D, NT>()) kv_split_kernel(const AttnArgs a) {
+    using Prep = SplitPrep<D, NT>;
     constexpr int ROWS = NT * 8, TILES = step_tiles<D>(), STEP = TILES * 16, KB = D / 64, MT = D / 16;
     constexpr int VW = D / 32;               // 32-bit words of values a lane holds of each token
-    constexpr int QPITCH = D + 4;            // fp16 elements: the lanes' 8-byte reads meet every bank once
+    constexpr int PER = D / 32;              // elements of a query row a lane has
     extern __shared__ __align__(16) uint8_t smem[];
-    __shared__ __align__(16) uint16_t s_q[ROWS * QPITCH];
-    __shared__ float s_qs[ROWS];
-    __shared__ int s_end[ROWS];              // tokens a row sees
-    __shared__ int s_page[64];               // pages of the split (at most 1,024 tokens at a time)
-    __shared__ float s_ks[64], s_lv[64];
-    float *s_o = reinterpret_cast<float *>(smem);          // [kWarps][ROWS][D], then m, l, m2
-    float *s_m = s_o + kWarps * ROWS * D, *s_l = s_m + kWarps * ROWS, *s_m2 = s_l + kWarps * ROWS;
-    int *s_items = reinterpret_cast<int *>(smem + split_smem_floats<D, NT>() * 4);   // [seqs + 1] first item of each sequence
+    __shared__ __align__(16) Prep s_prep[2];
     __shared__ int s_scan[kWarps], s_total;
+    float *s_o = reinterpret_cast<float *>(smem);          // [kWarps][ROWS][D], then m, l
+    float *s_m = s_o + kWarps * ROWS * D, *s_l = s_m + kWarps * ROWS;
+    int *s_items = reinterpret_cast<int *>(smem + split_smem_floats<D, NT>() * 4);   // [seqs + 1] first item of each sequence
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
     const int log2 = a.pool.page_log2, H = a.pool.heads;
     pdl_wait();
@@ -194,13 +246,10 @@ __global__ void __launch_bounds__(kThreads) kv_split_kernel(const AttnArgs a) {
         if (b0 + tid < a.tab.seqs) {
             int row0, n;
             query_rows(a, b0 + tid, row0, n);
-            if (n > 0) {
-                const int len = kv_length(a.tab, b0 + tid, log2, a.status);
-                const int rows = n * a.group;
-                // a sequence without tokens still has rows of zeros to write
-                const int sp = rows <= kFewRows ? max(1, split_count(len)) : 1;
-                cnt = sp * ((rows + ROWS - 1) / ROWS) * H;
-            }
+            const int rows = n * a.group;
+            // a sequence without tokens still has rows of zeros to write
+            if (rows > 0 && rows <= kFewRows)
+                cnt = max(1, split_count(kv_length(a.tab, b0 + tid, log2, a.status))) * ((rows + ROWS - 1) / ROWS) * H;
         }
         int inc = cnt;
 #pragma unroll
@@ -221,63 +270,168 @@ __global__ void __launch_bounds__(kThreads) kv_split_kernel(const AttnArgs a) {
         if (tid == 0) s_total += all;
         __syncthreads();
     }
-    if (tid == 0) s_items[a.tab.seqs] = s_total;
-    __syncthreads();
     const int items = s_total;
+    if ((int)blockIdx.x >= items) return;
 
-    for (int item = blockIdx.x; item < items; item += gridDim.x) {
-        // the item's sequence, split, head and rows
-        int b = 0;
-        {
-            int hi = a.tab.seqs;
-            while (hi - b > 1) {
-                const int mid = (b + hi) >> 1;
-                if (s_items[mid] <= item) b = mid;
-                else hi = mid;
-            }
+    const auto item_at = [&](int item) {
+        SplitItem t;
+        int b = 0, hi = a.tab.seqs;
+        while (hi - b > 1) {
+            const int mid = (b + hi) >> 1;
+            if (s_items[mid] <= item) b = mid;
+            else hi = mid;
         }
-        int row0, n;
-        query_rows(a, b, row0, n);
-        const int len = kv_length(a.tab, b, log2, a.status);
-        const int rows = n * a.group, groups = (rows + ROWS - 1) / ROWS;
+        t.b = b;
+        query_rows(a, b, t.row0, t.n);
+        t.len = kv_length(a.tab, b, log2, a.status);
+        t.rows = t.n * a.group;
+        const int groups = (t.rows + ROWS - 1) / ROWS;
         int rest = item - s_items[b];
-        const int head = rest % H;
+        t.head = rest % H;
         rest /= H;
-        const int rg = rest % groups, split = rest / groups;
-        const bool few = rows <= kFewRows;
-        const int splits = few ? max(1, split_count(len)) : 1;
-        const int tok0 = few ? split * split_tokens(len) : 0;
-        int tok1 = few ? min(len, tok0 + split_tokens(len)) : len;
-        const int r0 = rg * ROWS, rn = min(ROWS, rows - r0);
-        if (a.causal) tok1 = min(tok1, max(0, len - n + (r0 + rn - 1) / a.group + 1));   // what the last row sees
+        t.split = rest / groups;
+        t.r0 = (rest - t.split * groups) * ROWS;
+        t.rn = min(ROWS, t.rows - t.r0);
+        t.splits = max(1, split_count(t.len));
+        t.tok0 = t.split * split_tokens(t.len);
+        t.tok1 = min(t.len, t.tok0 + split_tokens(t.len));
+        if (a.causal) t.tok1 = min(t.tok1, max(0, t.len - t.n + (t.r0 + t.rn - 1) / a.group + 1));   // what the last row sees
+        return t;
+    };
 
-        __syncthreads();   // the item before is done with shared memory
-        // queries: row's largest magnitude to [2^13, 2^14), fp16
-        for (int r = warp; r < ROWS; r += kWarps) {
-            const int i = (r0 + r) / a.group, hq = head * a.group + (r0 + r) - i * a.group;
-            const uint16_t *src = a.q + (int64_t)(row0 + i) * a.ldq + (int64_t)hq * a.ldq_head;
-            float v[D / 32], top = 0.0f;
+    // the item's preparation in three parts, with a load's latency between them
+    uint32_t pq[ROWS / kWarps][PER / 2];
+    int p_page = -1;
+    float p_ks = 0.0f, p_vs = 0.0f;
+    const auto prep_rows = [&](const SplitItem &it) {
 #pragma unroll
-            for (int k = 0; k < D / 32; ++k) {
-                v[k] = r < rn ? __uint_as_float((uint32_t)*(src + lane + 32 * k) << 16) : 0.0f;
-                top = fmaxf(top, fabsf(v[k]));
-            }
-            top = __uint_as_float(__reduce_max_sync(0xFFFFFFFFu, __float_as_uint(top)));
-            const int e = top > 0.0f ? max(-100, min(120, 13 - (int)((__float_as_uint(top) >> 23) & 0xFF) + 127)) : 0;
-            const float up = __uint_as_float((uint32_t)(127 + e) << 23);
+        for (int k = 0; k < ROWS / kWarps; ++k) {
+            const int r = warp + k * kWarps;
 #pragma unroll
-            for (int k = 0; k < D / 32; ++k) {
-                const __half h = __float2half_rn(v[k] * up);
-                s_q[r * QPITCH + lane + 32 * k] = *reinterpret_cast<const uint16_t *>(&h);
-            }
-            if (lane == 0) {
-                s_qs[r] = a.scale_log2 * __uint_as_float((uint32_t)(127 - e) << 23);
-                s_end[r] = r >= rn ? 0 : a.causal ? max(0, len - n + i + 1) : len;
+            for (int w = 0; w < PER / 2; ++w) pq[k][w] = 0u;
+            if (r < it.rn) {
+                const int i = (it.r0 + r) / a.group, hq = it.head * a.group + (it.r0 + r) - i * a.group;
+                const uint32_t *src = reinterpret_cast<const uint32_t *>(a.q + (int64_t)(it.row0 + i) * a.ldq + (int64_t)hq * a.ldq_head);
+#pragma unroll
+                for (int w = 0; w < PER / 2; ++w) pq[k][w] = src[lane + 32 * w];
             }
         }
+        p_page = -1;
+        if (tid < Prep::kPages && it.tok0 + (tid << log2) < it.tok1) {
+            p_page = a.tab.table[(int64_t)it.b * a.tab.ldt + (it.tok0 >> log2) + tid];
+            if (p_page < 0 || p_page >= a.pool.pages) {
+                record_status(a.status, kStatusBadPage);
+                p_page = -1;
+            }
+        }
+    };
+    const auto prep_scales = [&](const SplitItem &it) {
+        p_ks = p_vs = 0.0f;
+        if (p_page >= 0) {
+            const int64_t tile = (int64_t)p_page * H + it.head;
+            p_ks = a.pool.scales[tile];
+            p_vs = a.pool.scales[a.pool.plane_scales + tile];
+        }
+    };
+    const auto prep_store = [&](const SplitItem &it, Prep &to) {
+#pragma unroll
+        for (int k = 0; k < ROWS / kWarps; ++k) {
+            const int r = warp + k * kWarps;
+            // the row's largest magnitude (bf16 bits order like integers) to [2^13, 2^14), in fp16
+            uint32_t top = 0;
+#pragma unroll
+            for (int w = 0; w < PER / 2; ++w) top = __vmaxu2(top, pq[k][w] & 0x7FFF7FFFu);
+            top = __reduce_max_sync(0xFFFFFFFFu, max(top & 0xFFFFu, top >> 16)) << 16;
+            const int e = top ? max(-100, min(120, 13 - (int)(top >> 23) + 127)) : 0;
+            // a negative scale turns the queries, so that x grows with S
+            float up = __uint_as_float((uint32_t)(127 + e) << 23);
+            if (a.scale_log2 < 0.0f) up = -up;
+#pragma unroll
+            for (int w = 0; w < PER / 2; ++w)
+                *reinterpret_cast<uint32_t *>(&to.q[r * Prep::kPitch + 2 * (lane + 32 * w)]) =
+                    pack_half(__uint_as_float(pq[k][w] << 16) * up, __uint_as_float(pq[k][w] & 0xFFFF0000u) * up);
+            if (lane == 0) {
+                const int i = (it.r0 + r) / a.group;
+                to.qs[r] = fabsf(a.scale_log2) * __uint_as_float((uint32_t)(127 - e) << 23);
+                to.end[r] = r >= it.rn || !a.causal ? it.len : max(0, it.len - it.n + i + 1);
+            }
+        }
+        if (tid < Prep::kPages) {
+            // a page whose value scale is zero counts in the sum with a small scale, and gives no weight
+            const float vs = p_vs == 0.0f ? 0x1p-60f : p_vs;
+            to.page[tid] = p_page;
+            to.ks[tid] = p_ks;
+            to.lv[tid] = log2f(vs);
+            to.inv[tid] = p_vs == 0.0f ? -0x1p60f : __fdiv_rn(1.0f, vs);      // the sign marks it
+        }
+    };
 
-        float acc[NT][MT][4];
-        float m[NT][2], m2[NT][2], l[NT][2];
+    uint4 kc[TILES][2][KB];
+    uint32_t vc[TILES][4][VW];
+    const auto load_k = [&](const SplitItem &it, const Prep &pr, int s0) {
+#pragma unroll
+        for (int u = 0; u < TILES; ++u) {
+            const int tk = s0 + u * 16, page = tk < it.tok1 ? pr.page[(tk - it.tok0) >> log2] : -1;
+            const uint8_t *base = a.pool.codes + ((((int64_t)page * H + it.head) << log2) + (tk & (a.pool.page - 1)) + g) * D + t * 16;
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+#pragma unroll
+                for (int k = 0; k < KB; ++k)
+                    kc[u][h][k] = page >= 0 ? load_codes(base + h * 8 * D + k * 64) : make_uint4(0, 0, 0, 0);
+        }
+    };
+    const auto load_v = [&](const SplitItem &it, const Prep &pr, int s0) {
+#pragma unroll
+        for (int u = 0; u < TILES; ++u) {
+            const int tk = s0 + u * 16, page = tk < it.tok1 ? pr.page[(tk - it.tok0) >> log2] : -1;
+            const uint8_t *base = a.pool.codes + a.pool.plane_codes +
+                                  ((((int64_t)page * H + it.head) << log2) + (tk & (a.pool.page - 1)) + 2 * t) * D + g * (D >= 128 ? 16 : 8);
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+                const int row = (c & 1) + 8 * (c >> 1);
+                // what lies past the sequence's end may be anything, NaN codes included: read as zeros
+                const bool in = page >= 0 && tk + 2 * t + row < it.len;
+                if constexpr (D == 64) {
+                    const uint2 v = in ? load_codes8(base + row * D) : make_uint2(0, 0);
+                    vc[u][c][0] = v.x;
+                    vc[u][c][1] = v.y;
+                } else {
+#pragma unroll
+                    for (int k = 0; k < D / 128; ++k) {
+                        const uint4 v = in ? load_codes(base + row * D + k * 128) : make_uint4(0, 0, 0, 0);
+                        vc[u][c][4 * k] = v.x;
+                        vc[u][c][4 * k + 1] = v.y;
+                        vc[u][c][4 * k + 2] = v.z;
+                        vc[u][c][4 * k + 3] = v.w;
+                    }
+                }
+            }
+        }
+    };
+
+    SplitItem it = item_at(blockIdx.x);
+    prep_rows(it);
+    prep_scales(it);
+    prep_store(it, s_prep[0]);
+    __syncthreads();
+    int s0 = it.tok0 + warp * STEP;
+    if (s0 < it.tok1) {
+        load_k(it, s_prep[0], s0);
+        load_v(it, s_prep[0], s0);
+    }
+    int turn = 0;
+    for (int item = blockIdx.x; item < items; item += gridDim.x, turn ^= 1) {
+        const Prep &pr = s_prep[turn];
+        const bool more = item + (int)gridDim.x < items;
+        SplitItem next = it;
+        if (more) {
+            next = item_at(item + gridDim.x);
+            prep_rows(next);
+        }
+        bool scales_due = more;
+
+        float acc[NT][MT][4], m[NT][2], l[NT][2], qs[NT][2];
+        int end[NT][2];
 #pragma unroll
         for (int x = 0; x < NT; ++x) {
 #pragma unroll
@@ -286,195 +440,140 @@ __global__ void __launch_bounds__(kThreads) kv_split_kernel(const AttnArgs a) {
                 for (int i = 0; i < 4; ++i) acc[x][k][i] = 0.0f;
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
-                m[x][i] = m2[x][i] = -INFINITY;
+                m[x][i] = -INFINITY;
                 l[x][i] = 0.0f;
+                qs[x][i] = pr.qs[x * 8 + 2 * t + i];
+                end[x][i] = min(pr.end[x * 8 + 2 * t + i], it.tok1);
             }
         }
+        int all_see = min(end[0][0], end[0][1]);
+        if (NT == 2) all_see = min(all_see, min(end[NT - 1][0], end[NT - 1][1]));
+        all_see = __reduce_min_sync(0xFFFFFFFFu, all_see);
 
-        // at most 1,024 tokens at a time, whose pages fit the arrays in shared memory
-        for (int c0 = tok0; c0 < tok1; c0 += 1024) {
-            const int c1 = min(tok1, c0 + 1024);
-            if (c0 > tok0) __syncthreads();
-            for (int p = tid; p <= ((c1 - 1) >> log2) - (c0 >> log2); p += kThreads) {
-                int page = a.tab.table[(int64_t)b * a.tab.ldt + (c0 >> log2) + p];
-                float ks = 0.0f, lv = -INFINITY;
-                if (page < 0 || page >= a.pool.pages) {
-                    record_status(a.status, kStatusBadPage);
-                    page = -1;
-                } else {
-                    const int64_t tile = (int64_t)page * H + head;
-                    ks = a.pool.scales[tile];
-                    lv = log2f(a.pool.scales[a.pool.plane_scales + tile]);
-                }
-                s_page[p] = page;
-                s_ks[p] = ks;
-                s_lv[p] = lv;
-            }
-            __syncthreads();
-
-            uint4 kc[TILES][2][KB];
-            uint32_t vc[TILES][4][VW];
-            const auto load_k = [&](int s0) {
+        for (; s0 < it.tok1; s0 += kWarps * STEP) {
+            const int s1 = s0 + kWarps * STEP;
+            // S^T
+            float s[NT][TILES][4];
 #pragma unroll
-                for (int u = 0; u < TILES; ++u) {
-                    const int tk = s0 + u * 16, page = tk < c1 ? s_page[(tk - c0) >> log2] : -1;
-                    const uint8_t *base = a.pool.codes + ((((int64_t)page * H + head) << log2) + (tk & (a.pool.page - 1)) + g) * D + t * 16;
-#pragma unroll
-                    for (int h = 0; h < 2; ++h)
-#pragma unroll
-                        for (int k = 0; k < KB; ++k)
-                            kc[u][h][k] = page >= 0 ? load_codes(base + h * 8 * D + k * 64) : make_uint4(0, 0, 0, 0);
-                }
-            };
-            const auto load_v = [&](int s0) {
-#pragma unroll
-                for (int u = 0; u < TILES; ++u) {
-                    const int tk = s0 + u * 16, page = tk < c1 ? s_page[(tk - c0) >> log2] : -1;
-                    const uint8_t *base = a.pool.codes + a.pool.plane_codes +
-                                          ((((int64_t)page * H + head) << log2) + (tk & (a.pool.page - 1)) + 2 * t) * D + g * (D >= 128 ? 16 : 8);
-#pragma unroll
-                    for (int c = 0; c < 4; ++c) {
-                        const int row = (c & 1) + 8 * (c >> 1);
-                        // what lies past the sequence's end may be anything, NaN codes included: read as zeros
-                        const bool in = page >= 0 && tk + 2 * t + row < len;
-                        if constexpr (D == 64) {
-                            const uint2 v = in ? load_codes8(base + row * D) : make_uint2(0, 0);
-                            vc[u][c][0] = v.x;
-                            vc[u][c][1] = v.y;
-                        } else {
-#pragma unroll
-                            for (int k = 0; k < D / 128; ++k) {
-                                const uint4 v = in ? load_codes(base + row * D + k * 128) : make_uint4(0, 0, 0, 0);
-                                vc[u][c][4 * k] = v.x;
-                                vc[u][c][4 * k + 1] = v.y;
-                                vc[u][c][4 * k + 2] = v.z;
-                                vc[u][c][4 * k + 3] = v.w;
-                            }
-                        }
-                    }
-                }
-            };
-
-            int s0 = c0 + warp * STEP;
-            if (s0 < c1) {
-                load_k(s0);
-                load_v(s0);
-            }
-            for (; s0 < c1; s0 += kWarps * STEP) {
-                const int next = s0 + kWarps * STEP;
-                // S^T
-                float s[NT][TILES][4];
-#pragma unroll
-                for (int x = 0; x < NT; ++x)
-#pragma unroll
-                    for (int u = 0; u < TILES; ++u)
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) s[x][u][i] = 0.0f;
-#pragma unroll
-                for (int k = 0; k < KB; ++k) {
-#pragma unroll
-                    for (int w = 0; w < 4; ++w) {
-                        uint2 qf[NT];
-#pragma unroll
-                        for (int x = 0; x < NT; ++x)
-                            qf[x] = *reinterpret_cast<const uint2 *>(&s_q[(x * 8 + g) * QPITCH + k * 64 + t * 16 + w * 4]);
-#pragma unroll
-                        for (int u = 0; u < TILES; ++u) {
-                            uint32_t f[4];
-                            const uint4 &ka = kc[u][0][k], &kb = kc[u][1][k];
-                            widen4<KIND>(w == 0 ? ka.x : w == 1 ? ka.y : w == 2 ? ka.z : ka.w, f[0], f[2]);
-                            widen4<KIND>(w == 0 ? kb.x : w == 1 ? kb.y : w == 2 ? kb.z : kb.w, f[1], f[3]);
-#pragma unroll
-                            for (int x = 0; x < NT; ++x) mma_f16(s[x][u], f, qf[x].x, qf[x].y);
-                        }
-                    }
-                }
-                if (next < c1) load_k(next);
-
-                // softmax: this lane has rows 2 t, 2 t + 1 and tokens g, g + 8 of each tile
-                uint32_t pf[NT][TILES][2];
-                float lv[TILES], ks[TILES];
-#pragma unroll
-                for (int u = 0; u < TILES; ++u) {
-                    const int p = min(s0 + u * 16, c1 - 1) - c0;
-                    lv[u] = s_lv[p >> log2];
-                    ks[u] = s_ks[p >> log2];
-                }
-#pragma unroll
-                for (int x = 0; x < NT; ++x) {
-                    float top[2] = {-INFINITY, -INFINITY}, top2[2] = {-INFINITY, -INFINITY};
-#pragma unroll
-                    for (int u = 0; u < TILES; ++u)
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            const int row = x * 8 + 2 * t + (i & 1), tk = s0 + u * 16 + g + 8 * (i >> 1);
-                            float v = s[x][u][i] * (s_qs[row] * ks[u]);
-                            if (tk >= min(s_end[row], c1)) v = -INFINITY;
-                            s[x][u][i] = v;
-                            top[i & 1] = fmaxf(top[i & 1], v);
-                            top2[i & 1] = fmaxf(top2[i & 1], v + lv[u]);
-                        }
-#pragma unroll
-                    for (int o = 4; o < 32; o <<= 1)
-#pragma unroll
-                        for (int i = 0; i < 2; ++i) {
-                            top[i] = fmaxf(top[i], __shfl_xor_sync(0xFFFFFFFFu, top[i], o));
-                            top2[i] = fmaxf(top2[i], __shfl_xor_sync(0xFFFFFFFFu, top2[i], o));
-                        }
-                    float cl[2], co[2], base[2], lift[2][TILES];
-#pragma unroll
-                    for (int i = 0; i < 2; ++i) {
-                        const float mn = fmaxf(m[x][i], top[i]), mn2 = fmaxf(m2[x][i], top2[i]);
-                        cl[i] = ex2_diff(m[x][i], mn);
-                        co[i] = ex2_diff(m2[x][i], mn2);
-                        m[x][i] = mn;
-                        m2[x][i] = mn2;
-                        base[i] = mn == -INFINITY ? 0.0f : mn;
-                        l[x][i] *= cl[i];
-#pragma unroll
-                        for (int u = 0; u < TILES; ++u)
-                            lift[i][u] = (mn2 == -INFINITY || lv[u] == -INFINITY) ? 0.0f : ex2(fminf(base[i] - mn2 + lv[u], 126.0f));
-                    }
-                    if (__any_sync(0xFFFFFFFFu, co[0] != 1.0f || co[1] != 1.0f)) {
-#pragma unroll
-                        for (int k = 0; k < MT; ++k)
-#pragma unroll
-                            for (int i = 0; i < 4; ++i) acc[x][k][i] *= co[i & 1];
-                    }
-#pragma unroll
-                    for (int u = 0; u < TILES; ++u) {
-                        float p[4];
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            p[i] = ex2(s[x][u][i] - base[i & 1]);
-                            l[x][i & 1] += p[i];
-                        }
-                        pf[x][u][0] = transpose8x8(pack_half(p[0] * lift[0][u], p[1] * lift[1][u]));
-                        pf[x][u][1] = transpose8x8(pack_half(p[2] * lift[0][u], p[3] * lift[1][u]));
-                    }
-                }
-                // O^T
+            for (int x = 0; x < NT; ++x)
 #pragma unroll
                 for (int u = 0; u < TILES; ++u)
 #pragma unroll
-                    for (int w = 0; w < VW; ++w) {
-                        const uint32_t v0 = vc[u][0][w], v1 = vc[u][1][w], v2 = vc[u][2][w], v3 = vc[u][3][w];
-                        uint32_t fa[4], fb[4];   // bytes 0, 1 and bytes 2, 3 of the four tokens
-                        widen4<KIND>(__byte_perm(v0, v1, 0x5140), fa[0], fa[1]);
-                        widen4<KIND>(__byte_perm(v2, v3, 0x5140), fa[2], fa[3]);
-                        widen4<KIND>(__byte_perm(v0, v1, 0x7362), fb[0], fb[1]);
-                        widen4<KIND>(__byte_perm(v2, v3, 0x7362), fb[2], fb[3]);
+                    for (int i = 0; i < 4; ++i) s[x][u][i] = 0.0f;
 #pragma unroll
-                        for (int x = 0; x < NT; ++x) {
-                            mma_f16(acc[x][2 * w], fa, pf[x][u][0], pf[x][u][1]);
-                            mma_f16(acc[x][2 * w + 1], fb, pf[x][u][0], pf[x][u][1]);
-                        }
+            for (int k = 0; k < KB; ++k) {
+#pragma unroll
+                for (int w = 0; w < 4; ++w) {
+                    uint2 qf[NT];
+#pragma unroll
+                    for (int x = 0; x < NT; ++x)
+                        qf[x] = *reinterpret_cast<const uint2 *>(&pr.q[(x * 8 + g) * Prep::kPitch + k * 64 + t * 16 + w * 4]);
+#pragma unroll
+                    for (int u = 0; u < TILES; ++u) {
+                        uint32_t f[4];
+                        const uint4 &ka = kc[u][0][k], &kb = kc[u][1][k];
+                        widen4<KIND>(w == 0 ? ka.x : w == 1 ? ka.y : w == 2 ? ka.z : ka.w, f[0], f[2]);
+                        widen4<KIND>(w == 0 ? kb.x : w == 1 ? kb.y : w == 2 ? kb.z : kb.w, f[1], f[3]);
+#pragma unroll
+                        for (int x = 0; x < NT; ++x) mma_regs(s[x][u], f, qf[x].x, qf[x].y);
                     }
-                if (next < c1) load_v(next);
+                }
             }
+            if (s1 < it.tok1) load_k(it, pr, s1);
+            if (scales_due) {
+                prep_scales(next);
+                scales_due = false;
+            }
+
+            // softmax: this lane has rows 2 t, 2 t + 1 and tokens g, g + 8 of each tile
+            uint32_t pf[NT][TILES][2];
+            float ks[TILES], lv[TILES], inv[TILES];
+#pragma unroll
+            for (int u = 0; u < TILES; ++u) {
+                const int p = (min(s0 + u * 16, it.tok1 - 1) - it.tok0) >> log2;
+                ks[u] = pr.ks[p];
+                lv[u] = pr.lv[p];
+                inv[u] = pr.inv[p];
+            }
+            const bool whole = s0 + STEP <= all_see;
+#pragma unroll
+            for (int x = 0; x < NT; ++x) {
+                if (!whole) {
+#pragma unroll
+                    for (int u = 0; u < TILES; ++u)
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)
+                            if (s0 + u * 16 + g + 8 * (i >> 1) >= end[x][i & 1]) s[x][u][i] = -INFINITY;
+                }
+                // the largest x + log2 vs
+                float top[2] = {-INFINITY, -INFINITY};
+#pragma unroll
+                for (int u = 0; u < TILES; ++u)
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        const float v = fmaxf(s[x][u][i], s[x][u][i + 2]);
+                        if (whole || v != -INFINITY) top[i] = fmaxf(top[i], fmaf(v, qs[x][i] * ks[u], lv[u]));
+                    }
+#pragma unroll
+                for (int o = 4; o < 32; o <<= 1)
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) top[i] = fmaxf(top[i], __shfl_xor_sync(0xFFFFFFFFu, top[i], o));
+                float co[2], ref[2];
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    const float mn = fmaxf(m[x][i], top[i]);
+                    co[i] = ex2_diff(m[x][i], mn);
+                    m[x][i] = mn;
+                    ref[i] = mn == -INFINITY ? 0.0f : mn - kLift;
+                    l[x][i] *= co[i];
+                }
+                if (__any_sync(0xFFFFFFFFu, co[0] != 1.0f || co[1] != 1.0f)) {
+#pragma unroll
+                    for (int k = 0; k < MT; ++k)
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) acc[x][k][i] *= co[i & 1];
+                }
+#pragma unroll
+                for (int u = 0; u < TILES; ++u) {
+                    float p[4];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const float v = fmaf(s[x][u][i], qs[x][i & 1] * ks[u], lv[u] - ref[i & 1]);
+                        p[i] = ex2(whole || s[x][u][i] != -INFINITY ? v : -INFINITY);
+                    }
+                    l[x][0] = fmaf(p[0] + p[2], fabsf(inv[u]), l[x][0]);
+                    l[x][1] = fmaf(p[1] + p[3], fabsf(inv[u]), l[x][1]);
+                    const uint32_t keep = inv[u] < 0.0f ? 0u : 0xFFFFFFFFu;
+                    pf[x][u][0] = transpose8x8(pack_half(p[0], p[1]) & keep);
+                    pf[x][u][1] = transpose8x8(pack_half(p[2], p[3]) & keep);
+                }
+            }
+            // O^T
+#pragma unroll
+            for (int u = 0; u < TILES; ++u)
+#pragma unroll
+                for (int w = 0; w < VW; ++w) {
+                    const uint32_t v0 = vc[u][0][w], v1 = vc[u][1][w], v2 = vc[u][2][w], v3 = vc[u][3][w];
+                    uint32_t fa[4], fb[4];   // bytes 0, 1 and bytes 2, 3 of the four tokens
+                    widen4<KIND>(__byte_perm(v0, v1, 0x5140), fa[0], fa[1]);
+                    widen4<KIND>(__byte_perm(v2, v3, 0x5140), fa[2], fa[3]);
+                    widen4<KIND>(__byte_perm(v0, v1, 0x7362), fb[0], fb[1]);
+                    widen4<KIND>(__byte_perm(v2, v3, 0x7362), fb[2], fb[3]);
+#pragma unroll
+                    for (int x = 0; x < NT; ++x) {
+                        mma_regs(acc[x][2 * w], fa, pf[x][u][0], pf[x][u][1]);
+                        mma_regs(acc[x][2 * w + 1], fb, pf[x][u][0], pf[x][u][1]);
+                    }
+                }
+            if (s1 < it.tok1) load_v(it, pr, s1);
+        }
+        if (more) {
+            if (scales_due) prep_scales(next);
+            prep_store(next, s_prep[turn ^ 1]);
         }
 
         // the warps' results meet in shared memory
+        __syncthreads();      // which the item before is done with
 #pragma unroll
         for (int x = 0; x < NT; ++x) {
 #pragma unroll
@@ -485,7 +584,6 @@ __global__ void __launch_bounds__(kThreads) kv_split_kernel(const AttnArgs a) {
                     const int row = x * 8 + 2 * t + i;
                     s_m[warp * ROWS + row] = m[x][i];
                     s_l[warp * ROWS + row] = l[x][i];
-                    s_m2[warp * ROWS + row] = m2[x][i];
                 }
             }
 #pragma unroll
@@ -499,24 +597,31 @@ __global__ void __launch_bounds__(kThreads) kv_split_kernel(const AttnArgs a) {
                 }
         }
         __syncthreads();
-        for (int r = warp; r < rn; r += kWarps) {
+        const SplitItem done = it;
+        it = next;
+        s0 = it.tok0 + warp * STEP;
+        if (more && s0 < it.tok1) {
+            load_k(it, s_prep[turn ^ 1], s0);
+            load_v(it, s_prep[turn ^ 1], s0);
+        }
+        for (int r = warp; r < done.rn; r += kWarps) {
             float mm = -INFINITY, ll = 0.0f;
 #pragma unroll
             for (int w = 0; w < kWarps; ++w) mm = fmaxf(mm, s_m[w * ROWS + r]);
             float f[kWarps];
 #pragma unroll
             for (int w = 0; w < kWarps; ++w) {
-                ll += s_l[w * ROWS + r] * ex2_diff(s_m[w * ROWS + r], mm);
-                f[w] = mm == -INFINITY ? 0.0f : ex2_diff(s_m2[w * ROWS + r], mm);
+                f[w] = ex2_diff(s_m[w * ROWS + r], mm);
+                ll = fmaf(s_l[w * ROWS + r], f[w], ll);
             }
             const float inv = ll > 0.0f ? __fdiv_rn(1.0f, ll) : 0.0f;
-            const float lse = ll > 0.0f ? mm + log2f(ll) : -INFINITY;
-            const int i = (r0 + r) / a.group, hq = head * a.group + (r0 + r) - i * a.group;
-            const int64_t slot = ((int64_t)b * H + head) * a.row_cap + r0 + r;
-            if (splits > 1) {
-                if (lane == 0) a.part_lse[slot * a.split_cap + split] = lse;
+            const float lse = ll > 0.0f ? mm - kLift + log2f(ll) : -INFINITY;
+            const int i = (done.r0 + r) / a.group, hq = done.head * a.group + (done.r0 + r) - i * a.group;
+            const int64_t place = done.b * a.part_units + ((int64_t)done.head * done.rows + done.r0 + r) * done.splits + done.split;
+            if (done.splits > 1) {
+                if (lane == 0) a.part_lse[place] = lse;
             } else if (a.lse && lane == 0) {
-                a.lse[(int64_t)(row0 + i) * a.q_heads + hq] = lse == -INFINITY ? -INFINITY : lse * (1.0f / kLog2e);
+                a.lse[(int64_t)(done.row0 + i) * a.q_heads + hq] = lse == -INFINITY ? -INFINITY : lse * (1.0f / kLog2e);
             }
 #pragma unroll
             for (int k = 0; k < D / 64; ++k) {
@@ -525,16 +630,16 @@ __global__ void __launch_bounds__(kThreads) kv_split_kernel(const AttnArgs a) {
 #pragma unroll
                 for (int w = 0; w < kWarps; ++w) {
                     const float2 v = *reinterpret_cast<const float2 *>(&s_o[(w * ROWS + r) * D + d]);
-                    o0 += v.x * f[w];
-                    o1 += v.y * f[w];
+                    o0 = fmaf(v.x, f[w], o0);
+                    o1 = fmaf(v.y, f[w], o1);
                 }
                 o0 *= inv;
                 o1 *= inv;
-                if (splits > 1) {
-                    *reinterpret_cast<float2 *>(a.part + (slot * a.split_cap + split) * D + d) = make_float2(o0, o1);
+                if (done.splits > 1) {
+                    *reinterpret_cast<float2 *>(a.part + place * D + d) = make_float2(o0, o1);
                 } else {
                     const __nv_bfloat162 h = __floats2bfloat162_rn(o0, o1);
-                    *reinterpret_cast<__nv_bfloat162 *>(a.out + (int64_t)(row0 + i) * a.ldo + (int64_t)hq * a.ldo_head + d) = h;
+                    *reinterpret_cast<__nv_bfloat162 *>(a.out + (int64_t)(done.row0 + i) * a.ldo + (int64_t)hq * a.ldo_head + d) = h;
                 }
             }
         }
@@ -542,55 +647,921 @@ __global__ void __launch_bounds__(kThreads) kv_split_kernel(const AttnArgs a) {
     pdl_launch_dependents();
 }
 
-// Joins the splits of each row: a warp a row, the splits in order.
+// ---------------------------------------------------------------- many rows
+
+constexpr float kSlack = 4.0f;        // how far a row's maximum may outgrow its reference (log2)
+
+// Roles, shared memory and tensor memory of kv_tile_kernel.
 template <int D>
-__global__ void __launch_bounds__(kThreads) kv_join_kernel(const AttnArgs a) {
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    pdl_wait();
-    const int64_t slots = (int64_t)a.tab.seqs * a.pool.heads * a.row_cap;
-    for (int64_t slot = (int64_t)blockIdx.x * kWarps + warp; slot < slots; slot += (int64_t)gridDim.x * kWarps) {
-        const int64_t bh = slot / a.row_cap;
-        const int r = (int)(slot - bh * a.row_cap), b = (int)(bh / a.pool.heads), head = (int)(bh - (int64_t)b * a.pool.heads);
-        int row0, n;
-        query_rows(a, b, row0, n);
-        const int rows = n * a.group;
-        if (r >= rows || rows > kFewRows) continue;
-        const int splits = split_count(kv_length(a.tab, b, a.pool.page_log2, a.status));
-        if (splits <= 1) continue;
-        const float *pl = a.part_lse + slot * a.split_cap, *po = a.part + slot * a.split_cap * D;
-        float w0 = lane < splits ? pl[lane] : -INFINITY, w1 = lane + 32 < splits ? pl[lane + 32] : -INFINITY;
-        float mm = fmaxf(w0, w1);
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) mm = fmaxf(mm, __shfl_xor_sync(0xFFFFFFFFu, mm, o));
-        w0 = ex2_diff(w0, mm);
-        w1 = ex2_diff(w1, mm);
-        float sum = w0 + w1;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
-        const float inv = sum > 0.0f ? __fdiv_rn(1.0f, sum) : 0.0f;
-        float o[D / 32];
-#pragma unroll
-        for (int k = 0; k < D / 32; ++k) o[k] = 0.0f;
-#pragma unroll 4
-        for (int s = 0; s < splits; ++s) {
-            const float w = __shfl_sync(0xFFFFFFFFu, s < 32 ? w0 : w1, s & 31);
-            const float2 *p = reinterpret_cast<const float2 *>(po + (int64_t)s * D);
-#pragma unroll
-            for (int k = 0; k < D / 64; ++k) {
-                const float2 v = p[lane + 32 * k];
-                o[2 * k] += w * v.x;
-                o[2 * k + 1] += w * v.y;
+struct Tile {
+    static constexpr int kQ = D <= 128 ? 2 : 1;              // 128-row query tiles on chip
+    static constexpr int kStep = D <= 128 ? 128 : 64;        // tokens of a step
+    static constexpr int kSub = kStep / 64;                  // blocks of 64 tokens of a step
+    static constexpr int kSlots = D <= 128 ? 1 : 2;          // places for S of a row tile
+    static constexpr int kKStages = D <= 128 ? 2 : 1, kVStages = D == 64 ? 2 : 1;   // steps of keys and of values as operands
+    static constexpr int kRaw = D == 64 ? 4 : D == 128 ? 3 : 2;      // blocks of codes on their way, of keys and of values
+    static constexpr int kCols = kStep * kQ / 2;             // columns of S that a softmax thread has
+    static constexpr int kOutCols = kQ == 2 ? D : D / 2;     // and of O
+    // 20 warps of 96 registers in whole warpgroups: eight of softmax (four for each row tile, or eight
+    // for one), four that turn keys into operands and four for values, then one that issues the products,
+    // one that copies codes and two idle ones.  Each of the SM's four register files holds two warps of
+    // softmax, two of conversion and one of the last group, and setmaxnreg's 2 x 144 + 2 x 56 + 80 =
+    // 5 x 96 fit in every one of them.
+    static constexpr int kSoftWarps = 8, kConvWarps = 4;     // conversion: for each operand
+    static constexpr int kMmaWarp = kSoftWarps + 2 * kConvWarps, kCopyWarp = kMmaWarp + 1;
+    static constexpr int kThreadsAll = (kMmaWarp + 4) * 32;
+    static constexpr int kChunks = D / 64;                   // 64-element columns of 128-byte rows
+    static constexpr int kChunkQ = 128 * 128, kChunkKV = kStep * 128;
+    static constexpr int kQuery = kChunks * kChunkQ;         // 128 x D in fp16
+    static constexpr int kOperand = kChunks * kChunkKV;      // kStep x D
+    static constexpr int kCodes = 64 * D;                    // a block's
+    static constexpr int kSmemQ = 0, kSmemK = kQ * kQuery, kSmemV = kSmemK + kKStages * kOperand;
+    static constexpr int kSmemRaw = kSmemV + kVStages * kOperand;     // keys' blocks, then values'
+    static constexpr int kSmemEnd = kSmemRaw + kRaw * 2 * kCodes;
+    static constexpr int kSmem = kSmemEnd + 1024;
+    // tensor memory: 256 columns for S (P takes the first half of the columns of its threads), then O.
+    // More than half an SM's shared memory is taken, so no two CTAs of an SM wait for one another's
+    // tensor memory.
+    static constexpr uint32_t kTmemO = 256;
+    static constexpr uint32_t kTmemCols = 512;
+    static_assert(kSmem > 114 * 1024, "one CTA an SM");
+};
+constexpr int kRing = 16;             // blocks of page scales
+constexpr int kItemStep = 4;          // sequences of an entry of the item table
+
+struct TileItem {
+    int b, row0, n, len, rows, head, tile, split, splits, first, rn, tok0, steps;
+};
+
+// The item of a CTA's round: rounds go through the CTAs forth and back, so that
+// the CTA with the longest item of one round has the shortest of the next.
+__device__ __forceinline__ int round_item(int round) {
+    return round * (int)gridDim.x + ((round & 1) ? (int)(gridDim.x - 1 - blockIdx.x) : (int)blockIdx.x);
+}
+
+// Items of sequence b.
+template <int D>
+__device__ __forceinline__ int tile_items(const AttnArgs &a, int b) {
+    int row0, n;
+    query_rows(a, b, row0, n);
+    const int rows = n * a.group;
+    if (rows <= kFewRows) return 0;
+    return tile_splits(rows, kv_length(a.tab, b, a.pool.page_log2, a.status), a.pool.heads, D) *
+           ((rows + tile_rows(D) - 1) / tile_rows(D)) * a.pool.heads;
+}
+
+// What item number `item` is; s_items has the first item of every kItemStep-th
+// sequence.  The row tiles of a sequence come last one first: with a causal mask
+// it has the most tokens to see.
+template <int D>
+__device__ __forceinline__ TileItem tile_item(const AttnArgs &a, const int *s_items, int item) {
+    TileItem t;
+    int b = 0, hi = (a.tab.seqs + kItemStep - 1) / kItemStep;
+    while (hi - b > 1) {
+        const int mid = (b + hi) >> 1;
+        if (s_items[mid] <= item) b = mid;
+        else hi = mid;
+    }
+    int rest = item - s_items[b];
+    b *= kItemStep;
+    for (int k = 1; k < kItemStep; ++k) {
+        const int cnt = tile_items<D>(a, b);
+        if (rest < cnt) break;
+        rest -= cnt;
+        ++b;
+    }
+    t.b = b;
+    query_rows(a, b, t.row0, t.n);
+    t.len = kv_length(a.tab, b, a.pool.page_log2, a.status);
+    t.rows = t.n * a.group;
+    t.splits = tile_splits(t.rows, t.len, a.pool.heads, D);
+    const int tiles = (t.rows + tile_rows(D) - 1) / tile_rows(D);
+    t.head = rest % a.pool.heads;
+    rest /= a.pool.heads;
+    t.split = rest % t.splits;
+    t.tile = tiles - 1 - rest / t.splits;
+    t.first = t.tile * tile_rows(D);
+    t.rn = min(tile_rows(D), t.rows - t.first);
+    const int per = tile_split_tokens(t.len, t.splits);
+    t.tok0 = t.split * per;
+    int end = min(t.len, t.tok0 + per);
+    if (a.causal) end = min(end, max(0, t.len - t.n + (t.first + t.rn - 1) / a.group + 1));
+    t.steps = end > t.tok0 ? (end - t.tok0 + Tile<D>::kStep - 1) / Tile<D>::kStep : 0;
+    return t;
+}
+
+// Products and commits issued by one lane of a warp that stays together
+// (elect.sync picks the same lane each time): an MMA then costs its warp about 24
+// cycles of issue, against 55 to 90 from a branch that one thread runs alone.
+__device__ __forceinline__ void mma_f16_warp(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
+                                             uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p, e;\n\telect.sync _|e, 0xffffffff;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}\n"
+        ::"r"(d_tmem), "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+__device__ __forceinline__ void mma_f16_tmem(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc,
+                                             uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p, e;\n\telect.sync _|e, 0xffffffff;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}\n"
+        ::"r"(d_tmem), "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+__device__ __forceinline__ void commit_warp(uint64_t *bar) {
+    asm volatile(
+        "{\n\t.reg .pred e;\n\telect.sync _|e, 0xffffffff;\n\t"
+        "@e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}\n"
+        ::"r"(smem_u32(bar)) : "memory");
+}
+
+__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16]) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
+        "{%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};"
+        ::"r"(taddr), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]),
+          "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+        : "memory");
+}
+
+// Untiled copy to shared memory: 16-byte aligned addresses and size; completion
+// is signalled as transaction bytes on `bar`.
+__device__ __forceinline__ void bulk_copy(void *dst, const void *src, uint32_t bytes, uint64_t *bar) {
+    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];"
+                 ::"r"(smem_u32(dst)), "l"(src), "r"(bytes), "r"(smem_u32(bar)) : "memory");
+}
+
+__device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+// Descriptor of the values as the right-hand operand of O = P V, "MN-major":
+// 64 dimensions of a token are a 128-byte row, eight tokens a 1,024-byte atom
+// (the stride between groups of eight k, bits 32-45), the next 64 dimensions a
+// chunk further (bits 16-29); 128-byte swizzle.
+__device__ __forceinline__ uint64_t sdesc_values(uint32_t smem_addr, uint32_t chunk_bytes) {
+    return (uint64_t)((smem_addr & 0x3FFFFu) >> 4) | ((uint64_t)(chunk_bytes >> 4) << 16) |
+           ((uint64_t)(1024 >> 4) << 32) | ((uint64_t)1 << 46) | ((uint64_t)2 << 61);
+}
+
+__device__ __forceinline__ uint64_t pair_of(float x) {
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %1};" : "=l"(r) : "f"(x));
+    return r;
+}
+
+// Quotients of small numbers by the number of query heads that share a
+// key/value head: x / g = umulhi(x, ceil(2^32 / g)), exact while x * g < 2^32.
+struct GroupDiv {
+    int g;
+    uint32_t mul;
+    __device__ __forceinline__ explicit GroupDiv(int group) : g(group), mul(0xFFFFFFFFu / (uint32_t)group + 1u) {}
+    __device__ __forceinline__ int div(int x) const { return g == 1 ? x : (int)__umulhi((uint32_t)x, mul); }
+};
+
+// mbar_wait for a whole warp: the same answer in every lane, so that the warp
+// stays together for the aligned instructions that follow.
+__device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t parity, const WaitCtx &w, unsigned int site) {
+    return __all_sync(0xFFFFFFFFu, mbar_wait(bar, parity, w, site));
+}
+
+struct TileBars {
+    uint64_t q_full[2], k_full[2], k_empty[2], v_full[2], v_empty[2], s_full[2], p_full[2], o_done[2];
+    uint64_t raw_full[2][4], raw_empty[2][4];      // of keys and of values
+    uint64_t pair[4], never, drain;
+};
+
+// Step number i of a pipeline of N stages: its stage, and the parity of the
+// barrier phase that its use number completes.
+template <int N>
+__device__ __forceinline__ int stage_of(uint32_t i) { return (int)(i % N); }
+template <int N>
+__device__ __forceinline__ uint32_t parity_of(uint32_t i) { return i / N & 1u; }
+
+// Where S number n of row tile q is and, the same way, the product P V number n:
+// its place and barriers, and the parity of the phase.  With one row tile the
+// next S is under way before the last product is, so two of each may be
+// outstanding; they take turns on two places, as a parity tells a phase only
+// from the one before it.
+template <typename T>
+__device__ __forceinline__ int slot_of(int q, uint32_t n) { return T::kSlots == 1 ? q : (int)(n & 1u); }
+template <typename T>
+__device__ __forceinline__ uint32_t turn_of(uint32_t n) { return T::kSlots == 1 ? n & 1u : n >> 1 & 1u; }
+
+// Scales of the pages of a block of 64 tokens, kRing blocks deep.
+struct BlockScales {
+    float ks[4], lv[4], inv[4];    // key scale; log2 of the value scale; its reciprocal
+    int there;                     // bit p: page p is one of the pool
+    int zero;                      // bit p: page p's value scale is zero
+};
+
+// 128 rows of query i * G + head g at a time (two such tiles up to dim 128),
+// against 128 tokens (64 at dim 256) a step.  Per row tile and step:
+//   S = Q K^T         tcgen05, both operands fp16 in shared memory
+//   softmax           a thread a row (two at dim 256): S from tensor memory, the row's
+//                     maximum, the exponentials, P in fp16 back over S
+//   O += P V          tcgen05, P from tensor memory, V from shared memory
+// One warp copies the codes of the steps' pages to shared memory, several blocks
+// ahead; eight turn them into fp16 operands in the 128-byte swizzle.  With two row
+// tiles the products of one run while the other's softmax does.  At dim 256,
+// whose O leaves room for one row tile only, the next step's S runs while the
+// softmax of this one does.
+//
+// The row's reference m is a running maximum of x_j + log2 vs(page(j)): the
+// weights of P are exp2(x_j + log2 vs - m + 11), and the softmax's sum takes each
+// page's part times 1 / vs.  O is rescaled only when the maximum has grown by
+// more than 2^4 (the weights are then at most 2^15, within fp16).
+template <int KIND, int D>
+__global__ void __launch_bounds__(Tile<D>::kThreadsAll, 1) kv_tile_kernel(const AttnArgs a) {
+    using T = Tile<D>;
+    extern __shared__ __align__(16) uint8_t smem_raw[];
+    __shared__ TileBars bar;
+    __shared__ BlockScales s_scale[kRing];
+    __shared__ float s_qs[T::kQ * 128], s_pair[2][2][128];   // rows' query scales; what the threads of a row exchange
+    __shared__ uint32_t s_tmem;
+    __shared__ int s_abort, s_scan[32], s_total;
+    uint8_t *smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+    int *s_items = reinterpret_cast<int *>(smem_raw + T::kSmem);
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, log2 = a.pool.page_log2, H = a.pool.heads;
+
+    if (tid == 0) {
+        s_abort = 0;
+        s_total = 0;
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&bar.q_full[i], 8 / T::kQ);
+            mbar_init(&bar.p_full[i], 8 / T::kQ);
+            mbar_init(&bar.k_full[i], T::kConvWarps);
+            mbar_init(&bar.v_full[i], T::kConvWarps);
+            mbar_init(&bar.k_empty[i], 1);
+            mbar_init(&bar.v_empty[i], 1);
+            mbar_init(&bar.s_full[i], 1);
+            mbar_init(&bar.o_done[i], 1);
+            for (int k = 0; k < 4; ++k) {
+                mbar_init(&bar.raw_full[i][k], 1);
+                mbar_init(&bar.raw_empty[i][k], T::kConvWarps);
             }
         }
-        const int i = r / a.group, hq = head * a.group + r - i * a.group;
-        uint16_t *dst = a.out + (int64_t)(row0 + i) * a.ldo + (int64_t)hq * a.ldo_head;
-#pragma unroll
-        for (int k = 0; k < D / 64; ++k)
-            *reinterpret_cast<__nv_bfloat162 *>(dst + 64 * k + 2 * lane) =
-                __floats2bfloat162_rn(o[2 * k] * inv, o[2 * k + 1] * inv);
-        if (a.lse && lane == 0)
-            a.lse[(int64_t)(row0 + i) * a.q_heads + hq] = sum > 0.0f ? (mm + log2f(sum)) * (1.0f / kLog2e) : -INFINITY;
+        for (int i = 0; i < 4; ++i) mbar_init(&bar.pair[i], 2);
+        mbar_init(&bar.never, 1);
+        mbar_init(&bar.drain, 1);
+        fence_barrier_init();
     }
+    if (warp == T::kMmaWarp) {
+        tmem_alloc(&s_tmem, T::kTmemCols);
+        tmem_relinquish();
+    }
+    pdl_wait();
+    __syncthreads();
+    for (int b0 = 0; b0 * kItemStep < a.tab.seqs; b0 += T::kThreadsAll) {
+        int cnt = 0;
+        for (int b = (b0 + tid) * kItemStep; b < min(a.tab.seqs, (b0 + tid + 1) * kItemStep); ++b) cnt += tile_items<D>(a, b);
+        int inc = cnt;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int v = __shfl_up_sync(0xFFFFFFFFu, inc, o);
+            if (lane >= o) inc += v;
+        }
+        if (lane == 31) s_scan[warp] = inc;
+        __syncthreads();
+        int base = s_total, all = 0;
+        for (int w = 0; w < T::kThreadsAll / 32; ++w) {
+            if (w < warp) base += s_scan[w];
+            all += s_scan[w];
+        }
+        if ((b0 + tid) * kItemStep < a.tab.seqs) s_items[b0 + tid] = base + inc - cnt;
+        __syncthreads();
+        if (tid == 0) s_total += all;
+        __syncthreads();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const int items = s_total;
+    const uint32_t tmem = s_tmem;
+    const WaitCtx wait = {a.wait_limit_ns, &s_abort, a.status};
+
+    if (warp < T::kSoftWarps) {
+        // ---------------------------------------------------------- softmax
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 144;");
+        const int q = T::kQ == 2 ? warp >> 2 : 0, half = T::kQ == 2 ? 0 : warp >> 2, quad = warp & 3;
+        const uint32_t lanes = (uint32_t)(quad * 32) << 16;
+        const GroupDiv by(a.group);
+        uint32_t ns = 0, npv = 0, step_no = 0, pairs = 0;   // S and O products of this row tile so far; steps of the CTA
+        bool ok = true;
+        // the warps that share rows meet (a time-limited wait, unlike a named barrier)
+        const auto pair_sync = [&]() -> bool {
+            __syncwarp();
+            if constexpr (T::kQ == 1) {
+                if (lane == 0) mbar_arrive(&bar.pair[quad]);
+                return warp_wait(&bar.pair[quad], pairs++ & 1u, wait, kSiteKvSoftmax);
+            }
+            return true;
+        };
+        for (int round = 0; round * (int)gridDim.x < items && ok; ++round) {
+            const int item = round_item(round);
+            if (item >= items) continue;
+            const TileItem t = tile_item<D>(a, s_items, item);
+            const uint32_t step0 = step_no;
+            step_no += (uint32_t)t.steps;
+            const int mine = min(128, t.rn - q * 128);     // rows of this tile
+            if (mine <= 0) continue;
+            const int row = quad * 32 + lane;              // this thread's row of the tile
+            const int r = t.first + q * 128 + min(row, mine - 1);
+            // query and head of row rr of this tile: i0 + (g0 + rr) / G and the rest
+            const int i0 = (t.first + q * 128) / a.group, g0 = t.first + q * 128 - i0 * a.group;
+            const int i = i0 + by.div(g0 + min(row, mine - 1)), hq = t.head * a.group + r - i * a.group;
+            uint8_t *sq = smem + T::kSmemQ + q * T::kQuery;
+
+            // queries of the warp's rows to shared memory, each row scaled by a power of two
+            float qs = 0.0f;
+            if (t.steps > 0) {
+                constexpr int LPR = D / 16, RPI = 32 / LPR;              // lanes of a row, rows at a time
+                constexpr int WROWS = 32 * T::kQ / 2, ITER = WROWS / RPI;
+                const int lr = lane / LPR, lu = lane % LPR, base = quad * 32 + half * WROWS + lr;
+                // the loads of four rounds at a time
+#pragma unroll 1
+                for (int k0 = 0; k0 < ITER; k0 += 4) {
+                    uint4 v[4][2];
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        const int x = g0 + min(base + (k0 + k) * RPI, mine - 1), qi = by.div(x);
+                        const uint16_t *src = a.q + (int64_t)(t.row0 + i0 + qi) * a.ldq +
+                                              (int64_t)(t.head * a.group + x - qi * a.group) * a.ldq_head + lu * 8;
+                        v[k][0] = *reinterpret_cast<const uint4 *>(src);
+                        v[k][1] = *reinterpret_cast<const uint4 *>(src + LPR * 8);
+                    }
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        const int rr = base + (k0 + k) * RPI;
+                        uint32_t w[8] = {v[k][0].x, v[k][0].y, v[k][0].z, v[k][0].w, v[k][1].x, v[k][1].y, v[k][1].z, v[k][1].w};
+                        uint32_t top = 0;
+#pragma unroll
+                        for (int x = 0; x < 8; ++x) {
+                            if (rr >= mine) w[x] = 0u;
+                            top = __vmaxu2(top, w[x] & 0x7FFF7FFFu);
+                        }
+#pragma unroll
+                        for (int o = 1; o < LPR; o <<= 1) top = __vmaxu2(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
+                        top = max(top & 0xFFFFu, top >> 16) << 16;
+                        const int e = top ? max(-100, min(120, 13 - (int)(top >> 23) + 127)) : 0;
+                        // a negative scale turns the queries, so that x grows with S
+                        float up = __uint_as_float((uint32_t)(127 + e) << 23);
+                        if (a.scale_log2 < 0.0f) up = -up;
+#pragma unroll
+                        for (int x = 0; x < 8; ++x)
+                            w[x] = pack_half(__uint_as_float(w[x] << 16) * up, __uint_as_float(w[x] & 0xFFFF0000u) * up);
+#pragma unroll
+                        for (int x = 0; x < 2; ++x) {
+                            const int u = lu + x * LPR;
+                            *reinterpret_cast<uint4 *>(sq + (u >> 3) * T::kChunkQ + rr * 128 + (((u & 7) ^ (rr & 7)) << 4)) =
+                                make_uint4(w[4 * x], w[4 * x + 1], w[4 * x + 2], w[4 * x + 3]);
+                        }
+                        if (lu == 0) s_qs[q * 128 + rr] = fabsf(a.scale_log2) * __uint_as_float((uint32_t)(127 - e) << 23);
+                    }
+                }
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&bar.q_full[q]);
+                if (!pair_sync()) break;
+                qs = s_qs[q * 128 + row];
+            }
+
+            const int sees = a.causal ? max(0, t.len - t.n + i + 1) : t.len;    // tokens this row sees
+            float m = -INFINITY, l = 0.0f;
+            for (int s = 0; s < t.steps; ++s) {
+                const int slot = slot_of<T>(q, ns);
+                const uint32_t ts = tmem + (uint32_t)(slot * T::kStep + half * T::kCols) + lanes;
+                if (!warp_wait(&bar.s_full[slot], turn_of<T>(ns), wait, kSiteKvSoftmax)) {
+                    ok = false;
+                    break;
+                }
+                ++ns;
+                tc_fence_after();
+                const int seen = sees - (t.tok0 + s * T::kStep) - half * T::kCols;   // of this thread's columns, what its row sees
+                const int p0 = half * T::kCols;      // first column, for the page of a column
+                const auto scales_at = [&](int c) -> const BlockScales & {
+                    return s_scale[((step0 + (uint32_t)s) * T::kSub + (uint32_t)((p0 + c) >> 6)) % kRing];
+                };
+                bool zeros = scales_at(0).zero != 0;
+                if (T::kCols > 64) zeros = zeros || scales_at(64).zero != 0;
+                // whole steps take code without masks (the compiler turns a test in the loops into selects
+                // for every column: 1,120 + 2,040 cycles for 128 columns instead of 450 + 1,350)
+                const bool whole = __reduce_min_sync(0xFFFFFFFFu, seen) >= T::kCols && !zeros;
+
+                // the largest x + log2 vs
+                uint32_t va[32], vb[32];
+                float top = -INFINITY;
+                if (whole) {
+#pragma unroll
+                    for (int c = 0; c < T::kCols; c += 64) {
+                        tmem_ld32(ts + (uint32_t)c, va);
+                        if constexpr (T::kCols >= 64) tmem_ld32(ts + (uint32_t)c + 32u, vb);
+                        tmem_ld_wait();
+                        const BlockScales &sc = scales_at(c);
+#pragma unroll
+                        for (int h = 0; h < (T::kCols < 64 ? T::kCols : 64) / 16; ++h) {
+                            const uint32_t *v = h < 2 ? va + h * 16 : vb + (h - 2) * 16;
+                            const int p = ((p0 + c + h * 16) & 63) >> log2;
+                            float g[8];
+#pragma unroll
+                            for (int k = 0; k < 8; ++k) g[k] = fmaxf(__uint_as_float(v[k]), __uint_as_float(v[8 + k]));
+#pragma unroll
+                            for (int w = 4; w > 0; w >>= 1)
+#pragma unroll
+                                for (int k = 0; k < w; ++k) g[k] = fmaxf(g[k], g[k + w]);
+                            top = fmaxf(top, fmaf(g[0], qs * sc.ks[p], sc.lv[p]));
+                        }
+                    }
+                } else {
+#pragma unroll 1
+                    for (int c = 0; c < T::kCols; c += 16) {
+                        uint32_t v[16];
+                        tmem_ld16(ts + (uint32_t)c, v);
+                        tmem_ld_wait();
+                        const BlockScales &sc = scales_at(c);
+                        const int p = ((p0 + c) & 63) >> log2;
+                        float g = -INFINITY;
+#pragma unroll
+                        for (int k = 0; k < 16; ++k) g = fmaxf(g, c + k < seen ? __uint_as_float(v[k]) : -INFINITY);
+                        if (c < seen) top = fmaxf(top, fmaf(g, qs * sc.ks[p], sc.lv[p]));
+                    }
+                }
+                if constexpr (T::kQ == 1) {
+                    s_pair[s & 1][half][row] = top;
+                    if (!pair_sync()) {
+                        ok = false;
+                        break;
+                    }
+                    top = fmaxf(top, s_pair[s & 1][half ^ 1][row]);
+                }
+                if (__any_sync(0xFFFFFFFFu, top > m + kSlack || (m == -INFINITY && top != -INFINITY))) {
+                    const float mn = fmaxf(m, top), f = ex2_diff(m, mn);
+                    m = mn;
+                    l *= f;
+                    if (s > 0) {
+                        // O is at rest once the product before this step's is done
+                        if (!warp_wait(&bar.o_done[slot_of<T>(q, npv - 1)], turn_of<T>(npv - 1), wait, kSiteKvSoftmax)) {
+                            ok = false;
+                            break;
+                        }
+                        tc_fence_after();
+                        const uint32_t to = tmem + T::kTmemO + (uint32_t)(q * 128 + half * T::kOutCols) + lanes;
+#pragma unroll 1
+                        for (int c = 0; c < T::kOutCols / 16; ++c) {
+                            uint32_t v[16];
+                            tmem_ld16(to + (uint32_t)(c * 16), v);
+                            tmem_ld_wait();
+#pragma unroll
+                            for (int k = 0; k < 16; ++k) v[k] = __float_as_uint(__uint_as_float(v[k]) * f);
+                            tmem_st16(to + (uint32_t)(c * 16), v);
+                        }
+                        tmem_st_wait();
+                    }
+                }
+                const float ref = m == -INFINITY ? 0.0f : m - (kLift - kSlack);
+                if (whole) {
+#pragma unroll
+                    for (int c = 0; c < T::kCols; c += 64) {
+                        if constexpr (T::kCols > 64) {
+                            tmem_ld32(ts + (uint32_t)c, va);
+                            tmem_ld32(ts + (uint32_t)c + 32u, vb);
+                            tmem_ld_wait();
+                        }
+                        const BlockScales &sc = scales_at(c);
+#pragma unroll
+                        for (int hh = 0; hh < (T::kCols < 64 ? T::kCols : 64) / 32; ++hh) {
+                            uint32_t o[16];
+#pragma unroll
+                            for (int h = 0; h < 2; ++h) {
+                                const uint32_t *v = hh == 0 ? va + h * 16 : vb + h * 16;
+                                const int p = ((p0 + c + hh * 32 + h * 16) & 63) >> log2;
+                                const uint64_t f2 = pair_of(qs * sc.ks[p]), off2 = pair_of(sc.lv[p] - ref);
+                                uint64_t g[2] = {0, 0};
+#pragma unroll
+                                for (int k = 0; k < 8; ++k) {
+                                    uint64_t x;
+                                    float y, z;
+                                    asm("mov.b64 %0, {%1, %2};" : "=l"(x) : "r"(v[2 * k]), "r"(v[2 * k + 1]));
+                                    asm("fma.rn.f32x2 %0, %0, %1, %2;" : "+l"(x) : "l"(f2), "l"(off2));
+                                    asm("mov.b64 {%0, %1}, %2;" : "=f"(y), "=f"(z) : "l"(x));
+                                    y = ex2(y);
+                                    z = ex2(z);
+                                    asm("mov.b64 %0, {%1, %2};" : "=l"(x) : "f"(y), "f"(z));
+                                    asm("add.rn.f32x2 %0, %0, %1;" : "+l"(g[k & 1]) : "l"(x));
+                                    o[h * 8 + k] = pack_half(y, z);
+                                }
+                                float y, z;
+                                asm("add.rn.f32x2 %0, %0, %1;" : "+l"(g[0]) : "l"(g[1]));
+                                asm("mov.b64 {%0, %1}, %2;" : "=f"(y), "=f"(z) : "l"(g[0]));
+                                l = fmaf(y + z, sc.inv[p], l);
+                            }
+                            tmem_st16(ts + (uint32_t)(c / 2 + hh * 16), o);
+                        }
+                    }
+                } else {
+#pragma unroll 1
+                    for (int c = 0; c < T::kCols; c += 32) {
+                        uint32_t o[16];
+                        tmem_ld32(ts + (uint32_t)c, va);
+                        tmem_ld_wait();
+                        const BlockScales &sc = scales_at(c);
+#pragma unroll
+                        for (int h = 0; h < 2; ++h) {
+                            const int c0 = c + h * 16, p = ((p0 + c0) & 63) >> log2;
+                            const float f = qs * sc.ks[p], off = sc.lv[p] - ref;
+                            const uint32_t keep = (sc.zero >> p & 1) ? 0u : 0xFFFFFFFFu;
+                            float g = 0.0f;
+#pragma unroll
+                            for (int k = 0; k < 16; k += 2) {
+                                const float y = c0 + k < seen ? ex2(fmaf(__uint_as_float(va[h * 16 + k]), f, off)) : 0.0f;
+                                const float z = c0 + k + 1 < seen ? ex2(fmaf(__uint_as_float(va[h * 16 + k + 1]), f, off)) : 0.0f;
+                                g += y + z;
+                                o[h * 8 + k / 2] = pack_half(y, z) & keep;
+                            }
+                            l = fmaf(g, sc.inv[p], l);
+                        }
+                        tmem_st16(ts + (uint32_t)(c / 2), o);
+                    }
+                }
+                tmem_st_wait();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&bar.p_full[slot]);
+                ++npv;
+            }
+            if (!ok) break;
+
+            // the rows' results, through shared memory in the place and layout of the warp's
+            // queries (whose last product is done), so that whole rows leave at a time
+            if (t.steps > 0 && !warp_wait(&bar.o_done[slot_of<T>(q, npv - 1)], turn_of<T>(npv - 1), wait, kSiteKvSoftmax)) break;
+            tc_fence_after();
+            if constexpr (T::kQ == 1) {
+                s_pair[0][half][row] = l;
+                if (!pair_sync()) break;
+                l += s_pair[0][half ^ 1][row];
+            }
+            const float inv = l > 0.0f ? __fdiv_rn(1.0f, l) : 0.0f;
+            if (row < mine && half == 0) {
+                const float lse = l > 0.0f ? m - (kLift - kSlack) + log2f(l) : -INFINITY;
+                if (t.splits > 1)
+                    a.part_lse[t.b * a.part_units + ((int64_t)t.head * t.rows + r) * t.splits + t.split] = lse;
+                else if (a.lse)
+                    a.lse[(int64_t)(t.row0 + i) * a.q_heads + hq] = lse == -INFINITY ? -INFINITY : lse * (1.0f / kLog2e);
+            }
+            constexpr int CHUNKS = T::kOutCols / 64;             // 128-byte chunks of the warp's rows
+            const bool part = t.splits > 1, none = !(inv > 0.0f);
+            uint8_t *stage = sq + half * CHUNKS * T::kChunkQ + quad * 32 * 128;
+            for (int pass = 0; pass < (part ? 2 : 1); ++pass) {          // fp32 takes two
+                // 16 columns at a time: two 16-byte units of bf16, or four of fp32
+                const int groups = part ? T::kOutCols / 32 : T::kOutCols / 16;
+                const auto put = [&](int u, uint4 o) {
+                    *reinterpret_cast<uint4 *>(stage + (u >> 3) * T::kChunkQ + lane * 128 + (((u & 7) ^ (lane & 7)) << 4)) = o;
+                };
+#pragma unroll 1
+                for (int c = 0; c < groups; ++c) {
+                    uint32_t v[16];
+                    if (t.steps > 0) {
+                        tmem_ld16(tmem + T::kTmemO + (uint32_t)(q * 128 + half * T::kOutCols + (pass * groups + c) * 16) + lanes, v);
+                        tmem_ld_wait();
+                    }
+#pragma unroll
+                    for (int k = 0; k < 16; ++k) v[k] = none ? 0u : __float_as_uint(__uint_as_float(v[k]) * inv);
+                    if (part) {
+#pragma unroll
+                        for (int u = 0; u < 4; ++u) put(c * 4 + u, make_uint4(v[4 * u], v[4 * u + 1], v[4 * u + 2], v[4 * u + 3]));
+                    } else {
+                        uint32_t w[8];
+#pragma unroll
+                        for (int k = 0; k < 8; ++k) {
+                            const __nv_bfloat162 b2 = __floats2bfloat162_rn(__uint_as_float(v[2 * k]), __uint_as_float(v[2 * k + 1]));
+                            w[k] = *reinterpret_cast<const uint32_t *>(&b2);
+                        }
+                        put(c * 2, make_uint4(w[0], w[1], w[2], w[3]));
+                        put(c * 2 + 1, make_uint4(w[4], w[5], w[6], w[7]));
+                    }
+                }
+                __syncwarp();
+                constexpr int UNITS = CHUNKS * 8, RPI = 32 / UNITS;      // 16-byte units of a row, rows at a time
+                const int u = lane % UNITS, lr = lane / UNITS;
+#pragma unroll 4
+                for (int k = 0; k < 32; k += RPI) {
+                    const int rr = quad * 32 + k + lr;
+                    if (rr < mine) {
+                        const uint4 o = *reinterpret_cast<const uint4 *>(stage + (u >> 3) * T::kChunkQ + (k + lr) * 128 +
+                                                                         (((u & 7) ^ ((k + lr) & 7)) << 4));
+                        const int ra = t.first + q * 128 + rr;
+                        if (t.splits > 1) {
+                            const int64_t place = t.b * a.part_units + ((int64_t)t.head * t.rows + ra) * t.splits + t.split;
+                            *reinterpret_cast<uint4 *>(a.part + place * D + half * T::kOutCols + pass * (T::kOutCols / 2) + u * 4) = o;
+                        } else {
+                            const int x = g0 + rr, qi = by.div(x);
+                            *reinterpret_cast<uint4 *>(a.out + (int64_t)(t.row0 + i0 + qi) * a.ldo +
+                                                       (int64_t)(t.head * a.group + x - qi * a.group) * a.ldo_head +
+                                                       half * T::kOutCols + u * 8) = o;
+                        }
+                    }
+                }
+                __syncwarp();
+            }
+            tc_fence_before();
+            // before the next queries are written where the other warp of these rows may still be reading
+            if (!pair_sync()) break;
+        }
+    } else if (warp < T::kMmaWarp) {
+        // ---------------------------------------------------------- codes to operands
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
+        const bool values = warp >= T::kSoftWarps + T::kConvWarps;
+        const int ct = (tid - T::kSoftWarps * 32) % (T::kConvWarps * 32);
+        constexpr int PIECES = D / 16, N = 64 * PIECES / (T::kConvWarps * 32);   // 16-byte pieces of a row; of a thread and block
+        constexpr int AT_ONCE = N < 4 ? N : 4;
+        const int crow = ct / PIECES, piece = ct % PIECES;
+        // a piece becomes two 16-byte units of a row; lanes of every second chunk write them the other
+        // way round, so that the eight lanes of a store meet every bank once
+        const int chunk = piece >> 2, unit = (piece & 3) * 2;
+        const bool swap = chunk & 1;
+        const int stages = values ? T::kVStages : T::kKStages;
+        uint64_t *full = values ? bar.v_full : bar.k_full, *empty = values ? bar.v_empty : bar.k_empty;
+        uint64_t *raw_full = bar.raw_full[values], *raw_empty = bar.raw_empty[values];
+        const uint8_t *raw = smem + T::kSmemRaw + (values ? T::kRaw * T::kCodes : 0);
+        uint8_t *operands = smem + (values ? T::kSmemV : T::kSmemK) + chunk * T::kChunkKV;
+        uint32_t step_no = 0, block = 0;
+        bool ok = true;
+        for (int round = 0; round * (int)gridDim.x < items && ok; ++round) {
+            const int item = round_item(round);
+            if (item >= items) continue;
+            const TileItem t = tile_item<D>(a, s_items, item);
+            for (int s = 0; s < t.steps && ok; ++s, ++step_no) {
+                const uint32_t st = step_no % (uint32_t)stages;
+                uint8_t *dst = operands + st * T::kOperand;
+#pragma unroll 1
+                for (int sub = 0; sub < T::kSub; ++sub, ++block) {
+                    const int rs = stage_of<T::kRaw>(block);
+                    ok = warp_wait(&raw_full[rs], parity_of<T::kRaw>(block), wait, kSiteKvLoad);
+                    if (sub == 0)
+                        ok = ok && warp_wait(&empty[st], (step_no / (uint32_t)stages & 1u) ^ 1u, wait, kSiteKvLoad);
+                    if (!ok) break;
+                    const int there = s_scale[block % kRing].there, left = t.len - t.tok0 - s * T::kStep - sub * 64;
+                    const uint8_t *src = raw + rs * T::kCodes + piece * 16;
+#pragma unroll
+                    for (int k0 = 0; k0 < N; k0 += AT_ONCE) {
+                        uint4 v[AT_ONCE];
+#pragma unroll
+                        for (int k = 0; k < AT_ONCE; ++k) {
+                            // past the sequence's end anything may lie, NaN codes included
+                            const int rr = crow + (k0 + k) * (64 / N);
+                            v[k] = *reinterpret_cast<const uint4 *>(src + rr * D);
+                            if (rr >= left || !(there >> (rr >> log2) & 1)) v[k] = make_uint4(0, 0, 0, 0);
+                        }
+#pragma unroll
+                        for (int k = 0; k < AT_ONCE; ++k) {
+                            const int rr = sub * 64 + crow + (k0 + k) * (64 / N);
+                            uint32_t h[8];
+                            widen4<KIND>(v[k].x, h[0], h[1]);
+                            widen4<KIND>(v[k].y, h[2], h[3]);
+                            widen4<KIND>(v[k].z, h[4], h[5]);
+                            widen4<KIND>(v[k].w, h[6], h[7]);
+                            uint8_t *row = dst + rr * 128;
+                            const uint4 u0 = make_uint4(h[0], h[1], h[2], h[3]), u1 = make_uint4(h[4], h[5], h[6], h[7]);
+                            *reinterpret_cast<uint4 *>(row + (((unit + (swap ? 1 : 0)) ^ (rr & 7)) << 4)) = swap ? u1 : u0;
+                            *reinterpret_cast<uint4 *>(row + (((unit + (swap ? 0 : 1)) ^ (rr & 7)) << 4)) = swap ? u0 : u1;
+                        }
+                    }
+                    if (sub == T::kSub - 1) fence_proxy_async_smem();
+                    __syncwarp();
+                    if (lane == 0) {
+                        mbar_arrive(&raw_empty[rs]);
+                        if (sub == T::kSub - 1) mbar_arrive(&full[st]);
+                    }
+                }
+            }
+        }
+    } else {
+      asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
+      if (warp == T::kCopyWarp) {
+        // ---------------------------------------------------------- codes to shared memory
+        // A lane a page of the block: the page's run of tokens of this head is contiguous, one copy for
+        // its keys and one for its values.
+        const int run = min(64, a.pool.page), per = 64 / run;      // tokens of a page in a block; pages of a block
+        uint32_t block = 0, keys_only = 0;
+        bool ok = true;
+        for (int round = 0; round * (int)gridDim.x < items && ok; ++round) {
+            const int item = round_item(round);
+            if (item >= items) continue;
+            const TileItem t = tile_item<D>(a, s_items, item);
+            if (t.steps == 0) continue;
+            // 32 pages of the item and the next 32, one of each a lane: their numbers (-1 where there is
+            // none) and scales, so that no step waits for a look-up
+            struct Page {
+                int page;
+                float ks, vs;
+            };
+            const auto look_up = [&](int p) {
+                Page x = {-1, 0.0f, 1.0f};
+                if (p < (t.len + a.pool.page - 1) >> log2) {
+                    x.page = a.tab.table[(int64_t)t.b * a.tab.ldt + p];
+                    if (x.page < 0 || x.page >= a.pool.pages) {
+                        record_status(a.status, kStatusBadPage);
+                        x.page = -1;
+                    } else {
+                        const int64_t tile = (int64_t)x.page * H + t.head;
+                        x.ks = a.pool.scales[tile];
+                        x.vs = a.pool.scales[a.pool.plane_scales + tile];
+                    }
+                }
+                return x;
+            };
+            int page0 = t.tok0 >> log2;
+            Page now = look_up(page0 + lane), next = look_up(page0 + 32 + lane);
+            for (int s = 0; s < t.steps * T::kSub; ++s, ++block) {
+                const int rs = stage_of<T::kRaw>(block);
+                const int t0 = t.tok0 + s * 64;
+                if ((t0 >> log2) - page0 >= 32) {
+                    page0 += 32;
+                    now = next;
+                    next = look_up(page0 + 32 + lane);
+                }
+                const int p = (t0 >> log2) - page0 + (lane < per ? lane : 0);      // under 64
+                const bool later = p >= 32;
+                const int page_a = __shfl_sync(0xFFFFFFFFu, now.page, p & 31), page_b = __shfl_sync(0xFFFFFFFFu, next.page, p & 31);
+                const float ks_a = __shfl_sync(0xFFFFFFFFu, now.ks, p & 31), ks_b = __shfl_sync(0xFFFFFFFFu, next.ks, p & 31);
+                const float vs_a = __shfl_sync(0xFFFFFFFFu, now.vs, p & 31), vs_b = __shfl_sync(0xFFFFFFFFu, next.vs, p & 31);
+                const int page = lane < per && t0 + lane * run < t.len ? (later ? page_b : page_a) : -1;
+                const float ks = page >= 0 ? (later ? ks_b : ks_a) : 0.0f;
+                float vs = page >= 0 ? (later ? vs_b : vs_a) : 1.0f;
+                if (!warp_wait(&bar.raw_empty[0][rs], parity_of<T::kRaw>(block) ^ 1u, wait, kSiteKvLoad)) {
+                    ok = false;
+                    break;
+                }
+                BlockScales &sc = s_scale[block % kRing];
+                const unsigned int zero = __ballot_sync(0xFFFFFFFFu, vs == 0.0f), there = __ballot_sync(0xFFFFFFFFu, page >= 0);
+                if (vs == 0.0f) vs = 0x1p-60f;
+                if (lane < 4) {
+                    sc.ks[lane] = ks;
+                    sc.lv[lane] = log2f(vs);
+                    sc.inv[lane] = __fdiv_rn(1.0f, vs);
+                }
+                if (lane == 0) {
+                    sc.zero = (int)zero;
+                    sc.there = (int)there;
+                }
+                const uint32_t bytes = (uint32_t)(__popc(there) * run * D);
+                const int64_t at = ((((int64_t)page * H + t.head) << log2) + (t0 & (a.pool.page - 1))) * D;
+                uint8_t *dst = smem + T::kSmemRaw + rs * T::kCodes + lane * run * D;
+                __syncwarp();
+                if (lane == 0) mbar_arrive_expect_tx(&bar.raw_full[0][rs], bytes);
+                __syncwarp();
+                if (page >= 0) bulk_copy(dst, a.pool.codes + at, (uint32_t)(run * D), &bar.raw_full[0][rs]);
+                if (!warp_wait(&bar.raw_empty[1][rs], parity_of<T::kRaw>(block) ^ 1u, wait, kSiteKvLoad)) {
+                    keys_only = 1;
+                    ok = false;
+                    break;
+                }
+                if (lane == 0) mbar_arrive_expect_tx(&bar.raw_full[1][rs], bytes);
+                __syncwarp();
+                if (page >= 0)
+                    bulk_copy(dst + T::kRaw * T::kCodes, a.pool.codes + a.pool.plane_codes + at, (uint32_t)(run * D), &bar.raw_full[1][rs]);
+            }
+        }
+        // no copy is in flight when the CTA ends (after a wait that ran out, one block may have its keys only)
+        for (int plane = 0; plane < 2; ++plane) {
+            const uint32_t end = block + (plane == 0 ? keys_only : 0u);
+            for (uint32_t k = end > T::kRaw ? end - T::kRaw : 0; k < end; ++k)
+                warp_wait(&bar.raw_full[plane][stage_of<T::kRaw>(k)], parity_of<T::kRaw>(k), wait, kSiteDrain);
+        }
+      } else if (warp == T::kMmaWarp) {
+        // ---------------------------------------------------------- products
+        const uint32_t is = idesc_f32acc(0, 0, 128, T::kStep);
+        const uint32_t io = idesc_f32acc(0, 0, 128, D) | (1u << 16);    // bit 16: the right-hand operand is MN-major
+        const uint64_t dq = sdesc_sw128(smem_u32(smem + T::kSmemQ)), dk = sdesc_sw128(smem_u32(smem + T::kSmemK));
+        const uint64_t dv = sdesc_values(smem_u32(smem + T::kSmemV), T::kChunkKV);      // offsets add to the address field
+        uint32_t nk = 0, nv = 0, nq[2] = {0, 0}, ns[2] = {0, 0}, npv[2] = {0, 0};
+        bool ok = !a.force_timeout || warp_wait(&bar.never, 0, wait, kSiteKvMma);
+        for (int round = 0; round * (int)gridDim.x < items && ok; ++round) {
+            const int item = round_item(round);
+            if (item >= items) continue;
+            const TileItem t = tile_item<D>(a, s_items, item);
+            const int tiles = T::kQ == 2 && t.rn > 128 ? 2 : 1;
+            const auto issue_s = [&](int q, int s) -> bool {      // S of step s
+                const int st = stage_of<T::kKStages>(nk);
+                if (s == 0 && !warp_wait(&bar.q_full[q], nq[q]++ & 1u, wait, kSiteKvMma)) return false;
+                // its place is free once the product that read P from there is done
+                if (npv[q] > 0 && !warp_wait(&bar.o_done[slot_of<T>(q, npv[q] - 1)], turn_of<T>(npv[q] - 1), wait, kSiteKvMma))
+                    return false;
+                tc_fence_after();
+                const int slot = slot_of<T>(q, ns[q]);
+#pragma unroll
+                for (int k = 0; k < D / 16; ++k)
+                    mma_f16_warp(tmem + (uint32_t)(slot * T::kStep),
+                                 dq + (uint32_t)((q * T::kQuery + (k >> 2) * T::kChunkQ + (k & 3) * 32) >> 4),
+                                 dk + (uint32_t)((st * T::kOperand + (k >> 2) * T::kChunkKV + (k & 3) * 32) >> 4), is, k > 0);
+                commit_warp(&bar.s_full[slot]);
+                ++ns[q];
+                return true;
+            };
+            const auto issue_o = [&](int q, int s) -> bool {      // O += P V of step s
+                const int st = stage_of<T::kVStages>(nv), slot = slot_of<T>(q, npv[q]);
+                if (!warp_wait(&bar.p_full[slot], turn_of<T>(npv[q]), wait, kSiteKvMma)) return false;
+                tc_fence_after();
+#pragma unroll
+                for (int k = 0; k < T::kStep / 16; ++k)
+                    mma_f16_tmem(tmem + T::kTmemO + (uint32_t)(q * 128),
+                                 tmem + (uint32_t)(slot * T::kStep + k * 16 / T::kCols * T::kCols + k * 16 % T::kCols / 2),
+                                 dv + (uint32_t)((st * T::kOperand + k * 2048) >> 4), io, s > 0 || k > 0);
+                commit_warp(&bar.o_done[slot]);
+                ++npv[q];
+                return true;
+            };
+            for (int s = 0; s <= t.steps && t.steps > 0 && ok; ++s) {
+                const bool has_s = s < t.steps, has_o = s > 0;
+                if (has_s) ok = warp_wait(&bar.k_full[stage_of<T::kKStages>(nk)], parity_of<T::kKStages>(nk), wait, kSiteKvMma);
+                // with two places the step's S goes ahead of the last step's O
+                if (T::kSlots == 2 && has_s) ok = ok && issue_s(0, s);
+                if (has_o) ok = ok && warp_wait(&bar.v_full[stage_of<T::kVStages>(nv)], parity_of<T::kVStages>(nv), wait, kSiteKvMma);
+#pragma unroll
+                for (int q = 0; q < T::kQ; ++q) {
+                    if (q >= tiles) break;
+                    if (has_o) ok = ok && issue_o(q, s - 1);
+                    if (T::kSlots == 1 && has_s) ok = ok && issue_s(q, s);
+                }
+                if (!ok) break;
+                if (has_s) {
+                    commit_warp(&bar.k_empty[stage_of<T::kKStages>(nk)]);
+                    ++nk;
+                }
+                if (has_o) {
+                    commit_warp(&bar.v_empty[stage_of<T::kVStages>(nv)]);
+                    ++nv;
+                }
+            }
+        }
+        // nothing is in flight when tensor memory is given back
+        commit_warp(&bar.drain);
+        warp_wait(&bar.drain, 0, wait, kSiteDrain);
+      }
+      __syncwarp();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    if (warp == T::kMmaWarp) tmem_dealloc(tmem, T::kTmemCols);
+    pdl_launch_dependents();
+}
+
+// Joins the splits of each row: a CTA a row, its warps taking turns on the
+// splits; the warps' sums are added in their order.
+template <int D>
+__global__ void __launch_bounds__(kThreads) kv_join_kernel(const AttnArgs a) {
+    __shared__ float s_max[kWarps], s_sum[kWarps], s_o[kWarps][D];
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, b = blockIdx.y, H = a.pool.heads;
+    pdl_wait();
+    int row0, n;
+    query_rows(a, b, row0, n);
+    const int rows = n * a.group, len = kv_length(a.tab, b, a.pool.page_log2, a.status);
+    const int splits = rows <= kFewRows ? split_count(len) : tile_splits(rows, len, H, D);
+    if (splits > 1)
+        for (int64_t slot = blockIdx.x; slot < (int64_t)rows * H; slot += gridDim.x) {
+            const int head = (int)(slot / rows), r = (int)(slot - (int64_t)head * rows);
+            const float *pl = a.part_lse + b * a.part_units + slot * splits, *po = a.part + (b * a.part_units + slot * splits) * D;
+            float mm = -INFINITY;
+            for (int s = tid; s < splits; s += kThreads) mm = fmaxf(mm, pl[s]);
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) mm = fmaxf(mm, __shfl_xor_sync(0xFFFFFFFFu, mm, o));
+            __syncthreads();      // the row before is done with shared memory
+            if (lane == 0) s_max[warp] = mm;
+            __syncthreads();
+#pragma unroll
+            for (int w = 0; w < kWarps; ++w) mm = fmaxf(mm, s_max[w]);
+            float o[D / 32], sum = 0.0f;
+#pragma unroll
+            for (int k = 0; k < D / 32; ++k) o[k] = 0.0f;
+#pragma unroll 4
+            for (int s = warp; s < splits; s += kWarps) {
+                const float w = ex2_diff(pl[s], mm);
+                const float2 *p = reinterpret_cast<const float2 *>(po + (int64_t)s * D);
+                sum += w;
+#pragma unroll
+                for (int k = 0; k < D / 64; ++k) {
+                    const float2 v = p[lane + 32 * k];
+                    o[2 * k] = fmaf(w, v.x, o[2 * k]);
+                    o[2 * k + 1] = fmaf(w, v.y, o[2 * k + 1]);
+                }
+            }
+            if (lane == 0) s_sum[warp] = sum;
+#pragma unroll
+            for (int k = 0; k < D / 64; ++k)
+                *reinterpret_cast<float2 *>(&s_o[warp][64 * k + 2 * lane]) = make_float2(o[2 * k], o[2 * k + 1]);
+            __syncthreads();
+            sum = (s_sum[0] + s_sum[1]) + (s_sum[2] + s_sum[3]);
+            const float inv = sum > 0.0f ? __fdiv_rn(1.0f, sum) : 0.0f;
+            const int i = r / a.group, hq = head * a.group + r - i * a.group;
+            uint16_t *dst = a.out + (int64_t)(row0 + i) * a.ldo + (int64_t)hq * a.ldo_head;
+            for (int d = tid * 2; d < D; d += 2 * kThreads) {
+                const float x = (s_o[0][d] + s_o[1][d]) + (s_o[2][d] + s_o[3][d]);
+                const float y = (s_o[0][d + 1] + s_o[1][d + 1]) + (s_o[2][d + 1] + s_o[3][d + 1]);
+                *reinterpret_cast<__nv_bfloat162 *>(dst + d) = __floats2bfloat162_rn(x * inv, y * inv);
+            }
+            if (a.lse && tid == 0)
+                a.lse[(int64_t)(row0 + i) * a.q_heads + hq] = sum > 0.0f ? (mm + log2f(sum)) * (1.0f / kLog2e) : -INFINITY;
+        }
     pdl_launch_dependents();
 }
 
@@ -601,29 +1572,87 @@ cudaError_t launch_split(const AttnArgs &a, int64_t items, int sms, cudaStream_t
     cudaError_t e = opt.set(reinterpret_cast<const void *>(kv_split_kernel<KIND, D, NT>),
                             (size_t)split_smem_floats<D, NT>() * 4 + (kKvMaxSeqs + 1) * 4);
     if (e != cudaSuccess) return e;
-    const int64_t most = (int64_t)sms * 4;
+    const int64_t most = (int64_t)sms * split_ctas<D, NT>();
     return launch_kernel(kv_split_kernel<KIND, D, NT>, dim3((unsigned)(items < most ? items : most)), dim3(kThreads), smem,
                          st, 1, true, a);
 }
 
-template <int D>
-cudaError_t launch_attention(const AttnArgs &a, int kind, int row_max, int64_t items, int64_t slots, bool join, int sms,
-                             cudaStream_t st) {
-    cudaError_t e;
-    if (row_max <= 8)
-        e = kind == kKvInt8 ? launch_split<kKvInt8, D, 1>(a, items, sms, st) : launch_split<kKvE4m3, D, 1>(a, items, sms, st);
-    else
-        e = kind == kKvInt8 ? launch_split<kKvInt8, D, 2>(a, items, sms, st) : launch_split<kKvE4m3, D, 2>(a, items, sms, st);
-    if (e != cudaSuccess || !join) return e;
-    const int64_t blocks = (slots + kWarps - 1) / kWarps, most = (int64_t)sms * 16;
-    return launch_kernel(kv_join_kernel<D>, dim3((unsigned)(blocks < most ? blocks : most)), dim3(kThreads), 0, st, 1, true, a);
+template <int KIND, int D>
+cudaError_t launch_tile(const AttnArgs &a, int64_t items, int sms, cudaStream_t st) {
+    using T = Tile<D>;
+    const size_t smem = (size_t)T::kSmem + (size_t)((a.tab.seqs + kItemStep - 1) / kItemStep + 1) * 4;
+    static SmemOptIn opt;
+    cudaError_t e = opt.set(reinterpret_cast<const void *>(kv_tile_kernel<KIND, D>), (size_t)T::kSmem + (kKvMaxSeqs / kItemStep + 1) * 4);
+    if (e != cudaSuccess) return e;
+    return launch_kernel(kv_tile_kernel<KIND, D>, dim3((unsigned)(items < sms ? items : sms)), dim3(T::kThreadsAll), smem,
+                         st, 1, true, a);
 }
 
-// Rows of a key/value head that may be split, for the workspace: exact when
-// every sequence has the same number of queries.
-int row_capacity(int64_t rows, int64_t seqs, bool ragged, int group) {
-    const int64_t r = ragged ? kFewRows : seqs > 0 ? rows / seqs * group : 0;
-    return (int)(r <= kFewRows ? r : 0);
+// What the host knows of a call's rows: which kernels it needs, how many items
+// each may have, and the places for partial results of a sequence.
+struct Plan {
+    bool few, tile;
+    int row_max;                     // most rows a key/value head of a sequence with few
+    int64_t few_items, tile_items;   // at most
+    int64_t units;                   // places of a sequence; 0: nothing is split
+    int64_t join_rows;               // rows of a sequence that may be split, over its heads, at most
+};
+
+Plan make_plan(int64_t rows, bool ragged, int64_t seqs, int group, int heads, int dim, int64_t max_len) {
+    Plan p = {};
+    if (rows == 0 || seqs == 0) return p;
+    // a shorter sequence may be cut into more runs than the longest: the cut grows in steps
+    int few_splits = 1;
+    for (int64_t len : {max_len, (int64_t)1024, (int64_t)4096, (int64_t)16384})
+        if (len <= max_len && split_count((int)len) > few_splits) few_splits = split_count((int)len);
+    const int64_t per = ragged ? rows * group : rows / seqs * group;   // rows of one sequence, at most
+    p.few = ragged || per <= kFewRows;
+    p.tile = per > kFewRows;
+    if (p.few) {
+        p.row_max = (int)(per < kFewRows ? per : kFewRows);
+        p.few_items = seqs * heads * ((p.row_max + 7) / 8) * few_splits;
+        if (few_splits > 1) {
+            p.units = (int64_t)heads * p.row_max * few_splits;
+            p.join_rows = (int64_t)heads * p.row_max;
+        }
+    }
+    if (p.tile) {
+        const int tr = tile_rows(dim);
+        // a split sequence has at most kTileSlots items
+        p.tile_items = ragged ? (rows * group / tr + seqs) * heads + seqs * kTileSlots
+                              : seqs * (((per + tr - 1) / tr) * heads * tile_splits((int)per, (int)max_len, heads, dim));
+        const bool cut = ragged ? max_len > 512 : tile_splits((int)per, (int)max_len, heads, dim) > 1;
+        if (cut) {
+            int64_t units = (int64_t)kTileSlots * tr, join = units / 2;
+            const int64_t most = per * heads;
+            if (join > most) join = most;
+            if (units > most * kTileMaxSplits) units = most * kTileMaxSplits;
+            if (p.units < units) p.units = units;
+            if (p.join_rows < join) p.join_rows = join;
+        }
+    }
+    return p;
+}
+
+template <int D>
+cudaError_t launch_attention(const AttnArgs &a, int kind, const Plan &p, int sms, cudaStream_t st) {
+    cudaError_t e = cudaSuccess;
+    if (p.tile)
+        e = kind == kKvInt8 ? launch_tile<kKvInt8, D>(a, p.tile_items, sms, st) : launch_tile<kKvE4m3, D>(a, p.tile_items, sms, st);
+    if (e == cudaSuccess && p.few) {
+        if (p.row_max <= 8)
+            e = kind == kKvInt8 ? launch_split<kKvInt8, D, 1>(a, p.few_items, sms, st)
+                                : launch_split<kKvE4m3, D, 1>(a, p.few_items, sms, st);
+        else
+            e = kind == kKvInt8 ? launch_split<kKvInt8, D, 2>(a, p.few_items, sms, st)
+                                : launch_split<kKvE4m3, D, 2>(a, p.few_items, sms, st);
+    }
+    if (e != cudaSuccess || p.units == 0) return e;
+    // a CTA a row, up to 16 CTAs an SM over all sequences
+    int64_t x = p.join_rows;
+    const int64_t most = (int64_t)sms * 16 / a.tab.seqs + 1;
+    if (x > most) x = most;
+    return launch_kernel(kv_join_kernel<D>, dim3((unsigned)x, (unsigned)a.tab.seqs), dim3(kThreads), 0, st, 1, true, a);
 }
 
 }  // namespace
@@ -639,15 +1668,7 @@ extern "C" int clef_kv_attention_workspace(int64_t rows, int ragged, int64_t seq
     if (heads < 1 || q_heads < heads || q_heads % heads != 0) return kv_fail("q_heads must be a multiple of heads");
     if (dim != 64 && dim != 128 && dim != 256) return kv_fail("dim must be 64, 128 or 256");
     if (max_len < 0 || max_len > 0x7FFFFFFF) return kv_fail("max_len out of range");
-    const int cap = row_capacity(rows, seqs, ragged != 0, q_heads / heads);
-    // a shorter sequence may have more splits than the longest: the cut grows in steps
-    int splits = 0;
-    for (int64_t len : {max_len, (int64_t)2048, (int64_t)8192, (int64_t)32768})
-        if (len <= max_len) {
-            const int s = split_count((int)len);
-            if (s > splits) splits = s;
-        }
-    *bytes = splits <= 1 ? 0 : (int64_t)seqs * heads * cap * splits * (dim + 1) * 4;
+    *bytes = seqs * make_plan(rows, ragged != 0, seqs, q_heads / heads, heads, dim, max_len).units * (dim + 1) * 4;
     return CLEF_OK;
 }
 
@@ -674,9 +1695,9 @@ extern "C" int clef_kv_attention(const void *q, int64_t ldq, int64_t ldq_head, i
     if (kv_misaligned(q, 16) || kv_misaligned(out, 16) || kv_misaligned(workspace, 16) || kv_misaligned(lse, 4) ||
         kv_misaligned(row_start, 4))
         return kv_fail("q, out and workspace must be 16-byte, lse and row_start 4-byte aligned");
-    int64_t need = 0;
     const int64_t top = width * page < 0x7FFFFFFF ? width * page : 0x7FFFFFFF;
-    if ((rc = clef_kv_attention_workspace(rows, row_start != nullptr, seqs, q_heads, heads, dim, top, &need))) return rc;
+    const Plan plan = make_plan(rows, row_start != nullptr, seqs, q_heads / heads, heads, dim, top);
+    const int64_t need = seqs * plan.units * (dim + 1) * 4;
     if (need > 0 && (!workspace || workspace_bytes < need)) return kv_fail("workspace smaller than clef_kv_attention_workspace says");
     int sms = 0;
     if ((rc = internal_device(&sms, &a.status))) return rc;
@@ -694,20 +1715,14 @@ extern "C" int clef_kv_attention(const void *q, int64_t ldq, int64_t ldq_head, i
     a.q_heads = q_heads;
     a.causal = causal != 0;
     a.scale_log2 = scale * kLog2e;
-    a.row_cap = row_capacity(rows, seqs, row_start != nullptr, a.group);
-    const int64_t slots = seqs * heads * a.row_cap;
-    if (need > 0) {
-        a.split_cap = (int)(need / (slots * (dim + 1) * 4));
-        a.part = static_cast<float *>(workspace);
-        a.part_lse = a.part + slots * a.split_cap * dim;
-    }
-    // rows of a key/value head, as far as the host knows
-    const int64_t row_max = row_start ? kFewRows : (int64_t)a.per_seq * a.group;
-    const int64_t items = row_start ? (int64_t)1 << 30 : seqs * heads * ((row_max + 7) / 8) * (need > 0 ? a.split_cap : 1);
+    a.part_units = plan.units;
+    a.part = static_cast<float *>(workspace);
+    a.part_lse = a.part + seqs * plan.units * dim;
+    a.wait_limit_ns = internal_wait_limit(&a.force_timeout);
+    sms = internal_launch_sms(sms);
     cudaStream_t st = static_cast<cudaStream_t>(stream);
-    const int rm = (int)(row_max < 64 ? row_max : 64);
-    const cudaError_t e = dim == 64    ? launch_attention<64>(a, kind, rm, items, slots, need > 0, sms, st)
-                          : dim == 128 ? launch_attention<128>(a, kind, rm, items, slots, need > 0, sms, st)
-                                       : launch_attention<256>(a, kind, rm, items, slots, need > 0, sms, st);
+    const cudaError_t e = dim == 64    ? launch_attention<64>(a, kind, plan, sms, st)
+                          : dim == 128 ? launch_attention<128>(a, kind, plan, sms, st)
+                                       : launch_attention<256>(a, kind, plan, sms, st);
     return e == cudaSuccess ? CLEF_OK : internal_cuda_error(e, "cache attention launch");
 }

@@ -22,7 +22,7 @@ enum : unsigned int {
 
 enum KvKind : int { kKvInt8 = 0, kKvE4m3 = 1 };
 
-constexpr int kKvMaxSeqs = 16384;
+constexpr int kKvMaxSeqs = 4096;
 constexpr int kKvMaxWidth = 1 << 20;    // pages of a sequence
 constexpr int kKvMaxPages = 1 << 24;
 

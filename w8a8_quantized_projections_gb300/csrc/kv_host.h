@@ -45,7 +45,7 @@ inline int kv_pool_args(KvPool &p, int kind, void *codes, int64_t plane_bytes, f
 }
 
 inline int kv_table_args(KvTable &t, const int32_t *table, int64_t ldt, int64_t seqs, int64_t width, const int32_t *lens) {
-    if (seqs < 0 || seqs > kKvMaxSeqs) return kv_fail("sequences must be in 0..16384");
+    if (seqs < 0 || seqs > kKvMaxSeqs) return kv_fail("sequences must be in 0..4096");
     if (width < 0 || width > kKvMaxWidth || ldt < width) return kv_fail("table width out of range, or its pitch is smaller");
     if (kv_misaligned(table, 4) || kv_misaligned(lens, 4)) return kv_fail("table and lens must be 4-byte aligned");
     t.table = table;

@@ -437,7 +437,7 @@ extern "C" int clef_kv_fork(void *codes, int64_t plane_bytes, float *scales, int
     if (!rc) rc = book_args(a, table, ldt, seqs, width, lens, refs, pages, page);
     if (rc) return rc;
     if (planes < 1 || planes > 4096) return kv_fail("planes must be in 1..4096");
-    if (n < 0 || n > kKvMaxSeqs) return kv_fail("forks must be in 0..16384");
+    if (n < 0 || n > kKvMaxSeqs) return kv_fail("forks must be in 0..4096");
     if (kv_misaligned(src, 4) || kv_misaligned(dst, 4) || kv_misaligned(scratch, 4))
         return kv_fail("src, dst and scratch must be 4-byte aligned");
     if (n == 0) return CLEF_OK;

@@ -32,8 +32,7 @@ namespace {
 
 constexpr int kBlockK = 128;      // weights of a packed block
 constexpr int kWarps = 8;
-constexpr int kRows = 16 * kWarps;  // output columns (weight rows) of a CTA
-constexpr int kChunk = 16;        // blocks of x held in shared memory at a time
+constexpr int kParts = 8;         // runs of K that are summed apart, then added in order
 constexpr int kDepth = 4;         // blocks of weights a warp has in flight
 
 // Two codes (nibbles in bits 0-3 and 16-19 of w) as bf16: 0x4300 | u is
@@ -88,83 +87,91 @@ struct W4Args {
     const uint16_t *bias;
     uint16_t *y;
     int64_t ldy;
-    int M, N, K, kb;   // kb: blocks of a weight row
-    int slice;         // blocks of one CTA of a cluster
+    int M, N, K;
+    int kb, part;      // blocks of a weight row, and of one of its kParts parts
+    int tiles;         // of 16 * cluster rows
 };
 
-// A CTA takes 128 weight rows (16 a warp) and, as one of a cluster of S, a
-// run of `slice` blocks of K.  The S partial sums meet in shared memory of
-// the cluster, added in the order of K.  S and the runs follow N and K alone,
-// so a row of y has the same bits whatever M is.
+// A cluster of S CTAs takes tiles of 16 S weight rows in turn.  K is cut into
+// eight parts whatever S is; CTA r of the cluster has 8 / S of them, and its
+// eight warps are 8 / S parts times S groups of 16 rows.  A tile's eight
+// partial sums meet in shared memory (of the cluster) and are added in the order
+// of K, so a row of y has the same bits whatever M, S and the grid are.
+//
+// A warp streams its part of 16 rows into registers, kDepth blocks ahead, across
+// the tiles: the loads never wait for a sum.  x's columns of the CTA's parts are
+// read once into shared memory; S is as large as it takes to fit them.
 template <int NT, int GROUP>
 __global__ void __launch_bounds__(kWarps * 32, 2) w4_linear_kernel(const W4Args a) {
     extern __shared__ __align__(16) uint8_t smem[];
-    constexpr int kPitch = kChunk * kBlockK * 2 + 64;      // bytes of a row of x: 64 past a multiple of 128
-    float *part = reinterpret_cast<float *>(smem + NT * 8 * kPitch);   // [NT * 8][kRows]
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
     uint32_t rank, csize;
     asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(rank));
     asm("mov.u32 %0, %%cluster_nctaid.x;" : "=r"(csize));
-    const int n0 = (int)(blockIdx.x / csize) * kRows;
-    const int m0 = (int)blockIdx.y * NT * 8;
-    const int kb0 = (int)rank * a.slice, kb1 = min(a.kb, kb0 + a.slice);
-    const int nk = max(0, kb1 - kb0);
+    const int S = (int)csize, own = kParts / S;                  // parts of this CTA
+    const int rows = 16 * S, m0 = (int)blockIdx.y * NT * 8, mn = min(NT * 8, a.M - m0);
+    const int kb_own = (int)rank * own * a.part;                 // first block of this CTA
+    const int slice = own * a.part;                              // its blocks
+    const int pitch = slice * kBlockK * 2 + 64;                  // bytes of a row of x: 64 past a multiple of 128
+    float *part_sums = reinterpret_cast<float *>(smem + mn * pitch);      // [2][own][NT * 8][rows]
+    const int wp = warp % own, wr = warp / own;                  // this warp's part and rows
+    const int b0 = kb_own + wp * a.part;
+    const int first = (int)blockIdx.x / S, stride = (int)gridDim.x / S;
+    constexpr int kPer = kBlockK / GROUP;
 
     pdl_wait();
 
-    // this lane's two weight rows (rows past N read the last one and are dropped)
-    const int r0 = min(n0 + warp * 16 + g, a.N - 1), r1 = min(n0 + warp * 16 + g + 8, a.N - 1);
-    const uint8_t *w0 = a.qw + ((int64_t)r0 * a.kb + kb0) * 64 + t * 16;
-    const uint8_t *w1 = a.qw + ((int64_t)r1 * a.kb + kb0) * 64 + t * 16;
-    constexpr int kPer = kBlockK / GROUP;
-    const uint16_t *s0 = a.sw + ((int64_t)r0 * a.kb + kb0) * kPer;
-    const uint16_t *s1 = a.sw + ((int64_t)r1 * a.kb + kb0) * kPer;
-
     uint4 wa[kDepth], wb[kDepth];
     Scales<GROUP> sa[kDepth], sb[kDepth];
-#pragma unroll
-    for (int i = 0; i < kDepth; ++i)
-        if (i < nk) {
-            wa[i] = load_stream(w0 + i * 64);
-            wb[i] = load_stream(w1 + i * 64);
-            sa[i].load(s0 + i * kPer);
-            sb[i].load(s1 + i * kPer);
+    // where the next load is: tile and block of the part
+    int lt = first, lb = 0;
+    const auto load = [&](uint4 &va, uint4 &vb, Scales<GROUP> &ua, Scales<GROUP> &ub) {
+        if (lt < a.tiles && b0 + lb < a.kb) {
+            // rows past N read the last one and are dropped
+            const int n = lt * rows + wr * 16 + g, r0 = min(n, a.N - 1), r1 = min(n + 8, a.N - 1);
+            const int64_t i0 = (int64_t)r0 * a.kb + b0 + lb, i1 = (int64_t)r1 * a.kb + b0 + lb;
+            va = load_stream(a.qw + i0 * 64 + t * 16);
+            vb = load_stream(a.qw + i1 * 64 + t * 16);
+            ua.load(a.sw + i0 * kPer);
+            ub.load(a.sw + i1 * kPer);
         }
+        if (++lb == a.part) {
+            lb = 0;
+            lt += stride;
+        }
+    };
+#pragma unroll
+    for (int d = 0; d < kDepth; ++d) load(wa[d], wb[d], sa[d], sb[d]);
 
+    // x's columns of this CTA, zeros past K
+    {
+        const int words = slice * (kBlockK / 8);
+        for (int m = 0; m < mn; ++m)
+            for (int o = tid; o < words; o += kWarps * 32) {
+                const int k = kb_own * kBlockK + o * 8;
+                uint4 v = make_uint4(0, 0, 0, 0);
+                if (k < a.K) v = *reinterpret_cast<const uint4 *>(a.x + (int64_t)(m0 + m) * a.ldx + k);
+                *reinterpret_cast<uint4 *>(smem + m * pitch + o * 16) = v;
+            }
+    }
+    __syncthreads();
+
+    const uint8_t *xs = smem + wp * a.part * 256 + t * 16;
     float acc[NT][4];
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
         for (int i = 0; i < 4; ++i) acc[nt][i] = 0.0f;
-
-    for (int c0 = 0; c0 < nk; c0 += kChunk) {
-        const int cn = min(kChunk, nk - c0);
-        if (c0) __syncthreads();
-        // x rows m0 .. of this chunk, zeros past K and past M
-        const int words = cn * (kBlockK / 8);
-        for (int i = tid; i < NT * 8 * words; i += kWarps * 32) {
-            const int m = i / words, o = i - m * words;
-            const int k = (kb0 + c0) * kBlockK + o * 8;
-            uint4 v = make_uint4(0, 0, 0, 0);
-            if (m0 + m < a.M && k < a.K) v = *reinterpret_cast<const uint4 *>(a.x + (int64_t)(m0 + m) * a.ldx + k);
-            *reinterpret_cast<uint4 *>(smem + m * kPitch + o * 16) = v;
-        }
-        __syncthreads();
-        for (int b0 = 0; b0 < cn; b0 += kDepth) {
+    int tile = first, b = 0, turn = 0;
+    while (tile < a.tiles) {
 #pragma unroll
-            for (int d = 0; d < kDepth; ++d) {
-                const int b = b0 + d;
-                if (b >= cn) break;
+        for (int d = 0; d < kDepth; ++d) {
+            if (tile >= a.tiles) break;
+            if (b0 + b < a.kb) {
                 const uint32_t ra[4] = {wa[d].x, wa[d].y, wa[d].z, wa[d].w};
                 const uint32_t rb[4] = {wb[d].x, wb[d].y, wb[d].z, wb[d].w};
                 const Scales<GROUP> ua = sa[d], ub = sb[d];
-                const int next = c0 + b + kDepth;
-                if (next < nk) {
-                    wa[d] = load_stream(w0 + next * 64);
-                    wb[d] = load_stream(w1 + next * 64);
-                    sa[d].load(s0 + next * kPer);
-                    sb[d].load(s1 + next * kPer);
-                }
+                load(wa[d], wb[d], sa[d], sb[d]);
                 float gr[NT][4];
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
@@ -182,8 +189,9 @@ __global__ void __launch_bounds__(kWarps * 32, 2) w4_linear_kernel(const W4Args 
                     }
 #pragma unroll
                     for (int nt = 0; nt < NT; ++nt) {
-                        const uint4 xv = *reinterpret_cast<const uint4 *>(smem + (nt * 8 + g) * kPitch + b * 256 +
-                                                                          j * 64 + t * 16);
+                        uint4 xv = make_uint4(0, 0, 0, 0);
+                        if (nt * 8 + g < mn)
+                            xv = *reinterpret_cast<const uint4 *>(xs + (nt * 8 + g) * pitch + b * 256 + j * 64);
                         mma_bf16(gr[nt], pa[0], pb[0], pa[1], pb[1], xv.x, xv.y);
                         mma_bf16(gr[nt], pa[2], pb[2], pa[3], pb[3], xv.z, xv.w);
                     }
@@ -198,40 +206,56 @@ __global__ void __launch_bounds__(kWarps * 32, 2) w4_linear_kernel(const W4Args 
                         }
                     }
                 }
+            } else {
+                load(wa[d], wb[d], sa[d], sb[d]);
             }
-        }
-    }
-
-    // partial sums to shared memory as [row of x][weight row]
+            if (++b < a.part) continue;
+            // the tile's partial sums, [part][row of x][weight row]; two buffers in turns, so that one
+            // meeting of the warps a tile is enough
+            float *sums = part_sums + turn * own * NT * 8 * rows;
+            float *mine = sums + wp * NT * 8 * rows + wr * 16;
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt) {
-        const int m = nt * 8 + 2 * t, n = warp * 16 + g;
-        part[m * kRows + n] = acc[nt][0];
-        part[(m + 1) * kRows + n] = acc[nt][1];
-        part[m * kRows + n + 8] = acc[nt][2];
-        part[(m + 1) * kRows + n + 8] = acc[nt][3];
-    }
-    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
-    // each CTA finishes its share of the weight rows
-    const int share = kRows / (int)csize, first = (int)rank * share;
-    const uint32_t base = smem_u32(part);
-    for (int i = tid; i < NT * 8 * share; i += kWarps * 32) {
-        const int m = i / share, n = first + (i - m * share);
-        if (m0 + m >= a.M || n0 + n >= a.N) continue;
-        float v = 0.0f;
-        for (uint32_t c = 0; c < csize; ++c) {
-            uint32_t addr;
-            float p;
-            asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(addr) : "r"(base + (uint32_t)(m * kRows + n) * 4u), "r"(c));
-            asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(p) : "r"(addr));
-            v += p;
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const int m = nt * 8 + 2 * t + (i & 1);
+                    if (m < mn) mine[m * rows + g + 8 * (i >> 1)] = acc[nt][i];
+                    acc[nt][i] = 0.0f;
+                }
+            if (S == 1)
+                __syncthreads();
+            else
+                asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+            // each CTA finishes 16 of the rows
+            for (int i = tid; i < mn * 16; i += kWarps * 32) {
+                const int m = i >> 4, r = (int)rank * 16 + (i & 15), n = tile * rows + r;
+                if (n < a.N) {
+                    float v = 0.0f;
+                    for (int p = 0; p < kParts; ++p) {
+                        const float *at = sums + ((p % own) * NT * 8 + m) * rows + r;
+                        if (S == 1) {
+                            v += *at;
+                        } else {
+                            uint32_t addr;
+                            float q;
+                            asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(addr) : "r"(smem_u32(at)), "r"((uint32_t)(p / own)));
+                            asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(q) : "r"(addr) : "memory");
+                            v += q;
+                        }
+                    }
+                    if (a.bias) v += __uint_as_float((uint32_t)a.bias[n] << 16);
+                    const __nv_bfloat16 o = __float2bfloat16_rn(v);
+                    a.y[(int64_t)(m0 + m) * a.ldy + n] = *reinterpret_cast<const uint16_t *>(&o);
+                }
+            }
+            b = 0;
+            turn ^= 1;
+            tile += stride;
         }
-        if (a.bias) v += __uint_as_float((uint32_t)*(a.bias + n0 + n) << 16);
-        const __nv_bfloat16 o = __float2bfloat16_rn(v);
-        a.y[(int64_t)(m0 + m) * a.ldy + n0 + n] = *reinterpret_cast<const uint16_t *>(&o);
     }
     pdl_launch_dependents();
-    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+    // no CTA of a cluster ends while another reads its sums
+    if (S > 1) asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 
 // Packs bf16 weight rows: s = bf16(amax / 7) of each group, codes
@@ -288,24 +312,29 @@ int fail(const char *msg) {
 
 bool misaligned(const void *p, unsigned to) { return (reinterpret_cast<uintptr_t>(p) & (to - 1)) != 0; }
 
-constexpr int64_t kMaxW4 = (int64_t)1 << 24;
+constexpr int64_t kMaxW4 = (int64_t)1 << 24, kMaxK = 65536;
 
 template <int NT, int GROUP>
-cudaError_t launch_w4(const W4Args &a, int split, int blocks_m, cudaStream_t st) {
-    const size_t smem = (size_t)NT * 8 * (kChunk * kBlockK * 2 + 64) + (size_t)NT * 8 * kRows * 4;
+cudaError_t launch_w4(const W4Args &a, int split, int blocks_m, int sms, cudaStream_t st) {
+    const int own = kParts / split, rows = 16 * split, m = a.M < NT * 8 ? a.M : NT * 8;
+    const size_t smem = (size_t)m * (own * a.part * kBlockK * 2 + 64) + (size_t)2 * own * NT * 8 * rows * 4;
     static SmemOptIn opt;
-    cudaError_t e = opt.set(reinterpret_cast<const void *>(w4_linear_kernel<NT, GROUP>), smem);
+    cudaError_t e = opt.set(reinterpret_cast<const void *>(w4_linear_kernel<NT, GROUP>), 220 * 1024);
     if (e != cudaSuccess) return e;
-    const dim3 grid((unsigned)((a.N + kRows - 1) / kRows * split), (unsigned)blocks_m);
-    return launch_kernel(w4_linear_kernel<NT, GROUP>, grid, dim3(kWarps * 32), smem, st, split, true, a);
+    const int per_sm = smem <= 110 * 1024 ? 2 : 1;
+    int clusters = sms * per_sm / split;
+    if (clusters < 1) clusters = 1;
+    if (clusters > a.tiles) clusters = a.tiles;
+    return launch_kernel(w4_linear_kernel<NT, GROUP>, dim3((unsigned)(clusters * split), (unsigned)blocks_m), dim3(kWarps * 32),
+                         smem, st, split, true, a);
 }
 
 template <int NT>
-cudaError_t launch_w4_group(const W4Args &a, int group, int split, int blocks_m, cudaStream_t st) {
+cudaError_t launch_w4_group(const W4Args &a, int group, int split, int blocks_m, int sms, cudaStream_t st) {
     switch (group) {
-        case 32: return launch_w4<NT, 32>(a, split, blocks_m, st);
-        case 64: return launch_w4<NT, 64>(a, split, blocks_m, st);
-        default: return launch_w4<NT, 128>(a, split, blocks_m, st);
+        case 32: return launch_w4<NT, 32>(a, split, blocks_m, sms, st);
+        case 64: return launch_w4<NT, 64>(a, split, blocks_m, sms, st);
+        default: return launch_w4<NT, 128>(a, split, blocks_m, sms, st);
     }
 }
 
@@ -318,7 +347,7 @@ using namespace clef;
 extern "C" int clef_quant_w4(const void *w, int64_t N, int64_t K, int64_t ldw, int group, void *qw, void *sw,
                              void *stream) {
     if (N < 0 || N > kMaxW4) return fail("invalid argument: N out of range");
-    if (K <= 0 || K > kMaxW4 || K % 8 != 0) return fail("invalid argument: K must be positive and a multiple of 8");
+    if (K <= 0 || K > kMaxK || K % 8 != 0) return fail("invalid argument: K must be in (0, 65536] and a multiple of 8");
     if (ldw < K || ldw % 8 != 0) return fail("invalid argument: ldw must be >= K and a multiple of 8");
     if (group != 32 && group != 64 && group != 128) return fail("invalid argument: group must be 32, 64 or 128");
     if (N == 0) return CLEF_OK;
@@ -344,7 +373,7 @@ extern "C" int clef_w4_linear(const void *x, int64_t ldx, const void *qw, const 
                               int64_t M, int64_t N, int64_t K, void *y, int64_t ldy, void *stream) {
     if (M < 0 || M > kMaxW4 / 32) return fail("invalid argument: M out of range");
     if (N <= 0 || N > kMaxW4) return fail("invalid argument: N out of range");
-    if (K <= 0 || K > kMaxW4 || K % 8 != 0) return fail("invalid argument: K must be positive and a multiple of 8");
+    if (K <= 0 || K > kMaxK || K % 8 != 0) return fail("invalid argument: K must be in (0, 65536] and a multiple of 8");
     if (group != 32 && group != 64 && group != 128) return fail("invalid argument: group must be 32, 64 or 128");
     if (ldx < K || ldx % 8 != 0) return fail("invalid argument: ldx must be >= K and a multiple of 8");
     if (ldy < N) return fail("invalid argument: ldy must be >= N");
@@ -358,12 +387,12 @@ extern "C" int clef_w4_linear(const void *x, int64_t ldx, const void *qw, const 
     int rc = internal_device(&sms, &status);
     if (rc) return rc;
     const int kb = (int)((K + kBlockK - 1) / kBlockK);
-    // CTAs a weight row block is split over along K: the fewest that give two
-    // CTAs to every SM, and never less than two blocks of K each.  A rule on N
-    // and K alone (the order of a row's sum must not follow M).
+    const int part = (kb + kParts - 1) / kParts;
+    // CTAs of a cluster: so many that a CTA's columns of x leave room for two CTAs an SM
+    const auto x_bytes = [&](int64_t m, int split) { return m * (kParts / split * part * kBlockK * 2 + 64); };
+    const int64_t block_m = M > 8 && x_bytes(M < 16 ? M : 16, kParts) <= 200 * 1024 ? 16 : 8;
     int split = 1;
-    const int64_t tiles = (N + kRows - 1) / kRows;
-    while (split < 8 && tiles * split < 304 && kb >= 4 * split) split *= 2;
+    while (split < kParts && x_bytes(M < block_m ? M : block_m, split) > 80 * 1024) split *= 2;
     W4Args a;
     a.x = static_cast<const uint16_t *>(x);
     a.ldx = ldx;
@@ -376,9 +405,12 @@ extern "C" int clef_w4_linear(const void *x, int64_t ldx, const void *qw, const 
     a.N = (int)N;
     a.K = (int)K;
     a.kb = kb;
-    a.slice = (kb + split - 1) / split;
+    a.part = part;
+    a.tiles = (int)((N + 16 * split - 1) / (16 * split));
+    sms = internal_launch_sms(sms);
     cudaStream_t st = static_cast<cudaStream_t>(stream);
-    const cudaError_t e = M <= 8 ? launch_w4_group<1>(a, group, split, 1, st)
-                                 : launch_w4_group<2>(a, group, split, (int)((M + 15) / 16), st);
+    const int blocks_m = (int)((M + block_m - 1) / block_m);
+    const cudaError_t e = block_m == 8 ? launch_w4_group<1>(a, group, split, blocks_m, sms, st)
+                                       : launch_w4_group<2>(a, group, split, blocks_m, sms, st);
     return e == cudaSuccess ? CLEF_OK : internal_cuda_error(e, "4-bit linear launch");
 }
