@@ -29,7 +29,7 @@ def check(x, codes, sw, group, bias, got):
 @pytest.mark.parametrize("M,N,K,bias", [
     (1, 128, 128, False), (1, 1, 8, True), (2, 7, 136, True), (3, 129, 256, False), (8, 300, 1000, True),
     (9, 257, 1152, False), (13, 1025, 520, True), (16, 64, 4096, False), (17, 130, 264, True), (40, 250, 2056, False),
-    (1, 5120, 6144, False), (5, 2048, 17408, True),
+    (1, 5120, 6144, False), (5, 2048, 17408, True), (12, 48, 65536, False), (16, 100, 17408, True), (1, 20000, 128, False),
 ])
 def test_linear(M, N, K, bias, group):
     rng = np.random.default_rng(M * 7 + N + K + group)
@@ -66,11 +66,12 @@ def test_pack(N, K, group):
     check(x, c[:, :K], s, group, None, clef.w4_linear(dev_bf16(x), qw, sw).float().cpu().numpy())
 
 
-def test_rows_do_not_depend_on_m():
+@pytest.mark.parametrize("group", [32, 64, 128])
+def test_rows_do_not_depend_on_m(group):
     """The bits of a row are the same alone, among others and at an output pitch."""
     rng = np.random.default_rng(5)
     x = dev_bf16(rng.standard_normal((37, 2176)))
-    qw, sw = clef.quant_w4(dev_bf16(rng.standard_normal((515, 2176)) * 0.02), 64)
+    qw, sw = clef.quant_w4(dev_bf16(rng.standard_normal((515, 2176)) * 0.02), group)
     whole = clef.w4_linear(x, qw, sw)
     for a, b in ((0, 1), (1, 3), (3, 11), (11, 24), (24, 37)):
         assert torch.equal(clef.w4_linear(x[a:b], qw, sw), whole[a:b])

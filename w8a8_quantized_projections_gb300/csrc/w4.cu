@@ -16,10 +16,20 @@
 // core, so that every mma stays inside one scale group whatever its length.
 // Nibble i < 4 of a word holds weight 2 i, nibble i + 4 weight 2 i + 1, so
 // that (w >> 4 i) & 0x000F000F is a pair of neighbours in two halfwords.  A
-// nibble holds c + 8.
+// nibble holds u = c + 8.
+//
+// Widening.  The halfword u is an fp16 number as it is: u 2^-24, below the
+// normal numbers and exact, and tensor cores take such numbers whole.  With
+// w & 0x00F000F0 it is u 2^-20, whose x is stored 2^-4 as large.  So a word's
+// eight codes become operands in five instructions: w and w >> 8 under two masks.
+// The 8 in u leaves by the sum's start value, -8 2^-24 sum x over the group.
+// x is held in fp16, each run of K that is summed apart scaled by a power of
+// two to a largest magnitude in [2^13, 2^14): bf16 has fewer bits than fp16,
+// so only values under 2^-23 of the run's largest lose any.
 #include <cstdint>
 
 #include <cuda_bf16.h>
+#include <cuda_fp16.h>
 #include <cuda_runtime.h>
 
 #include "../../include/clef.h"
@@ -33,50 +43,56 @@ namespace {
 constexpr int kBlockK = 128;      // weights of a packed block
 constexpr int kWarps = 8;
 constexpr int kParts = 8;         // runs of K that are summed apart, then added in order
-constexpr int kDepth = 4;         // blocks of weights a warp has in flight
+constexpr int kDepth = 3;         // stages of two blocks that a warp has on their way; one more is in use
+constexpr int kStage = 2048 + 256;    // bytes of a stage: 16 rows of 128, and their scales
 
-// Two codes (nibbles in bits 0-3 and 16-19 of w) as bf16: 0x4300 | u is
-// 128 + u, and 128 + u - 136 = u - 8 without rounding.
-__device__ __forceinline__ uint32_t widen(uint32_t w) {
-    uint32_t v;
-    asm("lop3.b32 %0, %1, 0x000F000F, 0x43004300, 0xEA;" : "=r"(v) : "r"(w));   // (w & mask) | 0x4300
-    asm("sub.rn.bf16x2 %0, %1, %2;" : "=r"(v) : "r"(v), "r"(0x43084308u));
-    return v;
+__device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                        uint32_t b1, float c0, float c1, float c2, float c3) {
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%11,%12,%13};"
+        : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(c0), "f"(c1), "f"(c2), "f"(c3));
 }
 
-__device__ __forceinline__ void mma_bf16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
-                                         uint32_t b0, uint32_t b1) {
-    asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
-        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
-}
-
-__device__ __forceinline__ uint4 load_stream(const uint8_t *p) {
-    uint4 v;
-    asm volatile("ld.global.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];"
-                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p));
-    return v;
+__device__ __forceinline__ uint32_t pack_half(float lo, float hi) {
+    uint32_t r;
+    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
 }
 
 // The scales of one block of a row: 128 / GROUP bf16 values.
 template <int GROUP>
 struct Scales {
     uint32_t w[GROUP == 32 ? 2 : 1];
-    __device__ __forceinline__ void load(const uint16_t *p) {
+    // block b (0 or 1) of a stage; GROUP 128: `odd`, which of the first word's two the first block has
+    __device__ __forceinline__ void load(const uint8_t *p, uint32_t odd, int b) {
         if constexpr (GROUP == 32) {
-            const uint2 v = *reinterpret_cast<const uint2 *>(p);
+            const uint2 v = *reinterpret_cast<const uint2 *>(p + 8 * b);
             w[0] = v.x;
             w[1] = v.y;
         } else if constexpr (GROUP == 64) {
-            w[0] = *reinterpret_cast<const uint32_t *>(p);
+            w[0] = *reinterpret_cast<const uint32_t *>(p + 4 * b);
         } else {
-            w[0] = *p;
+            w[0] = *reinterpret_cast<const uint16_t *>(p + 2 * (odd + b));
         }
     }
     __device__ __forceinline__ float get(int i) const {
         const uint32_t v = w[i / 2];
         return __uint_as_float((i & 1) ? (v & 0xFFFF0000u) : (v << 16));
     }
+};
+
+// 16 bytes, of which the last 16 - there are zeros
+__device__ __forceinline__ void copy16(uint32_t dst, const void *src, int there = 16) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(there) : "memory");
+}
+template <int BYTES>
+__device__ __forceinline__ void copy_some(uint32_t dst, const void *src, int there) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;" ::"r"(dst), "l"(src), "n"(BYTES), "r"(there) : "memory");
+}
+
+template <int N>
+struct Count {
+    static constexpr int value = N;
 };
 
 struct W4Args {
@@ -90,6 +106,7 @@ struct W4Args {
     int M, N, K;
     int kb, part;      // blocks of a weight row, and of one of its kParts parts
     int tiles;         // of 16 * cluster rows
+    int split_log2;    // CTAs of a cluster
 };
 
 // A cluster of S CTAs takes tiles of 16 S weight rows in turn.  K is cut into
@@ -98,159 +115,272 @@ struct W4Args {
 // partial sums meet in shared memory (of the cluster) and are added in the order
 // of K, so a row of y has the same bits whatever M, S and the grid are.
 //
-// A warp streams its part of 16 rows into registers, kDepth blocks ahead, across
-// the tiles: the loads never wait for a sum.  x's columns of the CTA's parts are
-// read once into shared memory; S is as large as it takes to fit them.
+// A warp streams its part of 16 rows through a ring of its own in shared memory,
+// kDepth blocks ahead, across the tiles: the copies never wait for a sum, and each
+// lane reads back the 16 bytes it copied itself.  x's columns of the CTA's parts
+// are read once into shared memory; S is as large as it takes to fit them.
 template <int NT, int GROUP>
-__global__ void __launch_bounds__(kWarps * 32, 2) w4_linear_kernel(const W4Args a) {
+__global__ void __launch_bounds__(kWarps * 32, NT == 1 ? 2 : 1) w4_linear_kernel(const W4Args a) {
     extern __shared__ __align__(16) uint8_t smem[];
+    __shared__ float s_unit[NT * 8][kParts];      // what a part's sum of a row of x is multiplied by
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
-    uint32_t rank, csize;
+    uint32_t rank;
     asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(rank));
-    asm("mov.u32 %0, %%cluster_nctaid.x;" : "=r"(csize));
-    const int S = (int)csize, own = kParts / S;                  // parts of this CTA
+    const int S = 1 << a.split_log2, own_log2 = 3 - a.split_log2, own = 1 << own_log2;      // own: parts of this CTA
     const int rows = 16 * S, m0 = (int)blockIdx.y * NT * 8, mn = min(NT * 8, a.M - m0);
     const int kb_own = (int)rank * own * a.part;                 // first block of this CTA
     const int slice = own * a.part;                              // its blocks
     const int pitch = slice * kBlockK * 2 + 64;                  // bytes of a row of x: 64 past a multiple of 128
-    float *part_sums = reinterpret_cast<float *>(smem + mn * pitch);      // [2][own][NT * 8][rows]
-    const int wp = warp % own, wr = warp / own;                  // this warp's part and rows
-    const int b0 = kb_own + wp * a.part;
-    const int first = (int)blockIdx.x / S, stride = (int)gridDim.x / S;
     constexpr int kPer = kBlockK / GROUP;
+    const int groups = slice * kPer;
+    float *x_sums = reinterpret_cast<float *>(smem + mn * pitch);         // [groups][NT * 8]: where the sums start
+    float *part_sums = x_sums + groups * NT * 8;                          // [2][own][NT * 8][rows]
+    const int wp = warp & (own - 1), wr = warp >> own_log2;                  // this warp's part and rows
+    const int b0 = kb_own + wp * a.part, nb = max(0, min(a.part, a.kb - b0));     // its blocks (a last part may have fewer)
+    const int first = (int)blockIdx.x >> a.split_log2, stride = (int)gridDim.x >> a.split_log2;
+    uint8_t *ring = reinterpret_cast<uint8_t *>(part_sums + 2 * own * NT * 8 * rows) + warp * (kDepth + 1) * kStage;
 
     pdl_wait();
 
-    uint4 wa[kDepth], wb[kDepth];
-    Scales<GROUP> sa[kDepth], sb[kDepth];
-    // where the next load is: tile and block of the part
-    int lt = first, lb = 0;
-    const auto load = [&](uint4 &va, uint4 &vb, Scales<GROUP> &ua, Scales<GROUP> &ub) {
-        if (lt < a.tiles && b0 + lb < a.kb) {
-            // rows past N read the last one and are dropped
-            const int n = lt * rows + wr * 16 + g, r0 = min(n, a.N - 1), r1 = min(n + 8, a.N - 1);
-            const int64_t i0 = (int64_t)r0 * a.kb + b0 + lb, i1 = (int64_t)r1 * a.kb + b0 + lb;
-            va = load_stream(a.qw + i0 * 64 + t * 16);
-            vb = load_stream(a.qw + i1 * 64 + t * 16);
-            ua.load(a.sw + i0 * kPer);
-            ub.load(a.sw + i1 * kPer);
-        }
-        if (++lb == a.part) {
-            lb = 0;
-            lt += stride;
-        }
-    };
+    // where the next copy is: its tile, block and addresses (rows past N read the last one and are
+    // dropped).  A lane copies 16 bytes of rows lane / 8 + 4 i, so that eight lanes take a whole 128-byte
+    // line, and the scales of a block of row lane % 16; in the stage the halves of every second row are
+    // swapped, so that the lanes' reads meet every bank once.
+    int lt = first, lb = 0, put = 0;
+    const uint8_t *wsrc = nullptr;
+    int woff[4];
+    const uint16_t *sc = nullptr;
+    const uint16_t *sc_end = a.sw + (int64_t)a.N * a.kb * kPer;
+    const auto to_tile = [&]() {
+        const int n = lt * rows + wr * 16, n0 = min(n + (lane >> 3), a.N - 1);
+        wsrc = a.qw + ((int64_t)n0 * a.kb + b0) * 64 + (lane & 7) * 16;
 #pragma unroll
-    for (int d = 0; d < kDepth; ++d) load(wa[d], wb[d], sa[d], sb[d]);
-
-    // x's columns of this CTA, zeros past K
-    {
-        const int words = slice * (kBlockK / 8);
-        for (int m = 0; m < mn; ++m)
-            for (int o = tid; o < words; o += kWarps * 32) {
-                const int k = kb_own * kBlockK + o * 8;
-                uint4 v = make_uint4(0, 0, 0, 0);
-                if (k < a.K) v = *reinterpret_cast<const uint4 *>(a.x + (int64_t)(m0 + m) * a.ldx + k);
-                *reinterpret_cast<uint4 *>(smem + m * pitch + o * 16) = v;
+        for (int i = 0; i < 4; ++i) woff[i] = (min(n + (lane >> 3) + 4 * i, a.N - 1) - n0) * a.kb * 64;
+        sc = a.sw + ((int64_t)min(n + (lane & 15), a.N - 1) * a.kb + b0) * kPer;
+        if constexpr (GROUP == 128)      // the aligned word that holds the row's first scale, or the next one
+            sc = reinterpret_cast<const uint16_t *>(reinterpret_cast<uintptr_t>(sc) & ~(uintptr_t)3) + 2 * (lane >> 4);
+        else
+            sc += (lane >> 4) * kPer;
+    };
+    const uint32_t ring_at = smem_u32(ring), lane_at = ring_at + (lane >> 3) * 128 + (((lane & 7) ^ ((lane >> 3 & 1) << 2)) << 4);
+    const auto fetch = [&]() {
+        if (nb > 0 && lt < a.tiles) {
+            const uint32_t dst = (uint32_t)(put * kStage);
+            // a part's odd last block is copied twice, the second time for nothing
+            const bool both = lb + 1 < nb;
+            const uint8_t *src = both || (lane & 4) == 0 ? wsrc : wsrc - 64;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) copy16(lane_at + dst + i * 512, src + woff[i]);
+            wsrc += 128;
+            const uint32_t at = ring_at + dst + 2048 + (lane & 15) * 16 + (lane >> 4) * (GROUP == 32 ? 8 : 4);
+            if constexpr (GROUP == 128) {      // past the array's end nothing is read
+                const int64_t left = sc_end - sc;
+                copy_some<4>(at, left > 0 ? sc : a.sw, left >= 2 ? 4 : left == 1 ? 2 : 0);
+            } else {
+                copy_some<2 * kPer>(at, both || lane < 16 ? sc : sc - kPer, 2 * kPer);
             }
+            sc += 2 * kPer;
+            lb += 2;
+            if (lb >= nb) {
+                lb = 0;
+                lt += stride;
+                to_tile();
+            }
+        }
+        put = put == kDepth ? 0 : put + 1;
+        asm volatile("cp.async.commit_group;" ::: "memory");
+    };
+
+    // x's columns of this CTA, zeros past K: a warp a (row, part)
+    for (int i = warp; i < mn * own; i += kWarps) {
+        const int m = i >> own_log2, p = i & (own - 1), words = a.part * (kBlockK / 8), k0 = (kb_own + p * a.part) * kBlockK;
+        const uint16_t *src = a.x + (int64_t)(m0 + m) * a.ldx;
+        const uint32_t dst = smem_u32(smem + m * pitch + p * a.part * 256);
+        for (int o = lane; o < words; o += 32) {
+            const int k = k0 + o * 8;
+            copy16(dst + o * 16, src + (k < a.K ? k : 0), k < a.K ? 16 : 0);
+        }
+    }
+    asm volatile("cp.async.commit_group;" ::: "memory");
+    if (nb > 0) to_tile();
+    for (int d = 0; d < kDepth; ++d) fetch();
+    asm volatile("cp.async.wait_group %0;" ::"n"(kDepth) : "memory");      // x is there
+    __syncwarp();
+
+    // to fp16
+    for (int i = warp; i < mn * own; i += kWarps) {
+        const int m = i >> own_log2, p = i & (own - 1), words = a.part * (kBlockK / 8);
+        uint4 *at = reinterpret_cast<uint4 *>(smem + m * pitch + p * a.part * 256);
+        uint32_t top = 0;
+#pragma unroll 4
+        for (int o = lane; o < words; o += 32) {
+            const uint4 v = at[o];
+            top = __vmaxu2(top, __vmaxu2(__vmaxu2(v.x & 0x7FFF7FFFu, v.y & 0x7FFF7FFFu), __vmaxu2(v.z & 0x7FFF7FFFu, v.w & 0x7FFF7FFFu)));
+        }
+        top = __reduce_max_sync(0xFFFFFFFFu, max(top & 0xFFFFu, top >> 16)) << 16;      // bf16 bits order like integers
+        const int e = top ? max(-100, min(120, 13 - (int)(top >> 23) + 127)) : 0;
+        const float up = __uint_as_float((uint32_t)(127 + e) << 23);
+#pragma unroll 2
+        for (int o = lane; o < (words + 31) / 32 * 32; o += 32) {
+            float sum = 0.0f;
+            if (o < words) {
+                const uint4 v = at[o];
+                const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+                uint32_t h[4];
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    // the second and fourth pair meet codes 2^4 as large
+                    const float f = (k & 1) ? up * 0.0625f : up, back = (k & 1) ? 16.0f : 1.0f;
+                    h[k] = pack_half(__uint_as_float(w[k] << 16) * f, __uint_as_float(w[k] & 0xFFFF0000u) * f);
+                    const __half2 r = *reinterpret_cast<const __half2 *>(&h[k]);
+                    sum = fmaf(back, __low2float(r) + __high2float(r), sum);
+                }
+                at[o] = make_uint4(h[0], h[1], h[2], h[3]);
+            }
+            // the lanes of a group: 8 weights each (words is a multiple of 16)
+#pragma unroll
+            for (int s = 1; s < GROUP / 8; s <<= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, s);
+            if (o < words && (o & (GROUP / 8 - 1)) == 0) x_sums[(p * a.part * kPer + o / (GROUP / 8)) * NT * 8 + m] = -0x1p-21f * sum;
+        }
+        if (lane == 0) s_unit[m][p] = __uint_as_float((uint32_t)(127 + 24 - e) << 23);
     }
     __syncthreads();
 
-    const uint8_t *xs = smem + wp * a.part * 256 + t * 16;
+    // x's rows of this lane's columns (columns that are not there read the last row and are dropped)
+    const uint8_t *xs[NT];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) xs[nt] = smem + min(nt * 8 + g, mn - 1) * pitch + wp * a.part * 256 + t * 16;
+    const float2 *starts = reinterpret_cast<const float2 *>(x_sums + wp * a.part * kPer * NT * 8) + t;
+    float unit[NT][2];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int i = 0; i < 2; ++i) unit[nt][i] = nt * 8 + 2 * t + i < mn ? s_unit[nt * 8 + 2 * t + i][wp] : 0.0f;
     float acc[NT][4];
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
         for (int i = 0; i < 4; ++i) acc[nt][i] = 0.0f;
-    int tile = first, b = 0, turn = 0;
-    while (tile < a.tiles) {
+    int turn = 0, get = 0;
+    const uint8_t *st = ring;
+    for (int tile = first; tile < a.tiles; tile += stride, turn ^= 1) {
+        // which half of its four bytes a row's first scale of the part is in
+        uint32_t odd_a = 0, odd_b = 0;
+        if constexpr (GROUP == 128) {
+            const int n = tile * rows + wr * 16 + g;
+            odd_a = (uint32_t)(((int64_t)min(n, a.N - 1) * a.kb + b0) & 1);
+            odd_b = (uint32_t)(((int64_t)min(n + 8, a.N - 1) * a.kb + b0) & 1);
+        }
+        // COUNT blocks of the stage, from the part's block b on
+        const auto multiply = [&](auto count, int b) {
+            constexpr int COUNT = decltype(count)::value, kRuns = GROUP / 32;
+            // the sums of each group; a single one in two chains, as a chain of products is as long as the
+            // tensor core is deep
+            constexpr int kChains = kPer == 1 ? 2 : 1;
+            float gr[COUNT * kPer * kChains][NT][4];
+            Scales<GROUP> ua[COUNT], ub[COUNT];
+            uint32_t ra[COUNT][4], rb[COUNT][4];
 #pragma unroll
-        for (int d = 0; d < kDepth; ++d) {
-            if (tile >= a.tiles) break;
-            if (b0 + b < a.kb) {
-                const uint32_t ra[4] = {wa[d].x, wa[d].y, wa[d].z, wa[d].w};
-                const uint32_t rb[4] = {wb[d].x, wb[d].y, wb[d].z, wb[d].w};
-                const Scales<GROUP> ua = sa[d], ub = sb[d];
-                load(wa[d], wb[d], sa[d], sb[d]);
-                float gr[NT][4];
+            for (int k = 0; k < COUNT; ++k) {
+                const int odd = (b + k) & 1;
+                const uint8_t *at = st + g * 128 + (((odd ^ (g & 1)) << 6) | (t << 4));
+                const uint4 va = *reinterpret_cast<const uint4 *>(at), vb = *reinterpret_cast<const uint4 *>(at + 1024);
+                ra[k][0] = va.x, ra[k][1] = va.y, ra[k][2] = va.z, ra[k][3] = va.w;
+                rb[k][0] = vb.x, rb[k][1] = vb.y, rb[k][2] = vb.z, rb[k][3] = vb.w;
+                ua[k].load(st + 2048 + g * 16, odd_a, odd);
+                ub[k].load(st + 2048 + (g + 8) * 16, odd_b, odd);
+            }
 #pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    if (j % (GROUP / 32) == 0) {
+            for (int j = 0; j < 4; ++j)
 #pragma unroll
-                        for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                            for (int i = 0; i < 4; ++i) gr[nt][i] = 0.0f;
-                    }
-                    uint32_t pa[4], pb[4];
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        pa[i] = widen(ra[j] >> (4 * i));
-                        pb[i] = widen(rb[j] >> (4 * i));
-                    }
+                for (int k = 0; k < COUNT; ++k) {
+                    const uint32_t la = ra[k][j], lb = rb[k][j], ha = la >> 8, hb = lb >> 8;
+                    const int group = k * kPer + j / kRuns;
 #pragma unroll
                     for (int nt = 0; nt < NT; ++nt) {
-                        uint4 xv = make_uint4(0, 0, 0, 0);
-                        if (nt * 8 + g < mn)
-                            xv = *reinterpret_cast<const uint4 *>(xs + (nt * 8 + g) * pitch + b * 256 + j * 64);
-                        mma_bf16(gr[nt], pa[0], pb[0], pa[1], pb[1], xv.x, xv.y);
-                        mma_bf16(gr[nt], pa[2], pb[2], pa[3], pb[3], xv.z, xv.w);
-                    }
-                    if ((j + 1) % (GROUP / 32) == 0) {
-                        const float fa = ua.get(j / (GROUP / 32)), fb = ub.get(j / (GROUP / 32));
-#pragma unroll
-                        for (int nt = 0; nt < NT; ++nt) {
-                            acc[nt][0] = fmaf(fa, gr[nt][0], acc[nt][0]);
-                            acc[nt][1] = fmaf(fa, gr[nt][1], acc[nt][1]);
-                            acc[nt][2] = fmaf(fb, gr[nt][2], acc[nt][2]);
-                            acc[nt][3] = fmaf(fb, gr[nt][3], acc[nt][3]);
-                        }
-                    }
-                }
-            } else {
-                load(wa[d], wb[d], sa[d], sb[d]);
-            }
-            if (++b < a.part) continue;
-            // the tile's partial sums, [part][row of x][weight row]; two buffers in turns, so that one
-            // meeting of the warps a tile is enough
-            float *sums = part_sums + turn * own * NT * 8 * rows;
-            float *mine = sums + wp * NT * 8 * rows + wr * 16;
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const int m = nt * 8 + 2 * t + (i & 1);
-                    if (m < mn) mine[m * rows + g + 8 * (i >> 1)] = acc[nt][i];
-                    acc[nt][i] = 0.0f;
-                }
-            if (S == 1)
-                __syncthreads();
-            else
-                asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
-            // each CTA finishes 16 of the rows
-            for (int i = tid; i < mn * 16; i += kWarps * 32) {
-                const int m = i >> 4, r = (int)rank * 16 + (i & 15), n = tile * rows + r;
-                if (n < a.N) {
-                    float v = 0.0f;
-                    for (int p = 0; p < kParts; ++p) {
-                        const float *at = sums + ((p % own) * NT * 8 + m) * rows + r;
-                        if (S == 1) {
-                            v += *at;
+                        const uint4 xv = *reinterpret_cast<const uint4 *>(xs[nt] + (b + k) * 256 + j * 64);
+                        float(&lo)[4] = gr[group * kChains][nt], (&hi)[4] = gr[group * kChains + kChains - 1][nt];
+                        float c[4], z[4];
+                        if (j % kRuns == 0) {
+                            const float2 v = starts[(b * kPer + group) * (NT * 4) + nt * 4];
+                            c[0] = c[2] = v.x;
+                            c[1] = c[3] = v.y;
                         } else {
-                            uint32_t addr;
-                            float q;
-                            asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(addr) : "r"(smem_u32(at)), "r"((uint32_t)(p / own)));
-                            asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(q) : "r"(addr) : "memory");
-                            v += q;
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) c[i] = lo[i];
                         }
+                        mma_f16(lo, la & 0x000F000Fu, lb & 0x000F000Fu, la & 0x00F000F0u, lb & 0x00F000F0u, xv.x, xv.y, c[0], c[1],
+                                c[2], c[3]);
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) z[i] = kChains == 2 && j == 0 ? 0.0f : hi[i];
+                        mma_f16(hi, ha & 0x000F000Fu, hb & 0x000F000Fu, ha & 0x00F000F0u, hb & 0x00F000F0u, xv.z, xv.w, z[0], z[1],
+                                z[2], z[3]);
                     }
-                    if (a.bias) v += __uint_as_float((uint32_t)a.bias[n] << 16);
-                    const __nv_bfloat16 o = __float2bfloat16_rn(v);
-                    a.y[(int64_t)(m0 + m) * a.ldy + n] = *reinterpret_cast<const uint16_t *>(&o);
                 }
+#pragma unroll
+            for (int p = 0; p < COUNT * kPer; ++p) {
+                const float fa = ua[p / kPer].get(p % kPer), fb = ub[p / kPer].get(p % kPer);
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const float v = kChains == 2 ? gr[p * kChains][nt][i] + gr[p * kChains + kChains - 1][nt][i] : gr[p][nt][i];
+                        acc[nt][i] = fmaf(i < 2 ? fa : fb, v, acc[nt][i]);
+                    }
             }
-            b = 0;
-            turn ^= 1;
-            tile += stride;
+        };
+        for (int b = 0; b < nb; b += 2) {
+            asm volatile("cp.async.wait_group %0;" ::"n"(kDepth - 1) : "memory");
+            __syncwarp();      // every lane's copies are there, and the stage that is filled next is read
+            st = ring + get * kStage;
+            get = get == kDepth ? 0 : get + 1;
+            fetch();
+            if (NT == 2 && b + 1 < nb) {      // both at once: two warps a scheduler leave gaps to fill
+                multiply(Count<2>(), b);
+            } else {
+                multiply(Count<1>(), b);
+                if (b + 1 < nb) multiply(Count<1>(), b + 1);
+            }
+        }
+        // the tile's partial sums, [part][row of x][weight row]; two buffers in turns, so that one
+        // meeting of the warps a tile is enough
+        float *sums = part_sums + turn * own * NT * 8 * rows;
+        float *mine = sums + wp * NT * 8 * rows + wr * 16;
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int m = nt * 8 + 2 * t + (i & 1);
+                if (m < mn) mine[m * rows + g + 8 * (i >> 1)] = acc[nt][i] * unit[nt][i & 1];
+                acc[nt][i] = 0.0f;
+            }
+        if (S == 1)
+            __syncthreads();
+        else
+            asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+        // each CTA finishes 16 of the rows
+        for (int i = tid; i < mn * 16; i += kWarps * 32) {
+            const int m = i >> 4, r = (int)rank * 16 + (i & 15), n = tile * rows + r;
+            if (n < a.N) {
+                float q[kParts];
+#pragma unroll
+                for (int p = 0; p < kParts; ++p) {
+                    const float *at = sums + ((p & (own - 1)) * NT * 8 + m) * rows + r;
+                    if (S == 1) {
+                        q[p] = *at;
+                    } else {
+                        uint32_t addr;
+                        asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(addr) : "r"(smem_u32(at)), "r"((uint32_t)(p >> own_log2)));
+                        asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(q[p]) : "r"(addr) : "memory");
+                    }
+                }
+                float v = q[0];
+#pragma unroll
+                for (int p = 1; p < kParts; ++p) v += q[p];
+                if (a.bias) v += __uint_as_float((uint32_t)a.bias[n] << 16);
+                const __nv_bfloat16 o = __float2bfloat16_rn(v);
+                a.y[(int64_t)(m0 + m) * a.ldy + n] = *reinterpret_cast<const uint16_t *>(&o);
+            }
         }
     }
     pdl_launch_dependents();
@@ -317,7 +447,8 @@ constexpr int64_t kMaxW4 = (int64_t)1 << 24, kMaxK = 65536;
 template <int NT, int GROUP>
 cudaError_t launch_w4(const W4Args &a, int split, int blocks_m, int sms, cudaStream_t st) {
     const int own = kParts / split, rows = 16 * split, m = a.M < NT * 8 ? a.M : NT * 8;
-    const size_t smem = (size_t)m * (own * a.part * kBlockK * 2 + 64) + (size_t)2 * own * NT * 8 * rows * 4;
+    const size_t smem = (size_t)m * (own * a.part * kBlockK * 2 + 64) + (size_t)own * a.part * (kBlockK / GROUP) * NT * 8 * 4 +
+                        (size_t)2 * own * NT * 8 * rows * 4 + (size_t)kWarps * (kDepth + 1) * kStage;
     static SmemOptIn opt;
     cudaError_t e = opt.set(reinterpret_cast<const void *>(w4_linear_kernel<NT, GROUP>), 220 * 1024);
     if (e != cudaSuccess) return e;
@@ -389,10 +520,10 @@ extern "C" int clef_w4_linear(const void *x, int64_t ldx, const void *qw, const 
     const int kb = (int)((K + kBlockK - 1) / kBlockK);
     const int part = (kb + kParts - 1) / kParts;
     // CTAs of a cluster: so many that a CTA's columns of x leave room for two CTAs an SM
-    const auto x_bytes = [&](int64_t m, int split) { return m * (kParts / split * part * kBlockK * 2 + 64); };
-    const int64_t block_m = M > 8 && x_bytes(M < 16 ? M : 16, kParts) <= 200 * 1024 ? 16 : 8;
+    const auto x_bytes = [&](int64_t m, int split) { return m * (kParts / split * part * kBlockK * 2 + 64); };      // and a sixteenth of it, or less, for its sums
+    const int64_t block_m = M > 8 && x_bytes(M < 16 ? M : 16, kParts) <= 120 * 1024 ? 16 : 8;
     int split = 1;
-    while (split < kParts && x_bytes(M < block_m ? M : block_m, split) > 80 * 1024) split *= 2;
+    while (split < kParts && x_bytes(M < block_m ? M : block_m, split) > 40 * 1024) split *= 2;
     W4Args a;
     a.x = static_cast<const uint16_t *>(x);
     a.ldx = ldx;
@@ -406,6 +537,7 @@ extern "C" int clef_w4_linear(const void *x, int64_t ldx, const void *qw, const 
     a.K = (int)K;
     a.kb = kb;
     a.part = part;
+    a.split_log2 = split == 1 ? 0 : split == 2 ? 1 : split == 4 ? 2 : 3;
     a.tiles = (int)((N + 16 * split - 1) / (16 * split));
     sms = internal_launch_sms(sms);
     cudaStream_t st = static_cast<cudaStream_t>(stream);
