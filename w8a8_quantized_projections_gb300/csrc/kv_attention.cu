@@ -56,7 +56,7 @@ constexpr float kLift = 15.0f;     // the largest weight of P is 2^kLift
 // Tokens of a split of a sequence of `len` tokens: short enough that one
 // sequence spreads over the SMs, long enough that the partial results (4 B
 // written and read a value and split, against 1 B a code) stay a small part of the traffic.
-__host__ __device__ inline int split_tokens(int len) { return len <= 1024 ? 128 : len <= 4096 ? 256 : len <= 16384 ? 512 : 1024; }
+__host__ __device__ inline int split_tokens(int len) { return len <= 1024 ? 128 : len <= 2048 ? 256 : len <= 8192 ? 512 : 1024; }
 __host__ __device__ inline int split_count(int len) {
     const int t = split_tokens(len);
     return len / t + (len % t != 0);
@@ -179,12 +179,39 @@ __device__ __forceinline__ uint2 load_codes8(const uint8_t *p) {
     return v;
 }
 
+// Quotients of small numbers by one divisor (the query heads that share a
+// key/value head, or the heads): x / g = umulhi(x, ceil(2^32 / g)), exact while
+// x * g < 2^32.
+struct GroupDiv {
+    int g;
+    uint32_t mul;
+    __device__ __forceinline__ explicit GroupDiv(int group) : g(group), mul(0xFFFFFFFFu / (uint32_t)group + 1u) {}
+    __device__ __forceinline__ int div(int x) const { return g == 1 ? x : (int)__umulhi((uint32_t)x, mul); }
+};
+
+// Four codes of the keys as two pairs of fp16 operands.  INT8: c ^ 0x80 = c + 128
+// as the halfword it is, (c + 128) 2^-24, below fp16's normal numbers and exact;
+// tensor cores take such numbers whole.  That is three instructions for four
+// codes instead of five; the 128 leaves with the sum of the query.  (For the
+// values the same costs too much: next to one large weight, sums of 128 P leave
+// their rounding in dimensions whose codes are small.)
+template <int KIND>
+__device__ __forceinline__ void expand4(uint32_t w, uint32_t &lo, uint32_t &hi) {
+    if constexpr (KIND == kKvInt8) {
+        const uint32_t u = w ^ 0x80808080u;
+        lo = __byte_perm(u, 0u, 0x4140);
+        hi = __byte_perm(u, 0u, 0x4342);
+    } else {
+        widen4<KIND>(w, lo, hi);
+    }
+}
+
 // Tokens that a warp takes a step: two 16-token tiles where the registers allow.
 template <int D>
 __host__ __device__ constexpr int step_tiles() { return D <= 128 ? 2 : 1; }
 
 template <int D, int NT>
-__host__ __device__ constexpr int split_smem_floats() { return kWarps * NT * 8 * (D + 2); }
+__host__ __device__ constexpr int split_smem_floats() { return kWarps * NT * 8 * (D + 6); }
 
 // What a CTA needs of an item before it can stream: made while the item before
 // is streamed, so that no item waits for it.
@@ -194,7 +221,7 @@ struct SplitPrep {
     static constexpr int kPitch = D + 4;        // fp16 elements: the lanes' 8-byte reads meet every bank once
     static constexpr int kPages = kMaxSplitTokens / 16;
     uint16_t q[kRows * kPitch];
-    float qs[kRows];
+    float qs[kRows], lift[kRows];               // what S is multiplied by, after lift is taken off it
     int end[kRows];                             // tokens a row sees
     int page[kPages];
     float ks[kPages], lv[kPages], inv[kPages];  // key scale; log2 of the value scale; its reciprocal (0: no weight)
@@ -231,11 +258,13 @@ __global__ void __launch_bounds__(kThreads, split_ctas<D, NT>()) kv_split_kernel
     extern __shared__ __align__(16) uint8_t smem[];
     __shared__ __align__(16) Prep s_prep[2];
     __shared__ int s_scan[kWarps], s_total;
-    float *s_o = reinterpret_cast<float *>(smem);          // [kWarps][ROWS][D], then m, l
-    float *s_m = s_o + kWarps * ROWS * D, *s_l = s_m + kWarps * ROWS;
+    constexpr int OPITCH = D + 4;            // floats: the lanes' writes meet every bank once
+    float *s_o = reinterpret_cast<float *>(smem);          // [kWarps][ROWS][OPITCH], then m, l
+    float *s_m = s_o + kWarps * ROWS * OPITCH, *s_l = s_m + kWarps * ROWS;
     int *s_items = reinterpret_cast<int *>(smem + split_smem_floats<D, NT>() * 4);   // [seqs + 1] first item of each sequence
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
     const int log2 = a.pool.page_log2, H = a.pool.heads;
+    const GroupDiv by_group(a.group), by_heads(H);
     pdl_wait();
 
     // items of each sequence
@@ -287,15 +316,16 @@ __global__ void __launch_bounds__(kThreads, split_ctas<D, NT>()) kv_split_kernel
         t.rows = t.n * a.group;
         const int groups = (t.rows + ROWS - 1) / ROWS;
         int rest = item - s_items[b];
-        t.head = rest % H;
-        rest /= H;
-        t.split = rest / groups;
+        const int over = rest < (1 << 20) ? by_heads.div(rest) : rest / H;
+        t.head = rest - over * H;
+        rest = over;
+        t.split = groups == 1 ? rest : rest >> 1;      // at most 16 rows: one group or two
         t.r0 = (rest - t.split * groups) * ROWS;
         t.rn = min(ROWS, t.rows - t.r0);
         t.splits = max(1, split_count(t.len));
         t.tok0 = t.split * split_tokens(t.len);
         t.tok1 = min(t.len, t.tok0 + split_tokens(t.len));
-        if (a.causal) t.tok1 = min(t.tok1, max(0, t.len - t.n + (t.r0 + t.rn - 1) / a.group + 1));   // what the last row sees
+        if (a.causal) t.tok1 = min(t.tok1, max(0, t.len - t.n + by_group.div(t.r0 + t.rn - 1) + 1));   // what the last row sees
         return t;
     };
 
@@ -310,7 +340,7 @@ __global__ void __launch_bounds__(kThreads, split_ctas<D, NT>()) kv_split_kernel
 #pragma unroll
             for (int w = 0; w < PER / 2; ++w) pq[k][w] = 0u;
             if (r < it.rn) {
-                const int i = (it.r0 + r) / a.group, hq = it.head * a.group + (it.r0 + r) - i * a.group;
+                const int i = by_group.div(it.r0 + r), hq = it.head * a.group + (it.r0 + r) - i * a.group;
                 const uint32_t *src = reinterpret_cast<const uint32_t *>(a.q + (int64_t)(it.row0 + i) * a.ldq + (int64_t)hq * a.ldq_head);
 #pragma unroll
                 for (int w = 0; w < PER / 2; ++w) pq[k][w] = src[lane + 32 * w];
@@ -346,13 +376,23 @@ __global__ void __launch_bounds__(kThreads, split_ctas<D, NT>()) kv_split_kernel
             // a negative scale turns the queries, so that x grows with S
             float up = __uint_as_float((uint32_t)(127 + e) << 23);
             if (a.scale_log2 < 0.0f) up = -up;
+            float sum = 0.0f;
 #pragma unroll
-            for (int w = 0; w < PER / 2; ++w)
-                *reinterpret_cast<uint32_t *>(&to.q[r * Prep::kPitch + 2 * (lane + 32 * w)]) =
-                    pack_half(__uint_as_float(pq[k][w] << 16) * up, __uint_as_float(pq[k][w] & 0xFFFF0000u) * up);
+            for (int w = 0; w < PER / 2; ++w) {
+                const uint32_t h = pack_half(__uint_as_float(pq[k][w] << 16) * up, __uint_as_float(pq[k][w] & 0xFFFF0000u) * up);
+                *reinterpret_cast<uint32_t *>(&to.q[r * Prep::kPitch + 2 * (lane + 32 * w)]) = h;
+                const __half2 h2 = *reinterpret_cast<const __half2 *>(&h);
+                sum += __low2float(h2) + __high2float(h2);
+            }
+            if constexpr (KIND == kKvInt8) {
+#pragma unroll
+                for (int o = 1; o < 32; o <<= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
+            }
             if (lane == 0) {
-                const int i = (it.r0 + r) / a.group;
-                to.qs[r] = fabsf(a.scale_log2) * __uint_as_float((uint32_t)(127 - e) << 23);
+                const int i = by_group.div(it.r0 + r);
+                // INT8: S comes as sums of (c + 128) 2^-24 q
+                to.qs[r] = fabsf(a.scale_log2) * __uint_as_float((uint32_t)(127 - e) << 23) * (KIND == kKvInt8 ? 0x1p24f : 1.0f);
+                to.lift[r] = KIND == kKvInt8 ? 0x1p-17f * sum : 0.0f;
                 to.end[r] = r >= it.rn || !a.causal ? it.len : max(0, it.len - it.n + i + 1);
             }
         }
@@ -430,7 +470,7 @@ __global__ void __launch_bounds__(kThreads, split_ctas<D, NT>()) kv_split_kernel
         }
         bool scales_due = more;
 
-        float acc[NT][MT][4], m[NT][2], l[NT][2], qs[NT][2];
+        float acc[NT][MT][4], m[NT][2], l[NT][2], qs[NT][2], lift[NT][2];
         int end[NT][2];
 #pragma unroll
         for (int x = 0; x < NT; ++x) {
@@ -443,6 +483,7 @@ __global__ void __launch_bounds__(kThreads, split_ctas<D, NT>()) kv_split_kernel
                 m[x][i] = -INFINITY;
                 l[x][i] = 0.0f;
                 qs[x][i] = pr.qs[x * 8 + 2 * t + i];
+                lift[x][i] = pr.lift[x * 8 + 2 * t + i];
                 end[x][i] = min(pr.end[x * 8 + 2 * t + i], it.tok1);
             }
         }
@@ -472,8 +513,8 @@ __global__ void __launch_bounds__(kThreads, split_ctas<D, NT>()) kv_split_kernel
                     for (int u = 0; u < TILES; ++u) {
                         uint32_t f[4];
                         const uint4 &ka = kc[u][0][k], &kb = kc[u][1][k];
-                        widen4<KIND>(w == 0 ? ka.x : w == 1 ? ka.y : w == 2 ? ka.z : ka.w, f[0], f[2]);
-                        widen4<KIND>(w == 0 ? kb.x : w == 1 ? kb.y : w == 2 ? kb.z : kb.w, f[1], f[3]);
+                        expand4<KIND>(w == 0 ? ka.x : w == 1 ? ka.y : w == 2 ? ka.z : ka.w, f[0], f[2]);
+                        expand4<KIND>(w == 0 ? kb.x : w == 1 ? kb.y : w == 2 ? kb.z : kb.w, f[1], f[3]);
 #pragma unroll
                         for (int x = 0; x < NT; ++x) mma_regs(s[x][u], f, qf[x].x, qf[x].y);
                     }
@@ -512,7 +553,8 @@ __global__ void __launch_bounds__(kThreads, split_ctas<D, NT>()) kv_split_kernel
 #pragma unroll
                     for (int i = 0; i < 2; ++i) {
                         const float v = fmaxf(s[x][u][i], s[x][u][i + 2]);
-                        if (whole || v != -INFINITY) top[i] = fmaxf(top[i], fmaf(v, qs[x][i] * ks[u], lv[u]));
+                        const float f = qs[x][i] * ks[u];
+                        if (whole || v != -INFINITY) top[i] = fmaxf(top[i], fmaf(v, f, fmaf(-lift[x][i], f, lv[u])));
                     }
 #pragma unroll
                 for (int o = 4; o < 32; o <<= 1)
@@ -535,10 +577,15 @@ __global__ void __launch_bounds__(kThreads, split_ctas<D, NT>()) kv_split_kernel
                 }
 #pragma unroll
                 for (int u = 0; u < TILES; ++u) {
-                    float p[4];
+                    float p[4], f[2], off[2];
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        f[i] = qs[x][i] * ks[u];
+                        off[i] = fmaf(-lift[x][i], f[i], lv[u] - ref[i]);
+                    }
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
-                        const float v = fmaf(s[x][u][i], qs[x][i & 1] * ks[u], lv[u] - ref[i & 1]);
+                        const float v = fmaf(s[x][u][i], f[i & 1], off[i & 1]);
                         p[i] = ex2(whole || s[x][u][i] != -INFINITY ? v : -INFINITY);
                     }
                     l[x][0] = fmaf(p[0] + p[2], fabsf(inv[u]), l[x][0]);
@@ -592,8 +639,7 @@ __global__ void __launch_bounds__(kThreads, split_ctas<D, NT>()) kv_split_kernel
                 for (int i = 0; i < 4; ++i) {
                     // tile k: word k / 2 of the lane's run of values, its bytes 2 (k & 1) and 2 (k & 1) + 1
                     const int byte = 4 * (k / 2) + 2 * (k & 1) + (i >> 1);
-                    const int d = D == 64 ? g * 8 + byte : (byte / 16) * 128 + g * 16 + byte % 16;
-                    s_o[(warp * ROWS + x * 8 + 2 * t + (i & 1)) * D + d] = acc[x][k][i];
+                    s_o[(warp * ROWS + x * 8 + 2 * t + (i & 1)) * OPITCH + byte * 8 + g] = acc[x][k][i];
                 }
         }
         __syncthreads();
@@ -616,7 +662,7 @@ __global__ void __launch_bounds__(kThreads, split_ctas<D, NT>()) kv_split_kernel
             }
             const float inv = ll > 0.0f ? __fdiv_rn(1.0f, ll) : 0.0f;
             const float lse = ll > 0.0f ? mm - kLift + log2f(ll) : -INFINITY;
-            const int i = (done.r0 + r) / a.group, hq = done.head * a.group + (done.r0 + r) - i * a.group;
+            const int i = by_group.div(done.r0 + r), hq = done.head * a.group + (done.r0 + r) - i * a.group;
             const int64_t place = done.b * a.part_units + ((int64_t)done.head * done.rows + done.r0 + r) * done.splits + done.split;
             if (done.splits > 1) {
                 if (lane == 0) a.part_lse[place] = lse;
@@ -625,13 +671,15 @@ __global__ void __launch_bounds__(kThreads, split_ctas<D, NT>()) kv_split_kernel
             }
 #pragma unroll
             for (int k = 0; k < D / 64; ++k) {
-                const int d = k * 64 + lane * 2;
+                // two neighbouring dimensions: bytes of run lane & 7 (its bytes past 16 are 128 dimensions on)
+                const int run = lane & 7, byte = 2 * ((lane >> 3) + 4 * k);
+                const int d = D == 64 ? run * 8 + byte : (byte / 16) * 128 + run * 16 + byte % 16;
                 float o0 = 0.0f, o1 = 0.0f;
 #pragma unroll
                 for (int w = 0; w < kWarps; ++w) {
-                    const float2 v = *reinterpret_cast<const float2 *>(&s_o[(w * ROWS + r) * D + d]);
-                    o0 = fmaf(v.x, f[w], o0);
-                    o1 = fmaf(v.y, f[w], o1);
+                    const float *at = &s_o[(w * ROWS + r) * OPITCH + byte * 8 + run];
+                    o0 = fmaf(at[0], f[w], o0);
+                    o1 = fmaf(at[8], f[w], o1);
                 }
                 o0 *= inv;
                 o1 *= inv;
@@ -808,15 +856,6 @@ __device__ __forceinline__ uint64_t pair_of(float x) {
     asm("mov.b64 %0, {%1, %1};" : "=l"(r) : "f"(x));
     return r;
 }
-
-// Quotients of small numbers by the number of query heads that share a
-// key/value head: x / g = umulhi(x, ceil(2^32 / g)), exact while x * g < 2^32.
-struct GroupDiv {
-    int g;
-    uint32_t mul;
-    __device__ __forceinline__ explicit GroupDiv(int group) : g(group), mul(0xFFFFFFFFu / (uint32_t)group + 1u) {}
-    __device__ __forceinline__ int div(int x) const { return g == 1 ? x : (int)__umulhi((uint32_t)x, mul); }
-};
 
 // mbar_wait for a whole warp: the same answer in every lane, so that the warp
 // stays together for the aligned instructions that follow.
@@ -1603,7 +1642,7 @@ Plan make_plan(int64_t rows, bool ragged, int64_t seqs, int group, int heads, in
     if (rows == 0 || seqs == 0) return p;
     // a shorter sequence may be cut into more runs than the longest: the cut grows in steps
     int few_splits = 1;
-    for (int64_t len : {max_len, (int64_t)1024, (int64_t)4096, (int64_t)16384})
+    for (int64_t len : {max_len, (int64_t)1024, (int64_t)2048, (int64_t)8192})
         if (len <= max_len && split_count((int)len) > few_splits) few_splits = split_count((int)len);
     const int64_t per = ragged ? rows * group : rows / seqs * group;   // rows of one sequence, at most
     p.few = ragged || per <= kFewRows;
