@@ -1,4 +1,4 @@
-"""A stack of decoder layers that reads prompts and answers token by token.
+"""Example: a stack of decoder layers that reads prompts and answers token by token.
 
 ``Decoder`` holds each projection twice: as INT8 codes for the W8A8 GEMMs that
 read prompts (many rows: tensor-bound) and as 4-bit codes for the linears that
@@ -10,7 +10,9 @@ kernels only and can be captured in a CUDA graph (``capture``), which also
 takes the host's cost per call out of short steps.
 
 RMS normalisation, the rotation of queries and keys by their position and the
-residual adds are torch's elementwise operations.
+residual adds are torch's elementwise operations here; they are not part of the library.
+
+    PYTHONPATH=. python examples/decoder.py        # random weights: a prompt, three answers of 40 tokens
 """
 from __future__ import annotations
 
@@ -18,8 +20,8 @@ from typing import Dict, List, Sequence
 
 import torch
 
-from . import (kv_append, kv_attention, kv_compact, kv_fork, kv_free, kv_reserve, quant_act, quant_w4, swiglu_bf16,
-               w4_linear, w8a8_gateup_swiglu, w8a8_linear)
+from w8a8_quantized_projections_gb300 import (kv_append, kv_attention, kv_compact, kv_fork, kv_free, kv_reserve, poll_status,
+                                              quant_act, quant_w4, swiglu_bf16, w4_linear, w8a8_gateup_swiglu, w8a8_linear)
 
 NAMES = ("qkv", "o", "gateup", "down")
 
@@ -156,3 +158,41 @@ class Decoder:
     def _rotate(t, cos, sin):
         a, b = t.float().chunk(2, -1)
         return torch.cat((a * cos - b * sin, b * cos + a * sin), -1).to(torch.bfloat16)
+
+
+def main():
+    hidden, q_heads, kv_heads, dim, ff, depth = 2048, 16, 4, 128, 5632, 4
+
+    def w(n, k):
+        return (torch.randn(n, k, device="cuda") * k ** -0.5).to(torch.bfloat16)
+
+    one = torch.ones(hidden, dtype=torch.bfloat16, device="cuda")
+    dec = Decoder([{"qkv": w((q_heads + 2 * kv_heads) * dim, hidden), "o": w(hidden, q_heads * dim), "gateup": w(2 * ff, hidden),
+                    "down": w(hidden, ff), "norm_attn": one, "norm_mlp": one} for _ in range(depth)],
+                  q_heads, kv_heads, dim, sequences=8, pages=256, width=64)
+    table = torch.randn(1000, hidden, device="cuda").to(torch.bfloat16)       # tokens' vectors, in and out
+    h = dec.prompt(table[torch.randint(1000, (1502,), device="cuda")], {0: 1502})
+    dec.fork([0, 0], [1, 2])
+    token = (h[-1].float() @ table.float().T).topk(3).indices                  # three first tokens
+    x = table[token].clone()
+    y = dec.capture(x, [0, 1, 2])
+
+    def tokens(n):
+        for _ in range(n):
+            dec.replay()
+            x.copy_(table[(y.float() @ table.float().T).argmax(-1)])
+
+    tokens(8)
+    start, end = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+    start.record()
+    tokens(32)
+    end.record()
+    torch.cuda.synchronize()
+    status = poll_status()
+    print(f"{dec.lens.tolist()[:3]} tokens, {start.elapsed_time(end) / 32 * 1000:.0f} us a token of three answers, status {status}")
+    dec.free([1, 2])
+    print(f"{int(dec.compact())} pages held after two answers are freed")
+
+
+if __name__ == "__main__":
+    main()

@@ -13,8 +13,8 @@ import torch
 
 import w8a8_quantized_projections_gb300 as clef
 from decode_util import Cache, attention, bf16_ulp, host_codes, w4_codes
-from w8a8_quantized_projections_gb300 import decoder as module
-from w8a8_quantized_projections_gb300.decoder import Decoder
+from examples import decoder as module
+from examples.decoder import Decoder
 
 pytestmark = pytest.mark.gpu
 HIDDEN, FF, HQ, HK, D, PAGE = 256, 384, 6, 2, 64, 16
