@@ -1,22 +1,27 @@
-"""Build the in-tree CUDA library ``_build/libclef.so`` for sm_103a.
+"""Build the in-tree CUDA library ``_build/libclef.so`` for sm_103a, and
+``_build/clef_decode.so``, the compiled argument marshalling of ``decode.py``.
 
 Each ``csrc/*.cu`` translation unit is compiled by nvcc in parallel
 (``-gencode arch=compute_103a,code=sm_103a``) and the objects are linked
 into one shared library against the shared CUDA runtime, so that it shares
-the runtime instance (and the primary context) of the host process.
+the runtime instance (and the primary context) of the host process.  The
+extension is one C++ file against torch's headers, linked to libclef.so.
 """
 from __future__ import annotations
 
+import importlib.util
 import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 from concurrent.futures import ThreadPoolExecutor
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(BUILD, "libclef.so")
+EXT = os.path.join(BUILD, "clef_decode.so")
 ROOT = os.path.dirname(HERE)
 SOURCES = ["abi.cu", "quant_act.cu", "gemm.cu", "swiglu.cu", "lora_noalloc.cu", "mma_peak.cu", "copy_sm.cu",
            "w4.cu", "kv_cache.cu", "kv_pages.cu", "kv_attention.cu"]
@@ -32,11 +37,41 @@ def nvcc() -> str:
 
 
 def _stale() -> bool:
-    if not os.path.exists(LIB):
+    if not os.path.exists(LIB) or not os.path.exists(EXT):
         return True
-    t = os.path.getmtime(LIB)
+    t = min(os.path.getmtime(LIB), os.path.getmtime(EXT))
     deps = [os.path.join(CSRC, f) for f in os.listdir(CSRC)] + [os.path.join(ROOT, "include", "clef.h")]
     return any(os.path.getmtime(d) > t for d in deps)
+
+
+def _run(what, cmd):
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"{what} failed:\n{r.stdout}\n{r.stderr}")
+
+
+def _torch_dir() -> str:
+    return importlib.util.find_spec("torch").submodule_search_locations[0]
+
+
+def _compile_extension() -> str:
+    inc = os.path.join(_torch_dir(), "include")
+    obj = os.path.join(BUILD, "py_decode.o")
+    dirs = [os.path.join(ROOT, "include"), inc, os.path.join(inc, "torch", "csrc", "api", "include"),
+            sysconfig.get_paths()["include"], os.path.join(os.path.dirname(os.path.dirname(nvcc())), "include")]
+    _run("g++ on py_decode.cpp", ["g++", "-O2", "-std=c++17", "-fPIC", "-Wall", *[a for d in dirs[:1] for a in ("-I", d)],
+                                  *[a for d in dirs[1:] for a in ("-isystem", d)],
+                                  "-c", os.path.join(CSRC, "py_decode.cpp"), "-o", obj])
+    return obj
+
+
+def _link_extension(obj: str) -> None:
+    """Against libclef.so beside it and the torch libraries that the process has loaded."""
+    tmp = EXT + f".{os.getpid()}.tmp"
+    _run("link of clef_decode.so", ["g++", "-shared", "-o", tmp, obj, "-L", BUILD, "-l:libclef.so", "-Wl,-rpath,$ORIGIN",
+                                    "-L", os.path.join(_torch_dir(), "lib"), "-ltorch_python", "-ltorch", "-ltorch_cpu",
+                                    "-lc10_cuda", "-lc10"])
+    os.replace(tmp, EXT)
 
 
 def build(force: bool = False, verbose: bool = False) -> str:
@@ -58,14 +93,13 @@ def build(force: bool = False, verbose: bool = False) -> str:
             sys.stderr.write(r.stderr)
         return obj
 
-    with ThreadPoolExecutor(max_workers=len(SOURCES)) as ex:
+    with ThreadPoolExecutor(max_workers=len(SOURCES) + 1) as ex:
+        ext = ex.submit(_compile_extension)
         objs = list(ex.map(compile_one, SOURCES))
     tmp = LIB + f".{os.getpid()}.tmp"
-    r = subprocess.run([cc, "-shared", "-cudart", "shared", "-o", tmp, *objs],
-                       capture_output=True, text=True)
-    if r.returncode != 0:
-        raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
+    _run("link", [cc, "-shared", "-cudart", "shared", "-o", tmp, *objs])
     os.replace(tmp, LIB)
+    _link_extension(ext.result())
     return LIB
 
 
