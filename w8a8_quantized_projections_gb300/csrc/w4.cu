@@ -26,6 +26,7 @@
 // x is held in fp16, each run of K that is summed apart scaled by a power of
 // two to a largest magnitude in [2^13, 2^14): bf16 has fewer bits than fp16,
 // so only values under 2^-23 of the run's largest lose any.
+#include <atomic>
 #include <cstdint>
 
 #include <cuda_bf16.h>
@@ -43,7 +44,7 @@ namespace {
 constexpr int kBlockK = 128;      // weights of a packed block
 constexpr int kWarps = 8;
 constexpr int kParts = 8;         // runs of K that are summed apart, then added in order
-constexpr int kDepth = 3;         // stages of two blocks that a warp has on their way; one more is in use
+constexpr int kDepth = 2;         // stages of two blocks that a warp has on their way; one more is in use
 constexpr int kStage = 2048 + 256;    // bytes of a stage: 16 rows of 128, and their scales
 
 __device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
@@ -444,16 +445,47 @@ bool misaligned(const void *p, unsigned to) { return (reinterpret_cast<uintptr_t
 
 constexpr int64_t kMaxW4 = (int64_t)1 << 24, kMaxK = 65536;
 
+constexpr size_t kMaxSmem = 220 * 1024;
+
+// Shared memory of a CTA: x's columns, the sums' starts, two tiles' partial sums and the rings.
+size_t w4_smem(int nt, int64_t m, int part, int group, int split) {
+    const int own = kParts / split, rows = 16 * split;
+    return (size_t)m * (own * part * kBlockK * 2 + 64) + (size_t)own * part * (kBlockK / group) * nt * 8 * 4 +
+           (size_t)2 * own * nt * 8 * rows * 4 + (size_t)kWarps * (kDepth + 1) * kStage;
+}
+
 template <int NT, int GROUP>
 cudaError_t launch_w4(const W4Args &a, int split, int blocks_m, int sms, cudaStream_t st) {
-    const int own = kParts / split, rows = 16 * split, m = a.M < NT * 8 ? a.M : NT * 8;
-    const size_t smem = (size_t)m * (own * a.part * kBlockK * 2 + 64) + (size_t)own * a.part * (kBlockK / GROUP) * NT * 8 * 4 +
-                        (size_t)2 * own * NT * 8 * rows * 4 + (size_t)kWarps * (kDepth + 1) * kStage;
+    const size_t smem = w4_smem(NT, a.M < NT * 8 ? a.M : NT * 8, a.part, GROUP, split);
     static SmemOptIn opt;
-    cudaError_t e = opt.set(reinterpret_cast<const void *>(w4_linear_kernel<NT, GROUP>), 220 * 1024);
+    cudaError_t e = opt.set(reinterpret_cast<const void *>(w4_linear_kernel<NT, GROUP>), kMaxSmem);
     if (e != cudaSuccess) return e;
-    const int per_sm = smem <= 110 * 1024 ? 2 : 1;
+    const int per_sm = NT == 1 && smem <= 110 * 1024 ? 2 : 1;
     int clusters = sms * per_sm / split;
+    if (split > 1) {   // clusters do not fill every group of SMs: of 152 CTAs, 15 clusters of eight run at once
+        static std::atomic<int> known[64][4][2];   // asked once for each device
+        int dev = 0;
+        e = cudaGetDevice(&dev);
+        if (e != cudaSuccess) return e;
+        std::atomic<int> &slot = known[dev & 63][a.split_log2][per_sm - 1];
+        int most = slot.load(std::memory_order_relaxed);
+        if (most == 0) {
+            cudaLaunchConfig_t cfg = {};
+            cudaLaunchAttribute attr;
+            attr.id = cudaLaunchAttributeClusterDimension;
+            attr.val.clusterDim.x = (unsigned)split;
+            attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+            cfg.gridDim = dim3((unsigned)split);
+            cfg.blockDim = dim3(kWarps * 32);
+            cfg.dynamicSmemBytes = smem;
+            cfg.attrs = &attr;
+            cfg.numAttrs = 1;
+            e = cudaOccupancyMaxActiveClusters(&most, w4_linear_kernel<NT, GROUP>, &cfg);
+            if (e != cudaSuccess) return e;
+            if (most > 0 && dev < 64) slot.store(most, std::memory_order_relaxed);
+        }
+        if (most > 0 && clusters > most) clusters = most;
+    }
     if (clusters < 1) clusters = 1;
     if (clusters > a.tiles) clusters = a.tiles;
     return launch_kernel(w4_linear_kernel<NT, GROUP>, dim3((unsigned)(clusters * split), (unsigned)blocks_m), dim3(kWarps * 32),
@@ -519,11 +551,13 @@ extern "C" int clef_w4_linear(const void *x, int64_t ldx, const void *qw, const 
     if (rc) return rc;
     const int kb = (int)((K + kBlockK - 1) / kBlockK);
     const int part = (kb + kParts - 1) / kParts;
-    // CTAs of a cluster: so many that a CTA's columns of x leave room for two CTAs an SM
+    // CTAs of a cluster: up to eight rows of x, so many that a CTA's columns of x leave room for two CTAs an SM;
+    // past that as few as it takes to fit, as larger clusters leave more SMs without work
     const auto x_bytes = [&](int64_t m, int split) { return m * (kParts / split * part * kBlockK * 2 + 64); };      // and a sixteenth of it, or less, for its sums
     const int64_t block_m = M > 8 && x_bytes(M < 16 ? M : 16, kParts) <= 120 * 1024 ? 16 : 8;
+    const int64_t m = M < block_m ? M : block_m;
     int split = 1;
-    while (split < kParts && x_bytes(M < block_m ? M : block_m, split) > 40 * 1024) split *= 2;
+    while (split < kParts && (block_m == 8 ? x_bytes(m, split) > 40 * 1024 : w4_smem(2, m, part, group, split) > kMaxSmem)) split *= 2;
     W4Args a;
     a.x = static_cast<const uint16_t *>(x);
     a.ldx = ldx;
