@@ -68,14 +68,15 @@ __host__ __device__ constexpr int tile_rows(int dim) { return dim <= 128 ? 256 :
 
 // Splits of a sequence with more than kFewRows rows: while its row tiles leave
 // SMs idle (152 on this GPU; a fixed number, so that a row's bits do not follow
-// an SM budget), runs of at least 512 tokens, at most 16 of them.
+// an SM budget), runs of at least 1,024 tokens, at most 16 of them.  A run's
+// partial results (128 KB a tile) and the join cost as much as 500 tokens.
 constexpr int kTileSlots = 152, kTileMaxSplits = 16;
 __host__ __device__ inline int tile_splits(int rows, int len, int heads, int dim) {
     const int tiles = (rows + tile_rows(dim) - 1) / tile_rows(dim) * heads;
     if (tiles < 1 || tiles > kTileSlots / 2) return 1;
     const int steps = (len >> 7) + ((len & 127) != 0);       // of 128 tokens
     int s = kTileSlots / tiles;
-    if (s > (steps + 3) / 4) s = (steps + 3) / 4;
+    if (s > steps / 8) s = steps / 8;
     if (s > kTileMaxSplits) s = kTileMaxSplits;
     if (s <= 1) return 1;
     const int per = (steps + s - 1) / s;      // equal splits, none of them empty
@@ -712,11 +713,11 @@ struct Tile {
     static constexpr int kOutCols = kQ == 2 ? D : D / 2;     // and of O
     // 20 warps of 96 registers in whole warpgroups: eight of softmax (four for each row tile, or eight
     // for one), four that turn keys into operands and four for values, then one that issues the products,
-    // one that copies codes and two idle ones.  Each of the SM's four register files holds two warps of
+    // one that copies codes of keys, one for values and an idle one.  Each of the SM's four register files holds two warps of
     // softmax, two of conversion and one of the last group, and setmaxnreg's 2 x 144 + 2 x 56 + 80 =
     // 5 x 96 fit in every one of them.
     static constexpr int kSoftWarps = 8, kConvWarps = 4;     // conversion: for each operand
-    static constexpr int kMmaWarp = kSoftWarps + 2 * kConvWarps, kCopyWarp = kMmaWarp + 1;
+    static constexpr int kMmaWarp = kSoftWarps + 2 * kConvWarps, kCopyWarp = kMmaWarp + 1;   // and the next
     static constexpr int kThreadsAll = (kMmaWarp + 4) * 32;
     static constexpr int kChunks = D / 64;                   // 64-element columns of 128-byte rows
     static constexpr int kChunkQ = 128 * 128, kChunkKV = kStep * 128;
@@ -758,7 +759,7 @@ __device__ __forceinline__ int tile_items(const AttnArgs &a, int b) {
            ((rows + tile_rows(D) - 1) / tile_rows(D)) * a.pool.heads;
 }
 
-// What item number `item` is; s_items has the first item of every kItemStep-th
+// What item number `item` is, for a whole warp; s_items has the first item of every kItemStep-th
 // sequence.  The row tiles of a sequence come last one first: with a causal mask
 // it has the most tokens to see.
 template <int D>
@@ -772,8 +773,9 @@ __device__ __forceinline__ TileItem tile_item(const AttnArgs &a, const int *s_it
     }
     int rest = item - s_items[b];
     b *= kItemStep;
-    for (int k = 1; k < kItemStep; ++k) {
-        const int cnt = tile_items<D>(a, b);
+    const int lane = (int)threadIdx.x & 31, own = lane < kItemStep && b + lane < a.tab.seqs ? tile_items<D>(a, b + lane) : 0;
+    for (int k = 0; k < kItemStep - 1; ++k) {
+        const int cnt = __shfl_sync(0xFFFFFFFFu, own, k);
         if (rest < cnt) break;
         rest -= cnt;
         ++b;
@@ -889,7 +891,6 @@ __device__ __forceinline__ uint32_t turn_of(uint32_t n) { return T::kSlots == 1 
 // Scales of the pages of a block of 64 tokens, kRing blocks deep.
 struct BlockScales {
     float ks[4], lv[4], inv[4];    // key scale; log2 of the value scale; its reciprocal
-    int there;                     // bit p: page p is one of the pool
     int zero;                      // bit p: page p's value scale is zero
 };
 
@@ -899,8 +900,8 @@ struct BlockScales {
 //   softmax           a thread a row (two at dim 256): S from tensor memory, the row's
 //                     maximum, the exponentials, P in fp16 back over S
 //   O += P V          tcgen05, P from tensor memory, V from shared memory
-// One warp copies the codes of the steps' pages to shared memory, several blocks
-// ahead; eight turn them into fp16 operands in the 128-byte swizzle.  With two row
+// Two warps copy the codes of the steps' pages to shared memory, several blocks
+// ahead, keys and values each at their own pace; eight turn them into fp16 operands in the 128-byte swizzle.  With two row
 // tiles the products of one run while the other's softmax does.  At dim 256,
 // whose O leaves room for one row tile only, the next step's S runs while the
 // softmax of this one does.
@@ -915,6 +916,7 @@ __global__ void __launch_bounds__(Tile<D>::kThreadsAll, 1) kv_tile_kernel(const 
     extern __shared__ __align__(16) uint8_t smem_raw[];
     __shared__ TileBars bar;
     __shared__ BlockScales s_scale[kRing];
+    __shared__ int s_there[2][kRing];              // bit p: page p of the block is one of the pool
     __shared__ float s_qs[T::kQ * 128], s_pair[2][2][128];   // rows' query scales; what the threads of a row exchange
     __shared__ uint32_t s_tmem;
     __shared__ int s_abort, s_scan[32], s_total;
@@ -950,9 +952,8 @@ __global__ void __launch_bounds__(Tile<D>::kThreadsAll, 1) kv_tile_kernel(const 
     }
     pdl_wait();
     __syncthreads();
-    for (int b0 = 0; b0 * kItemStep < a.tab.seqs; b0 += T::kThreadsAll) {
-        int cnt = 0;
-        for (int b = (b0 + tid) * kItemStep; b < min(a.tab.seqs, (b0 + tid + 1) * kItemStep); ++b) cnt += tile_items<D>(a, b);
+    for (int b0 = 0; b0 < a.tab.seqs; b0 += T::kThreadsAll) {
+        const int b = b0 + tid, cnt = b < a.tab.seqs ? tile_items<D>(a, b) : 0;
         int inc = cnt;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
@@ -966,7 +967,7 @@ __global__ void __launch_bounds__(Tile<D>::kThreadsAll, 1) kv_tile_kernel(const 
             if (w < warp) base += s_scan[w];
             all += s_scan[w];
         }
-        if ((b0 + tid) * kItemStep < a.tab.seqs) s_items[b0 + tid] = base + inc - cnt;
+        if (b < a.tab.seqs && b % kItemStep == 0) s_items[b / kItemStep] = base + inc - cnt;
         __syncthreads();
         if (tid == 0) s_total += all;
         __syncthreads();
@@ -1084,44 +1085,50 @@ __global__ void __launch_bounds__(Tile<D>::kThreadsAll, 1) kv_tile_kernel(const 
                 if (T::kCols > 64) zeros = zeros || scales_at(64).zero != 0;
                 // whole steps take code without masks (the compiler turns a test in the loops into selects
                 // for every column: 1,120 + 2,040 cycles for 128 columns instead of 450 + 1,350)
-                const bool whole = __reduce_min_sync(0xFFFFFFFFu, seen) >= T::kCols && !zeros;
+                const int least = __reduce_min_sync(0xFFFFFFFFu, seen);
+                const bool whole = least >= T::kCols && !zeros;
+
+                const int most = __reduce_max_sync(0xFFFFFFFFu, seen);
 
                 // the largest x + log2 vs
                 uint32_t va[32], vb[32];
                 float top = -INFINITY;
+                const auto largest = [&](const uint32_t *v, int c) {      // of columns c .. c + 15
+                    const BlockScales &sc = scales_at(c);
+                    const int p = ((p0 + c) & 63) >> log2;
+                    float g[8];
+#pragma unroll
+                    for (int k = 0; k < 8; ++k) g[k] = fmaxf(__uint_as_float(v[k]), __uint_as_float(v[8 + k]));
+#pragma unroll
+                    for (int w = 4; w > 0; w >>= 1)
+#pragma unroll
+                        for (int k = 0; k < w; ++k) g[k] = fmaxf(g[k], g[k + w]);
+                    top = fmaxf(top, fmaf(g[0], qs * sc.ks[p], sc.lv[p]));
+                };
                 if (whole) {
 #pragma unroll
                     for (int c = 0; c < T::kCols; c += 64) {
                         tmem_ld32(ts + (uint32_t)c, va);
                         if constexpr (T::kCols >= 64) tmem_ld32(ts + (uint32_t)c + 32u, vb);
                         tmem_ld_wait();
-                        const BlockScales &sc = scales_at(c);
 #pragma unroll
-                        for (int h = 0; h < (T::kCols < 64 ? T::kCols : 64) / 16; ++h) {
-                            const uint32_t *v = h < 2 ? va + h * 16 : vb + (h - 2) * 16;
-                            const int p = ((p0 + c + h * 16) & 63) >> log2;
-                            float g[8];
-#pragma unroll
-                            for (int k = 0; k < 8; ++k) g[k] = fmaxf(__uint_as_float(v[k]), __uint_as_float(v[8 + k]));
-#pragma unroll
-                            for (int w = 4; w > 0; w >>= 1)
-#pragma unroll
-                                for (int k = 0; k < w; ++k) g[k] = fmaxf(g[k], g[k + w]);
-                            top = fmaxf(top, fmaf(g[0], qs * sc.ks[p], sc.lv[p]));
-                        }
+                        for (int h = 0; h < (T::kCols < 64 ? T::kCols : 64) / 16; ++h)
+                            largest(h < 2 ? va + h * 16 : vb + (h - 2) * 16, c + h * 16);
                     }
                 } else {
 #pragma unroll 1
-                    for (int c = 0; c < T::kCols; c += 16) {
-                        uint32_t v[16];
-                        tmem_ld16(ts + (uint32_t)c, v);
+                    for (int c = 0; c < T::kCols && c < most; c += 32) {
+                        tmem_ld32(ts + (uint32_t)c, va);
                         tmem_ld_wait();
-                        const BlockScales &sc = scales_at(c);
-                        const int p = ((p0 + c) & 63) >> log2;
-                        float g = -INFINITY;
+                        if (c + 32 > least) {
 #pragma unroll
-                        for (int k = 0; k < 16; ++k) g = fmaxf(g, c + k < seen ? __uint_as_float(v[k]) : -INFINITY);
-                        if (c < seen) top = fmaxf(top, fmaf(g, qs * sc.ks[p], sc.lv[p]));
+                            for (int k = 0; k < 32; ++k)
+                                if (c + k >= seen) va[k] = 0xFF800000u;
+                        }
+                        // (keys of a column that is not seen have a place below all others, whatever their page's scale)
+#pragma unroll
+                        for (int h = 0; h < 2; ++h)
+                            if (c + h * 16 < seen) largest(va + h * 16, c + h * 16);
                     }
                 }
                 if constexpr (T::kQ == 1) {
@@ -1157,6 +1164,34 @@ __global__ void __launch_bounds__(Tile<D>::kThreadsAll, 1) kv_tile_kernel(const 
                     }
                 }
                 const float ref = m == -INFINITY ? 0.0f : m - (kLift - kSlack);
+                const auto weights = [&](const uint32_t *v, int c) {      // of columns c .. c + 31
+                    uint32_t o[16];
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        const BlockScales &sc = scales_at(c);
+                        const int p = ((p0 + c + h * 16) & 63) >> log2;
+                        const uint64_t f2 = pair_of(qs * sc.ks[p]), off2 = pair_of(sc.lv[p] - ref);
+                        uint64_t g[2] = {0, 0};
+#pragma unroll
+                        for (int k = 0; k < 8; ++k) {
+                            uint64_t x;
+                            float y, z;
+                            asm("mov.b64 %0, {%1, %2};" : "=l"(x) : "r"(v[h * 16 + 2 * k]), "r"(v[h * 16 + 2 * k + 1]));
+                            asm("fma.rn.f32x2 %0, %0, %1, %2;" : "+l"(x) : "l"(f2), "l"(off2));
+                            asm("mov.b64 {%0, %1}, %2;" : "=f"(y), "=f"(z) : "l"(x));
+                            y = ex2(y);
+                            z = ex2(z);
+                            asm("mov.b64 %0, {%1, %2};" : "=l"(x) : "f"(y), "f"(z));
+                            asm("add.rn.f32x2 %0, %0, %1;" : "+l"(g[k & 1]) : "l"(x));
+                            o[h * 8 + k] = pack_half(y, z);
+                        }
+                        float y, z;
+                        asm("add.rn.f32x2 %0, %0, %1;" : "+l"(g[0]) : "l"(g[1]));
+                        asm("mov.b64 {%0, %1}, %2;" : "=f"(y), "=f"(z) : "l"(g[0]));
+                        l = fmaf(y + z, sc.inv[p], l);
+                    }
+                    tmem_st16(ts + (uint32_t)(c / 2), o);
+                };
                 if (whole) {
 #pragma unroll
                     for (int c = 0; c < T::kCols; c += 64) {
@@ -1165,41 +1200,25 @@ __global__ void __launch_bounds__(Tile<D>::kThreadsAll, 1) kv_tile_kernel(const 
                             tmem_ld32(ts + (uint32_t)c + 32u, vb);
                             tmem_ld_wait();
                         }
-                        const BlockScales &sc = scales_at(c);
-#pragma unroll
-                        for (int hh = 0; hh < (T::kCols < 64 ? T::kCols : 64) / 32; ++hh) {
-                            uint32_t o[16];
-#pragma unroll
-                            for (int h = 0; h < 2; ++h) {
-                                const uint32_t *v = hh == 0 ? va + h * 16 : vb + h * 16;
-                                const int p = ((p0 + c + hh * 32 + h * 16) & 63) >> log2;
-                                const uint64_t f2 = pair_of(qs * sc.ks[p]), off2 = pair_of(sc.lv[p] - ref);
-                                uint64_t g[2] = {0, 0};
-#pragma unroll
-                                for (int k = 0; k < 8; ++k) {
-                                    uint64_t x;
-                                    float y, z;
-                                    asm("mov.b64 %0, {%1, %2};" : "=l"(x) : "r"(v[2 * k]), "r"(v[2 * k + 1]));
-                                    asm("fma.rn.f32x2 %0, %0, %1, %2;" : "+l"(x) : "l"(f2), "l"(off2));
-                                    asm("mov.b64 {%0, %1}, %2;" : "=f"(y), "=f"(z) : "l"(x));
-                                    y = ex2(y);
-                                    z = ex2(z);
-                                    asm("mov.b64 %0, {%1, %2};" : "=l"(x) : "f"(y), "f"(z));
-                                    asm("add.rn.f32x2 %0, %0, %1;" : "+l"(g[k & 1]) : "l"(x));
-                                    o[h * 8 + k] = pack_half(y, z);
-                                }
-                                float y, z;
-                                asm("add.rn.f32x2 %0, %0, %1;" : "+l"(g[0]) : "l"(g[1]));
-                                asm("mov.b64 {%0, %1}, %2;" : "=f"(y), "=f"(z) : "l"(g[0]));
-                                l = fmaf(y + z, sc.inv[p], l);
-                            }
-                            tmem_st16(ts + (uint32_t)(c / 2 + hh * 16), o);
-                        }
+                        weights(va, c);
+                        if constexpr (T::kCols >= 64) weights(vb, c + 32);
                     }
                 } else {
 #pragma unroll 1
                     for (int c = 0; c < T::kCols; c += 32) {
+                        if (c + 32 <= least && !zeros) {      // seen by every row of the warp
+                            tmem_ld32(ts + (uint32_t)c, va);
+                            tmem_ld_wait();
+                            weights(va, c);
+                            continue;
+                        }
                         uint32_t o[16];
+                        if (c >= most) {                      // by none
+#pragma unroll
+                            for (int k = 0; k < 16; ++k) o[k] = 0u;
+                            tmem_st16(ts + (uint32_t)(c / 2), o);
+                            continue;
+                        }
                         tmem_ld32(ts + (uint32_t)c, va);
                         tmem_ld_wait();
                         const BlockScales &sc = scales_at(c);
@@ -1250,32 +1269,31 @@ __global__ void __launch_bounds__(Tile<D>::kThreadsAll, 1) kv_tile_kernel(const 
             const bool part = t.splits > 1, none = !(inv > 0.0f);
             uint8_t *stage = sq + half * CHUNKS * T::kChunkQ + quad * 32 * 128;
             for (int pass = 0; pass < (part ? 2 : 1); ++pass) {          // fp32 takes two
-                // 16 columns at a time: two 16-byte units of bf16, or four of fp32
-                const int groups = part ? T::kOutCols / 32 : T::kOutCols / 16;
+                // 32 columns at a time: four 16-byte units of bf16, or eight of fp32
+                const int groups = part ? T::kOutCols / 64 : T::kOutCols / 32;
                 const auto put = [&](int u, uint4 o) {
                     *reinterpret_cast<uint4 *>(stage + (u >> 3) * T::kChunkQ + lane * 128 + (((u & 7) ^ (lane & 7)) << 4)) = o;
                 };
 #pragma unroll 1
                 for (int c = 0; c < groups; ++c) {
-                    uint32_t v[16];
-                    if (t.steps > 0) {
-                        tmem_ld16(tmem + T::kTmemO + (uint32_t)(q * 128 + half * T::kOutCols + (pass * groups + c) * 16) + lanes, v);
-                        tmem_ld_wait();
-                    }
+                    uint32_t v[32];
+                    // (rows without a step have nothing there, and `none`)
+                    tmem_ld32(tmem + T::kTmemO + (uint32_t)(q * 128 + half * T::kOutCols + (pass * groups + c) * 32) + lanes, v);
+                    tmem_ld_wait();
 #pragma unroll
-                    for (int k = 0; k < 16; ++k) v[k] = none ? 0u : __float_as_uint(__uint_as_float(v[k]) * inv);
+                    for (int k = 0; k < 32; ++k) v[k] = none ? 0u : __float_as_uint(__uint_as_float(v[k]) * inv);
                     if (part) {
 #pragma unroll
-                        for (int u = 0; u < 4; ++u) put(c * 4 + u, make_uint4(v[4 * u], v[4 * u + 1], v[4 * u + 2], v[4 * u + 3]));
+                        for (int u = 0; u < 8; ++u) put(c * 8 + u, make_uint4(v[4 * u], v[4 * u + 1], v[4 * u + 2], v[4 * u + 3]));
                     } else {
-                        uint32_t w[8];
+                        uint32_t w[16];
 #pragma unroll
-                        for (int k = 0; k < 8; ++k) {
+                        for (int k = 0; k < 16; ++k) {
                             const __nv_bfloat162 b2 = __floats2bfloat162_rn(__uint_as_float(v[2 * k]), __uint_as_float(v[2 * k + 1]));
                             w[k] = *reinterpret_cast<const uint32_t *>(&b2);
                         }
-                        put(c * 2, make_uint4(w[0], w[1], w[2], w[3]));
-                        put(c * 2 + 1, make_uint4(w[4], w[5], w[6], w[7]));
+#pragma unroll
+                        for (int u = 0; u < 4; ++u) put(c * 4 + u, make_uint4(w[4 * u], w[4 * u + 1], w[4 * u + 2], w[4 * u + 3]));
                     }
                 }
                 __syncwarp();
@@ -1338,7 +1356,7 @@ __global__ void __launch_bounds__(Tile<D>::kThreadsAll, 1) kv_tile_kernel(const 
                     if (sub == 0)
                         ok = ok && warp_wait(&empty[st], (step_no / (uint32_t)stages & 1u) ^ 1u, wait, kSiteKvLoad);
                     if (!ok) break;
-                    const int there = s_scale[block % kRing].there, left = t.len - t.tok0 - s * T::kStep - sub * 64;
+                    const int there = s_there[values][block % kRing], left = t.len - t.tok0 - s * T::kStep - sub * 64;
                     const uint8_t *src = raw + rs * T::kCodes + piece * 16;
 #pragma unroll
                     for (int k0 = 0; k0 < N; k0 += AT_ONCE) {
@@ -1375,12 +1393,15 @@ __global__ void __launch_bounds__(Tile<D>::kThreadsAll, 1) kv_tile_kernel(const 
         }
     } else {
       asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
-      if (warp == T::kCopyWarp) {
+      if (warp == T::kCopyWarp || warp == T::kCopyWarp + 1) {
         // ---------------------------------------------------------- codes to shared memory
-        // A lane a page of the block: the page's run of tokens of this head is contiguous, one copy for
-        // its keys and one for its values.
+        // A lane a page of the block: the page's run of tokens of this head is contiguous, one copy.  The
+        // keys' warp also keeps the pages' scales for the softmax.
+        const int plane = warp - T::kCopyWarp;
         const int run = min(64, a.pool.page), per = 64 / run;      // tokens of a page in a block; pages of a block
-        uint32_t block = 0, keys_only = 0;
+        const uint8_t *codes = a.pool.codes + plane * a.pool.plane_codes;
+        uint8_t *raw = smem + T::kSmemRaw + plane * (T::kRaw * T::kCodes);
+        uint32_t block = 0;
         bool ok = true;
         for (int round = 0; round * (int)gridDim.x < items && ok; ++round) {
             const int item = round_item(round);
@@ -1400,7 +1421,7 @@ __global__ void __launch_bounds__(Tile<D>::kThreadsAll, 1) kv_tile_kernel(const 
                     if (x.page < 0 || x.page >= a.pool.pages) {
                         record_status(a.status, kStatusBadPage);
                         x.page = -1;
-                    } else {
+                    } else if (plane == 0) {
                         const int64_t tile = (int64_t)x.page * H + t.head;
                         x.ks = a.pool.scales[tile];
                         x.vs = a.pool.scales[a.pool.plane_scales + tile];
@@ -1421,51 +1442,38 @@ __global__ void __launch_bounds__(Tile<D>::kThreadsAll, 1) kv_tile_kernel(const 
                 const int p = (t0 >> log2) - page0 + (lane < per ? lane : 0);      // under 64
                 const bool later = p >= 32;
                 const int page_a = __shfl_sync(0xFFFFFFFFu, now.page, p & 31), page_b = __shfl_sync(0xFFFFFFFFu, next.page, p & 31);
-                const float ks_a = __shfl_sync(0xFFFFFFFFu, now.ks, p & 31), ks_b = __shfl_sync(0xFFFFFFFFu, next.ks, p & 31);
-                const float vs_a = __shfl_sync(0xFFFFFFFFu, now.vs, p & 31), vs_b = __shfl_sync(0xFFFFFFFFu, next.vs, p & 31);
                 const int page = lane < per && t0 + lane * run < t.len ? (later ? page_b : page_a) : -1;
-                const float ks = page >= 0 ? (later ? ks_b : ks_a) : 0.0f;
-                float vs = page >= 0 ? (later ? vs_b : vs_a) : 1.0f;
-                if (!warp_wait(&bar.raw_empty[0][rs], parity_of<T::kRaw>(block) ^ 1u, wait, kSiteKvLoad)) {
+                const unsigned int there = __ballot_sync(0xFFFFFFFFu, page >= 0);
+                if (!warp_wait(&bar.raw_empty[plane][rs], parity_of<T::kRaw>(block) ^ 1u, wait, kSiteKvLoad)) {
                     ok = false;
                     break;
                 }
-                BlockScales &sc = s_scale[block % kRing];
-                const unsigned int zero = __ballot_sync(0xFFFFFFFFu, vs == 0.0f), there = __ballot_sync(0xFFFFFFFFu, page >= 0);
-                if (vs == 0.0f) vs = 0x1p-60f;
-                if (lane < 4) {
-                    sc.ks[lane] = ks;
-                    sc.lv[lane] = log2f(vs);
-                    sc.inv[lane] = __fdiv_rn(1.0f, vs);
+                if (plane == 0) {
+                    const float ks_a = __shfl_sync(0xFFFFFFFFu, now.ks, p & 31), ks_b = __shfl_sync(0xFFFFFFFFu, next.ks, p & 31);
+                    const float vs_a = __shfl_sync(0xFFFFFFFFu, now.vs, p & 31), vs_b = __shfl_sync(0xFFFFFFFFu, next.vs, p & 31);
+                    const float ks = page >= 0 ? (later ? ks_b : ks_a) : 0.0f;
+                    float vs = page >= 0 ? (later ? vs_b : vs_a) : 1.0f;
+                    BlockScales &sc = s_scale[block % kRing];
+                    const unsigned int zero = __ballot_sync(0xFFFFFFFFu, vs == 0.0f);
+                    if (vs == 0.0f) vs = 0x1p-60f;
+                    if (lane < 4) {
+                        sc.ks[lane] = ks;
+                        sc.lv[lane] = log2f(vs);
+                        sc.inv[lane] = __fdiv_rn(1.0f, vs);
+                    }
+                    if (lane == 0) sc.zero = (int)zero;
                 }
-                if (lane == 0) {
-                    sc.zero = (int)zero;
-                    sc.there = (int)there;
-                }
-                const uint32_t bytes = (uint32_t)(__popc(there) * run * D);
+                if (lane == 0) s_there[plane][block % kRing] = (int)there;
                 const int64_t at = ((((int64_t)page * H + t.head) << log2) + (t0 & (a.pool.page - 1))) * D;
-                uint8_t *dst = smem + T::kSmemRaw + rs * T::kCodes + lane * run * D;
                 __syncwarp();
-                if (lane == 0) mbar_arrive_expect_tx(&bar.raw_full[0][rs], bytes);
+                if (lane == 0) mbar_arrive_expect_tx(&bar.raw_full[plane][rs], (uint32_t)(__popc(there) * run * D));
                 __syncwarp();
-                if (page >= 0) bulk_copy(dst, a.pool.codes + at, (uint32_t)(run * D), &bar.raw_full[0][rs]);
-                if (!warp_wait(&bar.raw_empty[1][rs], parity_of<T::kRaw>(block) ^ 1u, wait, kSiteKvLoad)) {
-                    keys_only = 1;
-                    ok = false;
-                    break;
-                }
-                if (lane == 0) mbar_arrive_expect_tx(&bar.raw_full[1][rs], bytes);
-                __syncwarp();
-                if (page >= 0)
-                    bulk_copy(dst + T::kRaw * T::kCodes, a.pool.codes + a.pool.plane_codes + at, (uint32_t)(run * D), &bar.raw_full[1][rs]);
+                if (page >= 0) bulk_copy(raw + rs * T::kCodes + lane * run * D, codes + at, (uint32_t)(run * D), &bar.raw_full[plane][rs]);
             }
         }
-        // no copy is in flight when the CTA ends (after a wait that ran out, one block may have its keys only)
-        for (int plane = 0; plane < 2; ++plane) {
-            const uint32_t end = block + (plane == 0 ? keys_only : 0u);
-            for (uint32_t k = end > T::kRaw ? end - T::kRaw : 0; k < end; ++k)
-                warp_wait(&bar.raw_full[plane][stage_of<T::kRaw>(k)], parity_of<T::kRaw>(k), wait, kSiteDrain);
-        }
+        // no copy is in flight when the CTA ends
+        for (uint32_t k = block > T::kRaw ? block - T::kRaw : 0; k < block; ++k)
+            warp_wait(&bar.raw_full[plane][stage_of<T::kRaw>(k)], parity_of<T::kRaw>(k), wait, kSiteDrain);
       } else if (warp == T::kMmaWarp) {
         // ---------------------------------------------------------- products
         const uint32_t is = idesc_f32acc(0, 0, 128, T::kStep);
@@ -1511,15 +1519,17 @@ __global__ void __launch_bounds__(Tile<D>::kThreadsAll, 1) kv_tile_kernel(const 
             };
             for (int s = 0; s <= t.steps && t.steps > 0 && ok; ++s) {
                 const bool has_s = s < t.steps, has_o = s > 0;
-                if (has_s) ok = warp_wait(&bar.k_full[stage_of<T::kKStages>(nk)], parity_of<T::kKStages>(nk), wait, kSiteKvMma);
+                const auto keys = [&]() -> bool {
+                    return warp_wait(&bar.k_full[stage_of<T::kKStages>(nk)], parity_of<T::kKStages>(nk), wait, kSiteKvMma);
+                };
                 // with two places the step's S goes ahead of the last step's O
-                if (T::kSlots == 2 && has_s) ok = ok && issue_s(0, s);
+                if (T::kSlots == 2 && has_s) ok = keys() && issue_s(0, s);
                 if (has_o) ok = ok && warp_wait(&bar.v_full[stage_of<T::kVStages>(nv)], parity_of<T::kVStages>(nv), wait, kSiteKvMma);
 #pragma unroll
                 for (int q = 0; q < T::kQ; ++q) {
                     if (q >= tiles) break;
                     if (has_o) ok = ok && issue_o(q, s - 1);
-                    if (T::kSlots == 1 && has_s) ok = ok && issue_s(q, s);
+                    if (T::kSlots == 1 && has_s) ok = ok && (q > 0 || keys()) && issue_s(q, s);
                 }
                 if (!ok) break;
                 if (has_s) {
@@ -1660,7 +1670,7 @@ Plan make_plan(int64_t rows, bool ragged, int64_t seqs, int group, int heads, in
         // a split sequence has at most kTileSlots items
         p.tile_items = ragged ? (rows * group / tr + seqs) * heads + seqs * kTileSlots
                               : seqs * (((per + tr - 1) / tr) * heads * tile_splits((int)per, (int)max_len, heads, dim));
-        const bool cut = ragged ? max_len > 512 : tile_splits((int)per, (int)max_len, heads, dim) > 1;
+        const bool cut = ragged ? max_len > 1920 : tile_splits((int)per, (int)max_len, heads, dim) > 1;
         if (cut) {
             int64_t units = (int64_t)kTileSlots * tr, join = units / 2;
             const int64_t most = per * heads;
