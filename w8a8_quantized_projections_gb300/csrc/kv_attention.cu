@@ -707,8 +707,10 @@ struct Tile {
     static constexpr int kStep = D <= 128 ? 128 : 64;        // tokens of a step
     static constexpr int kSub = kStep / 64;                  // blocks of 64 tokens of a step
     static constexpr int kSlots = D <= 128 ? 1 : 2;          // places for S of a row tile
-    static constexpr int kKStages = D <= 128 ? 2 : 1, kVStages = D == 64 ? 2 : 1;   // steps of keys and of values as operands
-    static constexpr int kRaw = D == 64 ? 4 : D == 128 ? 3 : 2;      // blocks of codes on their way, of keys and of values
+    // Operands: two steps of keys; blocks of values, which the products take one by one: with more than
+    // a step's, the next step's first block is there before this step's are done with.
+    static constexpr int kKStages = 2, kVBlocks = D == 64 ? 4 : D == 128 ? 3 : 1;
+    static constexpr int kRawK = D == 64 ? 4 : D == 128 ? 2 : 1, kRawV = D == 64 ? 4 : D == 128 ? 3 : 2;   // blocks of codes on their way
     static constexpr int kCols = kStep * kQ / 2;             // columns of S that a softmax thread has
     static constexpr int kOutCols = kQ == 2 ? D : D / 2;     // and of O
     // 20 warps of 96 registers in whole warpgroups: eight of softmax (four for each row tile, or eight
@@ -720,13 +722,14 @@ struct Tile {
     static constexpr int kMmaWarp = kSoftWarps + 2 * kConvWarps, kCopyWarp = kMmaWarp + 1;   // and the next
     static constexpr int kThreadsAll = (kMmaWarp + 4) * 32;
     static constexpr int kChunks = D / 64;                   // 64-element columns of 128-byte rows
-    static constexpr int kChunkQ = 128 * 128, kChunkKV = kStep * 128;
+    static constexpr int kChunkQ = 128 * 128, kChunkK = kStep * 128;
     static constexpr int kQuery = kChunks * kChunkQ;         // 128 x D in fp16
-    static constexpr int kOperand = kChunks * kChunkKV;      // kStep x D
+    static constexpr int kOperand = kChunks * kChunkK;       // kStep x D
+    static constexpr int kChunkV = 64 * 128, kBlockV = kChunks * kChunkV;      // a block of values
     static constexpr int kCodes = 64 * D;                    // a block's
     static constexpr int kSmemQ = 0, kSmemK = kQ * kQuery, kSmemV = kSmemK + kKStages * kOperand;
-    static constexpr int kSmemRaw = kSmemV + kVStages * kOperand;     // keys' blocks, then values'
-    static constexpr int kSmemEnd = kSmemRaw + kRaw * 2 * kCodes;
+    static constexpr int kSmemRaw = kSmemV + kVBlocks * kBlockV;      // keys' blocks, then values'
+    static constexpr int kSmemEnd = kSmemRaw + (kRawK + kRawV) * kCodes;
     static constexpr int kSmem = kSmemEnd + 1024;
     // tensor memory: 256 columns for S (P takes the first half of the columns of its threads), then O.
     // More than half an SM's shared memory is taken, so no two CTAs of an SM wait for one another's
@@ -866,7 +869,7 @@ __device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t parity, const 
 }
 
 struct TileBars {
-    uint64_t q_full[2], k_full[2], k_empty[2], v_full[2], v_empty[2], s_full[2], p_full[2], o_done[2];
+    uint64_t q_full[2], k_full[2], k_empty[2], v_full[4], v_empty[4], s_full[2], p_full[2], o_done[2];
     uint64_t raw_full[2][4], raw_empty[2][4];      // of keys and of values
     uint64_t pair[4], never, drain;
 };
@@ -931,9 +934,7 @@ __global__ void __launch_bounds__(Tile<D>::kThreadsAll, 1) kv_tile_kernel(const 
             mbar_init(&bar.q_full[i], 8 / T::kQ);
             mbar_init(&bar.p_full[i], 8 / T::kQ);
             mbar_init(&bar.k_full[i], T::kConvWarps);
-            mbar_init(&bar.v_full[i], T::kConvWarps);
             mbar_init(&bar.k_empty[i], 1);
-            mbar_init(&bar.v_empty[i], 1);
             mbar_init(&bar.s_full[i], 1);
             mbar_init(&bar.o_done[i], 1);
             for (int k = 0; k < 4; ++k) {
@@ -941,7 +942,11 @@ __global__ void __launch_bounds__(Tile<D>::kThreadsAll, 1) kv_tile_kernel(const 
                 mbar_init(&bar.raw_empty[i][k], T::kConvWarps);
             }
         }
-        for (int i = 0; i < 4; ++i) mbar_init(&bar.pair[i], 2);
+        for (int i = 0; i < 4; ++i) {
+            mbar_init(&bar.v_full[i], T::kConvWarps);
+            mbar_init(&bar.v_empty[i], 1);
+            mbar_init(&bar.pair[i], 2);
+        }
         mbar_init(&bar.never, 1);
         mbar_init(&bar.drain, 1);
         fence_barrier_init();
@@ -1335,11 +1340,10 @@ __global__ void __launch_bounds__(Tile<D>::kThreadsAll, 1) kv_tile_kernel(const 
         // way round, so that the eight lanes of a store meet every bank once
         const int chunk = piece >> 2, unit = (piece & 3) * 2;
         const bool swap = chunk & 1;
-        const int stages = values ? T::kVStages : T::kKStages;
         uint64_t *full = values ? bar.v_full : bar.k_full, *empty = values ? bar.v_empty : bar.k_empty;
         uint64_t *raw_full = bar.raw_full[values], *raw_empty = bar.raw_empty[values];
-        const uint8_t *raw = smem + T::kSmemRaw + (values ? T::kRaw * T::kCodes : 0);
-        uint8_t *operands = smem + (values ? T::kSmemV : T::kSmemK) + chunk * T::kChunkKV;
+        const uint8_t *raw = smem + T::kSmemRaw + (values ? T::kRawK * T::kCodes : 0);
+        uint8_t *operands = smem + (values ? T::kSmemV + chunk * T::kChunkV : T::kSmemK + chunk * T::kChunkK);
         uint32_t step_no = 0, block = 0;
         bool ok = true;
         for (int round = 0; round * (int)gridDim.x < items && ok; ++round) {
@@ -1347,14 +1351,17 @@ __global__ void __launch_bounds__(Tile<D>::kThreadsAll, 1) kv_tile_kernel(const 
             if (item >= items) continue;
             const TileItem t = tile_item<D>(a, s_items, item);
             for (int s = 0; s < t.steps && ok; ++s, ++step_no) {
-                const uint32_t st = step_no % (uint32_t)stages;
-                uint8_t *dst = operands + st * T::kOperand;
 #pragma unroll 1
                 for (int sub = 0; sub < T::kSub; ++sub, ++block) {
-                    const int rs = stage_of<T::kRaw>(block);
-                    ok = warp_wait(&raw_full[rs], parity_of<T::kRaw>(block), wait, kSiteKvLoad);
-                    if (sub == 0)
-                        ok = ok && warp_wait(&empty[st], (step_no / (uint32_t)stages & 1u) ^ 1u, wait, kSiteKvLoad);
+                    // keys: a step a stage; values: a block
+                    const int st = values ? stage_of<T::kVBlocks>(block) : stage_of<T::kKStages>(step_no);
+                    const uint32_t turn = values ? parity_of<T::kVBlocks>(block) : parity_of<T::kKStages>(step_no);
+                    const int rs = values ? stage_of<T::kRawV>(block) : stage_of<T::kRawK>(block);
+                    const uint32_t raw_turn = values ? parity_of<T::kRawV>(block) : parity_of<T::kRawK>(block);
+                    const bool last = values || sub == T::kSub - 1;
+                    uint8_t *dst = operands + (values ? st * T::kBlockV : st * T::kOperand + sub * 64 * 128);
+                    ok = warp_wait(&raw_full[rs], raw_turn, wait, kSiteKvLoad);
+                    if (values || sub == 0) ok = ok && warp_wait(&empty[st], turn ^ 1u, wait, kSiteKvLoad);
                     if (!ok) break;
                     const int there = s_there[values][block % kRing], left = t.len - t.tok0 - s * T::kStep - sub * 64;
                     const uint8_t *src = raw + rs * T::kCodes + piece * 16;
@@ -1370,7 +1377,7 @@ __global__ void __launch_bounds__(Tile<D>::kThreadsAll, 1) kv_tile_kernel(const 
                         }
 #pragma unroll
                         for (int k = 0; k < AT_ONCE; ++k) {
-                            const int rr = sub * 64 + crow + (k0 + k) * (64 / N);
+                            const int rr = crow + (k0 + k) * (64 / N);
                             uint32_t h[8];
                             widen4<KIND>(v[k].x, h[0], h[1]);
                             widen4<KIND>(v[k].y, h[2], h[3]);
@@ -1382,11 +1389,11 @@ __global__ void __launch_bounds__(Tile<D>::kThreadsAll, 1) kv_tile_kernel(const 
                             *reinterpret_cast<uint4 *>(row + (((unit + (swap ? 0 : 1)) ^ (rr & 7)) << 4)) = swap ? u0 : u1;
                         }
                     }
-                    if (sub == T::kSub - 1) fence_proxy_async_smem();
+                    if (last) fence_proxy_async_smem();
                     __syncwarp();
                     if (lane == 0) {
                         mbar_arrive(&raw_empty[rs]);
-                        if (sub == T::kSub - 1) mbar_arrive(&full[st]);
+                        if (last) mbar_arrive(&full[st]);
                     }
                 }
             }
@@ -1400,7 +1407,7 @@ __global__ void __launch_bounds__(Tile<D>::kThreadsAll, 1) kv_tile_kernel(const 
         const int plane = warp - T::kCopyWarp;
         const int run = min(64, a.pool.page), per = 64 / run;      // tokens of a page in a block; pages of a block
         const uint8_t *codes = a.pool.codes + plane * a.pool.plane_codes;
-        uint8_t *raw = smem + T::kSmemRaw + plane * (T::kRaw * T::kCodes);
+        uint8_t *raw = smem + T::kSmemRaw + plane * (T::kRawK * T::kCodes);
         uint32_t block = 0;
         bool ok = true;
         for (int round = 0; round * (int)gridDim.x < items && ok; ++round) {
@@ -1432,7 +1439,7 @@ __global__ void __launch_bounds__(Tile<D>::kThreadsAll, 1) kv_tile_kernel(const 
             int page0 = t.tok0 >> log2;
             Page now = look_up(page0 + lane), next = look_up(page0 + 32 + lane);
             for (int s = 0; s < t.steps * T::kSub; ++s, ++block) {
-                const int rs = stage_of<T::kRaw>(block);
+                const int rs = plane ? stage_of<T::kRawV>(block) : stage_of<T::kRawK>(block);
                 const int t0 = t.tok0 + s * 64;
                 if ((t0 >> log2) - page0 >= 32) {
                     page0 += 32;
@@ -1444,7 +1451,8 @@ __global__ void __launch_bounds__(Tile<D>::kThreadsAll, 1) kv_tile_kernel(const 
                 const int page_a = __shfl_sync(0xFFFFFFFFu, now.page, p & 31), page_b = __shfl_sync(0xFFFFFFFFu, next.page, p & 31);
                 const int page = lane < per && t0 + lane * run < t.len ? (later ? page_b : page_a) : -1;
                 const unsigned int there = __ballot_sync(0xFFFFFFFFu, page >= 0);
-                if (!warp_wait(&bar.raw_empty[plane][rs], parity_of<T::kRaw>(block) ^ 1u, wait, kSiteKvLoad)) {
+                const uint32_t turn = plane ? parity_of<T::kRawV>(block) : parity_of<T::kRawK>(block);
+                if (!warp_wait(&bar.raw_empty[plane][rs], turn ^ 1u, wait, kSiteKvLoad)) {
                     ok = false;
                     break;
                 }
@@ -1472,14 +1480,16 @@ __global__ void __launch_bounds__(Tile<D>::kThreadsAll, 1) kv_tile_kernel(const 
             }
         }
         // no copy is in flight when the CTA ends
-        for (uint32_t k = block > T::kRaw ? block - T::kRaw : 0; k < block; ++k)
-            warp_wait(&bar.raw_full[plane][stage_of<T::kRaw>(k)], parity_of<T::kRaw>(k), wait, kSiteDrain);
+        const uint32_t depth = plane ? T::kRawV : T::kRawK;
+        for (uint32_t k = block > depth ? block - depth : 0; k < block; ++k)
+            warp_wait(&bar.raw_full[plane][plane ? stage_of<T::kRawV>(k) : stage_of<T::kRawK>(k)],
+                      plane ? parity_of<T::kRawV>(k) : parity_of<T::kRawK>(k), wait, kSiteDrain);
       } else if (warp == T::kMmaWarp) {
         // ---------------------------------------------------------- products
         const uint32_t is = idesc_f32acc(0, 0, 128, T::kStep);
         const uint32_t io = idesc_f32acc(0, 0, 128, D) | (1u << 16);    // bit 16: the right-hand operand is MN-major
         const uint64_t dq = sdesc_sw128(smem_u32(smem + T::kSmemQ)), dk = sdesc_sw128(smem_u32(smem + T::kSmemK));
-        const uint64_t dv = sdesc_values(smem_u32(smem + T::kSmemV), T::kChunkKV);      // offsets add to the address field
+        const uint64_t dv = sdesc_values(smem_u32(smem + T::kSmemV), T::kChunkV);      // offsets add to the address field
         uint32_t nk = 0, nv = 0, nq[2] = {0, 0}, ns[2] = {0, 0}, npv[2] = {0, 0};
         bool ok = !a.force_timeout || warp_wait(&bar.never, 0, wait, kSiteKvMma);
         for (int round = 0; round * (int)gridDim.x < items && ok; ++round) {
@@ -1499,20 +1509,29 @@ __global__ void __launch_bounds__(Tile<D>::kThreadsAll, 1) kv_tile_kernel(const 
                 for (int k = 0; k < D / 16; ++k)
                     mma_f16_warp(tmem + (uint32_t)(slot * T::kStep),
                                  dq + (uint32_t)((q * T::kQuery + (k >> 2) * T::kChunkQ + (k & 3) * 32) >> 4),
-                                 dk + (uint32_t)((st * T::kOperand + (k >> 2) * T::kChunkKV + (k & 3) * 32) >> 4), is, k > 0);
+                                 dk + (uint32_t)((st * T::kOperand + (k >> 2) * T::kChunkK + (k & 3) * 32) >> 4), is, k > 0);
                 commit_warp(&bar.s_full[slot]);
                 ++ns[q];
                 return true;
             };
             const auto issue_o = [&](int q, int s) -> bool {      // O += P V of step s
-                const int st = stage_of<T::kVStages>(nv), slot = slot_of<T>(q, npv[q]);
+                const int slot = slot_of<T>(q, npv[q]);
                 if (!warp_wait(&bar.p_full[slot], turn_of<T>(npv[q]), wait, kSiteKvMma)) return false;
                 tc_fence_after();
 #pragma unroll
-                for (int k = 0; k < T::kStep / 16; ++k)
-                    mma_f16_tmem(tmem + T::kTmemO + (uint32_t)(q * 128),
-                                 tmem + (uint32_t)(slot * T::kStep + k * 16 / T::kCols * T::kCols + k * 16 % T::kCols / 2),
-                                 dv + (uint32_t)((st * T::kOperand + k * 2048) >> 4), io, s > 0 || k > 0);
+                for (int h = 0; h < T::kSub; ++h) {
+                    const int st = stage_of<T::kVBlocks>(nv + h);
+                    if (q == 0 && !warp_wait(&bar.v_full[st], parity_of<T::kVBlocks>(nv + h), wait, kSiteKvMma)) return false;
+                    tc_fence_after();
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        const int k = h * 4 + j;
+                        mma_f16_tmem(tmem + T::kTmemO + (uint32_t)(q * 128),
+                                     tmem + (uint32_t)(slot * T::kStep + k * 16 / T::kCols * T::kCols + k * 16 % T::kCols / 2),
+                                     dv + (uint32_t)((st * T::kBlockV + j * 2048) >> 4), io, s > 0 || k > 0);
+                    }
+                    if (q == tiles - 1) commit_warp(&bar.v_empty[st]);
+                }
                 commit_warp(&bar.o_done[slot]);
                 ++npv[q];
                 return true;
@@ -1524,7 +1543,7 @@ __global__ void __launch_bounds__(Tile<D>::kThreadsAll, 1) kv_tile_kernel(const 
                 };
                 // with two places the step's S goes ahead of the last step's O
                 if (T::kSlots == 2 && has_s) ok = keys() && issue_s(0, s);
-                if (has_o) ok = ok && warp_wait(&bar.v_full[stage_of<T::kVStages>(nv)], parity_of<T::kVStages>(nv), wait, kSiteKvMma);
+                if (T::kSlots == 2 && has_s) commit_warp(&bar.k_empty[stage_of<T::kKStages>(nk)]);
 #pragma unroll
                 for (int q = 0; q < T::kQ; ++q) {
                     if (q >= tiles) break;
@@ -1532,14 +1551,9 @@ __global__ void __launch_bounds__(Tile<D>::kThreadsAll, 1) kv_tile_kernel(const 
                     if (T::kSlots == 1 && has_s) ok = ok && (q > 0 || keys()) && issue_s(q, s);
                 }
                 if (!ok) break;
-                if (has_s) {
-                    commit_warp(&bar.k_empty[stage_of<T::kKStages>(nk)]);
-                    ++nk;
-                }
-                if (has_o) {
-                    commit_warp(&bar.v_empty[stage_of<T::kVStages>(nv)]);
-                    ++nv;
-                }
+                if (T::kSlots == 1 && has_s) commit_warp(&bar.k_empty[stage_of<T::kKStages>(nk)]);
+                nk += has_s;
+                if (has_o) nv += T::kSub;
             }
         }
         // nothing is in flight when tensor memory is given back
