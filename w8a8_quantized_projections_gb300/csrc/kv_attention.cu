@@ -33,6 +33,7 @@
 // sum, and with weights of zero.  (The value scales of a sequence are taken to lie
 // within 2^100 of one another.)
 #include <cstdint>
+#include <type_traits>
 
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -714,12 +715,13 @@ struct Tile {
     static constexpr int kCols = kStep * kQ / 2;             // columns of S that a softmax thread has
     static constexpr int kOutCols = kQ == 2 ? D : D / 2;     // and of O
     // 20 warps of 96 registers in whole warpgroups: eight of softmax (four for each row tile, or eight
-    // for one), four that turn keys into operands and four for values, then one that issues the products,
-    // one that copies codes of keys, one for values and an idle one.  Each of the SM's four register files holds two warps of
+    // for one), four that turn keys into operands and four for values, then one that issues the products
+    // for each row tile (one that issued for two waited for one tile's product while the other's could
+    // have started: 77 us instead of 69 for 2,270 rows over as many tokens), one that copies the codes of keys and one for values.  Each of the SM's four register files holds two warps of
     // softmax, two of conversion and one of the last group, and setmaxnreg's 2 x 144 + 2 x 56 + 80 =
     // 5 x 96 fit in every one of them.
     static constexpr int kSoftWarps = 8, kConvWarps = 4;     // conversion: for each operand
-    static constexpr int kMmaWarp = kSoftWarps + 2 * kConvWarps, kCopyWarp = kMmaWarp + 1;   // and the next
+    static constexpr int kMmaWarp = kSoftWarps + 2 * kConvWarps, kCopyWarp = kMmaWarp + 2;
     static constexpr int kThreadsAll = (kMmaWarp + 4) * 32;
     static constexpr int kChunks = D / 64;                   // 64-element columns of 128-byte rows
     static constexpr int kChunkQ = 128 * 128, kChunkK = kStep * 128;
@@ -871,7 +873,7 @@ __device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t parity, const 
 struct TileBars {
     uint64_t q_full[2], k_full[2], k_empty[2], v_full[4], v_empty[4], s_full[2], p_full[2], o_done[2];
     uint64_t raw_full[2][4], raw_empty[2][4];      // of keys and of values
-    uint64_t pair[4], never, drain;
+    uint64_t pair[4], never, drain[2], item_full[2], item_empty[2];
 };
 
 // Step number i of a pipeline of N stages: its stage, and the parity of the
@@ -923,6 +925,7 @@ __global__ void __launch_bounds__(Tile<D>::kThreadsAll, 1) kv_tile_kernel(const 
     __shared__ float s_qs[T::kQ * 128], s_pair[2][2][128];   // rows' query scales; what the threads of a row exchange
     __shared__ uint32_t s_tmem;
     __shared__ int s_abort, s_scan[32], s_total;
+    __shared__ TileItem s_item[2];
     uint8_t *smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
     int *s_items = reinterpret_cast<int *>(smem_raw + T::kSmem);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, log2 = a.pool.page_log2, H = a.pool.heads;
@@ -934,7 +937,10 @@ __global__ void __launch_bounds__(Tile<D>::kThreadsAll, 1) kv_tile_kernel(const 
             mbar_init(&bar.q_full[i], 8 / T::kQ);
             mbar_init(&bar.p_full[i], 8 / T::kQ);
             mbar_init(&bar.k_full[i], T::kConvWarps);
-            mbar_init(&bar.k_empty[i], 1);
+            mbar_init(&bar.k_empty[i], T::kQ);
+            mbar_init(&bar.drain[i], 1);
+            mbar_init(&bar.item_full[i], 1);
+            mbar_init(&bar.item_empty[i], T::kSoftWarps + 2 * T::kConvWarps + T::kQ + 1);
             mbar_init(&bar.s_full[i], 1);
             mbar_init(&bar.o_done[i], 1);
             for (int k = 0; k < 4; ++k) {
@@ -944,11 +950,10 @@ __global__ void __launch_bounds__(Tile<D>::kThreadsAll, 1) kv_tile_kernel(const 
         }
         for (int i = 0; i < 4; ++i) {
             mbar_init(&bar.v_full[i], T::kConvWarps);
-            mbar_init(&bar.v_empty[i], 1);
+            mbar_init(&bar.v_empty[i], T::kQ);
             mbar_init(&bar.pair[i], 2);
         }
         mbar_init(&bar.never, 1);
-        mbar_init(&bar.drain, 1);
         fence_barrier_init();
     }
     if (warp == T::kMmaWarp) {
@@ -983,6 +988,14 @@ __global__ void __launch_bounds__(Tile<D>::kThreadsAll, 1) kv_tile_kernel(const 
     const int items = s_total;
     const uint32_t tmem = s_tmem;
     const WaitCtx wait = {a.wait_limit_ns, &s_abort, a.status};
+    // the item of a round, from the warp that looks it up for all (the one that copies values)
+    const auto take_item = [&](int round, TileItem &t) -> bool {
+        if (!warp_wait(&bar.item_full[round & 1], (uint32_t)round >> 1 & 1u, wait, kSiteKvLoad)) return false;
+        t = s_item[round & 1];
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bar.item_empty[round & 1]);
+        return true;
+    };
 
     if (warp < T::kSoftWarps) {
         // ---------------------------------------------------------- softmax
@@ -1002,9 +1015,9 @@ __global__ void __launch_bounds__(Tile<D>::kThreadsAll, 1) kv_tile_kernel(const 
             return true;
         };
         for (int round = 0; round * (int)gridDim.x < items && ok; ++round) {
-            const int item = round_item(round);
-            if (item >= items) continue;
-            const TileItem t = tile_item<D>(a, s_items, item);
+            if (round_item(round) >= items) break;
+            TileItem t;
+            if (!take_item(round, t)) break;
             const uint32_t step0 = step_no;
             step_no += (uint32_t)t.steps;
             const int mine = min(128, t.rn - q * 128);     // rows of this tile
@@ -1336,10 +1349,8 @@ __global__ void __launch_bounds__(Tile<D>::kThreadsAll, 1) kv_tile_kernel(const 
         constexpr int PIECES = D / 16, N = 64 * PIECES / (T::kConvWarps * 32);   // 16-byte pieces of a row; of a thread and block
         constexpr int AT_ONCE = N < 4 ? N : 4;
         const int crow = ct / PIECES, piece = ct % PIECES;
-        // a piece becomes two 16-byte units of a row; lanes of every second chunk write them the other
-        // way round, so that the eight lanes of a store meet every bank once
-        const int chunk = piece >> 2, unit = (piece & 3) * 2;
-        const bool swap = chunk & 1;
+        // a piece becomes two 16-byte units of a row
+        const int chunk = piece >> 2, unit = (piece & 3) * 2, swap = (chunk & 1) * 16;
         uint64_t *full = values ? bar.v_full : bar.k_full, *empty = values ? bar.v_empty : bar.k_empty;
         uint64_t *raw_full = bar.raw_full[values], *raw_empty = bar.raw_empty[values];
         const uint8_t *raw = smem + T::kSmemRaw + (values ? T::kRawK * T::kCodes : 0);
@@ -1347,9 +1358,9 @@ __global__ void __launch_bounds__(Tile<D>::kThreadsAll, 1) kv_tile_kernel(const 
         uint32_t step_no = 0, block = 0;
         bool ok = true;
         for (int round = 0; round * (int)gridDim.x < items && ok; ++round) {
-            const int item = round_item(round);
-            if (item >= items) continue;
-            const TileItem t = tile_item<D>(a, s_items, item);
+            if (round_item(round) >= items) break;
+            TileItem t;
+            if (!take_item(round, t)) break;
             for (int s = 0; s < t.steps && ok; ++s, ++step_no) {
 #pragma unroll 1
                 for (int sub = 0; sub < T::kSub; ++sub, ++block) {
@@ -1365,30 +1376,38 @@ __global__ void __launch_bounds__(Tile<D>::kThreadsAll, 1) kv_tile_kernel(const 
                     if (!ok) break;
                     const int there = s_there[values][block % kRing], left = t.len - t.tok0 - s * T::kStep - sub * 64;
                     const uint8_t *src = raw + rs * T::kCodes + piece * 16;
+                    // lanes of every second chunk take a piece's halves the other way round, so that the
+                    // eight lanes of a store meet every bank once
+                    const auto convert = [&](auto part) {
 #pragma unroll
-                    for (int k0 = 0; k0 < N; k0 += AT_ONCE) {
-                        uint4 v[AT_ONCE];
+                        for (int k0 = 0; k0 < N; k0 += AT_ONCE) {
+                            uint4 v[AT_ONCE];
 #pragma unroll
-                        for (int k = 0; k < AT_ONCE; ++k) {
-                            // past the sequence's end anything may lie, NaN codes included
-                            const int rr = crow + (k0 + k) * (64 / N);
-                            v[k] = *reinterpret_cast<const uint4 *>(src + rr * D);
-                            if (rr >= left || !(there >> (rr >> log2) & 1)) v[k] = make_uint4(0, 0, 0, 0);
+                            for (int k = 0; k < AT_ONCE; ++k) {
+                                const int rr = crow + (k0 + k) * (64 / N);
+                                v[k] = *reinterpret_cast<const uint4 *>(src + rr * D);
+                                // past the sequence's end anything may lie, NaN codes included
+                                if (decltype(part)::value && (rr >= left || !(there >> (rr >> log2) & 1))) v[k] = make_uint4(0, 0, 0, 0);
+                            }
+#pragma unroll
+                            for (int k = 0; k < AT_ONCE; ++k) {
+                                const int rr = crow + (k0 + k) * (64 / N);
+                                uint8_t *row = dst + rr * 128;
+                                uint4 h;
+                                const int at = ((unit ^ (rr & 7)) << 4) ^ swap;
+                                widen4<KIND>(swap ? v[k].z : v[k].x, h.x, h.y);
+                                widen4<KIND>(swap ? v[k].w : v[k].y, h.z, h.w);
+                                *reinterpret_cast<uint4 *>(row + at) = h;
+                                widen4<KIND>(swap ? v[k].x : v[k].z, h.x, h.y);
+                                widen4<KIND>(swap ? v[k].y : v[k].w, h.z, h.w);
+                                *reinterpret_cast<uint4 *>(row + (at ^ 16)) = h;
+                            }
                         }
-#pragma unroll
-                        for (int k = 0; k < AT_ONCE; ++k) {
-                            const int rr = crow + (k0 + k) * (64 / N);
-                            uint32_t h[8];
-                            widen4<KIND>(v[k].x, h[0], h[1]);
-                            widen4<KIND>(v[k].y, h[2], h[3]);
-                            widen4<KIND>(v[k].z, h[4], h[5]);
-                            widen4<KIND>(v[k].w, h[6], h[7]);
-                            uint8_t *row = dst + rr * 128;
-                            const uint4 u0 = make_uint4(h[0], h[1], h[2], h[3]), u1 = make_uint4(h[4], h[5], h[6], h[7]);
-                            *reinterpret_cast<uint4 *>(row + (((unit + (swap ? 1 : 0)) ^ (rr & 7)) << 4)) = swap ? u1 : u0;
-                            *reinterpret_cast<uint4 *>(row + (((unit + (swap ? 0 : 1)) ^ (rr & 7)) << 4)) = swap ? u0 : u1;
-                        }
-                    }
+                    };
+                    if (left >= 64 && there == (int)((2u << (63 >> log2)) - 1u))
+                        convert(std::false_type());
+                    else
+                        convert(std::true_type());
                     if (last) fence_proxy_async_smem();
                     __syncwarp();
                     if (lane == 0) {
@@ -1411,9 +1430,19 @@ __global__ void __launch_bounds__(Tile<D>::kThreadsAll, 1) kv_tile_kernel(const 
         uint32_t block = 0;
         bool ok = true;
         for (int round = 0; round * (int)gridDim.x < items && ok; ++round) {
-            const int item = round_item(round);
-            if (item >= items) continue;
-            const TileItem t = tile_item<D>(a, s_items, item);
+            if (round_item(round) >= items) break;
+            TileItem t;
+            if (plane == 0) {
+                if (!take_item(round, t)) break;
+            } else {
+                if (!warp_wait(&bar.item_empty[round & 1], ((uint32_t)round >> 1 & 1u) ^ 1u, wait, kSiteKvLoad)) break;
+                t = tile_item<D>(a, s_items, round_item(round));
+                if (lane == 0) {
+                    s_item[round & 1] = t;
+                    mbar_arrive(&bar.item_full[round & 1]);
+                }
+                __syncwarp();
+            }
             if (t.steps == 0) continue;
             // 32 pages of the item and the next 32, one of each a lane: their numbers (-1 where there is
             // none) and scales, so that no step waits for a look-up
@@ -1484,81 +1513,77 @@ __global__ void __launch_bounds__(Tile<D>::kThreadsAll, 1) kv_tile_kernel(const 
         for (uint32_t k = block > depth ? block - depth : 0; k < block; ++k)
             warp_wait(&bar.raw_full[plane][plane ? stage_of<T::kRawV>(k) : stage_of<T::kRawK>(k)],
                       plane ? parity_of<T::kRawV>(k) : parity_of<T::kRawK>(k), wait, kSiteDrain);
-      } else if (warp == T::kMmaWarp) {
-        // ---------------------------------------------------------- products
+      } else if (warp < T::kMmaWarp + T::kQ) {
+        // ---------------------------------------------------------- products of row tile q
+        const int q = warp - T::kMmaWarp;
         const uint32_t is = idesc_f32acc(0, 0, 128, T::kStep);
         const uint32_t io = idesc_f32acc(0, 0, 128, D) | (1u << 16);    // bit 16: the right-hand operand is MN-major
-        const uint64_t dq = sdesc_sw128(smem_u32(smem + T::kSmemQ)), dk = sdesc_sw128(smem_u32(smem + T::kSmemK));
+        const uint64_t dq = sdesc_sw128(smem_u32(smem + T::kSmemQ + q * T::kQuery)), dk = sdesc_sw128(smem_u32(smem + T::kSmemK));
         const uint64_t dv = sdesc_values(smem_u32(smem + T::kSmemV), T::kChunkV);      // offsets add to the address field
-        uint32_t nk = 0, nv = 0, nq[2] = {0, 0}, ns[2] = {0, 0}, npv[2] = {0, 0};
+        const uint32_t to = tmem + T::kTmemO + (uint32_t)(q * 128);
+        uint32_t nk = 0, nv = 0, nq = 0, ns = 0, npv = 0;
         bool ok = !a.force_timeout || warp_wait(&bar.never, 0, wait, kSiteKvMma);
         for (int round = 0; round * (int)gridDim.x < items && ok; ++round) {
-            const int item = round_item(round);
-            if (item >= items) continue;
-            const TileItem t = tile_item<D>(a, s_items, item);
-            const int tiles = T::kQ == 2 && t.rn > 128 ? 2 : 1;
-            const auto issue_s = [&](int q, int s) -> bool {      // S of step s
+            if (round_item(round) >= items) break;
+            TileItem t;
+            if (!take_item(round, t)) break;
+            const bool here = q * 128 < t.rn;       // a tile without rows only gives its operands back
+            const auto issue_s = [&](int s) -> bool {      // S of step s
                 const int st = stage_of<T::kKStages>(nk);
-                if (s == 0 && !warp_wait(&bar.q_full[q], nq[q]++ & 1u, wait, kSiteKvMma)) return false;
-                // its place is free once the product that read P from there is done
-                if (npv[q] > 0 && !warp_wait(&bar.o_done[slot_of<T>(q, npv[q] - 1)], turn_of<T>(npv[q] - 1), wait, kSiteKvMma))
-                    return false;
-                tc_fence_after();
-                const int slot = slot_of<T>(q, ns[q]);
+                if (!warp_wait(&bar.k_full[st], parity_of<T::kKStages>(nk), wait, kSiteKvMma)) return false;
+                if (here) {
+                    if (s == 0 && !warp_wait(&bar.q_full[q], nq++ & 1u, wait, kSiteKvMma)) return false;
+                    // its place is free once the product that read P from there is done
+                    if (npv > 0 && !warp_wait(&bar.o_done[slot_of<T>(q, npv - 1)], turn_of<T>(npv - 1), wait, kSiteKvMma))
+                        return false;
+                    tc_fence_after();
+                    const int slot = slot_of<T>(q, ns);
 #pragma unroll
-                for (int k = 0; k < D / 16; ++k)
-                    mma_f16_warp(tmem + (uint32_t)(slot * T::kStep),
-                                 dq + (uint32_t)((q * T::kQuery + (k >> 2) * T::kChunkQ + (k & 3) * 32) >> 4),
-                                 dk + (uint32_t)((st * T::kOperand + (k >> 2) * T::kChunkK + (k & 3) * 32) >> 4), is, k > 0);
-                commit_warp(&bar.s_full[slot]);
-                ++ns[q];
+                    for (int k = 0; k < D / 16; ++k)
+                        mma_f16_warp(tmem + (uint32_t)(slot * T::kStep), dq + (uint32_t)(((k >> 2) * T::kChunkQ + (k & 3) * 32) >> 4),
+                                     dk + (uint32_t)((st * T::kOperand + (k >> 2) * T::kChunkK + (k & 3) * 32) >> 4), is, k > 0);
+                    commit_warp(&bar.s_full[slot]);
+                    ++ns;
+                }
+                commit_warp(&bar.k_empty[st]);
+                ++nk;
                 return true;
             };
-            const auto issue_o = [&](int q, int s) -> bool {      // O += P V of step s
-                const int slot = slot_of<T>(q, npv[q]);
-                if (!warp_wait(&bar.p_full[slot], turn_of<T>(npv[q]), wait, kSiteKvMma)) return false;
-                tc_fence_after();
+            const auto issue_o = [&](int s) -> bool {      // O += P V of step s
+                const int slot = slot_of<T>(q, npv);
+                if (here && !warp_wait(&bar.p_full[slot], turn_of<T>(npv), wait, kSiteKvMma)) return false;
 #pragma unroll
-                for (int h = 0; h < T::kSub; ++h) {
-                    const int st = stage_of<T::kVBlocks>(nv + h);
-                    if (q == 0 && !warp_wait(&bar.v_full[st], parity_of<T::kVBlocks>(nv + h), wait, kSiteKvMma)) return false;
+                for (int h = 0; h < T::kSub; ++h, ++nv) {
+                    const int st = stage_of<T::kVBlocks>(nv);
+                    if (!warp_wait(&bar.v_full[st], parity_of<T::kVBlocks>(nv), wait, kSiteKvMma)) return false;
                     tc_fence_after();
+                    if (here) {
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        const int k = h * 4 + j;
-                        mma_f16_tmem(tmem + T::kTmemO + (uint32_t)(q * 128),
-                                     tmem + (uint32_t)(slot * T::kStep + k * 16 / T::kCols * T::kCols + k * 16 % T::kCols / 2),
-                                     dv + (uint32_t)((st * T::kBlockV + j * 2048) >> 4), io, s > 0 || k > 0);
+                        for (int j = 0; j < 4; ++j) {
+                            const int k = h * 4 + j;
+                            mma_f16_tmem(to, tmem + (uint32_t)(slot * T::kStep + k * 16 / T::kCols * T::kCols + k * 16 % T::kCols / 2),
+                                         dv + (uint32_t)((st * T::kBlockV + j * 2048) >> 4), io, s > 0 || k > 0);
+                        }
                     }
-                    if (q == tiles - 1) commit_warp(&bar.v_empty[st]);
+                    commit_warp(&bar.v_empty[st]);
                 }
-                commit_warp(&bar.o_done[slot]);
-                ++npv[q];
+                if (here) {
+                    commit_warp(&bar.o_done[slot]);
+                    ++npv;
+                }
                 return true;
             };
             for (int s = 0; s <= t.steps && t.steps > 0 && ok; ++s) {
                 const bool has_s = s < t.steps, has_o = s > 0;
-                const auto keys = [&]() -> bool {
-                    return warp_wait(&bar.k_full[stage_of<T::kKStages>(nk)], parity_of<T::kKStages>(nk), wait, kSiteKvMma);
-                };
                 // with two places the step's S goes ahead of the last step's O
-                if (T::kSlots == 2 && has_s) ok = keys() && issue_s(0, s);
-                if (T::kSlots == 2 && has_s) commit_warp(&bar.k_empty[stage_of<T::kKStages>(nk)]);
-#pragma unroll
-                for (int q = 0; q < T::kQ; ++q) {
-                    if (q >= tiles) break;
-                    if (has_o) ok = ok && issue_o(q, s - 1);
-                    if (T::kSlots == 1 && has_s) ok = ok && (q > 0 || keys()) && issue_s(q, s);
-                }
-                if (!ok) break;
-                if (T::kSlots == 1 && has_s) commit_warp(&bar.k_empty[stage_of<T::kKStages>(nk)]);
-                nk += has_s;
-                if (has_o) nv += T::kSub;
+                if (T::kSlots == 2 && has_s) ok = issue_s(s);
+                if (has_o) ok = ok && issue_o(s - 1);
+                if (T::kSlots == 1 && has_s) ok = ok && issue_s(s);
             }
         }
         // nothing is in flight when tensor memory is given back
-        commit_warp(&bar.drain);
-        warp_wait(&bar.drain, 0, wait, kSiteDrain);
+        commit_warp(&bar.drain[q]);
+        warp_wait(&bar.drain[q], 0, wait, kSiteDrain);
       }
       __syncwarp();
     }
