@@ -711,7 +711,7 @@ struct Tile {
     // Operands: two steps of keys; blocks of values, which the products take one by one: with more than
     // a step's, the next step's first block is there before this step's are done with.
     static constexpr int kKStages = 2, kVBlocks = D == 64 ? 4 : D == 128 ? 3 : 1;
-    static constexpr int kRawK = D == 64 ? 4 : D == 128 ? 2 : 1, kRawV = D == 64 ? 4 : D == 128 ? 3 : 2;   // blocks of codes on their way
+    static constexpr int kRawK = D == 64 ? 4 : 2, kRawV = D == 64 ? 4 : D == 128 ? 3 : 1;   // blocks of codes on their way
     static constexpr int kCols = kStep * kQ / 2;             // columns of S that a softmax thread has
     static constexpr int kOutCols = kQ == 2 ? D : D / 2;     // and of O
     // 20 warps of 96 registers in whole warpgroups: eight of softmax (four for each row tile, or eight
@@ -871,7 +871,7 @@ __device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t parity, const 
 }
 
 struct TileBars {
-    uint64_t q_full[2], k_full[2], k_empty[2], v_full[4], v_empty[4], s_full[2], p_full[2], o_done[2];
+    uint64_t q_full[2], k_full[2], k_empty[2], v_full[4], v_empty[4], s_full[2], p_half[2], p_full[2], o_done[2];
     uint64_t raw_full[2][4], raw_empty[2][4];      // of keys and of values
     uint64_t pair[4], never, drain[2], item_full[2], item_empty[2];
 };
@@ -936,6 +936,7 @@ __global__ void __launch_bounds__(Tile<D>::kThreadsAll, 1) kv_tile_kernel(const 
         for (int i = 0; i < 2; ++i) {
             mbar_init(&bar.q_full[i], 8 / T::kQ);
             mbar_init(&bar.p_full[i], 8 / T::kQ);
+            mbar_init(&bar.p_half[i], 8 / T::kQ);
             mbar_init(&bar.k_full[i], T::kConvWarps);
             mbar_init(&bar.k_empty[i], T::kQ);
             mbar_init(&bar.drain[i], 1);
@@ -1035,12 +1036,12 @@ __global__ void __launch_bounds__(Tile<D>::kThreadsAll, 1) kv_tile_kernel(const 
                 constexpr int LPR = D / 16, RPI = 32 / LPR;              // lanes of a row, rows at a time
                 constexpr int WROWS = 32 * T::kQ / 2, ITER = WROWS / RPI;
                 const int lr = lane / LPR, lu = lane % LPR, base = quad * 32 + half * WROWS + lr;
-                // the loads of four rounds at a time
+                constexpr int AHEAD = ITER < 8 ? ITER : 8;      // rounds whose loads are on their way at a time
 #pragma unroll 1
-                for (int k0 = 0; k0 < ITER; k0 += 4) {
-                    uint4 v[4][2];
+                for (int k0 = 0; k0 < ITER; k0 += AHEAD) {
+                    uint4 v[AHEAD][2];
 #pragma unroll
-                    for (int k = 0; k < 4; ++k) {
+                    for (int k = 0; k < AHEAD; ++k) {
                         const int x = g0 + min(base + (k0 + k) * RPI, mine - 1), qi = by.div(x);
                         const uint16_t *src = a.q + (int64_t)(t.row0 + i0 + qi) * a.ldq +
                                               (int64_t)(t.head * a.group + x - qi * a.group) * a.ldq_head + lu * 8;
@@ -1048,7 +1049,7 @@ __global__ void __launch_bounds__(Tile<D>::kThreadsAll, 1) kv_tile_kernel(const 
                         v[k][1] = *reinterpret_cast<const uint4 *>(src + LPR * 8);
                     }
 #pragma unroll
-                    for (int k = 0; k < 4; ++k) {
+                    for (int k = 0; k < AHEAD; ++k) {
                         const int rr = base + (k0 + k) * RPI;
                         uint32_t w[8] = {v[k][0].x, v[k][0].y, v[k][0].z, v[k][0].w, v[k][1].x, v[k][1].y, v[k][1].z, v[k][1].w};
                         uint32_t top = 0;
@@ -1210,6 +1211,13 @@ __global__ void __launch_bounds__(Tile<D>::kThreadsAll, 1) kv_tile_kernel(const 
                     }
                     tmem_st16(ts + (uint32_t)(c / 2), o);
                 };
+                // the product starts when the first of two blocks is there
+                const auto half_done = [&]() {
+                    tmem_st_wait();
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&bar.p_half[slot]);
+                };
                 if (whole) {
 #pragma unroll
                     for (int c = 0; c < T::kCols; c += 64) {
@@ -1220,10 +1228,12 @@ __global__ void __launch_bounds__(Tile<D>::kThreadsAll, 1) kv_tile_kernel(const 
                         }
                         weights(va, c);
                         if constexpr (T::kCols >= 64) weights(vb, c + 32);
+                        if (T::kCols > 64 && c == 0) half_done();
                     }
                 } else {
 #pragma unroll 1
                     for (int c = 0; c < T::kCols; c += 32) {
+                        if (T::kCols > 64 && c == 64) half_done();
                         if (c + 32 <= least && !zeros) {      // seen by every row of the warp
                             tmem_ld32(ts + (uint32_t)c, va);
                             tmem_ld_wait();
@@ -1551,9 +1561,10 @@ __global__ void __launch_bounds__(Tile<D>::kThreadsAll, 1) kv_tile_kernel(const 
             };
             const auto issue_o = [&](int s) -> bool {      // O += P V of step s
                 const int slot = slot_of<T>(q, npv);
-                if (here && !warp_wait(&bar.p_full[slot], turn_of<T>(npv), wait, kSiteKvMma)) return false;
 #pragma unroll
                 for (int h = 0; h < T::kSub; ++h, ++nv) {
+                    if (here && !warp_wait(h < T::kSub - 1 ? &bar.p_half[slot] : &bar.p_full[slot], turn_of<T>(npv), wait, kSiteKvMma))
+                        return false;
                     const int st = stage_of<T::kVBlocks>(nv);
                     if (!warp_wait(&bar.v_full[st], parity_of<T::kVBlocks>(nv), wait, kSiteKvMma)) return false;
                     tc_fence_after();
