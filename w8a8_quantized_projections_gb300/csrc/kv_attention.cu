@@ -1357,7 +1357,7 @@ __global__ void __launch_bounds__(Tile<D>::kThreadsAll, 1) kv_tile_kernel(const 
         const bool values = warp >= T::kSoftWarps + T::kConvWarps;
         const int ct = (tid - T::kSoftWarps * 32) % (T::kConvWarps * 32);
         constexpr int PIECES = D / 16, N = 64 * PIECES / (T::kConvWarps * 32);   // 16-byte pieces of a row; of a thread and block
-        constexpr int AT_ONCE = N < 4 ? N : 4;
+        constexpr int AT_ONCE = 2;
         const int crow = ct / PIECES, piece = ct % PIECES;
         // a piece becomes two 16-byte units of a row
         const int chunk = piece >> 2, unit = (piece & 3) * 2, swap = (chunk & 1) * 16;
