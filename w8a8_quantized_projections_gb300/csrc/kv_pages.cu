@@ -71,30 +71,44 @@ __device__ __forceinline__ uint32_t page_bits(const int32_t *refs, int p0, int p
     return m;
 }
 
-// Whether the pool has `need` free pages (need <= pages), and, with an
-// offsets array, hands the r-th lowest to give(r, page) for every r < need.
-__device__ __forceinline__ bool has_free(const int32_t *refs, int pages, int need, int *warps) {
-    int found = 0;
-    for (int p = 0; p < pages && found < need; p += kBook * kPer) {
-        int all;
-        block_scan(__popc(page_bits(refs, p + (int)threadIdx.x * kPer, pages, false)), warps, &all);
-        found += all;
-    }
-    return found >= need;
-}
+// The free pages of the first round (the whole pool, up to 16,384 pages): read
+// beside a call's other arguments, they save two trips to memory of the three
+// that follow one another.
+struct FreePages {
+    const int32_t *refs;
+    int pages;
+    uint32_t first;      // this thread's bits
+    int at, all;         // free pages before them, and of the round
 
-template <typename Give>
-__device__ __forceinline__ void give_free(const int32_t *refs, int pages, int need, int *warps, Give give) {
-    int found = 0;
-    for (int p = 0; p < pages && found < need; p += kBook * kPer) {
-        const int p0 = p + (int)threadIdx.x * kPer;
-        uint32_t m = page_bits(refs, p0, pages, false);
-        int all;
-        int r = found + block_scan(__popc(m), warps, &all);
-        for (; m && r < need; m &= m - 1, ++r) give(r, p0 + __ffs(m) - 1);
-        found += all;
+    __device__ __forceinline__ FreePages(const int32_t *refs, int pages)
+        : refs(refs), pages(pages), first(page_bits(refs, (int)threadIdx.x * kPer, pages, false)) {}
+
+    // Whether there are `need` (need <= pages).
+    __device__ __forceinline__ bool have(int need, int *warps) {
+        at = block_scan(__popc(first), warps, &all);
+        int found = all;
+        for (int p = kBook * kPer; p < pages && found < need; p += kBook * kPer) {
+            int more;
+            block_scan(__popc(page_bits(refs, p + (int)threadIdx.x * kPer, pages, false)), warps, &more);
+            found += more;
+        }
+        return found >= need;
     }
-}
+
+    // After have(): hands the r-th lowest to give(r, page) for every r < need.
+    template <typename Give>
+    __device__ __forceinline__ void hand_out(int need, int *warps, Give give) {
+        int found = 0;
+        for (int p = 0; p < pages && found < need; p += kBook * kPer) {
+            const int p0 = p + (int)threadIdx.x * kPer;
+            uint32_t m = p == 0 ? first : page_bits(refs, p0, pages, false);
+            int more = all, r = at;
+            if (p > 0) r = found + block_scan(__popc(m), warps, &more);
+            for (; m && r < need; m &= m - 1, ++r) give(r, p0 + __ffs(m) - 1);
+            found += more;
+        }
+    }
+};
 
 // The asker of allocation r: the last i with off[i] <= r (off is the
 // exclusive prefix sum of the needs, so askers of nothing are skipped).
@@ -127,6 +141,7 @@ __global__ void __launch_bounds__(kBook) kv_reserve_kernel(const BookArgs a, con
     __shared__ int warps[32];
     pdl_wait();
     const int tid = threadIdx.x;
+    FreePages free_pages(a.refs, a.pages);
     int64_t need = 0;
     int bad = 0;
     for (int b0 = 0; b0 < a.seqs; b0 += kBook) {
@@ -144,12 +159,12 @@ __global__ void __launch_bounds__(kBook) kv_reserve_kernel(const BookArgs a, con
     }
     if (tid == 0) off[a.seqs] = (int)min((int64_t)0x7FFFFFFF, need);
     bad = __syncthreads_or(bad);
-    const bool fits = !bad && need <= a.pages && has_free(a.refs, a.pages, (int)need, warps);
+    const bool fits = !bad && need <= a.pages && free_pages.have((int)need, warps);
     if (!fits) {
         if (tid == 0) record_status(a.status, bad ? kStatusBadPage : kStatusNoPages);
     } else {
         if (need > 0)
-            give_free(a.refs, a.pages, (int)need, warps, [&](int r, int p) {
+            free_pages.hand_out((int)need, warps, [&](int r, int p) {
                 const int b = asker(off, a.seqs, r);
                 a.table[(int64_t)b * a.ldt + pages_of(a.lens[b], a.page_log2) + (r - off[b])] = p;
                 a.refs[p] = 1;
@@ -170,6 +185,7 @@ __global__ void __launch_bounds__(kBook) kv_fork_kernel(const BookArgs a, const 
     uint32_t *seen = reinterpret_cast<uint32_t *>(off + n + 1);
     pdl_wait();
     const int tid = threadIdx.x;
+    FreePages free_pages(a.refs, a.pages);
     for (int i = tid; i < (a.seqs + 31) / 32; i += kBook) seen[i] = 0;
     __syncthreads();
     const int in_page = (1 << a.page_log2) - 1;
@@ -205,12 +221,12 @@ __global__ void __launch_bounds__(kBook) kv_fork_kernel(const BookArgs a, const 
                 if (p < 0 || p >= a.pages) bad = 1;
             }
     bad = __syncthreads_or(bad);
-    const bool fits = !bad && need <= a.pages && has_free(a.refs, a.pages, need, warps);
+    const bool fits = !bad && need <= a.pages && free_pages.have(need, warps);
     if (!fits) {
         if (tid == 0) record_status(a.status, bad ? kStatusBadPage : kStatusNoPages);
     } else {
         if (need > 0)
-            give_free(a.refs, a.pages, need, warps, [&](int r, int p) {
+            free_pages.hand_out(need, warps, [&](int r, int p) {
                 const int i = asker(off, n, r), last = a.lens[src[i]] >> a.page_log2;
                 from[i] = a.table[(int64_t)src[i] * a.ldt + last];
                 to[i] = p;
