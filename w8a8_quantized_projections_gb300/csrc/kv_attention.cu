@@ -225,7 +225,7 @@ struct SplitPrep {
     uint16_t q[kRows * kPitch];
     float qs[kRows], lift[kRows];               // what S is multiplied by, after lift is taken off it
     int end[kRows];                             // tokens a row sees
-    int page[kPages];
+    int64_t at[kPages];                         // a page's first code of the head; -1: not there
     float ks[kPages], lv[kPages], inv[kPages];  // key scale; log2 of the value scale; its reciprocal (0: no weight)
 };
 
@@ -249,7 +249,7 @@ struct SplitItem {
 // A warp's registers hold a step of keys and one of values; each is loaded
 // again, for the next step, as soon as its products are done.
 template <int D, int NT>
-__host__ __device__ constexpr int split_ctas() { return D * NT <= 64 ? 4 : D * NT <= 128 ? 3 : 2; }     // of an SM, by registers
+__host__ __device__ constexpr int split_ctas() { return D * NT <= 64 ? 4 : D * NT <= 128 || NT == 1 ? 3 : 2; }     // of an SM, by registers
 
 template <int KIND, int D, int NT>
 __global__ void __launch_bounds__(kThreads, split_ctas<D, NT>()) kv_split_kernel(const AttnArgs a) {
@@ -401,7 +401,7 @@ __global__ void __launch_bounds__(kThreads, split_ctas<D, NT>()) kv_split_kernel
         if (tid < Prep::kPages) {
             // a page whose value scale is zero counts in the sum with a small scale, and gives no weight
             const float vs = p_vs == 0.0f ? 0x1p-60f : p_vs;
-            to.page[tid] = p_page;
+            to.at[tid] = p_page < 0 ? -1 : (((int64_t)p_page * H + it.head) << log2) * D;
             to.ks[tid] = p_ks;
             to.lv[tid] = log2f(vs);
             to.inv[tid] = p_vs == 0.0f ? -0x1p60f : __fdiv_rn(1.0f, vs);      // the sign marks it
@@ -410,45 +410,69 @@ __global__ void __launch_bounds__(kThreads, split_ctas<D, NT>()) kv_split_kernel
 
     uint4 kc[TILES][2][KB];
     uint32_t vc[TILES][4][VW];
+    // (a step whose tokens are all there, the usual one, without a test or a zero at each load)
+    const auto page_at = [&](const SplitItem &it, const Prep &pr, int tk) {
+        return tk < it.tok1 ? pr.at[(tk - it.tok0) >> log2] : (int64_t)-1;
+    };
     const auto load_k = [&](const SplitItem &it, const Prep &pr, int s0) {
+        int64_t at[TILES];
+        bool there = true;
 #pragma unroll
         for (int u = 0; u < TILES; ++u) {
-            const int tk = s0 + u * 16, page = tk < it.tok1 ? pr.page[(tk - it.tok0) >> log2] : -1;
-            const uint8_t *base = a.pool.codes + ((((int64_t)page * H + it.head) << log2) + (tk & (a.pool.page - 1)) + g) * D + t * 16;
-#pragma unroll
-            for (int h = 0; h < 2; ++h)
-#pragma unroll
-                for (int k = 0; k < KB; ++k)
-                    kc[u][h][k] = page >= 0 ? load_codes(base + h * 8 * D + k * 64) : make_uint4(0, 0, 0, 0);
+            at[u] = page_at(it, pr, s0 + u * 16);
+            there = there && at[u] >= 0;
         }
+        const auto load = [&](auto all) {
+#pragma unroll
+            for (int u = 0; u < TILES; ++u) {
+                const uint8_t *base = a.pool.codes + at[u] + (((s0 + u * 16) & (a.pool.page - 1)) + g) * D + t * 16;
+#pragma unroll
+                for (int h = 0; h < 2; ++h)
+#pragma unroll
+                    for (int k = 0; k < KB; ++k)
+                        kc[u][h][k] = decltype(all)::value || at[u] >= 0 ? load_codes(base + h * 8 * D + k * 64) : make_uint4(0, 0, 0, 0);
+            }
+        };
+        if (there) load(std::true_type());
+        else load(std::false_type());
     };
     const auto load_v = [&](const SplitItem &it, const Prep &pr, int s0) {
+        int64_t at[TILES];
+        bool there = s0 + STEP <= it.len;
 #pragma unroll
         for (int u = 0; u < TILES; ++u) {
-            const int tk = s0 + u * 16, page = tk < it.tok1 ? pr.page[(tk - it.tok0) >> log2] : -1;
-            const uint8_t *base = a.pool.codes + a.pool.plane_codes +
-                                  ((((int64_t)page * H + it.head) << log2) + (tk & (a.pool.page - 1)) + 2 * t) * D + g * (D >= 128 ? 16 : 8);
+            at[u] = page_at(it, pr, s0 + u * 16);
+            there = there && at[u] >= 0;
+        }
+        const auto load = [&](auto all) {
 #pragma unroll
-            for (int c = 0; c < 4; ++c) {
-                const int row = (c & 1) + 8 * (c >> 1);
-                // what lies past the sequence's end may be anything, NaN codes included: read as zeros
-                const bool in = page >= 0 && tk + 2 * t + row < it.len;
-                if constexpr (D == 64) {
-                    const uint2 v = in ? load_codes8(base + row * D) : make_uint2(0, 0);
-                    vc[u][c][0] = v.x;
-                    vc[u][c][1] = v.y;
-                } else {
+            for (int u = 0; u < TILES; ++u) {
+                const int tk = s0 + u * 16;
+                const uint8_t *base = a.pool.codes + a.pool.plane_codes + at[u] + ((tk & (a.pool.page - 1)) + 2 * t) * D + g * (D >= 128 ? 16 : 8);
 #pragma unroll
-                    for (int k = 0; k < D / 128; ++k) {
-                        const uint4 v = in ? load_codes(base + row * D + k * 128) : make_uint4(0, 0, 0, 0);
-                        vc[u][c][4 * k] = v.x;
-                        vc[u][c][4 * k + 1] = v.y;
-                        vc[u][c][4 * k + 2] = v.z;
-                        vc[u][c][4 * k + 3] = v.w;
+                for (int c = 0; c < 4; ++c) {
+                    const int row = (c & 1) + 8 * (c >> 1);
+                    // what lies past the sequence's end may be anything, NaN codes included: read as zeros
+                    const bool in = decltype(all)::value || (at[u] >= 0 && tk + 2 * t + row < it.len);
+                    if constexpr (D == 64) {
+                        const uint2 v = in ? load_codes8(base + row * D) : make_uint2(0, 0);
+                        vc[u][c][0] = v.x;
+                        vc[u][c][1] = v.y;
+                    } else {
+#pragma unroll
+                        for (int k = 0; k < D / 128; ++k) {
+                            const uint4 v = in ? load_codes(base + row * D + k * 128) : make_uint4(0, 0, 0, 0);
+                            vc[u][c][4 * k] = v.x;
+                            vc[u][c][4 * k + 1] = v.y;
+                            vc[u][c][4 * k + 2] = v.z;
+                            vc[u][c][4 * k + 3] = v.w;
+                        }
                     }
                 }
             }
-        }
+        };
+        if (there) load(std::true_type());
+        else load(std::false_type());
     };
 
     SplitItem it = item_at(blockIdx.x);
