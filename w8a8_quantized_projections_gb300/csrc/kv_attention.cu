@@ -55,9 +55,13 @@ constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLift = 15.0f;     // the largest weight of P is 2^kLift
 
 // Tokens of a split of a sequence of `len` tokens: short enough that one
-// sequence spreads over the SMs, long enough that the partial results (4 B
-// written and read a value and split, against 1 B a code) stay a small part of the traffic.
-__host__ __device__ inline int split_tokens(int len) { return len <= 1024 ? 128 : len <= 2048 ? 256 : len <= 8192 ? 512 : 1024; }
+// sequence spreads over the SMs, long enough that an item's own work (finding
+// it, its queries, joining the warps' sums: as much as 90 tokens) and its
+// partial results stay a small part.  One sequence of 1,024 tokens takes 7.7,
+// 8.7 or 11 us in splits of 128, 256 or 512, of 2,000 tokens 8.9 or 11.2 us in
+// splits of 256 or 512; 16 of 1,000 take 17.3, 15.3 or 13.6 us, 128 of 1,000 to
+// 1,500 take 96 or 82 us (8 heads of 128, int8).
+__host__ __device__ inline int split_tokens(int len) { return len <= 512 ? 512 : len <= 1024 ? 256 : len <= 8192 ? 512 : 1024; }
 __host__ __device__ inline int split_count(int len) {
     const int t = split_tokens(len);
     return len / t + (len % t != 0);
@@ -1726,7 +1730,7 @@ Plan make_plan(int64_t rows, bool ragged, int64_t seqs, int group, int heads, in
     if (rows == 0 || seqs == 0) return p;
     // a shorter sequence may be cut into more runs than the longest: the cut grows in steps
     int few_splits = 1;
-    for (int64_t len : {max_len, (int64_t)1024, (int64_t)2048, (int64_t)8192})
+    for (int64_t len : {max_len, (int64_t)1024, (int64_t)8192})
         if (len <= max_len && split_count((int)len) > few_splits) few_splits = split_count((int)len);
     const int64_t per = ragged ? rows * group : rows / seqs * group;   // rows of one sequence, at most
     p.few = ragged || per <= kFewRows;
