@@ -208,40 +208,65 @@ struct GatherArgs {
     unsigned int *status;
 };
 
-// bf16(code * scale) of given tokens: 8 codes in, 16 bytes out per thread.
+// bf16(code * scale) of given tokens: 8 codes in, 16 bytes out per thread and
+// vector, four vectors on their way at a time.  A CTA takes kGatherVecs vectors
+// (a row, at least) at a time and looks the pages of its rows up once.  Bound by
+// the 3 bytes an element that move: 26 us for 24,032 rows of 8 heads of 128, keys
+// and values (148 MB, 5.6 TB/s).
+constexpr int kGatherVecs = 2048;
+
 template <int KIND>
-__global__ void __launch_bounds__(kThreads) kv_gather_kernel(const GatherArgs a) {
-    const int vecs = a.pool.dim >> 3, per_row = a.pool.heads * vecs, log2 = a.pool.page_log2;
-    const int plane = blockIdx.y;
+__global__ void __launch_bounds__(kThreads) kv_gather_kernel(const GatherArgs a, int rows_at_once, uint32_t per_row_mul) {
+    __shared__ int64_t s_code[kThreads];     // a row's first code of head 0, -1: not there
+    __shared__ int s_tile[kThreads];         // its page's first scale
+    const int log2 = a.pool.page_log2, plane = blockIdx.y, vec_log2 = __ffs(a.pool.dim) - 4, per_row = a.pool.heads << vec_log2;
+    const uint8_t *codes = a.pool.codes + plane * a.pool.plane_codes;
+    const float *scales = a.pool.scales + plane * a.pool.plane_scales;
+    const int64_t head_codes = (int64_t)a.pool.dim << log2, step = (int64_t)gridDim.x * rows_at_once;
     pdl_wait();
-    const int64_t total = a.rows * per_row, stride = (int64_t)gridDim.x * kThreads;
-    for (int64_t i = blockIdx.x * (int64_t)kThreads + threadIdx.x; i < total; i += stride) {
-        const int64_t row = i / per_row;
-        const int rest = (int)(i - row * per_row), head = rest / vecs, c = rest - head * vecs;
-        const int b = *(a.seq + row), p = *(a.pos + row);
-        uint4 o = make_uint4(0, 0, 0, 0);
-        int page = -1;
-        if (b >= 0 && b < a.tab.seqs && p >= 0 && (p >> log2) < a.tab.width)
-            page = *(a.tab.table + (int64_t)b * a.tab.ldt + (p >> log2));
-        if (page >= 0 && page < a.pool.pages) {
-            const int64_t tile = (int64_t)page * a.pool.heads + head;
-            const float s = a.pool.scales[plane * a.pool.plane_scales + tile];
-            const uint2 q = *reinterpret_cast<const uint2 *>(
-                a.pool.codes + plane * a.pool.plane_codes +
-                ((tile << log2) + (p & (a.pool.page - 1))) * a.pool.dim + c * 8);
-            const uint32_t w[4] = {q.x & 0xFFFFu, q.x >> 16, q.y & 0xFFFFu, q.y >> 16};
-            uint32_t r[4];
+    for (int64_t row0 = (int64_t)blockIdx.x * rows_at_once; row0 < a.rows; row0 += step) {
+        const int n = (int)min((int64_t)rows_at_once, a.rows - row0);
+        if ((int)threadIdx.x < n) {
+            const int b = a.seq[row0 + threadIdx.x], p = a.pos[row0 + threadIdx.x];
+            int page = -1;
+            if (b >= 0 && b < a.tab.seqs && p >= 0 && (p >> log2) < a.tab.width) page = a.tab.table[(int64_t)b * a.tab.ldt + (p >> log2)];
+            const bool there = page >= 0 && page < a.pool.pages;
+            if (!there) record_status(a.status, kStatusBadPage);
+            s_tile[threadIdx.x] = there ? page : 0;
+            s_code[threadIdx.x] = there ? (int64_t)page * a.pool.heads * head_codes + (int64_t)(p & (a.pool.page - 1)) * a.pool.dim : -1;
+        }
+        __syncthreads();
+        for (int u0 = threadIdx.x; u0 < n * per_row; u0 += 4 * kThreads) {
+            uint2 q[4];
+            float s[4];
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
-                const float2 f = kv_decode2<KIND>(w[k]);
-                const __nv_bfloat162 h = __floats2bfloat162_rn(__fmul_rn(f.x, s), __fmul_rn(f.y, s));
-                r[k] = *reinterpret_cast<const uint32_t *>(&h);
+                const int u = min(u0 + k * kThreads, n * per_row - 1), r = (int)__umulhi((uint32_t)u, per_row_mul), rest = u - r * per_row;
+                const int head = rest >> vec_log2;
+                const int64_t at = s_code[r];
+                q[k] = make_uint2(0, 0);
+                s[k] = 0.0f;
+                if (at >= 0) {
+                    q[k] = *reinterpret_cast<const uint2 *>(codes + at + head * head_codes + ((rest & ((1 << vec_log2) - 1)) << 3));
+                    s[k] = scales[(int64_t)s_tile[r] * a.pool.heads + head];
+                }
             }
-            o = make_uint4(r[0], r[1], r[2], r[3]);
-        } else {
-            record_status(a.status, kStatusBadPage);
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                const int u = u0 + k * kThreads, r = (int)__umulhi((uint32_t)u, per_row_mul), rest = u - r * per_row;
+                if (u >= n * per_row) break;
+                const uint32_t w[4] = {q[k].x & 0xFFFFu, q[k].x >> 16, q[k].y & 0xFFFFu, q[k].y >> 16};
+                uint32_t o[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const float2 f = kv_decode2<KIND>(w[i]);
+                    const __nv_bfloat162 h = __floats2bfloat162_rn(__fmul_rn(f.x, s[k]), __fmul_rn(f.y, s[k]));
+                    o[i] = *reinterpret_cast<const uint32_t *>(&h);
+                }
+                *reinterpret_cast<uint4 *>(a.out[plane] + (row0 + r) * a.ld[plane] + rest * 8) = make_uint4(o[0], o[1], o[2], o[3]);
+            }
         }
-        *reinterpret_cast<uint4 *>(a.out[plane] + row * a.ld[plane] + rest * 8) = o;
+        __syncthreads();      // before the next rows' places
     }
     pdl_launch_dependents();
 }
@@ -316,10 +341,15 @@ extern "C" int clef_kv_gather(int kind, const void *codes, int64_t plane_bytes, 
     a.out[1] = static_cast<uint16_t *>(v_out);
     a.ld[0] = ldk;
     a.ld[1] = ldv;
-    int64_t blocks = (rows * (row / 8) + kThreads - 1) / kThreads;
-    if (blocks > (int64_t)sms * 16) blocks = (int64_t)sms * 16;
+    // fewer rows at a time where they would not reach every SM
+    const int per_row = (int)(row / 8);
+    int64_t at_once = kGatherVecs / per_row;
+    if (at_once > (rows + sms - 1) / sms) at_once = (rows + sms - 1) / sms;
+    at_once = at_once < 1 ? 1 : at_once > kThreads ? kThreads : at_once;
+    int64_t blocks = (rows + at_once - 1) / at_once;
+    if (blocks > (int64_t)sms * 8) blocks = (int64_t)sms * 8;
     const cudaError_t e = launch_kernel(kind == kKvInt8 ? kv_gather_kernel<kKvInt8> : kv_gather_kernel<kKvE4m3>,
-                                        dim3((unsigned)blocks, 2), dim3(kThreads), 0,
-                                        static_cast<cudaStream_t>(stream), 1, true, a);
+                                        dim3((unsigned)blocks, 2), dim3(kThreads), 0, static_cast<cudaStream_t>(stream), 1, true,
+                                        a, (int)at_once, 0xFFFFFFFFu / (uint32_t)per_row + 1u);
     return e == cudaSuccess ? CLEF_OK : internal_cuda_error(e, "cache gather launch");
 }
