@@ -117,9 +117,15 @@ struct W4Args {
 // of K, so a row of y has the same bits whatever M, S and the grid are.
 //
 // A warp streams its part of 16 rows through a ring of its own in shared memory,
-// kDepth blocks ahead, across the tiles: the copies never wait for a sum, and each
-// lane reads back the 16 bytes it copied itself.  x's columns of the CTA's parts
+// kDepth stages ahead, across the tiles: the copies never wait for a sum.  x's columns of the CTA's parts
 // are read once into shared memory; S is as large as it takes to fit them.
+//
+// Measured (K x N, us a call back to back, weights from memory): one row 5120 x
+// 34816 in groups of 64, 19.8 us, 4.8 TB/s, of which 6 us before the first
+// product (the launch, x to fp16); 6144 x 5120 in groups of 128, 6.8 us.  13 rows
+// of 17408 x 5120 in groups of 32, 32 us: 9 us before the first product, then
+// three rounds of tiles (2.2 would do), each as long as mma.sync and the reads of x
+// from shared memory take.
 template <int NT, int GROUP>
 __global__ void __launch_bounds__(kWarps * 32, NT == 1 ? 2 : 1) w4_linear_kernel(const W4Args a) {
     extern __shared__ __align__(16) uint8_t smem[];
