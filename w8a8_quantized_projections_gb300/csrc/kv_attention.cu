@@ -1790,9 +1790,9 @@ cudaError_t launch_attention(const AttnArgs &a, int kind, const Plan &p, int sms
                                 : launch_split<kKvE4m3, D, 2>(a, p.few_items, sms, st);
     }
     if (e != cudaSuccess || p.units == 0) return e;
-    // a CTA a row, up to 16 CTAs an SM over all sequences
+    // a CTA a row, up to 64 CTAs an SM over all sequences
     int64_t x = p.join_rows;
-    const int64_t most = (int64_t)sms * 16 / a.tab.seqs + 1;
+    const int64_t most = (int64_t)sms * 64 / a.tab.seqs + 1;
     if (x > most) x = most;
     return launch_kernel(kv_join_kernel<D>, dim3((unsigned)x, (unsigned)a.tab.seqs), dim3(kThreads), 0, st, 1, true, a);
 }
