@@ -426,7 +426,8 @@ int clef_w4_linear(const void *x, int64_t ldx, const void *qw, const void *sw, i
  *   where s grew, earlier codes become encode(value(code) * fp32(s_old / s));
  *   new codes are encode(v * min(fp32(1 / s), FLT_MAX)), zeros where s = 0.
  * The pages written must belong to one sequence each (clef_kv_reserve and
- * clef_kv_fork see to it).
+ * clef_kv_fork see to it), and k and v must be finite: a page of a head has one
+ * scale, so an infinity or a NaN is felt by the page's other tokens too.
  *
  * clef_kv_gather -- k_out[r], v_out[r] = bf16(code * scale) of token pos[r]
  * of sequence seq[r]; outputs bf16 [rows][heads * dim], pitches ldk, ldv;
