@@ -10,8 +10,8 @@
 // amax the largest magnitude of the call's tokens in that page and head.  A
 // scale of zero (only zeros seen) gives codes of zero.
 //
-// Bound by the rows read (2 bytes an element) and the codes written (1 byte): 31 us
-// for 16 x 1,502 tokens of 8 heads of 128, keys and values (148 MB, 4.7 TB/s).
+// Bound by the rows read (2 bytes an element) and the codes written (1 byte): 26 us
+// for 16 x 1,502 tokens of 8 heads of 128, keys and values (148 MB, 5.6 TB/s).
 // One CTA takes one (touched page, head) of the keys or of the values: the
 // rows stay in registers between the maximum and the codes, so they are read
 // once.
@@ -132,12 +132,12 @@ __global__ void __launch_bounds__(kThreads) kv_append_kernel(const AppendArgs a)
         if (tid == 0) record_status(a.status, kStatusBadPage);
         return;
     }
-    const int head = blockIdx.y, plane = blockIdx.z, D = a.pool.dim, vecs = D >> 3;   // vectors of 8 of a row
+    const int head = blockIdx.y, plane = blockIdx.z, D = a.pool.dim, vec_log2 = __ffs(D) - 4;   // vectors of 8 of a row
     const uint16_t *src = a.src[plane] + (int64_t)(row0 + p0 - first) * a.ld_tok[plane] + (int64_t)head * a.ld_head[plane];
     uint8_t *codes = a.pool.codes + plane * a.pool.plane_codes +
                      (((int64_t)page * a.pool.heads + head) << log2) * D;
     float *scale = a.pool.scales + plane * a.pool.plane_scales + (int64_t)page * a.pool.heads + head;
-    const int total = (p1 - p0) * vecs;
+    const int total = (p1 - p0) << vec_log2;
 
     uint4 v[NV];
     uint32_t top2 = 0;   // the largest magnitudes, as bf16 bits: they order like integers
@@ -146,7 +146,7 @@ __global__ void __launch_bounds__(kThreads) kv_append_kernel(const AppendArgs a)
         const int u = tid + i * kThreads;
         v[i] = make_uint4(0, 0, 0, 0);
         if (u < total) {
-            const int tok = u / vecs, c = u - tok * vecs;
+            const int tok = u >> vec_log2, c = u & ((1 << vec_log2) - 1);
             v[i] = *reinterpret_cast<const uint4 *>(src + (int64_t)tok * a.ld_tok[plane] + c * 8);
         }
     }
@@ -209,53 +209,47 @@ struct GatherArgs {
     unsigned int *status;
 };
 
-// bf16(code * scale) of given tokens: 8 codes in, 16 bytes out per thread and
-// vector, four vectors on their way at a time.  A CTA takes kGatherVecs vectors
-// (a row, at least) at a time and looks the pages of its rows up once.  Bound by
-// the 3 bytes an element that move: 26 us for 24,032 rows of 8 heads of 128, keys
-// and values (148 MB, 5.6 TB/s).
-constexpr int kGatherVecs = 2048;
-
+// bf16(code * scale) of given tokens: 8 codes in, 16 bytes out per lane and
+// vector, four vectors on their way at a time.  2^lanes_log2 lanes, a warp or the
+// part of one that a row fills, take a row, so that its page is looked up and its
+// places are found once.  Bound by the 3 bytes an element that move: 27 us for 24,032 rows of 8
+// heads of 128, keys and values (148 MB, 5.5 TB/s).
 template <int KIND>
-__global__ void __launch_bounds__(kThreads) kv_gather_kernel(const GatherArgs a, int rows_at_once, uint32_t per_row_mul) {
-    __shared__ int64_t s_code[kThreads];     // a row's first code of head 0, -1: not there
-    __shared__ int s_tile[kThreads];         // its page's first scale
+__global__ void __launch_bounds__(kThreads) kv_gather_kernel(const GatherArgs a, int lanes_log2) {
     const int log2 = a.pool.page_log2, plane = blockIdx.y, vec_log2 = __ffs(a.pool.dim) - 4, per_row = a.pool.heads << vec_log2;
-    const uint8_t *codes = a.pool.codes + plane * a.pool.plane_codes;
-    const float *scales = a.pool.scales + plane * a.pool.plane_scales;
-    const int64_t head_codes = (int64_t)a.pool.dim << log2, step = (int64_t)gridDim.x * rows_at_once;
+    const int lanes = 1 << lanes_log2, sub = (int)threadIdx.x & (lanes - 1), in_head = (1 << vec_log2) - 1;
+    const int head_codes = a.pool.dim << log2;
+    const int64_t step = (int64_t)gridDim.x * kThreads >> lanes_log2;
     pdl_wait();
-    for (int64_t row0 = (int64_t)blockIdx.x * rows_at_once; row0 < a.rows; row0 += step) {
-        const int n = (int)min((int64_t)rows_at_once, a.rows - row0);
-        if ((int)threadIdx.x < n) {
-            const int b = a.seq[row0 + threadIdx.x], p = a.pos[row0 + threadIdx.x];
-            int page = -1;
-            if (b >= 0 && b < a.tab.seqs && p >= 0 && (p >> log2) < a.tab.width) page = a.tab.table[(int64_t)b * a.tab.ldt + (p >> log2)];
-            const bool there = page >= 0 && page < a.pool.pages;
-            if (!there) record_status(a.status, kStatusBadPage);
-            s_tile[threadIdx.x] = there ? page : 0;
-            s_code[threadIdx.x] = there ? (int64_t)page * a.pool.heads * head_codes + (int64_t)(p & (a.pool.page - 1)) * a.pool.dim : -1;
+    for (int64_t row = ((int64_t)blockIdx.x * kThreads + threadIdx.x) >> lanes_log2; row < a.rows; row += step) {
+        const int b = a.seq[row], p = a.pos[row];
+        int page = -1;
+        if (b >= 0 && b < a.tab.seqs && p >= 0 && (p >> log2) < a.tab.width) page = a.tab.table[(int64_t)b * a.tab.ldt + (p >> log2)];
+        const bool there = page >= 0 && page < a.pool.pages;
+        if (!there) {
+            record_status(a.status, kStatusBadPage);
+            page = 0;
         }
-        __syncthreads();
-        for (int u0 = threadIdx.x; u0 < n * per_row; u0 += 4 * kThreads) {
+        const float *scales = a.pool.scales + plane * a.pool.plane_scales + (int64_t)page * a.pool.heads;
+        const uint8_t *codes = a.pool.codes + plane * a.pool.plane_codes + (int64_t)page * a.pool.heads * head_codes +
+                               (p & (a.pool.page - 1)) * a.pool.dim;
+        uint16_t *out = a.out[plane] + row * a.ld[plane];
+        for (int v0 = sub; v0 < per_row; v0 += 4 * lanes) {
             uint2 q[4];
             float s[4];
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
-                const int u = min(u0 + k * kThreads, n * per_row - 1), r = (int)__umulhi((uint32_t)u, per_row_mul), rest = u - r * per_row;
-                const int head = rest >> vec_log2;
-                const int64_t at = s_code[r];
+                const int v = v0 + k * lanes, head = v >> vec_log2;
                 q[k] = make_uint2(0, 0);
                 s[k] = 0.0f;
-                if (at >= 0) {
-                    q[k] = *reinterpret_cast<const uint2 *>(codes + at + head * head_codes + ((rest & ((1 << vec_log2) - 1)) << 3));
-                    s[k] = scales[(int64_t)s_tile[r] * a.pool.heads + head];
+                if (there && v < per_row) {
+                    q[k] = *reinterpret_cast<const uint2 *>(codes + (int64_t)head * head_codes + ((v & in_head) << 3));
+                    s[k] = scales[head];
                 }
             }
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
-                const int u = u0 + k * kThreads, r = (int)__umulhi((uint32_t)u, per_row_mul), rest = u - r * per_row;
-                if (u >= n * per_row) break;
+                const int v = v0 + k * lanes;
                 const uint32_t w[4] = {q[k].x & 0xFFFFu, q[k].x >> 16, q[k].y & 0xFFFFu, q[k].y >> 16};
                 uint32_t o[4];
 #pragma unroll
@@ -264,10 +258,9 @@ __global__ void __launch_bounds__(kThreads) kv_gather_kernel(const GatherArgs a,
                     const __nv_bfloat162 h = __floats2bfloat162_rn(__fmul_rn(f.x, s[k]), __fmul_rn(f.y, s[k]));
                     o[i] = *reinterpret_cast<const uint32_t *>(&h);
                 }
-                *reinterpret_cast<uint4 *>(a.out[plane] + (row0 + r) * a.ld[plane] + rest * 8) = make_uint4(o[0], o[1], o[2], o[3]);
+                if (v < per_row) *reinterpret_cast<uint4 *>(out + v * 8) = make_uint4(o[0], o[1], o[2], o[3]);
             }
         }
-        __syncthreads();      // before the next rows' places
     }
     pdl_launch_dependents();
 }
@@ -342,15 +335,12 @@ extern "C" int clef_kv_gather(int kind, const void *codes, int64_t plane_bytes, 
     a.out[1] = static_cast<uint16_t *>(v_out);
     a.ld[0] = ldk;
     a.ld[1] = ldv;
-    // fewer rows at a time where they would not reach every SM
-    const int per_row = (int)(row / 8);
-    int64_t at_once = kGatherVecs / per_row;
-    if (at_once > (rows + sms - 1) / sms) at_once = (rows + sms - 1) / sms;
-    at_once = at_once < 1 ? 1 : at_once > kThreads ? kThreads : at_once;
+    const int per_row = (int)(row / 8), lanes_log2 = per_row >= 32 ? 5 : per_row >= 16 ? 4 : 3;
+    const int64_t at_once = kThreads >> lanes_log2;
     int64_t blocks = (rows + at_once - 1) / at_once;
     if (blocks > (int64_t)sms * 8) blocks = (int64_t)sms * 8;
     const cudaError_t e = launch_kernel(kind == kKvInt8 ? kv_gather_kernel<kKvInt8> : kv_gather_kernel<kKvE4m3>,
                                         dim3((unsigned)blocks, 2), dim3(kThreads), 0, static_cast<cudaStream_t>(stream), 1, true,
-                                        a, (int)at_once, 0xFFFFFFFFu / (uint32_t)per_row + 1u);
+                                        a, lanes_log2);
     return e == cudaSuccess ? CLEF_OK : internal_cuda_error(e, "cache gather launch");
 }
