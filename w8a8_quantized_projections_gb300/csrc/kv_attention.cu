@@ -254,11 +254,11 @@ struct SplitItem {
 // again, for the next step, as soon as its products are done.
 //
 // Measured: 64 sequences of 512 to 8,192 int8 tokens, 8 heads of 128 read by 40
-// query heads: 93 us with the join, 4.1 TB/s; three of 32,768 e4m3 tokens at dim
+// query heads: 92 us with the join, 4.1 TB/s; three of 32,768 e4m3 tokens at dim
 // 256: 46 us, 4.2 TB/s (57 us with two CTAs an SM instead of three, although the
-// third spills a few registers).  Bound by instructions: 47% of the issue slots at
-// three warps a scheduler, about 320 a 16-token tile and as many as six such tiles an
-// item.  One sequence of 298 tokens: 7.4 us, two launches.
+// third spills a few registers).  Bound by the latency of a warp's own chain: 43% of
+// the issue slots at three warps a scheduler, about 320 instructions a 16-token tile
+// and as many as six such tiles an item.  One sequence of 298 tokens: 7.4 us.
 template <int D, int NT>
 __host__ __device__ constexpr int split_ctas() { return D * NT <= 64 ? 4 : D * NT <= 128 || NT == 1 ? 3 : 2; }     // of an SM, by registers
 
