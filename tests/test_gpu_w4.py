@@ -124,3 +124,25 @@ def test_refusals():
     with pytest.raises(clef.ClefError):
         clef.quant_w4(torch.zeros((2, 20), dtype=torch.bfloat16, device="cuda"))                         # K % 8
     assert clef.poll_status() == 0
+
+
+@pytest.mark.parametrize("group", [32, 64, 128])
+@pytest.mark.parametrize("M,N,K", [(13, 5000, 17408), (16, 5120, 17408), (9, 9001, 6144), (12, 8200, 9000)])
+def test_many_tiles(M, N, K, group):
+    """More tiles than CTAs: the bits of single rows, and 64-bit sums for the first and last weight rows."""
+    g = torch.Generator(device="cuda").manual_seed(M + N + group)
+    kp = (K + 127) // 128 * 128
+    qw = torch.randint(0, 256, (N, kp // 2), generator=g, device="cuda", dtype=torch.uint8)
+    if kp > K:      # the padding's codes are those of zero; K is a multiple of 8, so whole bytes belong to it
+        zeros = np.zeros((1, kp), np.int64)
+        mask = w4_pack(np.where(np.arange(kp) < K, 7, -8)[None]) == 0xFF
+        qw = torch.where(torch.from_numpy(mask).cuda(), qw, torch.from_numpy(w4_pack(zeros)).cuda())
+    sw = (torch.rand((N, kp // group), generator=g, device="cuda") * 0.05 + 0.001).to(torch.bfloat16)
+    x = torch.randn((M, K), generator=g, device="cuda").to(torch.bfloat16)
+    y = clef.w4_linear(x, qw, sw)
+    for m in (0, M // 2, M - 1):
+        assert torch.equal(clef.w4_linear(x[m:m + 1], qw, sw)[0], y[m])
+    for rows in (slice(0, 40), slice(N - 40, N)):
+        check(x.float().cpu().numpy(), w4_codes(qw[rows].cpu().numpy(), K), sw[rows].float().cpu().numpy(), group, None,
+              y[:, rows].float().cpu().numpy())
+    assert clef.poll_status() == 0

@@ -42,7 +42,6 @@ namespace clef {
 namespace {
 
 constexpr int kBlockK = 128;      // weights of a packed block
-constexpr int kWarps = 8;
 constexpr int kParts = 8;         // runs of K that are summed apart, then added in order
 constexpr int kDepth = 2;         // stages of two blocks that a warp has on their way; one more is in use
 constexpr int kStage = 2048 + 256;    // bytes of a stage: 16 rows of 128, and their scales
@@ -106,13 +105,13 @@ struct W4Args {
     int64_t ldy;
     int M, N, K;
     int kb, part;      // blocks of a weight row, and of one of its kParts parts
-    int tiles;         // of 16 * cluster rows
+    int tiles;         // of 2 * warps * cluster rows
     int split_log2;    // CTAs of a cluster
 };
 
-// A cluster of S CTAs takes tiles of 16 S weight rows in turn.  K is cut into
-// eight parts whatever S is; CTA r of the cluster has 8 / S of them, and its
-// eight warps are 8 / S parts times S groups of 16 rows.  A tile's eight
+// A cluster of S CTAs takes tiles of 16 S weight rows (24 S with twelve warps) in
+// turn.  K is cut into eight parts whatever S is; CTA r of the cluster has 8 / S of
+// them, and its eight warps are 8 / S parts times S groups of 16 rows.  A tile's eight
 // partial sums meet in shared memory (of the cluster) and are added in the order
 // of K, so a row of y has the same bits whatever M, S and the grid are.
 //
@@ -123,18 +122,18 @@ struct W4Args {
 // Measured (K x N, us a call back to back, weights from memory): one row 5120 x
 // 34816 in groups of 64, 19.8 us, 4.8 TB/s, of which 6 us before the first
 // product (the launch, x to fp16); 6144 x 5120 in groups of 128, 6.8 us.  13 rows
-// of 17408 x 5120 in groups of 32, 32 us: 9 us before the first product, then
-// three rounds of tiles (2.2 would do), each as long as mma.sync and the reads of x
-// from shared memory take.
-template <int NT, int GROUP>
-__global__ void __launch_bounds__(kWarps * 32, NT == 1 ? 2 : 1) w4_linear_kernel(const W4Args a) {
+// of 17408 x 5120 in groups of 32, 29.7 us: 9 us before the first product, then
+// two rounds of tiles (1.5 would do), in which three warps a scheduler wait for
+// products and for x from shared memory.
+template <int NT, int GROUP, int WARPS>
+__global__ void __launch_bounds__(WARPS * 32, NT == 1 ? 2 : 1) w4_linear_kernel(const W4Args a) {
     extern __shared__ __align__(16) uint8_t smem[];
     __shared__ float s_unit[NT * 8][kParts];      // what a part's sum of a row of x is multiplied by
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
     uint32_t rank;
     asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(rank));
     const int S = 1 << a.split_log2, own_log2 = 3 - a.split_log2, own = 1 << own_log2;      // own: parts of this CTA
-    const int rows = 16 * S, m0 = (int)blockIdx.y * NT * 8, mn = min(NT * 8, a.M - m0);
+    const int rows = 16 * (WARPS >> own_log2), m0 = (int)blockIdx.y * NT * 8, mn = min(NT * 8, a.M - m0);
     const int kb_own = (int)rank * own * a.part;                 // first block of this CTA
     const int slice = own * a.part;                              // its blocks
     const int pitch = slice * kBlockK * 2 + 64;                  // bytes of a row of x: 64 past a multiple of 128
@@ -199,7 +198,7 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 ? 2 : 1) w4_linear_kernel
     };
 
     // x's columns of this CTA, zeros past K: a warp a (row, part)
-    for (int i = warp; i < mn * own; i += kWarps) {
+    for (int i = warp; i < mn * own; i += WARPS) {
         const int m = i >> own_log2, p = i & (own - 1), words = a.part * (kBlockK / 8), k0 = (kb_own + p * a.part) * kBlockK;
         const uint16_t *src = a.x + (int64_t)(m0 + m) * a.ldx;
         const uint32_t dst = smem_u32(smem + m * pitch + p * a.part * 256);
@@ -215,7 +214,7 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 ? 2 : 1) w4_linear_kernel
     __syncwarp();
 
     // to fp16
-    for (int i = warp; i < mn * own; i += kWarps) {
+    for (int i = warp; i < mn * own; i += WARPS) {
         const int m = i >> own_log2, p = i & (own - 1), words = a.part * (kBlockK / 8);
         uint4 *at = reinterpret_cast<uint4 *>(smem + m * pitch + p * a.part * 256);
         uint32_t top = 0;
@@ -365,9 +364,10 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 ? 2 : 1) w4_linear_kernel
             __syncthreads();
         else
             asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
-        // each CTA finishes 16 of the rows
-        for (int i = tid; i < mn * 16; i += kWarps * 32) {
-            const int m = i >> 4, r = (int)rank * 16 + (i & 15), n = tile * rows + r;
+        // each CTA finishes its share of the rows
+        constexpr int SHARE = 2 * WARPS;      // 16 S (WARPS / 8) rows over S CTAs
+        for (int i = tid; i < mn * SHARE; i += WARPS * 32) {
+            const int m = i / SHARE, r = (int)rank * SHARE + i - m * SHARE, n = tile * rows + r;
             if (n < a.N) {
                 float q[kParts];
 #pragma unroll
@@ -451,29 +451,30 @@ bool misaligned(const void *p, unsigned to) { return (reinterpret_cast<uintptr_t
 
 constexpr int64_t kMaxW4 = (int64_t)1 << 24, kMaxK = 65536;
 
-constexpr size_t kMaxSmem = 220 * 1024;
+constexpr size_t kMaxSmem = 226 * 1024;
 
 // Shared memory of a CTA: x's columns, the sums' starts, two tiles' partial sums and the rings.
-size_t w4_smem(int nt, int64_t m, int part, int group, int split) {
-    const int own = kParts / split, rows = 16 * split;
+size_t w4_smem(int nt, int64_t m, int part, int group, int split, int warps) {
+    const int own = kParts / split, rows = 2 * warps * split;
     return (size_t)m * (own * part * kBlockK * 2 + 64) + (size_t)own * part * (kBlockK / group) * nt * 8 * 4 +
-           (size_t)2 * own * nt * 8 * rows * 4 + (size_t)kWarps * (kDepth + 1) * kStage;
+           (size_t)2 * own * nt * 8 * rows * 4 + (size_t)warps * (kDepth + 1) * kStage;
 }
 
-template <int NT, int GROUP>
-cudaError_t launch_w4(const W4Args &a, int split, int blocks_m, int sms, cudaStream_t st) {
-    const size_t smem = w4_smem(NT, a.M < NT * 8 ? a.M : NT * 8, a.part, GROUP, split);
+// How many clusters run at once: they do not fill every group of SMs (of 152
+// CTAs, 15 clusters of eight do).
+template <int NT, int GROUP, int WARPS>
+cudaError_t resident_clusters(int split, size_t smem, int sms, int *clusters) {
     static SmemOptIn opt;
-    cudaError_t e = opt.set(reinterpret_cast<const void *>(w4_linear_kernel<NT, GROUP>), kMaxSmem);
+    cudaError_t e = opt.set(reinterpret_cast<const void *>(w4_linear_kernel<NT, GROUP, WARPS>), kMaxSmem);
     if (e != cudaSuccess) return e;
     const int per_sm = NT == 1 && smem <= 110 * 1024 ? 2 : 1;
-    int clusters = sms * per_sm / split;
-    if (split > 1) {   // clusters do not fill every group of SMs: of 152 CTAs, 15 clusters of eight run at once
+    *clusters = sms * per_sm / split;
+    if (split > 1) {
         static std::atomic<int> known[64][4][2];   // asked once for each device
         int dev = 0;
         e = cudaGetDevice(&dev);
         if (e != cudaSuccess) return e;
-        std::atomic<int> &slot = known[dev & 63][a.split_log2][per_sm - 1];
+        std::atomic<int> &slot = known[dev & 63][split == 2 ? 1 : split == 4 ? 2 : 3][per_sm - 1];
         int most = slot.load(std::memory_order_relaxed);
         if (most == 0) {
             cudaLaunchConfig_t cfg = {};
@@ -482,28 +483,61 @@ cudaError_t launch_w4(const W4Args &a, int split, int blocks_m, int sms, cudaStr
             attr.val.clusterDim.x = (unsigned)split;
             attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
             cfg.gridDim = dim3((unsigned)split);
-            cfg.blockDim = dim3(kWarps * 32);
+            cfg.blockDim = dim3(WARPS * 32);
             cfg.dynamicSmemBytes = smem;
             cfg.attrs = &attr;
             cfg.numAttrs = 1;
-            e = cudaOccupancyMaxActiveClusters(&most, w4_linear_kernel<NT, GROUP>, &cfg);
+            e = cudaOccupancyMaxActiveClusters(&most, w4_linear_kernel<NT, GROUP, WARPS>, &cfg);
             if (e != cudaSuccess) return e;
             if (most > 0 && dev < 64) slot.store(most, std::memory_order_relaxed);
         }
-        if (most > 0 && clusters > most) clusters = most;
+        if (most > 0 && *clusters > most) *clusters = most;
     }
-    if (clusters < 1) clusters = 1;
+    if (*clusters < 1) *clusters = 1;
+    return cudaSuccess;
+}
+
+template <int NT, int GROUP, int WARPS>
+cudaError_t launch_w4(W4Args a, int split, int clusters, int blocks_m, size_t smem, cudaStream_t st) {
+    a.tiles = (a.N + 2 * WARPS * split - 1) / (2 * WARPS * split);
     if (clusters > a.tiles) clusters = a.tiles;
-    return launch_kernel(w4_linear_kernel<NT, GROUP>, dim3((unsigned)(clusters * split), (unsigned)blocks_m), dim3(kWarps * 32),
+    return launch_kernel(w4_linear_kernel<NT, GROUP, WARPS>, dim3((unsigned)(clusters * split), (unsigned)blocks_m), dim3(WARPS * 32),
                          smem, st, split, true, a);
+}
+
+template <int NT, int GROUP>
+cudaError_t launch_w4_warps(const W4Args &a, int split, int blocks_m, int sms, cudaStream_t st) {
+    const int m = a.M < NT * 8 ? a.M : NT * 8;
+    const size_t smem = w4_smem(NT, m, a.part, GROUP, split, 8);
+    int clusters = 0;
+    cudaError_t e = resident_clusters<NT, GROUP, 8>(split, smem, sms, &clusters);
+    if (e != cudaSuccess) return e;
+    if constexpr (NT == 2) {
+        // With a CTA an SM the warps wait more than they issue: a tile of twelve warps takes less than 4 / 3
+        // of the time of one of eight.  Twelve where that saves more rounds than it lengthens: 13 x 17408 x
+        // 5120, three rounds of eight take 32.1 us, two of twelve 29.7.
+        const size_t smem12 = w4_smem(NT, m, a.part, GROUP, split, 12);
+        if (split > 1 && smem12 <= kMaxSmem) {
+            int clusters12 = 0;
+            e = resident_clusters<NT, GROUP, 12>(split, smem12, sms, &clusters12);
+            if (e != cudaSuccess) return e;
+            const auto rounds = [&](int warps, int at_once) {
+                const int tiles = (a.N + 2 * warps * split - 1) / (2 * warps * split);
+                return (tiles + at_once - 1) / at_once;
+            };
+            if (rounds(12, clusters12) * 4 < rounds(8, clusters) * 3 + 1)
+                return launch_w4<NT, GROUP, 12>(a, split, clusters12, blocks_m, smem12, st);
+        }
+    }
+    return launch_w4<NT, GROUP, 8>(a, split, clusters, blocks_m, smem, st);
 }
 
 template <int NT>
 cudaError_t launch_w4_group(const W4Args &a, int group, int split, int blocks_m, int sms, cudaStream_t st) {
     switch (group) {
-        case 32: return launch_w4<NT, 32>(a, split, blocks_m, sms, st);
-        case 64: return launch_w4<NT, 64>(a, split, blocks_m, sms, st);
-        default: return launch_w4<NT, 128>(a, split, blocks_m, sms, st);
+        case 32: return launch_w4_warps<NT, 32>(a, split, blocks_m, sms, st);
+        case 64: return launch_w4_warps<NT, 64>(a, split, blocks_m, sms, st);
+        default: return launch_w4_warps<NT, 128>(a, split, blocks_m, sms, st);
     }
 }
 
@@ -563,7 +597,7 @@ extern "C" int clef_w4_linear(const void *x, int64_t ldx, const void *qw, const 
     const int64_t block_m = M > 8 && x_bytes(M < 16 ? M : 16, kParts) <= 120 * 1024 ? 16 : 8;
     const int64_t m = M < block_m ? M : block_m;
     int split = 1;
-    while (split < kParts && (block_m == 8 ? x_bytes(m, split) > 40 * 1024 : w4_smem(2, m, part, group, split) > kMaxSmem)) split *= 2;
+    while (split < kParts && (block_m == 8 ? x_bytes(m, split) > 40 * 1024 : w4_smem(2, m, part, group, split, 8) > kMaxSmem)) split *= 2;
     W4Args a;
     a.x = static_cast<const uint16_t *>(x);
     a.ldx = ldx;
@@ -578,7 +612,7 @@ extern "C" int clef_w4_linear(const void *x, int64_t ldx, const void *qw, const 
     a.kb = kb;
     a.part = part;
     a.split_log2 = split == 1 ? 0 : split == 2 ? 1 : split == 4 ? 2 : 3;
-    a.tiles = (int)((N + 16 * split - 1) / (16 * split));
+    a.tiles = 0;      // by the number of warps
     sms = internal_launch_sms(sms);
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     const int blocks_m = (int)((M + block_m - 1) / block_m);
