@@ -79,17 +79,9 @@ class Decoder:
 
     def capture(self, x: torch.Tensor, seqs: Sequence[int]) -> torch.Tensor:
         """Records step(x, seqs) into a CUDA graph and returns the tensor that
-        ``replay()`` fills; refill x in place for the next token.  The state of
-        the sequences is as before the call."""
+        ``replay()`` fills; refill x in place for the next token.  Recording runs
+        nothing: the sequences are as before the call."""
         seqs = self._ids(seqs)
-        kept = [t.clone() for t in (self.table, self.lens, self.refs, self.codes, self.scales)]
-        side = torch.cuda.Stream()
-        side.wait_stream(torch.cuda.current_stream())
-        with torch.cuda.stream(side):
-            self.step(x, seqs)          # one-time set-up of the library happens outside the capture
-            for t, was in zip((self.table, self.lens, self.refs, self.codes, self.scales), kept):
-                t.copy_(was)
-        torch.cuda.current_stream().wait_stream(side)
         torch.cuda.synchronize()
         self.graph = torch.cuda.CUDAGraph()
         self._captured = (x, seqs)
