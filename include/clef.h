@@ -448,9 +448,9 @@ int clef_w4_linear(const void *x, int64_t ldx, const void *qw, const void *sw, i
  *
  * clef_kv_reserve -- lens[b] += grow[b] for every sequence, with the pages
  * that takes: the lowest free ones, in the order of the sequences.
- * clef_kv_fork -- sequence dst[i], empty before, becomes a copy of src[i]:
- * whole pages are shared (refs + 1), a part-filled last page is copied to the
- * lowest free page.  scratch: int32 [2 n].
+ * clef_kv_fork -- sequence dst[i], empty before, becomes a copy of src[i] as it
+ * was before the call: whole pages are shared (refs + 1), a part-filled last
+ * page is copied to the lowest free page.  scratch: int32 [2 n].
  * Either changes nothing and records CLEF_ERR_NO_PAGES if the free pages do
  * not suffice, CLEF_ERR_BAD_PAGE if an argument on the device is out of range.
  * clef_kv_free -- the sequences list[0 .. n - 1] become empty; their pages'

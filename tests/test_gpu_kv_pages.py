@@ -202,3 +202,26 @@ def test_refusals():
         with pytest.raises(clef.ClefError):
             call()
     assert clef.poll_status() == 0
+
+
+@pytest.mark.parametrize("order", ["before", "after"])
+@pytest.mark.parametrize("pairs", [1, 40, 1300])
+def test_fork_of_a_target(pairs, order):
+    """A target that is a source too was empty before the call, so its copy is empty:
+    no length, no page and no reference, wherever the two pairs stand in the list."""
+    rng = np.random.default_rng(pairs)
+    seqs = 1 + 2 * pairs
+    pool = Pool(rng, pairs + 8, seqs, 3, planes=1)
+    assert pool.reserve([37] + [0] * (seqs - 1))
+    first, second = list(range(1, 1 + pairs)), list(range(1 + pairs, seqs))
+    a, b = ([0] * pairs, first), (first, second)
+    if order == "after":
+        a, b = b, a
+    clef.kv_fork(pool.codes, pool.scales, pool.table, pool.lens, pool.refs, dev_i32(a[0] + b[0]), dev_i32(a[1] + b[1]))
+    assert clef.poll_status() == 0
+    assert pool.lens.tolist() == [37] * (1 + pairs) + [0] * pairs
+    assert (pool.table[second] == -1).all()
+    refs = pool.refs.tolist()
+    assert refs[:2] == [1 + pairs] * 2 and refs[2:3 + pairs] == [1] * (1 + pairs) and not any(refs[3 + pairs:])
+    clef.kv_free(pool.table, pool.lens, pool.refs, dev_i32(list(range(seqs))), 16)
+    assert clef.poll_status() == 0 and not pool.refs.any()

@@ -177,8 +177,8 @@ __global__ void __launch_bounds__(kBook) kv_reserve_kernel(const BookArgs a, con
     pdl_launch_dependents();
 }
 
-// Sequence dst[i], empty so far, becomes a copy of src[i]: whole pages shared,
-// a part-filled last page given a page of its own, which the copy launch after
+// Sequence dst[i], empty so far, becomes a copy of src[i] as it was before the call: whole
+// pages shared, a part-filled last page given a page of its own, which the copy launch after
 // this one fills: moves[i] = (from, to), or (-1, -1).
 __global__ void __launch_bounds__(kBook) kv_fork_kernel(const BookArgs a, const int32_t *src, const int32_t *dst, int n,
                                                         int32_t *from, int32_t *to) {
@@ -243,7 +243,15 @@ __global__ void __launch_bounds__(kBook) kv_fork_kernel(const BookArgs a, const 
                 atomicAdd(&a.refs[p], 1);      // whole numbers: the order does not matter
             }
         __syncthreads();
-        for (int i = tid; i < n; i += kBook) a.lens[dst[i]] = a.lens[src[i]];
+        // a target may be a source too (an empty one): every length is read before any is written
+        constexpr int kRounds = kKvMaxSeqs / kBook;
+        int len[kRounds];
+#pragma unroll
+        for (int k = 0; k < kRounds; ++k) len[k] = tid + k * kBook < n ? a.lens[src[tid + k * kBook]] : 0;
+        __syncthreads();
+#pragma unroll
+        for (int k = 0; k < kRounds; ++k)
+            if (tid + k * kBook < n) a.lens[dst[tid + k * kBook]] = len[k];
     }
     pdl_launch_dependents();
 }

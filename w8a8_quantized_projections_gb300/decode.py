@@ -94,8 +94,8 @@ def kv_reserve(table, lens, refs, grow, page: int, stream=None) -> None:
 
 
 def kv_fork(codes, scales, table, lens, refs, src, dst, stream=None) -> None:
-    """Sequence dst[i] (empty before) becomes a copy of src[i]: whole pages are
-    shared, a part-filled last page is copied to the lowest free page.  Changes
+    """Sequence dst[i] (empty before) becomes a copy of src[i] as it was before the
+    call: whole pages are shared, a part-filled last page is copied to the lowest free page.  Changes
     nothing if the pool has too few free pages."""
     (_ext or _load()).kv_fork(codes, scales, table, lens, refs, src, dst, stream)
 
