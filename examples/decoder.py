@@ -49,6 +49,8 @@ class Decoder:
         self.table = torch.zeros((sequences, width), dtype=torch.int32, device=device)
         self.lens = torch.zeros(sequences, dtype=torch.int32, device=device)
         self.refs = torch.zeros(pages, dtype=torch.int32, device=device)
+        self.rows = torch.zeros(sequences + 1, dtype=torch.int32, device=device)      # of a reservation
+        self.numbers = torch.arange(sequences + 1, dtype=torch.int32, device=device)
         self.freq = theta ** (-torch.arange(0, dim, 2, dtype=torch.float32, device=device) / dim)
         self.graph = None
 
@@ -63,19 +65,21 @@ class Decoder:
         n = torch.tensor(list(counts.values()), dtype=torch.int32, device=x.device)
         start = torch.zeros(len(counts) + 1, dtype=torch.int32, device=x.device)
         torch.cumsum(n, 0, dtype=torch.int32, out=start[1:])
-        table, lens = self._grow(seqs, n)
+        table, lens, rows = self._grow(seqs, n)
         seq_of = torch.repeat_interleave(torch.arange(len(counts), device=x.device), n.long(), output_size=x.shape[0])
         # row r is token len - n + (r - start) of its sequence
         at = torch.arange(x.shape[0], device=x.device) + (lens - start[1:])[seq_of]
-        return self._run(x, at, table, lens, start, self._many_rows)
+        return self._run(x, at, table, lens, torch.minimum(start, rows), start, self._many_rows)
 
     def step(self, x: torch.Tensor, seqs: Sequence[int] | torch.Tensor) -> torch.Tensor:
-        """One token on the end of each sequence listed: x bf16 [len(seqs)][hidden]."""
+        """One token on the end of each sequence listed: x bf16 [len(seqs)][hidden].  Where the pool
+        has no page left for one of them, none grows, the cache stays as it is, the result
+        means nothing and poll_status() is 6."""
         seqs = self._ids(seqs)
         if x.shape[0] != seqs.shape[0]:
             raise ValueError(f"{x.shape[0]} rows for {seqs.shape[0]} sequences")
-        table, lens = self._grow(seqs, torch.ones_like(seqs))
-        return self._run(x, lens - 1, table, lens, None, self._few_rows)
+        table, lens, rows = self._grow(seqs, torch.ones_like(seqs))
+        return self._run(x, lens - 1, table, lens, torch.minimum(self.numbers[: len(seqs) + 1], rows), None, self._few_rows)
 
     def capture(self, x: torch.Tensor, seqs: Sequence[int]) -> torch.Tensor:
         """Records step(x, seqs) into a CUDA graph and returns the tensor that
@@ -116,11 +120,13 @@ class Decoder:
         return torch.tensor(list(seqs), dtype=torch.int32, device=self.lens.device)
 
     def _grow(self, seqs, n):
+        """The sequences' pages and lengths with n more tokens, and how many rows were given a
+        place: all, or none where the pool is full."""
         grow = torch.zeros_like(self.lens).index_copy_(0, seqs.long(), n)
-        kv_reserve(self.table, self.lens, self.refs, grow, self.page)
-        return self.table.index_select(0, seqs), self.lens.index_select(0, seqs)
+        kv_reserve(self.table, self.lens, self.refs, grow, self.page, row_start=self.rows)
+        return self.table.index_select(0, seqs), self.lens.index_select(0, seqs), self.rows[-1:]
 
-    def _run(self, x, at, table, lens, start, project):
+    def _run(self, x, at, table, lens, placed, start, project):
         hq, hk, d = self.q_heads, self.kv_heads, self.dim
         angle = at.to(torch.float32)[:, None] * self.freq
         cos, sin = angle.cos()[:, None], angle.sin()[:, None]
@@ -128,7 +134,7 @@ class Decoder:
             codes, scales = self.codes[2 * i : 2 * i + 2], self.scales[2 * i : 2 * i + 2]
             qkv = project(i, "qkv", self._norm(x, norm_attn)).view(-1, hq + 2 * hk, d)
             qk = self._rotate(qkv[:, : hq + hk], cos, sin)
-            kv_append(qk[:, hq:], qkv[:, hq + hk :], codes, scales, table, lens, start)
+            kv_append(qk[:, hq:], qkv[:, hq + hk :], codes, scales, table, lens, placed)
             o = kv_attention(qk[:, :hq], codes, scales, table, lens, start)
             x = x + project(i, "o", o.view(-1, hq * d))
             x = x + project(i, "down", project(i, "gateup", self._norm(x, norm_mlp)))

@@ -425,8 +425,12 @@ int clef_w4_linear(const void *x, int64_t ldx, const void *qw, const void *sw, i
  *   s = max(s_old, fp32(amax / top)), s_old = 0 for a page without tokens;
  *   where s grew, earlier codes become encode(value(code) * fp32(s_old / s));
  *   new codes are encode(v * min(fp32(1 / s), FLT_MAX)), zeros where s = 0.
- * The pages written must belong to one sequence each (clef_kv_reserve and
- * clef_kv_fork see to it), and k and v must be finite: a page of a head has one
+ * The pages written must belong to one sequence each.  clef_kv_reserve and
+ * clef_kv_fork see to it where the reservation of the new tokens was made;
+ * where it was not (CLEF_ERR_NO_PAGES), the lengths do not hold the new tokens
+ * and an append would write over the last ones, in pages that may be shared.
+ * So a call that may find the pool full takes row_start from
+ * clef_kv_reserve_rows.  k and v must be finite: a page of a head has one
  * scale, so an infinity or a NaN is felt by the page's other tokens too.
  *
  * clef_kv_gather -- k_out[r], v_out[r] = bf16(code * scale) of token pos[r]
@@ -448,6 +452,10 @@ int clef_w4_linear(const void *x, int64_t ldx, const void *qw, const void *sw, i
  *
  * clef_kv_reserve -- lens[b] += grow[b] for every sequence, with the pages
  * that takes: the lowest free ones, in the order of the sequences.
+ * clef_kv_reserve_rows also writes row_start (int32 [seqs + 1], or NULL): the
+ * running sum of grow, row_start[seqs] the rows in all, or zeros where nothing
+ * was reserved.  An append that takes it, or takes min(row_start[seqs], its own
+ * row_start[i]), writes the rows that have a place, and nothing after a failure.
  * clef_kv_fork -- sequence dst[i], empty before, becomes a copy of src[i] as it
  * was before the call: whole pages are shared (refs + 1), a part-filled last
  * page is copied to the lowest free page.  scratch: int32 [2 n].
@@ -482,6 +490,8 @@ int clef_kv_attention(const void *q, int64_t ldq, int64_t ldq_head, int64_t rows
                       int64_t workspace_bytes, void *stream);
 int clef_kv_reserve(int32_t *table, int64_t ldt, int64_t seqs, int64_t width, int32_t *lens, int32_t *refs,
                     int64_t pages, int page, const int32_t *grow, void *stream);
+int clef_kv_reserve_rows(int32_t *table, int64_t ldt, int64_t seqs, int64_t width, int32_t *lens, int32_t *refs,
+                         int64_t pages, int page, const int32_t *grow, int32_t *row_start, void *stream);
 int clef_kv_fork(void *codes, int64_t plane_bytes, float *scales, int64_t plane_scales, int64_t planes,
                  int64_t pages, int heads, int page, int dim, int32_t *table, int64_t ldt, int64_t seqs,
                  int64_t width, int32_t *lens, int32_t *refs, const int32_t *src, const int32_t *dst, int64_t n,

@@ -161,3 +161,10 @@ def test_packed_layout_model(K):
     assert np.array_equal(w4_codes(q, K), c)
     kp = q.shape[1] * 2
     assert not w4_codes(q, kp)[:, K:].any()
+
+
+def test_reserve_rows():
+    L = clef.library()
+    res = [*TABLE, P, P, 4, 16, P, P, NUL]
+    refused(L.clef_kv_reserve_rows, res, TABLE_BAD + [(4, NUL), (5, NUL), (6, -1), (7, 24), (8, NUL), (8, ODD), (9, ODD)])
+    assert L.clef_kv_reserve_rows(NUL, 3, 0, 3, NUL, NUL, 4, 16, NUL, NUL, NUL) == 0

@@ -153,3 +153,32 @@ def test_refusals():
         dec.step(rows(1, 0), [0, 1])
     with pytest.raises(ValueError):
         Decoder([], HQ, HK, D, 1, 1, 1, kind="fp4")
+
+
+@pytest.mark.parametrize("kind", ["int8", "e4m3"])
+@pytest.mark.parametrize("captured", [False, True])
+def test_a_full_pool_is_left_alone(kind, captured):
+    """Two forks of a sequence whose last page is whole, and one free page: a step of both
+    and a prompt that find no place leave every byte as it was; a step that has one is right."""
+    a, b = build(kind, pages=3), build(kind)
+    p = rows(32, 5)
+    for d in (a, b):
+        d.prompt(p, {0: 32})
+    a.fork([0], [1])
+    assert clef.poll_status() == 0
+    x = rows(2, 6)
+    if captured:
+        a.capture(x, [0, 1])
+    was = [t.clone() for t in (a.codes.view(torch.uint8), a.scales, a.table, a.lens, a.refs)]
+    for call in range(3):
+        if captured:
+            a.replay()
+        else:
+            a.step(x, [0, 1])
+        assert clef.poll_status() == 6
+        assert all(torch.equal(t, w) for t, w in zip((a.codes.view(torch.uint8), a.scales, a.table, a.lens, a.refs), was))
+    a.prompt(rows(40, 7), {1: 3, 2: 37})
+    assert clef.poll_status() == 6
+    assert all(torch.equal(t, w) for t, w in zip((a.codes.view(torch.uint8), a.scales, a.table, a.lens, a.refs), was))
+    assert torch.equal(a.step(x[:1], [0]), b.step(x[:1], [0]))
+    assert clef.poll_status() == 0 and a.lens.tolist() == [33, 32, 0, 0, 0, 0]

@@ -225,3 +225,25 @@ def test_fork_of_a_target(pairs, order):
     assert refs[:2] == [1 + pairs] * 2 and refs[2:3 + pairs] == [1] * (1 + pairs) and not any(refs[3 + pairs:])
     clef.kv_free(pool.table, pool.lens, pool.refs, dev_i32(list(range(seqs))), 16)
     assert clef.poll_status() == 0 and not pool.refs.any()
+
+
+@pytest.mark.parametrize("seqs", [1, 5, 1025, 4096])
+def test_rows_of_a_reservation(seqs):
+    """The running sum of grow where it was served, zeros where it was not."""
+    rng = np.random.default_rng(seqs)
+    pool = Pool(rng, seqs + 1, seqs, 3, planes=1)
+    rows = torch.full((seqs + 1,), -7, dtype=torch.int32, device="cuda")
+    grow = rng.integers(0, 17, seqs)
+    clef.kv_reserve(pool.table, pool.lens, pool.refs, dev_i32(grow), 16, row_start=rows)
+    assert clef.poll_status() == 0 and rows.tolist() == [0] + np.cumsum(grow).tolist()
+    was = pool.table.clone(), pool.lens.clone(), pool.refs.clone()
+    for bad, status in (([32] * seqs, 6 if seqs > 1 else None), ([-1] + [0] * (seqs - 1), 5), ([49] + [1] * (seqs - 1), 5)):
+        if status is None:
+            continue
+        rows.fill_(-7)
+        clef.kv_reserve(pool.table, pool.lens, pool.refs, dev_i32(bad), 16, row_start=rows)
+        assert clef.poll_status() == status and not rows.any()
+        assert all(torch.equal(x, y) for x, y in zip(was, (pool.table, pool.lens, pool.refs)))
+    for rows in (torch.zeros(seqs, dtype=torch.int32, device="cuda"), torch.zeros(seqs + 1, device="cuda")):
+        with pytest.raises(ValueError):
+            clef.kv_reserve(pool.table, pool.lens, pool.refs, dev_i32(grow), 16, row_start=rows)

@@ -90,6 +90,7 @@ def library():
                 "clef_kv_attention": [vp, i64, i64, i64, vp, i32, i32, vp, i64, vp, i64, i64, i32, i32, i32, vp, i64,
                                       i64, i64, vp, C.c_float, i32, vp, i64, i64, vp, vp, i64, vp],
                 "clef_kv_reserve": [vp, i64, i64, i64, vp, vp, i64, i32, vp, vp],
+                "clef_kv_reserve_rows": [vp, i64, i64, i64, vp, vp, i64, i32, vp, vp, vp],
                 "clef_kv_fork": [vp, i64, vp, i64, i64, i64, i32, i32, i32, vp, i64, i64, i64, vp, vp, vp, vp, i64, vp,
                                  vp],
                 "clef_kv_free": [vp, i64, i64, i64, vp, vp, i64, i32, vp, i64, vp],

@@ -137,8 +137,10 @@ __device__ __forceinline__ int pages_of(int64_t len, int log2) {
     return (int)((len + ((int64_t)1 << log2) - 1) >> log2);
 }
 
-// lens[b] += grow[b], with the pages that takes.
-__global__ void __launch_bounds__(kBook) kv_reserve_kernel(const BookArgs a, const int32_t *grow) {
+// lens[b] += grow[b], with the pages that takes.  row_start (may be null): the running sum of
+// grow, or zeros where nothing is reserved, so that an append of those rows writes nothing: without
+// it the rows would land on the last tokens that the sequences have.
+__global__ void __launch_bounds__(kBook) kv_reserve_kernel(const BookArgs a, const int32_t *grow, int32_t *row_start) {
     extern __shared__ int off[];     // [seqs + 1]
     __shared__ int warps[32];
     pdl_wait();
@@ -173,6 +175,17 @@ __global__ void __launch_bounds__(kBook) kv_reserve_kernel(const BookArgs a, con
             });
         __syncthreads();   // the lengths are read until here
         for (int b = tid; b < a.seqs; b += kBook) a.lens[b] += grow[b];
+    }
+    if (row_start) {
+        uint32_t rows = 0;      // under 2^32: at most a page for each sequence beside the pool's pages
+        for (int b0 = 0; b0 < a.seqs; b0 += kBook) {
+            const int b = b0 + tid;
+            int all;
+            const uint32_t at = rows + (uint32_t)block_scan(fits && b < a.seqs ? grow[b] : 0, warps, &all);
+            if (b < a.seqs) row_start[b] = (int)min(at, 0x7FFFFFFFu);
+            rows += (uint32_t)all;
+        }
+        if (tid == 0) row_start[a.seqs] = (int)min(rows, 0x7FFFFFFFu);
     }
     pdl_launch_dependents();
 }
@@ -437,10 +450,16 @@ using namespace clef;
 
 extern "C" int clef_kv_reserve(int32_t *table, int64_t ldt, int64_t seqs, int64_t width, int32_t *lens, int32_t *refs,
                                int64_t pages, int page, const int32_t *grow, void *stream) {
+    return clef_kv_reserve_rows(table, ldt, seqs, width, lens, refs, pages, page, grow, nullptr, stream);
+}
+
+extern "C" int clef_kv_reserve_rows(int32_t *table, int64_t ldt, int64_t seqs, int64_t width, int32_t *lens,
+                                    int32_t *refs, int64_t pages, int page, const int32_t *grow, int32_t *row_start,
+                                    void *stream) {
     BookArgs a;
     int rc = book_args(a, table, ldt, seqs, width, lens, refs, pages, page);
     if (rc) return rc;
-    if (kv_misaligned(grow, 4)) return kv_fail("grow must be 4-byte aligned");
+    if (kv_misaligned(grow, 4) || kv_misaligned(row_start, 4)) return kv_fail("grow and row_start must be 4-byte aligned");
     if (seqs == 0) return CLEF_OK;
     if (!table || !lens || !refs || !grow) return kv_fail("null pointer");
     int sms = 0;
@@ -449,7 +468,7 @@ extern "C" int clef_kv_reserve(int32_t *table, int64_t ldt, int64_t seqs, int64_
     cudaError_t e = opt.set(reinterpret_cast<const void *>(kv_reserve_kernel), (kKvMaxSeqs + 1) * 4);
     if (e == cudaSuccess)
         e = launch_kernel(kv_reserve_kernel, dim3(1), dim3(kBook), (size_t)(seqs + 1) * 4,
-                          static_cast<cudaStream_t>(stream), 1, true, a, grow);
+                          static_cast<cudaStream_t>(stream), 1, true, a, grow, row_start);
     return e == cudaSuccess ? CLEF_OK : internal_cuda_error(e, "page reservation launch");
 }
 

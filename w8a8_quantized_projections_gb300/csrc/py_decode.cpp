@@ -379,13 +379,14 @@ PyObject *kv_attention(PyObject *, Args a, Py_ssize_t n) {
 
 // ------------------------------------------------------------ pages
 
-PyObject *kv_reserve(PyObject *, Args a, Py_ssize_t n) {   // table, lens, refs, grow, page, stream
-    ARGS(6);
+PyObject *kv_reserve(PyObject *, Args a, Py_ssize_t n) {   // table, lens, refs, grow, page, stream, row_start
+    ARGS(7);
     const Table t = table(a[0], "table");
     const int dev = THPVariable_Unpack(a[0]).get_device();
     const Ints lens = ints(a[1], "lens", dev, t.seqs), refs = ints(a[2], "refs", dev), grow = ints(a[3], "grow", dev, t.seqs);
     const Stream s = stream_of(a[5], dev);
-    CLEF_CALL(clef_kv_reserve, TABLE(t), lens.at, refs.at, refs.n, (int)integer(a[4]), grow.at, s.at);
+    int32_t *rows = a[6] == Py_None ? nullptr : ints(a[6], "row_start", dev, t.seqs + 1).at;
+    CLEF_CALL(clef_kv_reserve_rows, TABLE(t), lens.at, refs.at, refs.n, (int)integer(a[4]), grow.at, rows, s.at);
     Py_RETURN_NONE;
     END_HANDLE_TH_ERRORS
 }

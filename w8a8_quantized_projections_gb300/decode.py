@@ -62,7 +62,7 @@ def kv_append(k, v, codes, scales, table, lens, row_start=None, stream=None) -> 
     """Writes the newest tokens' keys and values (bf16 [tokens][heads][dim]) of
     one layer into the cache.  `lens` counts them already; a sequence's rows
     are its last tokens: rows row_start[b] .. row_start[b + 1] - 1, or the same
-    number each."""
+    number each.  Where the pool may be full, take row_start from kv_reserve."""
     (_ext or _load()).kv_append(k, v, codes, scales, table, lens, row_start, stream)
 
 
@@ -86,11 +86,14 @@ def kv_attention(q, codes, scales, table, lens, row_start=None, scale=None, caus
 
 # ---------------------------------------------------------------- pages
 
-def kv_reserve(table, lens, refs, grow, page: int, stream=None) -> None:
+def kv_reserve(table, lens, refs, grow, page: int, stream=None, row_start=None) -> None:
     """lens += grow (int32 [sequences]), with the pages of `page` tokens that
     takes: the lowest free ones, in the order of the sequences.  Changes
-    nothing if the pool has too few (CLEF_ERR_NO_PAGES from poll_status)."""
-    (_ext or _load()).kv_reserve(table, lens, refs, grow, page, stream)
+    nothing if the pool has too few (CLEF_ERR_NO_PAGES from poll_status).
+    `row_start` (int32 [sequences + 1], optional) receives the running sum of
+    grow, or zeros if nothing was reserved: kv_append with it then writes
+    nothing, where it would write over the last tokens otherwise."""
+    (_ext or _load()).kv_reserve(table, lens, refs, grow, page, stream, row_start)
 
 
 def kv_fork(codes, scales, table, lens, refs, src, dst, stream=None) -> None:
