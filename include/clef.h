@@ -445,8 +445,9 @@ int clef_w4_linear(const void *x, int64_t ldx, const void *qw, const void *sw, i
  * ldq_head; rows and row_start as for append; out: bf16, pitches ldo,
  * ldo_head; lse: fp32 [rows][q_heads], log of the sum of exponentials
  * (-infinity for a row that sees nothing), or NULL.  Sums are fp32; the
- * weights that multiply values are rounded to fp16.  A row's bits depend on
- * its own sequence alone.  workspace: clef_kv_attention_workspace bytes with
+ * weights that multiply values are rounded to fp16.  The pages' scales may be
+ * any finite ones, however far apart.  A row's bits depend on its own sequence
+ * alone.  workspace: clef_kv_attention_workspace bytes with
  * ragged = (row_start != NULL) and max_len = width * page, 16-byte aligned; its
  * contents need no preparation and are not kept.
  *

@@ -1,0 +1,55 @@
+"""Attention over pages whose value scales lie anywhere in fp32: values down to bf16's
+smallest normal numbers, up to its largest, and both in one sequence.  Against fp64 with the
+bounds of decode_util.attention."""
+import numpy as np
+import pytest
+import torch
+
+from decode_util import Cache, bf16, scattered_table
+from test_gpu_kv_attention import check, run
+
+pytestmark = pytest.mark.gpu
+
+SIZES = {"tiny": (1e-37,), "tiny and normal": (1.0, 1e-37), "small and normal": (1.0, 1e-28), "large": (1e37,),
+         "all": (1.0, 1e-37, 1e36, 1e-20, 1e18), "middle": (1e-12, 1e-25), "large and zero": (1e36, 0.0)}
+
+
+@pytest.mark.parametrize("kind", ["int8", "e4m3"])
+@pytest.mark.parametrize("dim,n,len_,page", [(64, 1, 200, 16), (128, 1, 700, 32), (256, 1, 300, 16), (64, 10, 150, 16),
+                                             (64, 40, 200, 16), (128, 150, 300, 64), (256, 40, 200, 32)])
+@pytest.mark.parametrize("sizes", sorted(SIZES))
+def test_value_scales(kind, dim, n, len_, page, sizes):
+    """Pages of each size in turn, the softmax's weight spread over all of them or on those of one size."""
+    rng = np.random.default_rng(dim + n + len_)
+    table, pages = scattered_table(rng, [len_], page)
+    size = np.asarray(SIZES[sizes])
+    which = np.arange(len_) // page % len(size)
+    for on in [None, *range(len(size))][:3]:
+        c = Cache(kind, pages, 1, page, dim)
+        new = rng.standard_normal((2, len_, 1, dim))
+        new[0] *= np.where((on is None) | (which == on), 1.5, 0.01)[:, None, None]
+        new[1] = np.clip(new[1], -3, 3) * size[which][:, None, None]
+        new = bf16(new)
+        c.append(table[0], len_, new)
+        q = bf16(rng.standard_normal((n, 2, dim)) * 3)
+        got, lse = run(rng, c, table, [len_], q)
+        check(c, table, [len_], q, [0, n], got, lse)
+
+
+@pytest.mark.parametrize("kind", ["int8", "e4m3"])
+@pytest.mark.parametrize("n", [1, 20])
+@pytest.mark.parametrize("last", [1e-36, 1e36])
+def test_one_page_at_the_end(kind, n, last):
+    """The one page of another size comes after more pages than are looked up at a time, in
+    sequences of one split and of many."""
+    rng = np.random.default_rng(n)
+    lens, page, dim = [1500, 9000, 33], 16, 64
+    table, pages = scattered_table(rng, lens, page)
+    c = Cache(kind, pages, 1, page, dim)
+    for b, x in enumerate(lens):
+        new = rng.standard_normal((2, x, 1, dim))
+        new[1] *= np.where(np.arange(x) // page == (x - 1) // page - 1, last, 1.0)[:, None, None]
+        c.append(table[b], x, bf16(np.clip(new, -3e38, 3e38)))
+    q = bf16(rng.standard_normal((3 * n, 2, dim)))
+    got, lse = run(rng, c, table, lens, q)
+    check(c, table, lens, q, np.arange(4) * n, got, lse)

@@ -30,8 +30,11 @@
 // of the largest fall below fp16's normal numbers; the softmax's sum takes each
 // page's weights times 1 / vs.  A page whose value scale is zero counts with a
 // scale of 2^-60, small enough not to set the reference of the others, in the
-// sum, and with weights of zero.  (The value scales of a sequence are taken to lie
-// within 2^100 of one another.)
+// sum, and with weights of zero.
+// That holds while no scale is further than 2^40 from 1 (neither 1 / vs nor the sum leaves fp32, and a
+// weight times its vs is at least 2^-80 of the largest).  From the first page past that on, a row's sum has
+// a reference of its own, the running maximum of x alone: two exponentials a weight, and 2 to the power of
+// the references' difference comes back as a factor of the output.
 #include <cstdint>
 #include <type_traits>
 
@@ -136,6 +139,9 @@ __device__ __forceinline__ float ex2(float x) {
     return y;
 }
 
+// A value scale that needs the two references.
+__device__ __forceinline__ bool far_scale(float vs) { return vs != 0.0f && !(vs >= 0x1p-40f && vs <= 0x1p40f); }
+
 // 2^(a - b) for running maxima, 0 when a is -inf (b may be -inf then too)
 __device__ __forceinline__ float ex2_diff(float a, float b) { return a == -INFINITY ? 0.0f : ex2(a - b); }
 
@@ -230,7 +236,8 @@ struct SplitPrep {
     float qs[kRows], lift[kRows];               // what S is multiplied by, after lift is taken off it
     int end[kRows];                             // tokens a row sees
     int64_t at[kPages];                         // a page's first code of the head; -1: not there
-    float ks[kPages], lv[kPages], inv[kPages];  // key scale; log2 of the value scale; its reciprocal (0: no weight)
+    float ks[kPages], lv[kPages], inv[kPages];  // key scale; log2 of the value scale; its reciprocal (negative: no weight)
+    int far[kPages / 32];                       // whether a page's value scale needs the two references
 };
 
 struct SplitItem {
@@ -271,6 +278,7 @@ __global__ void __launch_bounds__(kThreads, split_ctas<D, NT>()) kv_split_kernel
     extern __shared__ __align__(16) uint8_t smem[];
     __shared__ __align__(16) Prep s_prep[2];
     __shared__ int s_scan[kWarps], s_total;
+    __shared__ float s_ref[2][kWarps * ROWS];      // items with far scales: the references of the sums
     constexpr int OPITCH = D + 4;            // floats: the lanes' writes meet every bank once
     float *s_o = reinterpret_cast<float *>(smem);          // [kWarps][ROWS][OPITCH], then m, l
     float *s_m = s_o + kWarps * ROWS * OPITCH, *s_l = s_m + kWarps * ROWS;
@@ -416,6 +424,8 @@ __global__ void __launch_bounds__(kThreads, split_ctas<D, NT>()) kv_split_kernel
             to.ks[tid] = p_ks;
             to.lv[tid] = log2f(vs);
             to.inv[tid] = p_vs == 0.0f ? -0x1p60f : __fdiv_rn(1.0f, vs);      // the sign marks it
+            const int far = __any_sync(0xFFFFFFFFu, far_scale(p_vs));
+            if (lane == 0) to.far[warp] = far;
         }
     };
 
@@ -527,6 +537,11 @@ __global__ void __launch_bounds__(kThreads, split_ctas<D, NT>()) kv_split_kernel
         int all_see = min(end[0][0], end[0][1]);
         if (NT == 2) all_see = min(all_see, min(end[NT - 1][0], end[NT - 1][1]));
         all_see = __reduce_min_sync(0xFFFFFFFFu, all_see);
+        static_assert(Prep::kPages == 64, "two flags");
+        const bool far = (pr.far[0] | pr.far[1]) != 0;
+        float *refs = &s_ref[turn][warp * ROWS];
+        if (far && lane < ROWS) refs[lane] = -INFINITY;
+        __syncwarp();
 
         for (; s0 < it.tok1; s0 += kWarps * STEP) {
             const int s1 = s0 + kWarps * STEP;
@@ -593,6 +608,38 @@ __global__ void __launch_bounds__(kThreads, split_ctas<D, NT>()) kv_split_kernel
                         const float f = qs[x][i] * ks[u];
                         if (whole || v != -INFINITY) top[i] = fmaxf(top[i], fmaf(v, f, fmaf(-lift[x][i], f, lv[u])));
                     }
+                if (__builtin_expect(far, 0)) {      // the sum over the step, and top without the pages of zeros
+                    float ml[2];
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        top[i] = ml[i] = -INFINITY;
+#pragma unroll
+                        for (int u = 0; u < TILES; ++u) {
+                            const float v = fmaxf(s[x][u][i], s[x][u][i + 2]), f = qs[x][i] * ks[u];
+                            if (v == -INFINITY) continue;
+                            ml[i] = fmaxf(ml[i], fmaf(v, f, -lift[x][i] * f));
+                            if (inv[u] >= 0.0f) top[i] = fmaxf(top[i], fmaf(v, f, fmaf(-lift[x][i], f, lv[u])));
+                        }
+#pragma unroll
+                        for (int o = 4; o < 32; o <<= 1) ml[i] = fmaxf(ml[i], __shfl_xor_sync(0xFFFFFFFFu, ml[i], o));
+                        const float was = refs[x * 8 + 2 * t + i];
+                        ml[i] = fmaxf(ml[i], was);
+                        l[x][i] *= ex2_diff(was, ml[i]);
+#pragma unroll
+                        for (int u = 0; u < TILES; ++u) {
+                            const float f = qs[x][i] * ks[u], off = fmaf(-lift[x][i], f, kLift - ml[i]);
+#pragma unroll
+                            for (int h = 0; h < 4; h += 2)
+                                if (s[x][u][i + h] != -INFINITY) l[x][i] += ex2(fmaf(s[x][u][i + h], f, off));
+                        }
+                    }
+                    __syncwarp();
+                    if (g == 0) {
+                        refs[x * 8 + 2 * t] = ml[0];
+                        refs[x * 8 + 2 * t + 1] = ml[1];
+                    }
+                    __syncwarp();
+                }
 #pragma unroll
                 for (int o = 4; o < 32; o <<= 1)
 #pragma unroll
@@ -604,7 +651,7 @@ __global__ void __launch_bounds__(kThreads, split_ctas<D, NT>()) kv_split_kernel
                     co[i] = ex2_diff(m[x][i], mn);
                     m[x][i] = mn;
                     ref[i] = mn == -INFINITY ? 0.0f : mn - kLift;
-                    l[x][i] *= co[i];
+                    l[x][i] *= far ? 1.0f : co[i];
                 }
                 if (__any_sync(0xFFFFFFFFu, co[0] != 1.0f || co[1] != 1.0f)) {
 #pragma unroll
@@ -625,8 +672,10 @@ __global__ void __launch_bounds__(kThreads, split_ctas<D, NT>()) kv_split_kernel
                         const float v = fmaf(s[x][u][i], f[i & 1], off[i & 1]);
                         p[i] = ex2(whole || s[x][u][i] != -INFINITY ? v : -INFINITY);
                     }
-                    l[x][0] = fmaf(p[0] + p[2], fabsf(inv[u]), l[x][0]);
-                    l[x][1] = fmaf(p[1] + p[3], fabsf(inv[u]), l[x][1]);
+                    // (selects, no branch: with far scales the sum has the step's weights already)
+                    const float back = far ? 0.0f : fabsf(inv[u]);
+                    l[x][0] = fmaf(far ? 0.0f : p[0] + p[2], back, l[x][0]);
+                    l[x][1] = fmaf(far ? 0.0f : p[1] + p[3], back, l[x][1]);
                     const uint32_t keep = inv[u] < 0.0f ? 0u : 0xFFFFFFFFu;
                     pf[x][u][0] = transpose8x8(pack_half(p[0], p[1]) & keep);
                     pf[x][u][1] = transpose8x8(pack_half(p[2], p[3]) & keep);
@@ -697,8 +746,17 @@ __global__ void __launch_bounds__(kThreads, split_ctas<D, NT>()) kv_split_kernel
                 f[w] = ex2_diff(s_m[w * ROWS + r], mm);
                 ll = fmaf(s_l[w * ROWS + r], f[w], ll);
             }
+            float ml = mm, back = 1.0f;      // the reference of the sum; the root of 2^(mm - ml)
+            if (__builtin_expect(far, 0)) {
+                const float *at = &s_ref[turn][r];
+                ml = fmaxf(fmaxf(at[0], at[ROWS]), fmaxf(at[2 * ROWS], at[3 * ROWS]));
+                ll = 0.0f;
+#pragma unroll
+                for (int w = 0; w < kWarps; ++w) ll = fmaf(s_l[w * ROWS + r], ex2_diff(at[w * ROWS], ml), ll);
+                back = ml == -INFINITY ? 0.0f : ex2(0.5f * (mm - ml));
+            }
             const float inv = ll > 0.0f ? __fdiv_rn(1.0f, ll) : 0.0f;
-            const float lse = ll > 0.0f ? mm - kLift + log2f(ll) : -INFINITY;
+            const float lse = ll > 0.0f ? ml - kLift + log2f(ll) : -INFINITY;
             const int i = by_group.div(done.r0 + r), hq = done.head * a.group + (done.r0 + r) - i * a.group;
             const int64_t place = done.b * a.part_units + ((int64_t)done.head * done.rows + done.r0 + r) * done.splits + done.split;
             if (done.splits > 1) {
@@ -720,6 +778,10 @@ __global__ void __launch_bounds__(kThreads, split_ctas<D, NT>()) kv_split_kernel
                 }
                 o0 *= inv;
                 o1 *= inv;
+                if (__builtin_expect(far, 0)) {
+                    o0 = o0 * back * back;
+                    o1 = o1 * back * back;
+                }
                 if (done.splits > 1) {
                     *reinterpret_cast<float2 *>(a.part + place * D + d) = make_float2(o0, o1);
                 } else {
@@ -931,7 +993,7 @@ __device__ __forceinline__ uint32_t turn_of(uint32_t n) { return T::kSlots == 1 
 // Scales of the pages of a block of 64 tokens, kRing blocks deep.
 struct BlockScales {
     float ks[4], lv[4], inv[4];    // key scale; log2 of the value scale; its reciprocal
-    int zero;                      // bit p: page p's value scale is zero
+    int odd;                       // bit p: page p's value scale is zero; bit 4: this block or one before it in the item has a far one
 };
 
 // 128 rows of query i * G + head g at a time (two such tiles up to dim 128),
@@ -948,8 +1010,8 @@ struct BlockScales {
 //
 // The row's reference m is a running maximum of x_j + log2 vs(page(j)): the
 // weights of P are exp2(x_j + log2 vs - m + 11), and the softmax's sum takes each
-// page's part times 1 / vs.  O is rescaled only when the maximum has grown by
-// more than 2^4 (the weights are then at most 2^15, within fp16).
+// page's part times 1 / vs (or, past a far scale, is a sum of its own).  O is rescaled only when the
+// maximum has grown by more than 2^4 (the weights are then at most 2^15, within fp16).
 //
 // Measured: 2,270 rows x 32 heads over as many e4m3 tokens, 8 heads of 128, causal:
 // 65 us, 650 TFLOP/s; 8 x 48 rows x 24 heads over 1,550 int8 tokens, 4 heads of 256:
@@ -965,6 +1027,7 @@ __global__ void __launch_bounds__(Tile<D>::kThreadsAll, 1) kv_tile_kernel(const 
     __shared__ BlockScales s_scale[kRing];
     __shared__ int s_there[2][kRing];              // bit p: page p of the block is one of the pool
     __shared__ float s_qs[T::kQ * 128], s_pair[2][2][128];   // rows' query scales; what the threads of a row exchange
+    __shared__ float s_ref[T::kSoftWarps * 32];              // past a far scale: the reference of a softmax thread's sum
     __shared__ uint32_t s_tmem;
     __shared__ int s_abort, s_scan[32], s_total;
     __shared__ TileItem s_item[2];
@@ -1128,6 +1191,7 @@ __global__ void __launch_bounds__(Tile<D>::kThreadsAll, 1) kv_tile_kernel(const 
 
             const int sees = a.causal ? max(0, t.len - t.n + i + 1) : t.len;    // tokens this row sees
             float m = -INFINITY, l = 0.0f;
+            bool apart = false;      // the sum's reference is s_ref[tid], not m
             for (int s = 0; s < t.steps; ++s) {
                 const int slot = slot_of<T>(q, ns);
                 const uint32_t ts = tmem + (uint32_t)(slot * T::kStep + half * T::kCols) + lanes;
@@ -1142,19 +1206,20 @@ __global__ void __launch_bounds__(Tile<D>::kThreadsAll, 1) kv_tile_kernel(const 
                 const auto scales_at = [&](int c) -> const BlockScales & {
                     return s_scale[((step0 + (uint32_t)s) * T::kSub + (uint32_t)((p0 + c) >> 6)) % kRing];
                 };
-                bool zeros = scales_at(0).zero != 0;
-                if (T::kCols > 64) zeros = zeros || scales_at(64).zero != 0;
+                int odd = scales_at(0).odd;
+                if (T::kCols > 64) odd |= scales_at(64).odd;
+                const bool far = odd >= 16;
                 // whole steps take code without masks (the compiler turns a test in the loops into selects
                 // for every column: 1,120 + 2,040 cycles for 128 columns instead of 450 + 1,350)
                 const int least = __reduce_min_sync(0xFFFFFFFFu, seen);
-                const bool whole = least >= T::kCols && !zeros;
+                const bool whole = least >= T::kCols && odd == 0;
 
                 const int most = __reduce_max_sync(0xFFFFFFFFu, seen);
 
                 // the largest x + log2 vs
                 uint32_t va[32], vb[32];
-                float top = -INFINITY;
-                const auto largest = [&](const uint32_t *v, int c) {      // of columns c .. c + 15
+                float top = -INFINITY, top_x = -INFINITY;
+                const auto largest = [&](const uint32_t *v, int c, auto two) {      // of columns c .. c + 15
                     const BlockScales &sc = scales_at(c);
                     const int p = ((p0 + c) & 63) >> log2;
                     float g[8];
@@ -1164,6 +1229,10 @@ __global__ void __launch_bounds__(Tile<D>::kThreadsAll, 1) kv_tile_kernel(const 
                     for (int w = 4; w > 0; w >>= 1)
 #pragma unroll
                         for (int k = 0; k < w; ++k) g[k] = fmaxf(g[k], g[k + w]);
+                    if constexpr (decltype(two)::value) {
+                        top_x = fmaxf(top_x, g[0] * (qs * sc.ks[p]));
+                        if (sc.odd >> p & 1) return;
+                    }
                     top = fmaxf(top, fmaf(g[0], qs * sc.ks[p], sc.lv[p]));
                 };
                 if (whole) {
@@ -1174,7 +1243,7 @@ __global__ void __launch_bounds__(Tile<D>::kThreadsAll, 1) kv_tile_kernel(const 
                         tmem_ld_wait();
 #pragma unroll
                         for (int h = 0; h < (T::kCols < 64 ? T::kCols : 64) / 16; ++h)
-                            largest(h < 2 ? va + h * 16 : vb + (h - 2) * 16, c + h * 16);
+                            largest(h < 2 ? va + h * 16 : vb + (h - 2) * 16, c + h * 16, std::false_type());
                     }
                 } else {
 #pragma unroll 1
@@ -1189,7 +1258,12 @@ __global__ void __launch_bounds__(Tile<D>::kThreadsAll, 1) kv_tile_kernel(const 
                         // (keys of a column that is not seen have a place below all others, whatever their page's scale)
 #pragma unroll
                         for (int h = 0; h < 2; ++h)
-                            if (c + h * 16 < seen) largest(va + h * 16, c + h * 16);
+                            if (!far && c + h * 16 < seen) largest(va + h * 16, c + h * 16, std::false_type());
+                        if (__builtin_expect(far, 0)) {
+#pragma unroll
+                            for (int h = 0; h < 2; ++h)
+                                if (c + h * 16 < seen) largest(va + h * 16, c + h * 16, std::true_type());
+                        }
                     }
                 }
                 if constexpr (T::kQ == 1) {
@@ -1200,10 +1274,30 @@ __global__ void __launch_bounds__(Tile<D>::kThreadsAll, 1) kv_tile_kernel(const 
                     }
                     top = fmaxf(top, s_pair[s & 1][half ^ 1][row]);
                 }
+                float ml = 0.0f;
+                if (__builtin_expect(far, 0)) {
+                    if constexpr (T::kQ == 1) {      // (read at the next exchange's place once all have passed this one)
+                        if (!pair_sync()) {
+                            ok = false;
+                            break;
+                        }
+                        s_pair[s & 1][half][row] = top_x;
+                        if (!pair_sync()) {
+                            ok = false;
+                            break;
+                        }
+                        top_x = fmaxf(top_x, s_pair[s & 1][half ^ 1][row]);
+                    }
+                    const float was = apart ? s_ref[tid] : m;
+                    apart = true;
+                    ml = fmaxf(was, top_x);
+                    l *= ex2_diff(was, ml);
+                    s_ref[tid] = ml;
+                }
                 if (__any_sync(0xFFFFFFFFu, top > m + kSlack || (m == -INFINITY && top != -INFINITY))) {
                     const float mn = fmaxf(m, top), f = ex2_diff(m, mn);
                     m = mn;
-                    l *= f;
+                    if (!far) l *= f;
                     if (s > 0) {
                         // O is at rest once the product before this step's is done
                         if (!warp_wait(&bar.o_done[slot_of<T>(q, npv - 1)], turn_of<T>(npv - 1), wait, kSiteKvSoftmax)) {
@@ -1276,7 +1370,7 @@ __global__ void __launch_bounds__(Tile<D>::kThreadsAll, 1) kv_tile_kernel(const 
 #pragma unroll 1
                     for (int c = 0; c < T::kCols; c += 32) {
                         if (T::kCols > 64 && c == 64) half_done();
-                        if (c + 32 <= least && !zeros) {      // seen by every row of the warp
+                        if (c + 32 <= least && odd == 0) {      // seen by every row of the warp
                             tmem_ld32(ts + (uint32_t)c, va);
                             tmem_ld_wait();
                             weights(va, c);
@@ -1296,7 +1390,7 @@ __global__ void __launch_bounds__(Tile<D>::kThreadsAll, 1) kv_tile_kernel(const 
                         for (int h = 0; h < 2; ++h) {
                             const int c0 = c + h * 16, p = ((p0 + c0) & 63) >> log2;
                             const float f = qs * sc.ks[p], off = sc.lv[p] - ref;
-                            const uint32_t keep = (sc.zero >> p & 1) ? 0u : 0xFFFFFFFFu;
+                            const uint32_t keep = (sc.odd >> p & 1) ? 0u : 0xFFFFFFFFu;
                             float g = 0.0f;
 #pragma unroll
                             for (int k = 0; k < 16; k += 2) {
@@ -1305,7 +1399,14 @@ __global__ void __launch_bounds__(Tile<D>::kThreadsAll, 1) kv_tile_kernel(const 
                                 g += y + z;
                                 o[h * 8 + k / 2] = pack_half(y, z) & keep;
                             }
-                            l = fmaf(g, sc.inv[p], l);
+                            if (__builtin_expect(far, 0)) {
+                                const float off_l = (kLift - kSlack) - ml;
+#pragma unroll
+                                for (int k = 0; k < 16; ++k)
+                                    l += c0 + k < seen ? ex2(fmaf(__uint_as_float(va[h * 16 + k]), f, off_l)) : 0.0f;
+                            } else {
+                                l = fmaf(g, sc.inv[p], l);
+                            }
                         }
                         tmem_st16(ts + (uint32_t)(c / 2), o);
                     }
@@ -1328,8 +1429,9 @@ __global__ void __launch_bounds__(Tile<D>::kThreadsAll, 1) kv_tile_kernel(const 
                 l += s_pair[0][half ^ 1][row];
             }
             const float inv = l > 0.0f ? __fdiv_rn(1.0f, l) : 0.0f;
+            const float ml = apart ? s_ref[tid] : m;
             if (row < mine && half == 0) {
-                const float lse = l > 0.0f ? m - (kLift - kSlack) + log2f(l) : -INFINITY;
+                const float lse = l > 0.0f ? ml - (kLift - kSlack) + log2f(l) : -INFINITY;
                 if (t.splits > 1)
                     a.part_lse[t.b * a.part_units + ((int64_t)t.head * t.rows + r) * t.splits + t.split] = lse;
                 else if (a.lse)
@@ -1352,6 +1454,11 @@ __global__ void __launch_bounds__(Tile<D>::kThreadsAll, 1) kv_tile_kernel(const 
                     tmem_ld_wait();
 #pragma unroll
                     for (int k = 0; k < 32; ++k) v[k] = none ? 0u : __float_as_uint(__uint_as_float(v[k]) * inv);
+                    if (apart) {
+                        const float back = ex2(0.5f * (m - ml));
+#pragma unroll
+                        for (int k = 0; k < 32; ++k) v[k] = none ? 0u : __float_as_uint(__uint_as_float(v[k]) * back * back);
+                    }
                     if (part) {
 #pragma unroll
                         for (int u = 0; u < 8; ++u) put(c * 8 + u, make_uint4(v[4 * u], v[4 * u + 1], v[4 * u + 2], v[4 * u + 3]));
@@ -1518,6 +1625,7 @@ __global__ void __launch_bounds__(Tile<D>::kThreadsAll, 1) kv_tile_kernel(const 
                 return x;
             };
             int page0 = t.tok0 >> log2;
+            bool far = false;
             Page now = look_up(page0 + lane), next = look_up(page0 + 32 + lane);
             for (int s = 0; s < t.steps * T::kSub; ++s, ++block) {
                 const int rs = plane ? stage_of<T::kRawV>(block) : stage_of<T::kRawK>(block);
@@ -1544,13 +1652,14 @@ __global__ void __launch_bounds__(Tile<D>::kThreadsAll, 1) kv_tile_kernel(const 
                     float vs = page >= 0 ? (later ? vs_b : vs_a) : 1.0f;
                     BlockScales &sc = s_scale[block % kRing];
                     const unsigned int zero = __ballot_sync(0xFFFFFFFFu, vs == 0.0f);
+                    far = __any_sync(0xFFFFFFFFu, far || far_scale(vs));
                     if (vs == 0.0f) vs = 0x1p-60f;
                     if (lane < 4) {
                         sc.ks[lane] = ks;
                         sc.lv[lane] = log2f(vs);
                         sc.inv[lane] = __fdiv_rn(1.0f, vs);
                     }
-                    if (lane == 0) sc.zero = (int)zero;
+                    if (lane == 0) sc.odd = (int)zero | (far ? 16 : 0);
                 }
                 if (lane == 0) s_there[plane][block % kRing] = (int)there;
                 const int64_t at = ((((int64_t)page * H + t.head) << log2) + (t0 & (a.pool.page - 1))) * D;
