@@ -387,7 +387,10 @@ int clef_bind_workspace(void *stream, void *ws, int64_t bytes);
  *
  * clef_w4_linear -- y[m][n] = bf16(sum_g sw[n][g] * (sum_{k in g} c[n][k] x[m][k]) + bias[n])
  * with fp32 sums, for calls of few rows: weights are read once for every 16
- * rows.  The order of a row's sum follows N and K alone, so its bits do not
+ * rows.  x counts to 2^-38 of the largest value of its row (in each eighth of
+ * K), and the sums' rounding goes by (|c| + 8) |x|, so values a millionth of
+ * another one in their group may be lost beside it.  Any finite x will do; an infinity
+ * or a NaN makes its row of y NaN.  The order of a row's sum follows N and K alone, so its bits do not
  * depend on M.  x: bf16 [M][K], pitch ldx; bias: bf16 [N] or NULL; y: bf16
  * [M][N], pitch ldy (any: y and bias need 2-byte alignment only).
  * Requirements: as above, M <= 2^19, ldx >= K, ldx % 8 == 0, ldy >= N.

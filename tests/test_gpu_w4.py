@@ -146,3 +146,30 @@ def test_many_tiles(M, N, K, group):
         check(x.float().cpu().numpy(), w4_codes(qw[rows].cpu().numpy(), K), sw[rows].float().cpu().numpy(), group, None,
               y[:, rows].float().cpu().numpy())
     assert clef.poll_status() == 0
+
+
+@pytest.mark.parametrize("group", [32, 64, 128])
+@pytest.mark.parametrize("M,N,K", [(1, 40, 256), (5, 130, 2056), (9, 300, 1152), (16, 100, 4096)])
+def test_magnitudes(M, N, K, group):
+    """Rows of x from bf16's smallest normal numbers to its largest."""
+    rng = np.random.default_rng(M + N + K + group)
+    amp = np.asarray([3e38, 1.0, 2.0 ** 116, 2.0 ** 113, 2.0 ** 120, 1e-37, 1e20, 2.0 ** 127])[np.arange(M) % 8][:, None]
+    x = bf16(rng.uniform(-1, 1, (M, K)) * amp)
+    codes = rng.integers(-8, 8, (N, K))
+    kp = (K + 127) // 128 * 128
+    sw = bf16(rng.uniform(1e-6, 2e-5, (N, kp // group)))
+    b = bf16(rng.standard_normal(N))
+    qw = torch.from_numpy(w4_pack(codes)).cuda()
+    y = clef.w4_linear(dev_bf16(x), qw, dev_bf16(sw), dev_bf16(b))
+    check(x, codes, sw, group, b, y.float().cpu().numpy())
+    for m in range(M):
+        assert torch.equal(clef.w4_linear(dev_bf16(x[m:m + 1]), qw, dev_bf16(sw), dev_bf16(b))[0], y[m])
+    if M > 1:      # what is not finite stays in its row
+        for bad in (np.inf, -np.inf, np.nan):
+            w = x.copy()
+            w[1, 7] = bad
+            z = clef.w4_linear(dev_bf16(w), qw, dev_bf16(sw), dev_bf16(b))
+            assert z[1].isnan().all()
+            z[1] = y[1]
+            assert torch.equal(z, y)
+    assert clef.poll_status() == 0

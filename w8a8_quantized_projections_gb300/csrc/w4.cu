@@ -25,7 +25,9 @@
 // The 8 in u leaves by the sum's start value, -8 2^-24 sum x over the group.
 // x is held in fp16, each run of K that is summed apart scaled by a power of
 // two to a largest magnitude in [2^13, 2^14): bf16 has fewer bits than fp16,
-// so only values under 2^-23 of the run's largest lose any.
+// so only values under 2^-23 of the run's largest lose any, and none more than 2^-38
+// of it.  As the sums are of (c + 8) x, their rounding goes by (|c| + 8) |x|: a value of x some 2^20 times as
+// large as the others hides theirs in its group, whatever its own code is.
 #include <atomic>
 #include <cstdint>
 
@@ -128,7 +130,9 @@ struct W4Args {
 template <int NT, int GROUP, int WARPS>
 __global__ void __launch_bounds__(WARPS * 32, NT == 1 ? 2 : 1) w4_linear_kernel(const W4Args a) {
     extern __shared__ __align__(16) uint8_t smem[];
-    __shared__ float s_unit[NT * 8][kParts];      // what a part's sum of a row of x is multiplied by
+    // what a part's sum of a row of x is multiplied by, but for 2^12 (up to 2^138 does not fit) that
+    // the finished sum is
+    __shared__ float s_unit[NT * 8][kParts];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
     uint32_t rank;
     asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(rank));
@@ -224,7 +228,7 @@ __global__ void __launch_bounds__(WARPS * 32, NT == 1 ? 2 : 1) w4_linear_kernel(
             top = __vmaxu2(top, __vmaxu2(__vmaxu2(v.x & 0x7FFF7FFFu, v.y & 0x7FFF7FFFu), __vmaxu2(v.z & 0x7FFF7FFFu, v.w & 0x7FFF7FFFu)));
         }
         top = __reduce_max_sync(0xFFFFFFFFu, max(top & 0xFFFFu, top >> 16)) << 16;      // bf16 bits order like integers
-        const int e = top ? max(-100, min(120, 13 - (int)(top >> 23) + 127)) : 0;
+        const int e = top ? min(120, 13 - (int)(top >> 23) + 127) : 0;      // -115 or more
         const float up = __uint_as_float((uint32_t)(127 + e) << 23);
 #pragma unroll 2
         for (int o = lane; o < (words + 31) / 32 * 32; o += 32) {
@@ -248,7 +252,7 @@ __global__ void __launch_bounds__(WARPS * 32, NT == 1 ? 2 : 1) w4_linear_kernel(
             for (int s = 1; s < GROUP / 8; s <<= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, s);
             if (o < words && (o & (GROUP / 8 - 1)) == 0) x_sums[(p * a.part * kPer + o / (GROUP / 8)) * NT * 8 + m] = -0x1p-21f * sum;
         }
-        if (lane == 0) s_unit[m][p] = __uint_as_float((uint32_t)(127 + 24 - e) << 23);
+        if (lane == 0) s_unit[m][p] = __uint_as_float((uint32_t)(127 + 12 - e) << 23);
     }
     __syncthreads();
 
@@ -384,6 +388,7 @@ __global__ void __launch_bounds__(WARPS * 32, NT == 1 ? 2 : 1) w4_linear_kernel(
                 float v = q[0];
 #pragma unroll
                 for (int p = 1; p < kParts; ++p) v += q[p];
+                v *= 0x1p12f;
                 if (a.bias) v += __uint_as_float((uint32_t)a.bias[n] << 16);
                 const __nv_bfloat16 o = __float2bfloat16_rn(v);
                 a.y[(int64_t)(m0 + m) * a.ldy + n] = *reinterpret_cast<const uint16_t *>(&o);
