@@ -168,3 +168,9 @@ def test_reserve_rows():
     res = [*TABLE, P, P, 4, 16, P, P, NUL]
     refused(L.clef_kv_reserve_rows, res, TABLE_BAD + [(4, NUL), (5, NUL), (6, -1), (7, 24), (8, NUL), (8, ODD), (9, ODD)])
     assert L.clef_kv_reserve_rows(NUL, 3, 0, 3, NUL, NUL, 4, 16, NUL, NUL, NUL) == 0
+
+
+def test_attention_scale_in_log2_units():
+    L = clef.library()
+    att = [P, 256, 64, 4, NUL, 4, 0, *LAYER, *TABLE, P, 0.125, 1, P, 256, 64, NUL, NUL, 0, NUL]
+    refused(L.clef_kv_attention, att, [(20, 3e38), (20, -3e38), (20, float("-inf"))])

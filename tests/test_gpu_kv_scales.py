@@ -53,3 +53,21 @@ def test_one_page_at_the_end(kind, n, last):
     q = bf16(rng.standard_normal((3 * n, 2, dim)))
     got, lse = run(rng, c, table, lens, q)
     check(c, table, lens, q, np.arange(4) * n, got, lse)
+
+
+@pytest.mark.parametrize("kind", ["int8", "e4m3"])
+@pytest.mark.parametrize("n,dim", [(1, 64), (1, 256), (5, 128), (33, 64), (200, 128), (33, 256)])
+@pytest.mark.parametrize("amp,key", [(2.0 ** 110, 1e-33), (2.0 ** 116, 1e-35), (1e38, 1e-37), (1e-37, 1e36), (1e-20, 1e20)])
+def test_query_and_key_sizes(kind, n, dim, amp, key):
+    """Queries up to bf16's largest numbers over keys so small that the products are ordinary, and
+    the other way round."""
+    rng = np.random.default_rng(n + dim)
+    lens, page = [140], 32
+    table, pages = scattered_table(rng, lens, page)
+    c = Cache(kind, pages, 1, page, dim)
+    new = rng.standard_normal((2, 140, 1, dim))
+    new[0] = np.clip(new[0], -3, 3) * key
+    c.append(table[0], 140, bf16(new))
+    q = bf16(np.clip(rng.standard_normal((n, 2, dim)), -3, 3) * amp)
+    got, lse = run(rng, c, table, lens, q)
+    check(c, table, lens, q, [0, n], got, lse)

@@ -393,7 +393,7 @@ __global__ void __launch_bounds__(kThreads, split_ctas<D, NT>()) kv_split_kernel
 #pragma unroll
             for (int w = 0; w < PER / 2; ++w) top = __vmaxu2(top, pq[k][w] & 0x7FFF7FFFu);
             top = __reduce_max_sync(0xFFFFFFFFu, max(top & 0xFFFFu, top >> 16)) << 16;
-            const int e = top ? max(-100, min(120, 13 - (int)(top >> 23) + 127)) : 0;
+            const int e = top ? min(120, 13 - (int)(top >> 23) + 127) : 0;      // -115 or more
             // a negative scale turns the queries, so that x grows with S
             float up = __uint_as_float((uint32_t)(127 + e) << 23);
             if (a.scale_log2 < 0.0f) up = -up;
@@ -411,8 +411,7 @@ __global__ void __launch_bounds__(kThreads, split_ctas<D, NT>()) kv_split_kernel
             }
             if (lane == 0) {
                 const int i = by_group.div(it.r0 + r);
-                // INT8: S comes as sums of (c + 128) 2^-24 q
-                to.qs[r] = fabsf(a.scale_log2) * __uint_as_float((uint32_t)(127 - e) << 23) * (KIND == kKvInt8 ? 0x1p24f : 1.0f);
+                to.qs[r] = fabsf(a.scale_log2) * __uint_as_float((uint32_t)(127 - e) << 23);
                 to.lift[r] = KIND == kKvInt8 ? 0x1p-17f * sum : 0.0f;
                 to.end[r] = r >= it.rn || !a.causal ? it.len : max(0, it.len - it.n + i + 1);
             }
@@ -543,6 +542,9 @@ __global__ void __launch_bounds__(kThreads, split_ctas<D, NT>()) kv_split_kernel
         if (far && lane < ROWS) refs[lane] = -INFINITY;
         __syncwarp();
 
+        // what a sum of products is multiplied by; INT8: the sums are of (c + 128) 2^-24 q, and 2^24
+        // comes last because 2^24 times a large row's own factor does not fit in fp32
+        const auto factor = [](float q, float k) { return KIND == kKvInt8 ? q * k * 0x1p24f : q * k; };
         for (; s0 < it.tok1; s0 += kWarps * STEP) {
             const int s1 = s0 + kWarps * STEP;
             // S^T
@@ -605,7 +607,7 @@ __global__ void __launch_bounds__(kThreads, split_ctas<D, NT>()) kv_split_kernel
 #pragma unroll
                     for (int i = 0; i < 2; ++i) {
                         const float v = fmaxf(s[x][u][i], s[x][u][i + 2]);
-                        const float f = qs[x][i] * ks[u];
+                        const float f = factor(qs[x][i], ks[u]);
                         if (whole || v != -INFINITY) top[i] = fmaxf(top[i], fmaf(v, f, fmaf(-lift[x][i], f, lv[u])));
                     }
                 if (__builtin_expect(far, 0)) {      // the sum over the step, and top without the pages of zeros
@@ -615,7 +617,7 @@ __global__ void __launch_bounds__(kThreads, split_ctas<D, NT>()) kv_split_kernel
                         top[i] = ml[i] = -INFINITY;
 #pragma unroll
                         for (int u = 0; u < TILES; ++u) {
-                            const float v = fmaxf(s[x][u][i], s[x][u][i + 2]), f = qs[x][i] * ks[u];
+                            const float v = fmaxf(s[x][u][i], s[x][u][i + 2]), f = factor(qs[x][i], ks[u]);
                             if (v == -INFINITY) continue;
                             ml[i] = fmaxf(ml[i], fmaf(v, f, -lift[x][i] * f));
                             if (inv[u] >= 0.0f) top[i] = fmaxf(top[i], fmaf(v, f, fmaf(-lift[x][i], f, lv[u])));
@@ -627,7 +629,7 @@ __global__ void __launch_bounds__(kThreads, split_ctas<D, NT>()) kv_split_kernel
                         l[x][i] *= ex2_diff(was, ml[i]);
 #pragma unroll
                         for (int u = 0; u < TILES; ++u) {
-                            const float f = qs[x][i] * ks[u], off = fmaf(-lift[x][i], f, kLift - ml[i]);
+                            const float f = factor(qs[x][i], ks[u]), off = fmaf(-lift[x][i], f, kLift - ml[i]);
 #pragma unroll
                             for (int h = 0; h < 4; h += 2)
                                 if (s[x][u][i + h] != -INFINITY) l[x][i] += ex2(fmaf(s[x][u][i + h], f, off));
@@ -664,7 +666,7 @@ __global__ void __launch_bounds__(kThreads, split_ctas<D, NT>()) kv_split_kernel
                     float p[4], f[2], off[2];
 #pragma unroll
                     for (int i = 0; i < 2; ++i) {
-                        f[i] = qs[x][i] * ks[u];
+                        f[i] = factor(qs[x][i], ks[u]);
                         off[i] = fmaf(-lift[x][i], f[i], lv[u] - ref[i]);
                     }
 #pragma unroll
@@ -1166,7 +1168,7 @@ __global__ void __launch_bounds__(Tile<D>::kThreadsAll, 1) kv_tile_kernel(const 
 #pragma unroll
                         for (int o = 1; o < LPR; o <<= 1) top = __vmaxu2(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
                         top = max(top & 0xFFFFu, top >> 16) << 16;
-                        const int e = top ? max(-100, min(120, 13 - (int)(top >> 23) + 127)) : 0;
+                        const int e = top ? min(120, 13 - (int)(top >> 23) + 127) : 0;      // -115 or more
                         // a negative scale turns the queries, so that x grows with S
                         float up = __uint_as_float((uint32_t)(127 + e) << 23);
                         if (a.scale_log2 < 0.0f) up = -up;
@@ -1939,7 +1941,7 @@ extern "C" int clef_kv_attention(const void *q, int64_t ldq, int64_t ldq_head, i
     if (rows == 0) return CLEF_OK;
     if (seqs == 0) return kv_fail("rows without a sequence");
     if (!row_start && rows % seqs != 0) return kv_fail("without row_start, rows must be a multiple of the sequences");
-    if (!(scale == scale) || scale > 3.0e38f || scale < -3.0e38f) return kv_fail("scale must be finite");
+    if (!(fabsf(scale * kLog2e) <= 3.402823466e38f)) return kv_fail("scale must be finite, in units of log2 too");
     if (ldq < 0 || ldq_head < 0 || ldq % 8 || ldq_head % 8) return kv_fail("query pitches must be multiples of 8");
     if (ldo < dim || ldo_head < dim || ldo % 8 || ldo_head % 8) return kv_fail("output pitches must be multiples of 8 that hold a head");
     if (!q || !codes || !scales || !table || !lens || !out) return kv_fail("null pointer");
