@@ -444,7 +444,8 @@ int clef_w4_linear(const void *x, int64_t ldx, const void *qw, const void *sw, i
  * row i of sequence b (n rows) and head h reading key/value head h / (q_heads
  * / heads):  o = sum_j softmax_j(scale * q . k_j) v_j over its tokens j <
  * lens[b], with causal only j <= lens[b] - n + i (the queries are the last
- * tokens).  Rows that see nothing are zeros.  q: bf16, pitches ldq (token) and
+ * tokens).  Rows that see nothing are zeros; a row of a head whose queries are
+ * not all finite is NaN.  q: bf16, pitches ldq (token) and
  * ldq_head; rows and row_start as for append; out: bf16, pitches ldo,
  * ldo_head; lse: fp32 [rows][q_heads], log of the sum of exponentials
  * (-infinity for a row that sees nothing), or NULL.  Sums are fp32; the

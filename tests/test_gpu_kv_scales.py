@@ -71,3 +71,32 @@ def test_query_and_key_sizes(kind, n, dim, amp, key):
     q = bf16(np.clip(rng.standard_normal((n, 2, dim)), -3, 3) * amp)
     got, lse = run(rng, c, table, lens, q)
     check(c, table, lens, q, [0, n], got, lse)
+
+
+@pytest.mark.parametrize("kind", ["int8", "e4m3"])
+@pytest.mark.parametrize("dim", [64, 128, 256])
+@pytest.mark.parametrize("n,len_", [(1, 40), (1, 1100), (5, 700), (40, 300), (20, 2300)])
+@pytest.mark.parametrize("value", [0.5, 1e-30])
+def test_queries_that_are_not_finite(kind, dim, n, len_, value):
+    """An infinity or a NaN makes its own row and head NaN, and nothing else; rows that see nothing are zeros."""
+    rng = np.random.default_rng(n + dim)
+    lens, page = [len_, n - 1], 16
+    table, pages = scattered_table(rng, lens, page)
+    c = Cache(kind, pages, 1, page, dim)
+    for b, x in enumerate(lens):
+        new = rng.standard_normal((2, x, 1, dim))
+        new[0] = -np.abs(new[0])                        # products with an infinity all of one sign
+        new[1] *= value
+        c.append(table[b], x, bf16(new))
+    q = bf16(rng.standard_normal((2 * n, 2, dim)))
+    ref, ref_lse = run(rng, c, table, lens, q)
+    assert np.isfinite(ref).all()
+    for bad in (np.inf, -np.inf, np.nan):
+        p = q.copy()
+        p[n // 2, 1, dim // 3] = bad
+        p[n, 0, 0] = bad                                # the first row of the second sequence sees nothing
+        got, lse = run(rng, c, table, lens, p)
+        assert np.isnan(got[n // 2, 1]).all() and np.isnan(lse[n // 2, 1])
+        assert not got[n, 0].any() and lse[n, 0] == -np.inf
+        got[n // 2, 1], lse[n // 2, 1] = ref[n // 2, 1], ref_lse[n // 2, 1]
+        assert np.array_equal(got, ref) and np.array_equal(lse, ref_lse)

@@ -145,6 +145,13 @@ __device__ __forceinline__ bool far_scale(float vs) { return vs != 0.0f && !(vs 
 // 2^(a - b) for running maxima, 0 when a is -inf (b may be -inf then too)
 __device__ __forceinline__ float ex2_diff(float a, float b) { return a == -INFINITY ? 0.0f : ex2(a - b); }
 
+// What a query row is multiplied by on its way to fp16, of whose largest magnitude top is the bits:
+// 2^e, or NaN for a row that is not finite, so that its result is whatever its tokens are (an infinity
+// as it is would make minus infinity of a product, which is a token that is not seen).
+__device__ __forceinline__ float row_factor(uint32_t top, int e) {
+    return __uint_as_float(top >= 0x7F800000u ? 0x7FC00000u : (uint32_t)(127 + e) << 23);
+}
+
 __device__ __forceinline__ void mma_regs(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
     asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
         : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
@@ -395,7 +402,7 @@ __global__ void __launch_bounds__(kThreads, split_ctas<D, NT>()) kv_split_kernel
             top = __reduce_max_sync(0xFFFFFFFFu, max(top & 0xFFFFu, top >> 16)) << 16;
             const int e = top ? min(120, 13 - (int)(top >> 23) + 127) : 0;      // -115 or more
             // a negative scale turns the queries, so that x grows with S
-            float up = __uint_as_float((uint32_t)(127 + e) << 23);
+            float up = row_factor(top, e);
             if (a.scale_log2 < 0.0f) up = -up;
             float sum = 0.0f;
 #pragma unroll
@@ -757,8 +764,8 @@ __global__ void __launch_bounds__(kThreads, split_ctas<D, NT>()) kv_split_kernel
                 for (int w = 0; w < kWarps; ++w) ll = fmaf(s_l[w * ROWS + r], ex2_diff(at[w * ROWS], ml), ll);
                 back = ml == -INFINITY ? 0.0f : ex2(0.5f * (mm - ml));
             }
-            const float inv = ll > 0.0f ? __fdiv_rn(1.0f, ll) : 0.0f;
-            const float lse = ll > 0.0f ? ml - kLift + log2f(ll) : -INFINITY;
+            const float inv = ll == 0.0f ? 0.0f : __fdiv_rn(1.0f, ll);      // (NaN stays)
+            const float lse = ll == 0.0f ? -INFINITY : ml - kLift + log2f(ll);
             const int i = by_group.div(done.r0 + r), hq = done.head * a.group + (done.r0 + r) - i * a.group;
             const int64_t place = done.b * a.part_units + ((int64_t)done.head * done.rows + done.r0 + r) * done.splits + done.split;
             if (done.splits > 1) {
@@ -1170,7 +1177,7 @@ __global__ void __launch_bounds__(Tile<D>::kThreadsAll, 1) kv_tile_kernel(const 
                         top = max(top & 0xFFFFu, top >> 16) << 16;
                         const int e = top ? min(120, 13 - (int)(top >> 23) + 127) : 0;      // -115 or more
                         // a negative scale turns the queries, so that x grows with S
-                        float up = __uint_as_float((uint32_t)(127 + e) << 23);
+                        float up = row_factor(top, e);
                         if (a.scale_log2 < 0.0f) up = -up;
 #pragma unroll
                         for (int x = 0; x < 8; ++x)
@@ -1430,17 +1437,17 @@ __global__ void __launch_bounds__(Tile<D>::kThreadsAll, 1) kv_tile_kernel(const 
                 if (!pair_sync()) break;
                 l += s_pair[0][half ^ 1][row];
             }
-            const float inv = l > 0.0f ? __fdiv_rn(1.0f, l) : 0.0f;
+            const float inv = l == 0.0f ? 0.0f : __fdiv_rn(1.0f, l);      // (NaN stays)
             const float ml = apart ? s_ref[tid] : m;
             if (row < mine && half == 0) {
-                const float lse = l > 0.0f ? ml - (kLift - kSlack) + log2f(l) : -INFINITY;
+                const float lse = l == 0.0f ? -INFINITY : ml - (kLift - kSlack) + log2f(l);
                 if (t.splits > 1)
                     a.part_lse[t.b * a.part_units + ((int64_t)t.head * t.rows + r) * t.splits + t.split] = lse;
                 else if (a.lse)
                     a.lse[(int64_t)(t.row0 + i) * a.q_heads + hq] = lse == -INFINITY ? -INFINITY : lse * (1.0f / kLog2e);
             }
             constexpr int CHUNKS = T::kOutCols / 64;             // 128-byte chunks of the warp's rows
-            const bool part = t.splits > 1, none = !(inv > 0.0f);
+            const bool part = t.splits > 1, none = l == 0.0f;
             uint8_t *stage = sq + half * CHUNKS * T::kChunkQ + quad * 32 * 128;
             for (int pass = 0; pass < (part ? 2 : 1); ++pass) {          // fp32 takes two
                 // 32 columns at a time: four 16-byte units of bf16, or eight of fp32
@@ -1804,7 +1811,7 @@ __global__ void __launch_bounds__(kThreads) kv_join_kernel(const AttnArgs a) {
                 *reinterpret_cast<float2 *>(&s_o[warp][64 * k + 2 * lane]) = make_float2(o[2 * k], o[2 * k + 1]);
             __syncthreads();
             sum = (s_sum[0] + s_sum[1]) + (s_sum[2] + s_sum[3]);
-            const float inv = sum > 0.0f ? __fdiv_rn(1.0f, sum) : 0.0f;
+            const float inv = sum == 0.0f ? 0.0f : __fdiv_rn(1.0f, sum);      // (NaN stays)
             const int i = r / a.group, hq = head * a.group + r - i * a.group;
             uint16_t *dst = a.out + (int64_t)(row0 + i) * a.ldo + (int64_t)hq * a.ldo_head;
             for (int d = tid * 2; d < D; d += 2 * kThreads) {
@@ -1813,7 +1820,7 @@ __global__ void __launch_bounds__(kThreads) kv_join_kernel(const AttnArgs a) {
                 *reinterpret_cast<__nv_bfloat162 *>(dst + d) = __floats2bfloat162_rn(x * inv, y * inv);
             }
             if (a.lse && tid == 0)
-                a.lse[(int64_t)(row0 + i) * a.q_heads + hq] = sum > 0.0f ? (mm + log2f(sum)) * (1.0f / kLog2e) : -INFINITY;
+                a.lse[(int64_t)(row0 + i) * a.q_heads + hq] = sum == 0.0f ? -INFINITY : (mm + log2f(sum)) * (1.0f / kLog2e);
         }
     pdl_launch_dependents();
 }
