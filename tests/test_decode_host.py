@@ -174,3 +174,31 @@ def test_attention_scale_in_log2_units():
     L = clef.library()
     att = [P, 256, 64, 4, NUL, 4, 0, *LAYER, *TABLE, P, 0.125, 1, P, 256, 64, NUL, NUL, 0, NUL]
     refused(L.clef_kv_attention, att, [(20, 3e38), (20, -3e38), (20, float("-inf"))])
+
+
+def test_ragged_workspace_is_near_the_equal_rows_form():
+    """With row_start the places follow the call's rows: at most those of the equal-rows form for
+    sequences of a few rows, and for those of many rows a place for each row, head and run."""
+    L = clef.library()
+    n = C.c_int64(-1)
+
+    def need(rows, ragged, seqs, hq, h, d, top):
+        assert L.clef_kv_attention_workspace(rows, ragged, seqs, hq, h, d, top, C.byref(n)) == 0
+        return n.value
+
+    for rows, seqs, hq, h, d, top in ((64, 64, 48, 8, 128, 8192), (256, 256, 32, 8, 128, 8192), (4096, 1024, 32, 8, 128, 4096),
+                                      (8, 8, 24, 4, 256, 32768), (1565, 64, 48, 8, 128, 8192), (40, 3, 8, 1, 64, 100000)):
+        runs = min(16, 152 // h, -(-top // 128) // 8)
+        few = 16 if top >= 8192 else 8
+        if top > 16384:
+            few = -(-top // 1024)
+        ragged = need(rows, 1, seqs, hq, h, d, top)
+        place = 4 * (d + 1)
+        assert ragged <= place * rows * hq * (few + runs), (rows, seqs)
+        if rows % seqs == 0 and rows // seqs * (hq // h) <= 16:
+            equal = need(rows, 0, seqs, hq, h, d, top)
+            assert equal <= ragged <= equal + place * min(rows * hq * runs, seqs * 152 * 256), (rows, seqs)
+    assert need(1, 1, 1, 8, 2, 128, 512) == 0                   # nothing is ever cut
+    # never more for more of the table
+    tops = [need(100, 1, 7, 8, 2, 64, t) for t in (100, 512, 513, 1024, 1900, 2048, 8192, 8193, 40000, 10 ** 6)]
+    assert tops == sorted(tops)

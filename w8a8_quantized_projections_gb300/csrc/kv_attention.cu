@@ -95,6 +95,17 @@ __host__ __device__ inline int tile_split_tokens(int len, int splits) {
     return (steps + splits - 1) / splits * 128;
 }
 
+// Where the places of a sequence begin: no sequence needs more than per_seq of
+// them, nor more than per_row for each of its rows of queries, so that sequence b, whose
+// first row is row0, may begin at the smaller of what those before it can have needed.
+struct Places {
+    int64_t first, per_seq, per_row;
+    __device__ __forceinline__ int64_t of(int b, int row0) const {
+        const int64_t x = b * per_seq, y = row0 * per_row;
+        return first + (x < y ? x : y);
+    }
+};
+
 struct AttnArgs {
     KvPool pool;
     KvTable tab;
@@ -106,11 +117,11 @@ struct AttnArgs {
     const int32_t *start;       // [seqs + 1] or null
     int rows, per_seq, group, q_heads, causal;
     float scale_log2;
-    // partial results of the sequences that are cut: each has part_units places
-    // of its own, place (head * rows + row) * splits + split
-    float *part;                // [seqs][part_units][dim]
-    float *part_lse;            // [seqs][part_units], base 2
-    int64_t part_units;
+    // partial results of the sequences that are cut, place (head * rows + row) * splits + split
+    // from the sequence's first one on
+    float *part;                // [places][dim]
+    float *part_lse;            // [places], base 2
+    Places few, many;           // of sequences with few and with many rows
     unsigned int *status;
     uint64_t wait_limit_ns;
     int force_timeout;
@@ -767,7 +778,7 @@ __global__ void __launch_bounds__(kThreads, split_ctas<D, NT>()) kv_split_kernel
             const float inv = ll == 0.0f ? 0.0f : __fdiv_rn(1.0f, ll);      // (NaN stays)
             const float lse = ll == 0.0f ? -INFINITY : ml - kLift + log2f(ll);
             const int i = by_group.div(done.r0 + r), hq = done.head * a.group + (done.r0 + r) - i * a.group;
-            const int64_t place = done.b * a.part_units + ((int64_t)done.head * done.rows + done.r0 + r) * done.splits + done.split;
+            const int64_t place = a.few.of(done.b, done.row0) + ((int64_t)done.head * done.rows + done.r0 + r) * done.splits + done.split;
             if (done.splits > 1) {
                 if (lane == 0) a.part_lse[place] = lse;
             } else if (a.lse && lane == 0) {
@@ -1442,7 +1453,7 @@ __global__ void __launch_bounds__(Tile<D>::kThreadsAll, 1) kv_tile_kernel(const 
             if (row < mine && half == 0) {
                 const float lse = l == 0.0f ? -INFINITY : ml - (kLift - kSlack) + log2f(l);
                 if (t.splits > 1)
-                    a.part_lse[t.b * a.part_units + ((int64_t)t.head * t.rows + r) * t.splits + t.split] = lse;
+                    a.part_lse[a.many.of(t.b, t.row0) + ((int64_t)t.head * t.rows + r) * t.splits + t.split] = lse;
                 else if (a.lse)
                     a.lse[(int64_t)(t.row0 + i) * a.q_heads + hq] = lse == -INFINITY ? -INFINITY : lse * (1.0f / kLog2e);
             }
@@ -1493,7 +1504,7 @@ __global__ void __launch_bounds__(Tile<D>::kThreadsAll, 1) kv_tile_kernel(const 
                                                                          (((u & 7) ^ ((k + lr) & 7)) << 4));
                         const int ra = t.first + q * 128 + rr;
                         if (t.splits > 1) {
-                            const int64_t place = t.b * a.part_units + ((int64_t)t.head * t.rows + ra) * t.splits + t.split;
+                            const int64_t place = a.many.of(t.b, t.row0) + ((int64_t)t.head * t.rows + ra) * t.splits + t.split;
                             *reinterpret_cast<uint4 *>(a.part + place * D + half * T::kOutCols + pass * (T::kOutCols / 2) + u * 4) = o;
                         } else {
                             const int x = g0 + rr, qi = by.div(x);
@@ -1777,10 +1788,11 @@ __global__ void __launch_bounds__(kThreads) kv_join_kernel(const AttnArgs a) {
     query_rows(a, b, row0, n);
     const int rows = n * a.group, len = kv_length(a.tab, b, a.pool.page_log2, a.status);
     const int splits = rows <= kFewRows ? split_count(len) : tile_splits(rows, len, H, D);
+    const int64_t first = (rows <= kFewRows ? a.few : a.many).of(b, row0);
     if (splits > 1)
         for (int64_t slot = blockIdx.x; slot < (int64_t)rows * H; slot += gridDim.x) {
             const int head = (int)(slot / rows), r = (int)(slot - (int64_t)head * rows);
-            const float *pl = a.part_lse + b * a.part_units + slot * splits, *po = a.part + (b * a.part_units + slot * splits) * D;
+            const float *pl = a.part_lse + first + slot * splits, *po = a.part + (first + slot * splits) * D;
             float mm = -INFINITY;
             for (int s = tid; s < splits; s += kThreads) mm = fmaxf(mm, pl[s]);
 #pragma unroll
@@ -1854,7 +1866,8 @@ struct Plan {
     bool few, tile;
     int row_max;                     // most rows a key/value head of a sequence with few
     int64_t few_items, tile_items;   // at most
-    int64_t units;                   // places of a sequence; 0: nothing is split
+    Places few_at, many_at;
+    int64_t places;                  // 0: nothing is split
     int64_t join_rows;               // rows of a sequence that may be split, over its heads, at most
 };
 
@@ -1866,14 +1879,18 @@ Plan make_plan(int64_t rows, bool ragged, int64_t seqs, int group, int heads, in
     for (int64_t len : {max_len, (int64_t)1024, (int64_t)8192})
         if (len <= max_len && split_count((int)len) > few_splits) few_splits = split_count((int)len);
     const int64_t per = ragged ? rows * group : rows / seqs * group;   // rows of one sequence, at most
+    const auto reserve = [&](Places &at, int64_t per_seq, int64_t per_row) {
+        at = {p.places, per_seq, per_row};
+        p.places += per_seq * seqs < per_row * rows ? per_seq * seqs : per_row * rows;
+    };
     p.few = ragged || per <= kFewRows;
     p.tile = per > kFewRows;
     if (p.few) {
         p.row_max = (int)(per < kFewRows ? per : kFewRows);
         p.few_items = seqs * heads * ((p.row_max + 7) / 8) * few_splits;
         if (few_splits > 1) {
-            p.units = (int64_t)heads * p.row_max * few_splits;
             p.join_rows = (int64_t)heads * p.row_max;
+            reserve(p.few_at, p.join_rows * few_splits, (int64_t)heads * group * few_splits);
         }
     }
     if (p.tile) {
@@ -1881,13 +1898,16 @@ Plan make_plan(int64_t rows, bool ragged, int64_t seqs, int group, int heads, in
         // a split sequence has at most kTileSlots items
         p.tile_items = ragged ? (rows * group / tr + seqs) * heads + seqs * kTileSlots
                               : seqs * (((per + tr - 1) / tr) * heads * tile_splits((int)per, (int)max_len, heads, dim));
-        const bool cut = ragged ? max_len > 1920 : tile_splits((int)per, (int)max_len, heads, dim) > 1;
+        // the most splits of a sequence of up to max_len tokens: of 1,024 and more, over the SMs that its
+        // heads leave (one row tile)
+        int64_t splits = ((max_len >> 7) + ((max_len & 127) != 0)) / 8;
+        if (splits > kTileMaxSplits) splits = kTileMaxSplits;
+        if (splits > kTileSlots / heads) splits = kTileSlots / heads;
+        const bool cut = ragged ? splits > 1 : tile_splits((int)per, (int)max_len, heads, dim) > 1;
         if (cut) {
-            int64_t units = (int64_t)kTileSlots * tr, join = units / 2;
-            const int64_t most = per * heads;
-            if (join > most) join = most;
-            if (units > most * kTileMaxSplits) units = most * kTileMaxSplits;
-            if (p.units < units) p.units = units;
+            const int64_t units = (int64_t)kTileSlots * tr, most = per * heads;      // a split sequence has at most kTileSlots items
+            const int64_t join = units / 2 < most ? units / 2 : most;
+            reserve(p.many_at, units < most * splits ? units : most * splits, (int64_t)heads * group * splits);
             if (p.join_rows < join) p.join_rows = join;
         }
     }
@@ -1907,7 +1927,7 @@ cudaError_t launch_attention(const AttnArgs &a, int kind, const Plan &p, int sms
             e = kind == kKvInt8 ? launch_split<kKvInt8, D, 2>(a, p.few_items, sms, st)
                                 : launch_split<kKvE4m3, D, 2>(a, p.few_items, sms, st);
     }
-    if (e != cudaSuccess || p.units == 0) return e;
+    if (e != cudaSuccess || p.places == 0) return e;
     // a CTA a row, up to 64 CTAs an SM over all sequences
     int64_t x = p.join_rows;
     const int64_t most = (int64_t)sms * 64 / a.tab.seqs + 1;
@@ -1928,7 +1948,7 @@ extern "C" int clef_kv_attention_workspace(int64_t rows, int ragged, int64_t seq
     if (heads < 1 || q_heads < heads || q_heads % heads != 0) return kv_fail("q_heads must be a multiple of heads");
     if (dim != 64 && dim != 128 && dim != 256) return kv_fail("dim must be 64, 128 or 256");
     if (max_len < 0 || max_len > 0x7FFFFFFF) return kv_fail("max_len out of range");
-    *bytes = seqs * make_plan(rows, ragged != 0, seqs, q_heads / heads, heads, dim, max_len).units * (dim + 1) * 4;
+    *bytes = make_plan(rows, ragged != 0, seqs, q_heads / heads, heads, dim, max_len).places * (dim + 1) * 4;
     return CLEF_OK;
 }
 
@@ -1957,7 +1977,7 @@ extern "C" int clef_kv_attention(const void *q, int64_t ldq, int64_t ldq_head, i
         return kv_fail("q, out and workspace must be 16-byte, lse and row_start 4-byte aligned");
     const int64_t top = width * page < 0x7FFFFFFF ? width * page : 0x7FFFFFFF;
     const Plan plan = make_plan(rows, row_start != nullptr, seqs, q_heads / heads, heads, dim, top);
-    const int64_t need = seqs * plan.units * (dim + 1) * 4;
+    const int64_t need = plan.places * (dim + 1) * 4;
     if (need > 0 && (!workspace || workspace_bytes < need)) return kv_fail("workspace smaller than clef_kv_attention_workspace says");
     int sms = 0;
     if ((rc = internal_device(&sms, &a.status))) return rc;
@@ -1975,9 +1995,10 @@ extern "C" int clef_kv_attention(const void *q, int64_t ldq, int64_t ldq_head, i
     a.q_heads = q_heads;
     a.causal = causal != 0;
     a.scale_log2 = scale * kLog2e;
-    a.part_units = plan.units;
+    a.few = plan.few_at;
+    a.many = plan.many_at;
     a.part = static_cast<float *>(workspace);
-    a.part_lse = a.part + seqs * plan.units * dim;
+    a.part_lse = a.part + plan.places * dim;
     a.wait_limit_ns = internal_wait_limit(&a.force_timeout);
     sms = internal_launch_sms(sms);
     cudaStream_t st = static_cast<cudaStream_t>(stream);
