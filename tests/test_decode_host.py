@@ -202,3 +202,11 @@ def test_ragged_workspace_is_near_the_equal_rows_form():
     # never more for more of the table
     tops = [need(100, 1, 7, 8, 2, 64, t) for t in (100, 512, 513, 1024, 1900, 2048, 8192, 8193, 40000, 10 ** 6)]
     assert tops == sorted(tops)
+
+
+def test_alignment_of_row_numbers():
+    L = clef.library()
+    app = [P, 128, 64, P, 128, 64, 4, P, 0, *LAYER, *TABLE, P, NUL]
+    refused(L.clef_kv_append, app, [(7, ODD)])
+    gat = [0, *LAYER, *TABLE, P, P, 5, P, 128, P, 128, NUL]
+    refused(L.clef_kv_gather, gat, [(13, ODD), (14, ODD)])

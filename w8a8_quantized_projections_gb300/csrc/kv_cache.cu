@@ -284,7 +284,8 @@ extern "C" int clef_kv_append(const void *k, int64_t ldk, int64_t ldk_head, cons
     if (rows == 0 || seqs == 0) return rows == 0 ? CLEF_OK : kv_fail("rows without a sequence");
     if (!row_start && rows % seqs != 0) return kv_fail("without row_start, rows must be a multiple of the sequences");
     if (!k || !v || !codes || !scales || !table || !lens) return kv_fail("null pointer");
-    if (kv_misaligned(k, 16) || kv_misaligned(v, 16)) return kv_fail("k and v must be 16-byte aligned");
+    if (kv_misaligned(k, 16) || kv_misaligned(v, 16) || kv_misaligned(row_start, 4))
+        return kv_fail("k and v must be 16-byte, row_start 4-byte aligned");
     if (ldk % 8 || ldv % 8 || ldk_head % 8 || ldv_head % 8 || ldk < 0 || ldv < 0 || ldk_head < 0 || ldv_head < 0)
         return kv_fail("token and head pitches must be multiples of 8");
     int sms = 0;
@@ -325,7 +326,8 @@ extern "C" int clef_kv_gather(int kind, const void *codes, int64_t plane_bytes, 
     if (ldk < row || ldv < row || ldk % 8 || ldv % 8) return kv_fail("output pitches must hold a row and be multiples of 8");
     if (rows == 0) return CLEF_OK;
     if (!codes || !scales || !table || !seq || !pos || !k_out || !v_out) return kv_fail("null pointer");
-    if (kv_misaligned(k_out, 16) || kv_misaligned(v_out, 16)) return kv_fail("outputs must be 16-byte aligned");
+    if (kv_misaligned(k_out, 16) || kv_misaligned(v_out, 16) || kv_misaligned(seq, 4) || kv_misaligned(pos, 4))
+        return kv_fail("outputs must be 16-byte, seq and pos 4-byte aligned");
     int sms = 0;
     if ((rc = internal_device(&sms, &a.status))) return rc;
     a.seq = seq;
