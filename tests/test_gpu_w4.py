@@ -173,3 +173,21 @@ def test_magnitudes(M, N, K, group):
             z[1] = y[1]
             assert torch.equal(z, y)
     assert clef.poll_status() == 0
+
+
+def test_most_rows():
+    """The most rows that are allowed, over a K whose blocks have eight rows: more blocks than a grid has."""
+    M, N, K = 1 << 19, 24, 29952
+    rng = np.random.default_rng(7)
+    qw, sw = clef.quant_w4(dev_bf16(rng.standard_normal((N, K)) * 0.02), 128)
+    x = torch.zeros((M, K), dtype=torch.bfloat16, device="cuda")
+    few = dev_bf16(rng.standard_normal((21, K)))
+    ref = clef.w4_linear(few, qw, sw)
+    at = torch.tensor([*range(8), M // 2, *range(65535 * 8 - 4, M)], device="cuda")
+    x[at] = few
+    y = torch.full((M, N + 2), 3.0, dtype=torch.bfloat16, device="cuda")
+    clef.w4_linear(x, qw, sw, y=y[:, :N])
+    assert torch.equal(y[at, :N], ref) and (y[:, N:] == 3).all()
+    y[at] = 0
+    assert not y[:, :N].any()
+    assert clef.poll_status() == 0

@@ -611,7 +611,6 @@ extern "C" int clef_w4_linear(const void *x, int64_t ldx, const void *qw, const 
     a.bias = static_cast<const uint16_t *>(bias);
     a.y = static_cast<uint16_t *>(y);
     a.ldy = ldy;
-    a.M = (int)M;
     a.N = (int)N;
     a.K = (int)K;
     a.kb = kb;
@@ -620,8 +619,15 @@ extern "C" int clef_w4_linear(const void *x, int64_t ldx, const void *qw, const 
     a.tiles = 0;      // by the number of warps
     sms = internal_launch_sms(sms);
     cudaStream_t st = static_cast<cudaStream_t>(stream);
-    const int blocks_m = (int)((M + block_m - 1) / block_m);
-    const cudaError_t e = block_m == 8 ? launch_w4_group<1>(a, group, split, blocks_m, sms, st)
-                                       : launch_w4_group<2>(a, group, split, blocks_m, sms, st);
+    // (a grid has up to 65,535 blocks of rows)
+    cudaError_t e = cudaSuccess;
+    for (int64_t left = M; left > 0 && e == cudaSuccess; left -= a.M) {
+        a.M = (int)(left < 65535 * block_m ? left : 65535 * block_m);
+        const int blocks_m = (int)((a.M + block_m - 1) / block_m);
+        e = block_m == 8 ? launch_w4_group<1>(a, group, split, blocks_m, sms, st)
+                         : launch_w4_group<2>(a, group, split, blocks_m, sms, st);
+        a.x += a.M * ldx;
+        a.y += a.M * ldy;
+    }
     return e == cudaSuccess ? CLEF_OK : internal_cuda_error(e, "4-bit linear launch");
 }
