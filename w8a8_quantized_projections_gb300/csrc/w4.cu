@@ -456,7 +456,7 @@ bool misaligned(const void *p, unsigned to) { return (reinterpret_cast<uintptr_t
 
 constexpr int64_t kMaxW4 = (int64_t)1 << 24, kMaxK = 65536;
 
-constexpr size_t kMaxSmem = 226 * 1024;
+constexpr size_t kMaxSmem = 226 * 1024, kPairSmem = 110 * 1024;      // of a CTA alone on an SM, and of one of two
 
 // Shared memory of a CTA: x's columns, the sums' starts, two tiles' partial sums and the rings.
 size_t w4_smem(int nt, int64_t m, int part, int group, int split, int warps) {
@@ -472,7 +472,7 @@ cudaError_t resident_clusters(int split, size_t smem, int sms, int *clusters) {
     static SmemOptIn opt;
     cudaError_t e = opt.set(reinterpret_cast<const void *>(w4_linear_kernel<NT, GROUP, WARPS>), kMaxSmem);
     if (e != cudaSuccess) return e;
-    const int per_sm = NT == 1 && smem <= 110 * 1024 ? 2 : 1;
+    const int per_sm = NT == 1 && smem <= kPairSmem ? 2 : 1;
     *clusters = sms * per_sm / split;
     if (split > 1) {
         static std::atomic<int> known[64][4][2];   // asked once for each device
@@ -596,13 +596,19 @@ extern "C" int clef_w4_linear(const void *x, int64_t ldx, const void *qw, const 
     if (rc) return rc;
     const int kb = (int)((K + kBlockK - 1) / kBlockK);
     const int part = (kb + kParts - 1) / kParts;
-    // CTAs of a cluster: up to eight rows of x, so many that a CTA's columns of x leave room for two CTAs an SM;
+    // CTAs of a cluster: up to eight rows of x, so many that two CTAs fit into an SM with their columns of x
+    // and the sums' starts (laid out for eight rows: half of one row's columns in groups of 32; 1 x 17408 x
+    // 5120 takes 17.2 us so, 17.6 where the columns alone decide), and that the columns stay under 40 KB
+    // (8 x 5120 x 14336: 14.5 us, 15.8 by the fit alone);
     // past that as few as it takes to fit, as larger clusters leave more SMs without work
-    const auto x_bytes = [&](int64_t m, int split) { return m * (kParts / split * part * kBlockK * 2 + 64); };      // and a sixteenth of it, or less, for its sums
+    const auto x_bytes = [&](int64_t m, int split) { return m * (kParts / split * part * kBlockK * 2 + 64); };
+    const auto too_large = [&](int64_t m, int split) {
+        return x_bytes(m, split) > 40 * 1024 || w4_smem(1, m, part, group, split, 8) > kPairSmem;
+    };
     const int64_t block_m = M > 8 && x_bytes(M < 16 ? M : 16, kParts) <= 120 * 1024 ? 16 : 8;
     const int64_t m = M < block_m ? M : block_m;
     int split = 1;
-    while (split < kParts && (block_m == 8 ? x_bytes(m, split) > 40 * 1024 : w4_smem(2, m, part, group, split, 8) > kMaxSmem)) split *= 2;
+    while (split < kParts && (block_m == 8 ? too_large(m, split) : w4_smem(2, m, part, group, split, 8) > kMaxSmem)) split *= 2;
     W4Args a;
     a.x = static_cast<const uint16_t *>(x);
     a.ldx = ldx;
