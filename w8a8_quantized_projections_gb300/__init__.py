@@ -53,7 +53,7 @@ def library():
     global _lib
     with _lock:
         if _lib is None:
-            path = _build.build()
+            path = _build.build_library()
             if not os.path.exists(path):
                 raise RuntimeError(f"CUDA library missing at {path}")
             L = C.CDLL(path)

@@ -33,6 +33,7 @@ def _load():
     """The compiled module (built with the library on first use if absent or stale)."""
     global _ext
     library()
+    _build.build_extension()
     loader = importlib.machinery.ExtensionFileLoader("clef_decode", _build.EXT)
     ext = importlib.util.module_from_spec(importlib.util.spec_from_file_location("clef_decode", _build.EXT, loader=loader))
     loader.exec_module(ext)
