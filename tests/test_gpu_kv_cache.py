@@ -172,3 +172,36 @@ def test_refusals():
         clef.kv_append(torch.zeros((2, 2, 96), dtype=torch.bfloat16, device="cuda"), torch.zeros((2, 2, 96), dtype=torch.bfloat16, device="cuda"),
                        torch.zeros((2, 4, 2, 16, 96), dtype=torch.int8, device="cuda"), scales, ok["table"], ok["lens"])
     assert clef.poll_status() == 0
+
+
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("page", [16, 64, 128])
+@pytest.mark.parametrize("grows", ["now and then", "every token", "by half a step"])
+def test_values_written_one_by_one(kind, page, grows):
+    """The bound of include/clef.h with the scales that the page went through: half a step of each
+    (int8), or 1/16 of the value as it was and 2^-10 of the scale each time (e4m3)."""
+    rng = np.random.default_rng(page)
+    heads, dim, n = 2, 64, page + 5
+    table, pages = scattered_table(rng, [n], page)
+    c = Cache(kind, pages, heads, page, dim)
+    codes, scales = c.device()
+    new = rng.standard_normal((2, n, heads, dim))
+    if grows != "now and then":
+        new *= (1.03 if grows == "every token" else 1 + 1 / 254) ** np.arange(n)[None, :, None, None]
+    new = bf16(new)
+    tab, seq = dev_i32(table), dev_i32([0] * n)
+    history = np.zeros((n, 2, n, heads))                      # the scale of each token's page after each call
+    at = table[0, np.arange(n) // page]
+    for i in range(n):
+        clef.kv_append(dev_bf16(new[0, i:i + 1]), dev_bf16(new[1, i:i + 1]), codes, scales, tab, dev_i32([i + 1]))
+        history[i] = scales.cpu().numpy().astype(np.float64)[:, at]
+    got = np.stack([t.double().cpu().numpy() for t in clef.kv_gather(codes, scales, tab, seq, dev_i32(np.arange(n)))])
+    for t in range(n):
+        s = history[t:, :, t]                                 # from the token's own append on
+        fresh = np.concatenate([np.ones_like(s[:1], bool), np.diff(s, axis=0) > 0])
+        total, g = (s * fresh).sum(0)[..., None], fresh.sum(0)[..., None] - 1
+        v = np.abs(new[:, t].astype(np.float64))
+        off = total / 2 if kind == "int8" else ((17 / 16) ** (g + 1) - 1) * v + total * (17 / 16) ** g * 2.0 ** -10
+        off = off * (1 + 2.0 ** -16)                          # the fp32 roundings of scales, factors and products
+        assert (np.abs(got[:, t] - new[:, t]) <= off + (v + off) * 2.0 ** -8).all(), t      # and the bf16 of the output
+    assert clef.poll_status() == 0

@@ -63,7 +63,9 @@ def kv_append(k, v, codes, scales, table, lens, row_start=None, stream=None) -> 
     """Writes the newest tokens' keys and values (bf16 [tokens][heads][dim]) of
     one layer into the cache.  `lens` counts them already; a sequence's rows
     are its last tokens: rows row_start[b] .. row_start[b + 1] - 1, or the same
-    number each.  Where the pool may be full, take row_start from kv_reserve."""
+    number each.  Where the pool may be full, take row_start from kv_reserve.
+    A page has one scale a head, so values written one by one are off by more
+    than those of a page written at once (include/clef.h has the bound)."""
     (_ext or _load()).kv_append(k, v, codes, scales, table, lens, row_start, stream)
 
 
