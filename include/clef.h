@@ -411,7 +411,8 @@ int clef_w4_linear(const void *x, int64_t ldx, const void *qw, const void *sw, i
  * take its key plane's address, the value plane following it.  A sequence is a
  * row of table (int32 [seqs][width], pitch ldt) and a length in lens: its
  * token i is at page table[i / page], place i % page.  Entries of a row past
- * the sequence's pages are never read.  refs: int32 [pages], how many
+ * the sequence's pages are never read, but by clef_kv_gather, which is not told
+ * the lengths.  refs: int32 [pages], how many
  * sequences hold a page (0: free).
  *
  * Indices and lengths live in device memory, so the host cannot check them:
@@ -446,7 +447,10 @@ int clef_w4_linear(const void *x, int64_t ldx, const void *qw, const void *sw, i
  *
  * clef_kv_gather -- k_out[r], v_out[r] = bf16(code * scale) of token pos[r]
  * of sequence seq[r]; outputs bf16 [rows][heads * dim], pitches ldk, ldv;
- * zeros where an index is out of range.
+ * zeros where a sequence is not one of the table, a position is past its width or the
+ * page there is not one of the pool.  A position past the sequence's length reads
+ * whatever the table's entry and the page last held, so the caller keeps pos[r]
+ * below it.
  *
  * clef_kv_attention -- softmax attention of queries over the cache, for query
  * row i of sequence b (n rows) and head h reading key/value head h / (q_heads

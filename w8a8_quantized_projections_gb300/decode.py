@@ -71,7 +71,9 @@ def kv_append(k, v, codes, scales, table, lens, row_start=None, stream=None) -> 
 
 def kv_gather(codes, scales, table, seq, pos, k=None, v=None, stream=None):
     """The keys and values that the cache of one layer stands for at token
-    pos[r] of sequence seq[r]: bf16 (k, v), each [rows][heads][dim]."""
+    pos[r] of sequence seq[r]: bf16 (k, v), each [rows][heads][dim].  The call is
+    not told the lengths: a position past a sequence's tokens gives whatever its
+    place last held."""
     return (_ext or _load()).kv_gather(codes, scales, table, seq, pos, k, v, stream)
 
 
