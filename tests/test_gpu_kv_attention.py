@@ -256,3 +256,31 @@ def test_refusals():
         with pytest.raises(clef.ClefError):
             clef.kv_attention(**ok, scale=scale)
     assert clef.poll_status() == 0
+
+
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("dim", [64, 128, 256])
+@pytest.mark.parametrize("n", [1, 5, 40])
+@pytest.mark.parametrize("mean", [0.0, 3.0])
+def test_one_large_key_a_page_and_queries_with_a_mean(kind, dim, n, mean):
+    """The page's key scale is set by one token, the other codes are a few steps: the sums of
+    int8 keys of few rows run over c + 128, whose fp32 rounding goes by 128 scale sum |q| beside
+    that of the products."""
+    rng = np.random.default_rng(dim + n)
+    lens, page = [150], 16
+    table, pages = scattered_table(rng, lens, page)
+    c = Cache(kind, pages, 1, page, dim)
+    new = rng.standard_normal((2, 150, 1, dim))
+    new[0, 3::page] *= 40
+    c.append(table[0], 150, bf16(new))
+    q = bf16(rng.standard_normal((n, 2, dim)) + mean)
+    got, lse = run(rng, c, table, lens, q)
+    kv = c.values(table[0], 150)
+    ref, ls, tol, tl = attention(q.astype(np.float64), kv, dim ** -0.5, True)
+    most = c.scales[0, table[0, :-(-150 // page)]].max()
+    dx = dim ** -0.5 * (dim / 16 + 4) * 2.0 ** -23 * 128 * most * np.abs(q).sum(-1, dtype=np.float64)
+    worst = np.abs(kv[1]).max(0)[0]
+    tol = tol + np.expm1(2 * dx)[..., None] * worst
+    assert (np.abs(got - ref) <= tol + bf16_ulp(ref)).all()
+    assert (np.abs(lse - ls) <= tl + dx).all()
+    assert clef.poll_status() == 0
