@@ -387,7 +387,7 @@ int clef_bind_workspace(void *stream, void *ws, int64_t bytes);
  *
  * clef_w4_linear -- y[m][n] = bf16(sum_g sw[n][g] * (sum_{k in g} c[n][k] x[m][k]) + bias[n])
  * with fp32 sums, for calls of few rows: weights are read once for every 16
- * rows.  x counts to 2^-38 of the largest value of its row (in each eighth of
+ * rows (for every 8 where 16 do not fit on chip, from K = 29,704 on).  x counts to 2^-38 of the largest value of its row (in each eighth of
  * K), and the sums' rounding goes by (|c| + 8) |x|, so values a millionth of
  * another one in their group may be lost beside it.  Any finite x will do; an infinity
  * or a NaN makes its row of y NaN.  The order of a row's sum follows N and K alone, so its bits do not
@@ -417,7 +417,8 @@ int clef_w4_linear(const void *x, int64_t ldx, const void *qw, const void *sw, i
  *
  * Indices and lengths live in device memory, so the host cannot check them:
  * the kernels do, leave out what is out of range and record
- * CLEF_ERR_BAD_PAGE (clef_poll_status).  Limits: 4,096 sequences, 2^20 pages a
+ * CLEF_ERR_BAD_PAGE (clef_poll_status); a token of an attention whose page is
+ * out of range counts with a key and a value of zeros.  Limits: 4,096 sequences, 2^20 pages a
  * sequence, 2^24 pages.  Codes must be 16-byte aligned, integers 4-byte.
  *
  * clef_kv_append -- writes the newest tokens' keys and values.  lens holds
@@ -483,7 +484,7 @@ int clef_w4_linear(const void *x, int64_t ldx, const void *qw, const void *sw, i
  * clef_kv_compact -- moves pages so that the L held ones are 0 .. L - 1 (the
  * k-th lowest held page past L - 1 to the k-th lowest free page below), with
  * every sequence's row written to table_out, refs to refs_out and L to *live
- * (may be NULL).  table_out and refs_out may be table and refs.  scratch: int32
+ * (may be NULL).  A pool of no pages is an empty call, which writes nothing.  table_out and refs_out may be table and refs.  scratch: int32
  * [3 pages + 1].
  * clef_kv_copy_pages -- page dst[i] = page src[i] in every plane; no target
  * may also be a source or listed twice.

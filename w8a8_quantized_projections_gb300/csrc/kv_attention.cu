@@ -278,12 +278,15 @@ struct SplitItem {
 // A warp's registers hold a step of keys and one of values; each is loaded
 // again, for the next step, as soon as its products are done.
 //
-// Measured: 64 sequences of 512 to 8,192 int8 tokens, 8 heads of 128 read by 40
-// query heads: 92 us with the join, 4.1 TB/s; three of 32,768 e4m3 tokens at dim
-// 256: 46 us, 4.2 TB/s (57 us with two CTAs an SM instead of three, although the
-// third spills a few registers).  Bound by the latency of a warp's own chain: 43% of
+// Measured: 64 sequences of 512 to 8,192 int8 tokens, 8 heads of 128 read by 48
+// query heads: 91.5 us with the join, 4.2 TB/s; three of 32,768 e4m3 tokens at dim
+// 256: 46 us, 4.2 TB/s (57 us with two CTAs an SM instead of three, although with
+// three a thread spills 140 bytes).  Bound by the latency of a warp's own chain: 45% of
 // the issue slots at three warps a scheduler, about 320 instructions a 16-token tile
-// and as many as six such tiles an item.  One sequence of 298 tokens: 7.4 us.
+// and as many as six such tiles an item.  One sequence of 298 tokens: 7.5 us, eight CTAs
+// whose warps take three steps one after the other.  The two references of far value
+// scales are one branch of a step; as two (at the maximum and at the sum) they cost the
+// 298 tokens 0.3 us by their place in the code alone.
 template <int D, int NT>
 __host__ __device__ constexpr int split_ctas() { return D * NT <= 64 ? 4 : D * NT <= 128 || NT == 1 ? 3 : 2; }     // of an SM, by registers
 
@@ -1034,8 +1037,8 @@ struct BlockScales {
 // maximum has grown by more than 2^4 (the weights are then at most 2^15, within fp16).
 //
 // Measured: 2,270 rows x 32 heads over as many e4m3 tokens, 8 heads of 128, causal:
-// 65 us, 650 TFLOP/s; 8 x 48 rows x 24 heads over 1,550 int8 tokens, 4 heads of 256:
-// 51 us, 280 TFLOP/s.  Bound by the chain of a row tile's step, S, softmax, P V
+// 65 us, 645 TFLOP/s; 8 x 48 rows x 24 heads over 1,550 int8 tokens, 4 heads of 256:
+// 50 us, 288 TFLOP/s.  Bound by the chain of a row tile's step, S, softmax, P V
 // (4,500 cycles for 128 tokens at dim 128, of which 2,300 softmax; the tensor cores
 // work for 2,000 of them with two row tiles), and by what surrounds the steps of an
 // item: 12,000 cycles before the first one, 7,000 to write the rows.

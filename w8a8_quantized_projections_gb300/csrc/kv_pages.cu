@@ -11,7 +11,7 @@
 // The bookkeeping reads at most a few hundred KB of integers and each step
 // of it needs the one before: it runs as one CTA of 1,024 threads, 16 pages a
 // thread and round: trips to memory one after the other, about 6 us a call alone
-// and 14 us for a fork, a reserve and a free back to back.  The page copies are
+// and 15 us for a fork, a reserve and a free back to back.  The page copies are
 // separate launches over all SMs, bound by memory bandwidth (2 bytes moved for a
 // byte copied): 91 us to compact a pool with 270 MB of pages to move, 5.9 TB/s.
 #include <cstdint>

@@ -122,11 +122,12 @@ struct W4Args {
 // are read once into shared memory; S is as large as it takes to fit them.
 //
 // Measured (K x N, us a call back to back, weights from memory): one row 5120 x
-// 34816 in groups of 64, 19.8 us, 4.8 TB/s, of which 6 us before the first
-// product (the launch, x to fp16); 6144 x 5120 in groups of 128, 6.8 us.  13 rows
-// of 17408 x 5120 in groups of 32, 29.7 us: 9 us before the first product, then
-// two rounds of tiles (1.5 would do), in which three warps a scheduler wait for
-// products and for x from shared memory.
+// 34816 in groups of 64, 19.8 us, 4.8 TB/s; 6144 x 5120 in groups of 128, 6.8 us.
+// The same over 16 weight rows alone, which leaves the launch, x to fp16 and one
+// tile, takes 3.5 and 3.8 us (2.0 us of them without x: K = 128).  13 rows
+// of 17408 x 5120 in groups of 32, 29.6 us; over 16 weight rows 15.6 us, most of it x to fp16 and the
+// length of a part.  They take two rounds of tiles (1.5 would do), in which three warps a scheduler wait
+// for products and for x from shared memory.
 template <int NT, int GROUP, int WARPS>
 __global__ void __launch_bounds__(WARPS * 32, NT == 1 ? 2 : 1) w4_linear_kernel(const W4Args a) {
     extern __shared__ __align__(16) uint8_t smem[];

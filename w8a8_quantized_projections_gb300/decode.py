@@ -53,7 +53,8 @@ def quant_w4(w: torch.Tensor, group: int = 128, qw=None, sw=None, stream=None):
 
 def w4_linear(x, qw, sw, bias=None, y=None, stream=None):
     """y = bf16(x W^T + bias) for bf16 x [M][K] and weights packed by quant_w4,
-    for calls of few rows (weights are read once for every 16)."""
+    for calls of few rows (weights are read once for every 16, or every 8 of
+    the largest K)."""
     return (_ext or _load()).w4_linear(x, qw, sw, bias, y, stream)
 
 
