@@ -21,7 +21,7 @@ import importlib.util
 
 import torch
 
-from . import ClefError, _build, library
+from . import ClefError, _build, _lock, library
 
 __all__ = ["quant_w4", "w4_linear", "kv_append", "kv_gather", "kv_attention", "kv_reserve", "kv_fork", "kv_free",
            "kv_compact", "kv_copy_pages"]
@@ -33,7 +33,8 @@ def _load():
     """The compiled module (built with the library on first use if absent or stale)."""
     global _ext
     library()
-    _build.build_extension()
+    with _lock:
+        _build.build_extension()
     loader = importlib.machinery.ExtensionFileLoader("clef_decode", _build.EXT)
     ext = importlib.util.module_from_spec(importlib.util.spec_from_file_location("clef_decode", _build.EXT, loader=loader))
     loader.exec_module(ext)
