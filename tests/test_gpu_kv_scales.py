@@ -100,3 +100,28 @@ def test_queries_that_are_not_finite(kind, dim, n, len_, value):
         assert not got[n, 0].any() and lse[n, 0] == -np.inf
         got[n // 2, 1], lse[n // 2, 1] = ref[n // 2, 1], ref_lse[n // 2, 1]
         assert np.array_equal(got, ref) and np.array_equal(lse, ref_lse)
+
+
+@pytest.mark.parametrize("kind", ["int8", "e4m3"])
+@pytest.mark.parametrize("dim", [64, 256])
+@pytest.mark.parametrize("n", [1, 3, 24])
+def test_many_items(kind, dim, n):
+    """Several items a CTA, with and without pages of far sizes, some of them of zeros, in turn; each
+    sequence as in a call of its own."""
+    rng = np.random.default_rng(dim + n)
+    lens = [int(x) for x in rng.integers(1, 170, 88)] + [1300, 700]
+    page, heads = 16, 8
+    table, pages = scattered_table(rng, lens, page)
+    c = Cache(kind, pages, heads, page, dim)
+    for b, x in enumerate(lens):
+        new = rng.standard_normal((2, x, heads, dim))
+        if b % 3:
+            size = rng.choice([1.0, 1.0, 1e-37, 0.0, 1e36], (-(-x // page), heads))
+            new[1] = np.clip(new[1], -3, 3) * size[np.arange(x) // page][..., None]
+        c.append(table[b], x, bf16(new))
+    q = bf16(rng.standard_normal((90 * n, 2 * heads, dim)))
+    got, lse = run(rng, c, table, lens, q)
+    check(c, table, lens, q, np.arange(91) * n, got, lse)
+    for b in (0, 1, 43, 88, 89):
+        one, one_lse = run(rng, c, table[b:b + 1], lens[b:b + 1], q[b * n:(b + 1) * n])
+        assert np.array_equal(one, got[b * n:(b + 1) * n]) and np.array_equal(one_lse, lse[b * n:(b + 1) * n])
