@@ -71,7 +71,9 @@ typedef enum clef_status {
 typedef enum clef_act_mode {
     CLEF_ACT_INT8_H128 = 0,     /* rotate 128-blocks, s = amax/127, int8 codes */
     CLEF_ACT_FP8_E4M3 = 1,      /* no rotation, s = amax/448, e4m3 codes */
-    CLEF_ACT_FP8_E4M3_H128 = 2  /* rotate 128-blocks, then the FP8 codes */
+    CLEF_ACT_FP8_E4M3_H128 = 2, /* rotate 128-blocks, then the FP8 codes */
+    CLEF_ACT_FP8_E4M3_B128 = 3  /* no rotation, a scale for each 128 values of a row
+                                   (clef_rms_norm_quant; clef_quant_fp8_block makes the same of any x) */
 } clef_act_mode;
 
 /*
@@ -523,6 +525,61 @@ int clef_kv_compact(void *codes, int64_t plane_bytes, float *scales, int64_t pla
 int clef_kv_copy_pages(void *codes, int64_t plane_bytes, float *scales, int64_t plane_scales, int64_t planes,
                        int64_t pages, int heads, int page, int dim, const int32_t *src, const int32_t *dst,
                        int64_t n, void *stream);
+
+/*
+ * ---- between the projections ----
+ *
+ * clef_rms_norm -- root-mean-square norm of the rows of x, with the residual's
+ * addition:  h = x + residual (x alone where residual is NULL),
+ *   residual_out = bf16(h),  y = bf16(h w / sqrt(mean(h^2) + eps)),
+ * from the fp32 sum h, before its rounding.  x, residual, residual_out, y: bf16
+ * [M][K] with pitches ldx, ldr, ldro, ldy; w: bf16 [K].  residual_out may be the
+ * residual, and y may be x.  A row's bits depend on the row and w alone.
+ *
+ * clef_rms_norm_quant -- the same with 8-bit codes of the unrounded result v = h w
+ * / sqrt(mean(h^2) + eps) as the linears take them: modes CLEF_ACT_INT8_H128,
+ * CLEF_ACT_FP8_E4M3 and CLEF_ACT_FP8_E4M3_H128 give a scale a row (clef_quant_act's
+ * definition on v, which is never rounded to bf16), CLEF_ACT_FP8_E4M3_B128 the
+ * scales [M][ceil(K / 128)] of clef_quant_fp8_block.  q: [M][K], dense; scale: fp32.
+ * y also receives bf16(v) (unrotated: what a LoRA's shrink takes) where it is not
+ * NULL.
+ * Requirements of both: K % 16 == 0 (% 128 for the rotated modes), K <= 32768,
+ * pitches >= K and multiples of 8, tensors 16-byte and scale 4-byte aligned, 1e-20
+ * <= eps <= 1e20; h and h w are within fp32.
+ *
+ * clef_quant_fp8_block -- e4m3 codes of x (bf16 [M][K], pitch ldx) with a scale for
+ * each block of `rows` (1: activations, 128: weights) rows by 128 columns (the last
+ * ones of either may be smaller):
+ *   s = amax / 448, q = e4m3_rn_satfinite(x * min(448 / amax, FLT_MAX)), zeros for zeros.
+ * q: e4m3 [M][K], dense; scale: fp32 [ceil(M / rows)][ceil(K / 128)].
+ * Requirements: K % 16 == 0, K <= 65536, ldx >= K, ldx % 8 == 0; x and q 16-byte
+ * aligned, scale 4-byte.
+ *
+ * clef_rotary -- rotation of heads by the positions of their tokens.  Pair i of
+ * rot / 2 is the values (i, i + rot / 2) of a head, or (2 i, 2 i + 1) where
+ * interleaved; with t_i the angle of pos[token] at pair i,
+ *   (a, b) -> gain (a cos t_i - b sin t_i, b cos t_i + a sin t_i)   (fp32, rounded once);
+ * values from rot on are copied.  turns: int64 [rot / 2], the turns (of 2 pi) a
+ * position in units of 2^-64, modulo one turn; t_i = 2 pi (pos turns_i mod 2^64) / 2^64,
+ * exact for every int32 position (a negative one turns back).
+ * x, out: bf16 [tokens][heads][dim] with token pitches ldx, ldo and head pitches
+ * ldx_head, ldo_head; out may be x with the same pitches, and is disjoint from it
+ * otherwise.  pos: int32 [tokens].
+ * Requirements: dim % 8 == 0, dim <= 1024, rot even, 2 <= rot <= dim, heads <= 1024,
+ * pitches >= dim and multiples of 8; x and out 16-byte, turns 8-byte, pos 4-byte
+ * aligned.  rot a multiple of 16 (8 where interleaved) takes 16-byte accesses,
+ * another one single values.
+ */
+int clef_rms_norm(const void *x, int64_t ldx, const void *residual, int64_t ldr, const void *w, int64_t M, int64_t K,
+                  float eps, void *residual_out, int64_t ldro, void *y, int64_t ldy, void *stream);
+int clef_rms_norm_quant(const void *x, int64_t ldx, const void *residual, int64_t ldr, const void *w, int64_t M,
+                        int64_t K, float eps, int mode, void *residual_out, int64_t ldro, void *y, int64_t ldy,
+                        void *q, float *scale, void *stream);
+int clef_quant_fp8_block(const void *x, int64_t M, int64_t K, int64_t ldx, int rows, void *q, float *scale,
+                         void *stream);
+int clef_rotary(const void *x, int64_t ldx, int64_t ldx_head, int64_t tokens, int heads, int dim, int rot,
+                int interleaved, const int32_t *pos, const int64_t *turns, float gain, void *out, int64_t ldo,
+                int64_t ldo_head, void *stream);
 
 /*
  * clef_mma_peak -- dense tensor-core rate of this device for one instruction

@@ -447,6 +447,158 @@ PyObject *kv_copy_pages(PyObject *, Args a, Py_ssize_t n) {   // codes, scales, 
     END_HANDLE_TH_ERRORS
 }
 
+// ------------------------------------------------------------ between the projections
+
+double real(PyObject *o) {
+    const double v = PyFloat_AsDouble(o);
+    if (v == -1.0 && PyErr_Occurred()) throw python_error();
+    return v;
+}
+
+// A bf16 [M][K] tensor with its row pitch.
+struct Matrix {
+    void *at;
+    int64_t ld;
+};
+
+Matrix matrix(const Tensor &t, const char *name, int64_t M, int64_t K) {
+    CHECK(t.dim() == 2 && t.size(0) == M && t.size(1) == K, name, " has shape ", t.sizes(), ", expected [", M, ", ", K, "]");
+    return {t.data_ptr(), pitch(t, name)};
+}
+
+struct NormCall {
+    Matrix x, r, r_out;
+    void *w;
+    int64_t M, K;
+    int dev;
+    float eps;
+};
+
+NormCall norm_args(PyObject *xo, PyObject *wo, PyObject *eps, PyObject *ro, PyObject *so) {
+    NormCall c{};
+    const Tensor &x = on(xo, "x", ScalarType::BFloat16);
+    CHECK(x.dim() == 2, "x must be 2-D");
+    c.dev = x.get_device();
+    c.M = x.size(0);
+    c.K = x.size(1);
+    c.x = matrix(x, "x", c.M, c.K);
+    const Tensor &w = dense(on(wo, "w", ScalarType::BFloat16, c.dev), "w");
+    CHECK(w.dim() == 1 && w.size(0) == c.K, "w has shape ", w.sizes(), ", expected [", c.K, "]");
+    c.w = w.data_ptr();
+    c.eps = (float)real(eps);
+    if (ro != Py_None) {
+        c.r = matrix(on(ro, "residual", ScalarType::BFloat16, c.dev), "residual", c.M, c.K);
+        c.r_out = so == Py_None ? c.r : matrix(on(so, "residual_out", ScalarType::BFloat16, c.dev), "residual_out", c.M, c.K);
+    } else {
+        CHECK(so == Py_None, "residual_out without a residual");
+    }
+    return c;
+}
+
+PyObject *rms_norm(PyObject *, Args a, Py_ssize_t n) {   // x, w, eps, residual, residual_out, y, stream
+    ARGS(7);
+    const NormCall c = norm_args(a[0], a[1], a[2], a[3], a[4]);
+    const Stream s = stream_of(a[6], c.dev);
+    Result out(a[5]);
+    if (!out.passed) out.own = fresh({c.M, c.K}, ScalarType::BFloat16, s);
+    const Matrix y = matrix(out.passed ? on(a[5], "y", ScalarType::BFloat16, c.dev) : out.own, "y", c.M, c.K);
+    CLEF_CALL(clef_rms_norm, c.x.at, c.x.ld, c.r.at, c.r.ld, c.w, c.M, c.K, c.eps, c.r_out.at, c.r_out.ld, y.at, y.ld, s.at);
+    return out.object();
+    END_HANDLE_TH_ERRORS
+}
+
+int64_t blocks_of(int64_t n) { return (n + 127) / 128; }
+
+// Codes [M][K] that the caller passed (int8, or e4m3 as uint8 or float8_e4m3fn).
+const Tensor &codes_of(PyObject *o, const char *name, int device, bool is_int8, int64_t M, int64_t K) {
+    const Tensor &q = dense(tensor(o, name), name);
+    const ScalarType t = q.scalar_type();
+    CHECK(is_int8 ? t == ScalarType::Char : (t == ScalarType::Byte || t == ScalarType::Float8_e4m3fn), name, " has dtype ", t);
+    CHECK(q.get_device() == device, name, " is on device ", (int)q.get_device(), ", other tensors on ", device);
+    CHECK(q.dim() == 2 && q.size(0) == M && q.size(1) == K, name, " has shape ", q.sizes(), ", expected [", M, ", ", K, "]");
+    return q;
+}
+
+// Scales of `count` values, of any shape.
+float *scales_of(PyObject *o, const char *name, int device, int64_t count) {
+    const Tensor &t = dense(on(o, name, ScalarType::Float, device), name);
+    CHECK(t.numel() == count, name, " has ", t.numel(), " values, expected ", count);
+    return (float *)t.data_ptr();
+}
+
+// x, w, mode, eps, residual, residual_out, y, q, scale, stream
+PyObject *rms_norm_quant(PyObject *, Args a, Py_ssize_t n) {
+    ARGS(10);
+    const int64_t mode = integer(a[2]);
+    const NormCall c = norm_args(a[0], a[1], a[3], a[4], a[5]);
+    const Stream s = stream_of(a[9], c.dev);
+    const bool is_int8 = mode == CLEF_ACT_INT8_H128, blocked = mode == CLEF_ACT_FP8_E4M3_B128;
+    Matrix y{};
+    if (a[6] != Py_None) y = matrix(on(a[6], "y", ScalarType::BFloat16, c.dev), "y", c.M, c.K);
+    Result q(a[7]), scale(a[8]);
+    if (!q.passed) q.own = fresh({c.M, c.K}, is_int8 ? ScalarType::Char : ScalarType::Byte, s);
+    const int64_t per = blocked ? blocks_of(c.K) : 1;
+    if (!scale.passed)
+        scale.own = blocked ? fresh({c.M, per}, ScalarType::Float, s) : fresh({c.M}, ScalarType::Float, s);
+    void *qp = (q.passed ? codes_of(a[7], "q", c.dev, is_int8, c.M, c.K) : q.own).data_ptr();
+    float *sp = scale.passed ? scales_of(a[8], "scale", c.dev, c.M * per) : (float *)scale.own.data_ptr();
+    CLEF_CALL(clef_rms_norm_quant, c.x.at, c.x.ld, c.r.at, c.r.ld, c.w, c.M, c.K, c.eps, (int)mode, c.r_out.at, c.r_out.ld, y.at,
+              y.ld, qp, sp, s.at);
+    return pair(q, scale);
+    END_HANDLE_TH_ERRORS
+}
+
+PyObject *quant_fp8_block(PyObject *, Args a, Py_ssize_t n) {   // x, rows, q, scale, stream
+    ARGS(5);
+    const Tensor &x = on(a[0], "x", ScalarType::BFloat16);
+    const int dev = x.get_device();
+    const int64_t ldx = pitch(x, "x"), M = x.size(0), K = x.size(1), rows = integer(a[1]);
+    CHECK(rows == 1 || rows == 128, "rows must be 1 or 128");
+    const Stream s = stream_of(a[4], dev);
+    const int64_t groups = (M + rows - 1) / rows, blocks = blocks_of(K);
+    Result q(a[2]), scale(a[3]);
+    if (!q.passed) q.own = fresh({M, K}, ScalarType::Byte, s);
+    if (!scale.passed) scale.own = fresh({groups, blocks}, ScalarType::Float, s);
+    void *qp = (q.passed ? codes_of(a[2], "q", dev, false, M, K) : q.own).data_ptr();
+    float *sp = scale.passed ? scales_of(a[3], "scale", dev, groups * blocks) : (float *)scale.own.data_ptr();
+    CLEF_CALL(clef_quant_fp8_block, x.data_ptr(), M, K, ldx, (int)rows, qp, sp, s.at);
+    return pair(q, scale);
+    END_HANDLE_TH_ERRORS
+}
+
+PyObject *rotary(PyObject *, Args a, Py_ssize_t n) {   // x, pos, turns, gain, interleaved, out, stream
+    ARGS(7);
+    const Tensor &x = on(a[0], "x", ScalarType::BFloat16);
+    const int dev = x.get_device();
+    CHECK(x.dim() == 3 && x.size(1) <= INT_MAX && x.size(2) <= INT_MAX, "x must be [tokens][heads][dim]");
+    const int64_t dim = x.size(2);
+    const Rows r = rows_of(x, "x", -1, dim);
+    const Ints pos = ints(a[1], "pos", dev, r.rows);
+    const Tensor &turns = dense(on(a[2], "turns", ScalarType::Long, dev), "turns");
+    CHECK(turns.dim() == 1 && turns.size(0) >= 1 && 2 * turns.size(0) <= dim, "turns has shape ", turns.sizes(), ": a value for each pair of up to ",
+          dim, " values");
+    const double gain = real(a[3]);
+    const int interleaved = PyObject_IsTrue(a[4]);
+    if (interleaved < 0) throw python_error();
+    const Stream s = stream_of(a[6], dev);
+    Result out(a[5]);
+    Rows o;
+    if (out.passed) {
+        o = rows_of(a[5], "out", dev, r.heads, dim);
+        CHECK(o.rows == r.rows, "out has ", o.rows, " rows, expected ", r.rows);
+        CHECK(o.rows == 0 || o.ld >= (o.heads - 1) * o.ld_head + dim ||
+                  (o.ld_head >= (o.rows - 1) * o.ld + dim && o.ld >= dim),
+              "out's rows overlap");
+    } else {
+        out.own = fresh({r.rows, r.heads, dim}, ScalarType::BFloat16, s);
+        o = {out.own.data_ptr(), r.heads * dim, dim, r.rows, r.heads};
+    }
+    CLEF_CALL(clef_rotary, r.at, r.ld, r.ld_head, r.rows, (int)r.heads, (int)dim, (int)(2 * turns.size(0)), interleaved, pos.at,
+              (const int64_t *)turns.data_ptr(), (float)gain, o.at, o.ld, o.ld_head, s.at);
+    return out.object();
+    END_HANDLE_TH_ERRORS
+}
+
 PyObject *set_error(PyObject *, PyObject *type) {
     Py_INCREF(type);
     Py_XSETREF(g_error, type);
@@ -457,7 +609,8 @@ PyObject *set_error(PyObject *, PyObject *type) {
 
 PyMethodDef methods[] = {METHOD(quant_w4),   METHOD(w4_linear),  METHOD(kv_append),     METHOD(kv_gather),
                          METHOD(kv_attention), METHOD(kv_reserve), METHOD(kv_fork),     METHOD(kv_free),
-                         METHOD(kv_compact), METHOD(kv_copy_pages), {"set_error", set_error, METH_O, nullptr},
+                         METHOD(kv_compact), METHOD(kv_copy_pages), METHOD(rms_norm), METHOD(rms_norm_quant),
+                         METHOD(quant_fp8_block), METHOD(rotary), {"set_error", set_error, METH_O, nullptr},
                          {nullptr, nullptr, 0, nullptr}};
 
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "clef_decode", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
