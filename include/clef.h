@@ -555,6 +555,17 @@ int clef_kv_copy_pages(void *codes, int64_t plane_bytes, float *scales, int64_t 
  * Requirements: K % 16 == 0, K <= 65536, ldx >= K, ldx % 8 == 0; x and q 16-byte
  * aligned, scale 4-byte.
  *
+ * clef_fp8_block_linear -- the linear over such codes: with b the blocks of 128 of K,
+ *   y[m][n] = bf16(sum_b sx[m][b] sw[n / 128][b] sum_{k in b} qx[m][k] qw[n][k] + bias[n])
+ * with fp32 sums: a block's in the tensor core's order, the blocks' in an order that
+ * follows the sizes M, N and K of the call.  sx: fp32 [M][ceil(K / 128)]; sw: fp32
+ * [ceil(N / 128)][ceil(K / 128)]; both 4-byte aligned.  Other arguments and
+ * requirements as clef_fp8_linear.
+ *
+ * clef_fp8_block_gateup_swiglu -- h = bf16(g / (1 + exp(-g)) * u) of the unrounded
+ * values g, u of rows n and N + n of the packed weight [2N][K]; N % 128 == 0, so that
+ * no block of scales holds rows of both.  silu as in clef_fp8_gateup_swiglu.
+ *
  * clef_rotary -- rotation of heads by the positions of their tokens.  Pair i of
  * rot / 2 is the values (i, i + rot / 2) of a head, or (2 i, 2 i + 1) where
  * interleaved; with t_i the angle of pos[token] at pair i,
@@ -577,6 +588,11 @@ int clef_rms_norm_quant(const void *x, int64_t ldx, const void *residual, int64_
                         void *q, float *scale, void *stream);
 int clef_quant_fp8_block(const void *x, int64_t M, int64_t K, int64_t ldx, int rows, void *q, float *scale,
                          void *stream);
+int clef_fp8_block_linear(const void *qx, const float *sx, const void *qw, const float *sw, const void *bias, int64_t M,
+                          int64_t N, int64_t K, void *y, int64_t ldy, void *stream);
+int clef_fp8_block_gateup_swiglu(const void *qx, const float *sx, const void *qw_gu, const float *sw_gu,
+                                 const void *bias_gu, int64_t M, int64_t N, int64_t K, void *h, int64_t ldh,
+                                 void *stream);
 int clef_rotary(const void *x, int64_t ldx, int64_t ldx_head, int64_t tokens, int heads, int dim, int rot,
                 int interleaved, const int32_t *pos, const int64_t *turns, float gain, void *out, int64_t ldo,
                 int64_t ldo_head, void *stream);

@@ -28,6 +28,7 @@ __all__ = [
     "bind_workspace", "mma_peak",
     "quant_w4", "w4_linear", "kv_append", "kv_gather", "kv_attention", "kv_reserve", "kv_fork", "kv_free",
     "kv_compact", "kv_copy_pages", "rms_norm", "rms_norm_quant", "rotary", "rotary_turns", "quant_fp8_block",
+    "fp8_block_linear", "fp8_block_gateup_swiglu",
 ]
 
 ACT_MODES = {"int8_h128": 0, "fp8": 1, "fp8_h128": 2}
@@ -100,6 +101,8 @@ def library():
                 "clef_rms_norm": [vp, i64, vp, i64, vp, i64, i64, C.c_float, vp, i64, vp, i64, vp],
                 "clef_rms_norm_quant": [vp, i64, vp, i64, vp, i64, i64, C.c_float, i32, vp, i64, vp, i64, vp, vp, vp],
                 "clef_quant_fp8_block": [vp, i64, i64, i64, i32, vp, vp, vp],
+                "clef_fp8_block_linear": [vp, vp, vp, vp, vp, i64, i64, i64, vp, i64, vp],
+                "clef_fp8_block_gateup_swiglu": [vp, vp, vp, vp, vp, i64, i64, i64, vp, i64, vp],
                 "clef_rotary": [vp, i64, i64, i64, i32, i32, i32, i32, vp, vp, C.c_float, vp, i64, i64, vp],
                 "clef_set_sm_budget": [i32],
                 "clef_copy_sm": [vp, vp, i64, i32, vp],
@@ -563,4 +566,5 @@ def test_force_timeout(on) -> None:
 
 from .decode import (kv_append, kv_attention, kv_compact, kv_copy_pages, kv_fork, kv_free, kv_gather, kv_reserve,  # noqa: E402
                      quant_w4, w4_linear)
-from .between import quant_fp8_block, rms_norm, rms_norm_quant, rotary, rotary_turns  # noqa: E402
+from .between import (fp8_block_gateup_swiglu, fp8_block_linear, quant_fp8_block, rms_norm, rms_norm_quant, rotary,  # noqa: E402
+                      rotary_turns)

@@ -1,5 +1,6 @@
 """Bindings for what stands between a layer's projections: the norm with the residual's
-addition and 8-bit outputs, the quantizer of blocks of 128, and rotary positions.
+addition and 8-bit outputs, rotary positions, and the linears over e4m3 codes with a
+scale for each block of 128.
 
 Arguments are checked and marshalled by the compiled module of ``decode.py``; what each
 call computes is in ``include/clef.h``.
@@ -12,7 +13,7 @@ import torch
 
 from . import decode as _decode
 
-__all__ = ["rms_norm", "rms_norm_quant", "quant_fp8_block", "rotary", "rotary_turns"]
+__all__ = ["rms_norm", "rms_norm_quant", "quant_fp8_block", "fp8_block_linear", "fp8_block_gateup_swiglu", "rotary", "rotary_turns"]
 
 NORM_MODES = {"int8_h128": 0, "fp8": 1, "fp8_h128": 2, "fp8_b128": 3}
 
@@ -44,6 +45,17 @@ def quant_fp8_block(x, rows: int = 1, q=None, scale=None, stream=None):
     """e4m3 codes of bf16 x [M][K] with a scale for each block of `rows` (1 for activations, 128
     for weights) by 128: (q uint8 [M][K], scale fp32 [ceil(M / rows)][ceil(K / 128)])."""
     return _ext().quant_fp8_block(x, rows, q, scale, stream)
+
+
+def fp8_block_linear(qx, sx, qw, sw, bias=None, y=None, stream=None):
+    """y = bf16(x W^T + bias) for e4m3 codes in blocks: qx [M][K] with sx [M][ceil(K / 128)], qw [N][K]
+    with sw [ceil(N / 128)][ceil(K / 128)] (quant_fp8_block with rows = 1 and 128, rms_norm_quant)."""
+    return _ext().fp8_block(qx, sx, qw, sw, bias, y, stream, False)
+
+
+def fp8_block_gateup_swiglu(qx, sx, qw_gu, sw_gu, bias_gu=None, h=None, stream=None):
+    """h = bf16(silu(g) * u) for packed gate/up codes in blocks, [2N][K] with N a multiple of 128."""
+    return _ext().fp8_block(qx, sx, qw_gu, sw_gu, bias_gu, h, stream, True)
 
 
 # ---------------------------------------------------------------- rotary positions

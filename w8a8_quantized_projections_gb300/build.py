@@ -27,7 +27,7 @@ EXT = os.path.join(BUILD, "clef_decode.so")
 KEY = os.path.join(BUILD, "clef_decode.key")
 ROOT = os.path.dirname(HERE)
 SOURCES = ["abi.cu", "quant_act.cu", "gemm.cu", "swiglu.cu", "lora_noalloc.cu", "mma_peak.cu", "copy_sm.cu",
-           "w4.cu", "kv_cache.cu", "kv_pages.cu", "kv_attention.cu", "norm.cu", "rotary.cu"]
+           "w4.cu", "kv_cache.cu", "kv_pages.cu", "kv_attention.cu", "norm.cu", "rotary.cu", "fp8_block.cu"]
 NVCC_FLAGS = ["-gencode", "arch=compute_103a,code=sm_103a", "-O3", "-lineinfo", "-std=c++17",
               "-Xcompiler", "-fPIC", "-I", os.path.join(ROOT, "include")]
 

@@ -1,0 +1,747 @@
+// fp8_block.cu -- linears over e4m3 codes with a scale for each block of 128
+// of K (activations) or 128 x 128 (weights):
+//
+//   y[m][n] = sum_b sx[m][b] sw[n / 128][b] * (sum_{k in block b} qx[m][k] qw[n][k])
+//
+// The tensor cores (tcgen05 kind::f8f6f4, fp32 accumulators in TMEM) sum one
+// block of 128 of K at a time, which is one k-block of 128 bytes in the 128-byte
+// swizzle; the scales differ from block to block, so each block's sums are read
+// back (tcgen05.ld) and added, scaled, to fp32 totals in registers while the
+// tensor core sums the next block into another TMEM buffer.
+//
+// Two kernels:
+//  wide  many rows.  A cluster of two CTAs (cta_group::2) owns a tile of 256
+//        rows by 256 columns (128 gate and the 128 matching up columns); each CTA
+//        stages its 128 rows and half of the weight rows of a k-block (32 KB) in
+//        a ring of seven stages.  A TMEM lane is a row of x, so a thread's scale is its
+//        row's times one of the weight's, the same for its 128 columns.  Reading
+//        back is 128 x 256 fp32 a k-block and CTA, 256 clocks of TMEM and 128 of
+//        packed fp32 multiply-adds on each of the SM's four parts, beside 512 of
+//        the tensor core.  Persistent over tiles, in bands of rows that stay in L2.
+//  few   few rows, bound by the weight's bytes; operands change places.  A CTA
+//        owns 128 rows of the weight (TMEM lanes) and up to 128 rows of x
+//        (columns), so that the weight streams once through a ring of
+//        about 200 KB a SM; K is cut among the CTAs of a cluster where the
+//        weight's tiles alone leave SMs without work, and their sums meet
+//        through distributed shared memory, added in K order.
+#include <algorithm>
+#include <atomic>
+#include <cstdint>
+#include <cuda.h>
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include "../../include/clef.h"
+#include "clef_kernels.h"
+#include "clef_pair.cuh"
+#include "clef_ptx.cuh"
+#include "kv_host.h"
+
+namespace clef {
+
+namespace {
+
+struct BlockArgs {
+    int M, N, nkb;            // rows, columns of the output, k-blocks
+    const float *sx, *sw;     // [M][nkb], [weight rows / 128][nkb]
+    const uint16_t *bias;     // of the weight's rows, or null
+    uint16_t *out;
+    int64_t ldo;
+    int v32;                  // every row of the output starts on a 32-byte boundary
+    int band;                 // wide: tiles of rows a band
+    int split;                // few: CTAs that share a tile's K
+    unsigned int *status;
+    uint64_t limit_ns;
+    int force_timeout;
+};
+
+__device__ __forceinline__ uint64_t pack_f2(float a, float b) {
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+    return r;
+}
+__device__ __forceinline__ uint64_t pack_u2(uint32_t a, uint32_t b) {
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "r"(a), "r"(b));
+    return r;
+}
+__device__ __forceinline__ void unpack_f2(uint64_t p, float &a, float &b) {
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(p));
+}
+__device__ __forceinline__ uint64_t fma_f2(uint64_t a, uint64_t b, uint64_t c) {
+    uint64_t d;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+    return d;
+}
+
+// Waits for this thread's TMEM loads; the registers are operands, so that no use of them moves before it.
+__device__ __forceinline__ void tmem_ready(uint32_t (&r)[32]) {
+    asm volatile("tcgen05.wait::ld.sync.aligned;"
+                 : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
+                   "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]),
+                   "+r"(r[15]), "+r"(r[16]), "+r"(r[17]), "+r"(r[18]), "+r"(r[19]), "+r"(r[20]), "+r"(r[21]),
+                   "+r"(r[22]), "+r"(r[23]), "+r"(r[24]), "+r"(r[25]), "+r"(r[26]), "+r"(r[27]), "+r"(r[28]),
+                   "+r"(r[29]), "+r"(r[30]), "+r"(r[31])
+                 :: "memory");
+}
+__device__ __forceinline__ void tmem_ready(uint32_t (&r)[16]) {
+    asm volatile("tcgen05.wait::ld.sync.aligned;"
+                 : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
+                   "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15])
+                 :: "memory");
+}
+
+__device__ __forceinline__ float bf16_at(const uint16_t *p) { return __uint_as_float((uint32_t)__ldg(p) << 16); }
+
+// ------------------------------------------------------------ many rows
+
+constexpr int kBoxBytes = 128 * 128;         // 128 rows of a k-block
+constexpr int kWideStage = 2 * kBoxBytes;    // rows of x, then of the weight
+constexpr int kWideStages = 7;
+constexpr int kWideEpi = 8;                  // warps that read TMEM back
+constexpr int kWideThreads = 128 + 32 * kWideEpi;
+constexpr int kWideSmem = kWideStages * kWideStage + 1024 + 512;
+static_assert(kWideSmem <= 232448, "shared memory");
+
+struct WideBars {
+    uint64_t full[kWideStages], empty[kWideStages];
+    uint64_t acc_full[2], acc_empty[2];
+    uint64_t drain, never;
+    uint32_t tmem;
+    int abort;
+};
+static_assert(sizeof(WideBars) <= 512, "barrier block");
+
+struct WideTile {
+    int mb, nb;
+};
+
+// Tile t in bands of `band` tiles of rows: all columns of a band, its rows fastest.
+__device__ __forceinline__ WideTile wide_tile(int t, int num_m, int num_n, int band) {
+    const int b = t / (band * num_n), m0 = b * band, rows = min(band, num_m - m0), i = t - b * band * num_n;
+    return {m0 + i % rows, i / rows};
+}
+
+template <bool GU>
+__global__ void __launch_bounds__(kWideThreads, 1)
+wide_kernel(const __grid_constant__ CUtensorMap tmx, const __grid_constant__ CUtensorMap tmw, const BlockArgs a) {
+    extern __shared__ uint8_t smem_raw[];
+    const uint32_t base = smem_u32(smem_raw);
+    uint8_t *smem = smem_raw + (((base + 1023u) & ~1023u) - base);
+    WideBars *bar = reinterpret_cast<WideBars *>(smem + kWideStages * kWideStage);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const uint32_t rank = cluster_rank();
+    constexpr int kCols = GU ? 128 : 256;     // columns of the output a tile
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < kWideStages; ++s) {
+            mbar_init(&bar->full[s], 1);
+            mbar_init(&bar->empty[s], 1);
+        }
+        for (int s = 0; s < 2; ++s) {
+            mbar_init(&bar->acc_full[s], 1);
+            mbar_init(&bar->acc_empty[s], 2 * kWideEpi);
+        }
+        mbar_init(&bar->drain, 1);
+        mbar_init(&bar->never, 1);
+        bar->abort = 0;
+        fence_barrier_init();
+        tma_prefetch_desc(&tmx);
+        tma_prefetch_desc(&tmw);
+    }
+    if (warp == 1) {
+        asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;"
+                     ::"r"(smem_u32(&bar->tmem)), "r"(512) : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+    }
+    tc_fence_before();
+    __syncthreads();
+    cluster_sync();
+    tc_fence_after();
+    pdl_wait();
+
+    const uint32_t own_tmem = bar->tmem;
+    uint32_t tmem;
+    asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(tmem) : "r"(leader_addr(&bar->tmem)));
+    const int slot = blockIdx.x >> 1, slots = gridDim.x >> 1;
+    const int num_m = (a.M + 255) / 256, num_n = (a.N + kCols - 1) / kCols, tiles = num_m * num_n, nkb = a.nkb;
+    const WaitCtx w{a.limit_ns, &bar->abort, a.status};
+
+    // 4 x 32 x 56 + 8 x 32 x 224 registers of the 384 x 168 launched
+    if (warp < 4) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
+        if (warp == 0 && lane == 0) {
+            uint32_t s = 0, ph = 0, filled = 0, last = 0;
+            bool ok = true;
+            for (int t = slot; t < tiles && ok; t += slots) {
+                const WideTile o = wide_tile(t, num_m, num_n, a.band);
+                const int row = o.mb * 256 + (int)rank * 128;
+                const int wrow = GU ? (rank ? a.N : 0) + o.nb * 128 : o.nb * 256 + (int)rank * 128;
+                for (int kb = 0; kb < nkb; ++kb) {
+                    if (!mbar_wait_cl(&bar->empty[s], ph ^ 1u, w, kSiteTmaEmpty)) {
+                        ok = false;
+                        break;
+                    }
+                    uint8_t *st = smem + s * kWideStage;
+                    const uint32_t full = leader_addr(&bar->full[s]);
+                    if (rank == 0) mbar_arrive_expect_tx(&bar->full[s], 2 * kWideStage);
+                    tma_load_2d_pair(st, &tmx, kb * 128, row, full);
+                    tma_load_2d_pair(st + kBoxBytes, &tmw, kb * 128, wrow, full);
+                    filled |= 1u << s;
+                    last = (last & ~(1u << s)) | ph << s;
+                    if (++s == kWideStages) {
+                        s = 0;
+                        ph ^= 1u;
+                    }
+                }
+            }
+            // every copy of the pair has landed (they are counted on the leader's barriers) before a CTA ends
+            if (rank == 0)
+                for (int i = 0; i < kWideStages; ++i)
+                    if (filled >> i & 1u) mbar_wait_drain(&bar->full[i], last >> i & 1u, 200000000ull, a.status);
+        } else if (warp == 1 && lane == 0 && rank == 0) {
+            constexpr uint32_t idesc = idesc_f32acc(0, 0, 256, 256);
+            if (a.force_timeout == 1 || (a.force_timeout >= 2 && a.force_timeout - 2 == slot)) {
+                mbar_wait(&bar->never, 0, w, kSiteMmaFull);
+            } else {
+                uint32_t s = 0, ph = 0, acc = 0, aph = 0;
+                bool ok = true;
+                for (int t = slot; t < tiles && ok; t += slots)
+                    for (int kb = 0; kb < nkb; ++kb) {
+                        if (!mbar_wait_cl(&bar->acc_empty[acc], aph ^ 1u, w, kSiteMmaAccEmpty) ||
+                            !mbar_wait_cl(&bar->full[s], ph, w, kSiteMmaFull)) {
+                            ok = false;
+                            break;
+                        }
+                        tc_fence_after();
+                        const uint32_t sa = smem_u32(smem + s * kWideStage), sb = sa + kBoxBytes;
+#pragma unroll
+                        for (int k = 0; k < 4; ++k)
+                            mma2_f8(tmem + acc * 256, sdesc_sw128(sa + 32 * k), sdesc_sw128(sb + 32 * k), idesc, k > 0);
+                        mma2_commit_both(&bar->empty[s]);
+                        mma2_commit_both(&bar->acc_full[acc]);
+                        if (++s == kWideStages) {
+                            s = 0;
+                            ph ^= 1u;
+                        }
+                        if (++acc == 2) {
+                            acc = 0;
+                            aph ^= 1u;
+                        }
+                    }
+            }
+            mma2_commit_local(&bar->drain);
+            mbar_wait_drain(&bar->drain, 0, 200000000ull, a.status);
+        }
+    } else {
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 224;");
+        const int quad = warp & 3, half = (warp - 4) >> 2;
+        const uint32_t lanes = (uint32_t)(quad * 32) << 16;
+        // TMEM columns of this warp's four pieces of 32: a half of the tile, or of its gate and of its up columns
+        const auto piece = [&](int j) { return GU ? (j >> 1) * 128 + half * 64 + (j & 1) * 32 : half * 128 + 32 * j; };
+        uint32_t acc = 0, aph = 0;
+        bool ok = true;
+        for (int t = slot; t < tiles && ok; t += slots) {
+            const WideTile o = wide_tile(t, num_m, num_n, a.band);
+            const int row = o.mb * 256 + (int)rank * 128 + quad * 32 + lane;
+            const float *sx = a.sx + (int64_t)min(row, a.M - 1) * nkb;
+            const int b0 = GU ? o.nb : min(2 * o.nb + half, (a.N - 1) / 128);
+            const float *sw0 = a.sw + (int64_t)b0 * nkb, *sw1 = GU ? sw0 + (int64_t)(a.N / 128) * nkb : sw0;
+            uint64_t sum[64];
+#pragma unroll
+            for (int i = 0; i < 64; ++i) sum[i] = 0;
+            float x = __ldg(sx), w0 = __ldg(sw0), w1 = GU ? __ldg(sw1) : 0.0f;
+            for (int kb = 0; kb < nkb; ++kb) {
+                const float f0 = x * w0, f1 = GU ? x * w1 : f0;
+                const int next = min(kb + 1, nkb - 1);      // its scales are on their way meanwhile
+                x = __ldg(sx + next);
+                w0 = __ldg(sw0 + next);
+                if (GU) w1 = __ldg(sw1 + next);
+                if (!mbar_wait_cl(&bar->acc_full[acc], aph, w, kSiteEpiAccFull)) {
+                    ok = false;
+                    break;
+                }
+                tc_fence_after();
+                const uint32_t at = tmem + acc * 256 + lanes;
+                uint32_t r[2][32];
+                tmem_ld32(at + piece(0), r[0]);
+                tmem_ready(r[0]);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    if (j < 3) tmem_ld32(at + piece(j + 1), r[(j + 1) & 1]);
+                    const float f = (GU && j >= 2) ? f1 : f0;
+                    const uint64_t ff = pack_f2(f, f);
+#pragma unroll
+                    for (int i = 0; i < 16; ++i)
+                        sum[16 * j + i] = fma_f2(ff, pack_u2(r[j & 1][2 * i], r[j & 1][2 * i + 1]), sum[16 * j + i]);
+                    if (j < 3) tmem_ready(r[(j + 1) & 1]);
+                    if (j == 2) {
+                        // the last piece is in registers: the buffer goes back.  (Relaxed: the values read are
+                        // held, nothing else passes between the two.)
+                        tc_fence_before();
+                        __syncwarp();
+                        if (lane == 0) arrive_cluster_relaxed(leader_addr(&bar->acc_empty[acc]));
+                    }
+                }
+                if (++acc == 2) {
+                    acc = 0;
+                    aph ^= 1u;
+                }
+            }
+            uint16_t *out = a.out + (int64_t)row * a.ldo;
+#pragma unroll
+            for (int j = 0; j < (GU ? 4 : 8); ++j) {     // sixteen columns each
+                if (!ok || row >= a.M) break;
+                const int n = o.nb * kCols + half * (kCols / 2) + 16 * j;
+                uint32_t p[8];
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    float v0, v1;
+                    unpack_f2(sum[8 * j + i], v0, v1);
+                    if (a.bias && n + 2 * i < a.N) {
+                        const uint32_t b = *reinterpret_cast<const uint32_t *>(a.bias + n + 2 * i);
+                        v0 += __uint_as_float(b << 16);
+                        v1 += __uint_as_float(b & 0xFFFF0000u);
+                    }
+                    if (GU) {
+                        float u0, u1;
+                        unpack_f2(sum[32 + 8 * j + i], u0, u1);
+                        if (a.bias) {
+                            const uint32_t b = *reinterpret_cast<const uint32_t *>(a.bias + a.N + n + 2 * i);
+                            u0 += __uint_as_float(b << 16);
+                            u1 += __uint_as_float(b & 0xFFFF0000u);
+                        }
+                        v0 = silu_mul_ieee(v0, u0);
+                        v1 = silu_mul_ieee(v1, u1);
+                    }
+                    p[i] = pack_bf16x2(v0, v1);
+                }
+                if (n >= a.N) continue;
+                if (a.v32 && n + 16 <= a.N) {
+                    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};"
+                                 :: "l"(out + n), "r"(p[0]), "r"(p[1]), "r"(p[2]), "r"(p[3]), "r"(p[4]), "r"(p[5]),
+                                    "r"(p[6]), "r"(p[7])
+                                 : "memory");
+                } else {
+                    *reinterpret_cast<uint4 *>(out + n) = make_uint4(p[0], p[1], p[2], p[3]);
+                    if (n + 8 < a.N) *reinterpret_cast<uint4 *>(out + n + 8) = make_uint4(p[4], p[5], p[6], p[7]);
+                }
+            }
+            __syncwarp();
+        }
+    }
+    pdl_launch_dependents();
+    tc_fence_before();
+    __syncthreads();
+    if (bar->abort) {   // copies that still signal the other CTA land first
+        const uint64_t t0 = globaltimer_ns();
+        while (globaltimer_ns() - t0 < 2000000ull) {
+        }
+    }
+    cluster_sync();
+    if (warp == 1) {
+        tc_fence_after();
+        asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(own_tmem), "r"(512) : "memory");
+    }
+}
+
+// ------------------------------------------------------------ few rows
+
+constexpr int kMaxStages = 12, kMaxSplit = 8;
+
+template <int T, bool GU>
+struct Few {
+    static constexpr int kEpi = T >= 64 ? 8 : 4;               // warps that read TMEM back
+    static constexpr int kCols = T / (kEpi / 4);               // rows of x a warp holds
+    static constexpr int kTiles = GU ? 2 : 1;                  // weight tiles: gate, up
+    static constexpr int kStage = kTiles * kBoxBytes + T * 128;
+    static constexpr int kAcc = kTiles * T;                    // TMEM columns of a buffer
+    static constexpr int kBufs = 512 / kAcc >= 4 ? 4 : 2;
+    static constexpr int kTmem = kBufs * kAcc;
+    static constexpr int kScales = kEpi * 2 * kTiles * kCols;  // floats
+    static constexpr int kRest = 1024 + 512 + kScales * 4;
+    static constexpr int kFit = (232448 - kRest) / kStage;
+    static constexpr int kStages = kFit > kMaxStages ? kMaxStages : kFit;
+    static constexpr int kSmem = kStages * kStage + kRest;
+    static constexpr int kThreads = 64 + 32 * kEpi;
+    static_assert(kTmem >= 32 && kTmem <= 512 && (kTmem & (kTmem - 1)) == 0, "TMEM columns");
+    static_assert(kStages >= 3, "stages");
+    static_assert(kTiles * T * 128 * 4 <= kStages * kStage, "the parts of a split K fit in the ring");
+};
+
+struct FewBars {
+    uint64_t full[kMaxStages], empty[kMaxStages];
+    uint64_t acc_full[4], acc_empty[4];
+    uint64_t drain, never;
+    uint32_t tmem;
+    int abort;
+};
+static_assert(sizeof(FewBars) <= 512, "barrier block");
+
+__device__ __forceinline__ float ld_cluster(uint32_t local, int rank) {
+    uint32_t at;
+    float v;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"(local), "r"(rank));
+    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(at) : "memory");
+    return v;
+}
+
+template <int T, bool GU>
+__global__ void __launch_bounds__(Few<T, GU>::kThreads, 1)
+few_kernel(const __grid_constant__ CUtensorMap tmx, const __grid_constant__ CUtensorMap tmw, const BlockArgs a) {
+    using F = Few<T, GU>;
+    extern __shared__ uint8_t smem_raw[];
+    const uint32_t base = smem_u32(smem_raw);
+    uint8_t *smem = smem_raw + (((base + 1023u) & ~1023u) - base);
+    FewBars *bar = reinterpret_cast<FewBars *>(smem + F::kStages * F::kStage);
+    float *scales = reinterpret_cast<float *>(smem + F::kStages * F::kStage + 512);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < F::kStages; ++s) {
+            mbar_init(&bar->full[s], 1);
+            mbar_init(&bar->empty[s], 1);
+        }
+        for (int s = 0; s < F::kBufs; ++s) {
+            mbar_init(&bar->acc_full[s], 1);
+            mbar_init(&bar->acc_empty[s], F::kEpi);
+        }
+        mbar_init(&bar->drain, 1);
+        mbar_init(&bar->never, 1);
+        bar->abort = 0;
+        fence_barrier_init();
+        tma_prefetch_desc(&tmx);
+        tma_prefetch_desc(&tmw);
+    }
+    if (warp == 1) {
+        tmem_alloc(&bar->tmem, F::kTmem);
+        tmem_relinquish();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    pdl_wait();
+
+    const uint32_t tmem = bar->tmem;
+    const int split = a.split, rank = split > 1 ? (int)cluster_rank() : 0, tile = (int)blockIdx.x / split;
+    const int n0 = tile * 128, m0 = (int)blockIdx.y * T;
+    // (k-blocks times CTAs stay far below 2^31: K is at most 65,536)
+    const int k0 = rank * a.nkb / split, k1 = (rank + 1) * a.nkb / split;
+    const WaitCtx w{a.limit_ns, &bar->abort, a.status};
+
+    if (warp == 0) {
+        if (lane == 0) {
+            uint32_t s = 0, ph = 0, filled = 0, last = 0;
+            for (int kb = k0; kb < k1; ++kb) {
+                if (!mbar_wait(&bar->empty[s], ph ^ 1u, w, kSiteTmaEmpty)) break;
+                uint8_t *st = smem + s * F::kStage;
+                mbar_arrive_expect_tx(&bar->full[s], F::kStage);
+                tma_load_2d(st, &tmw, kb * 128, n0, &bar->full[s]);
+                if (GU) tma_load_2d(st + kBoxBytes, &tmw, kb * 128, a.N + n0, &bar->full[s]);
+                tma_load_2d(st + F::kTiles * kBoxBytes, &tmx, kb * 128, m0, &bar->full[s]);
+                filled |= 1u << s;
+                last = (last & ~(1u << s)) | ph << s;
+                if (++s == F::kStages) {
+                    s = 0;
+                    ph ^= 1u;
+                }
+            }
+            for (int i = 0; i < F::kStages; ++i)
+                if (filled >> i & 1u) mbar_wait_drain(&bar->full[i], last >> i & 1u, 200000000ull, a.status);
+        }
+    } else if (warp == 1) {
+        if (lane == 0) {
+            constexpr uint32_t idesc = idesc_f32acc(0, 0, 128, T);
+            if (a.force_timeout == 1 || (a.force_timeout >= 2 && a.force_timeout - 2 == (int)blockIdx.x)) {
+                mbar_wait(&bar->never, 0, w, kSiteMmaFull);
+            } else {
+                uint32_t s = 0, ph = 0, acc = 0, aph = 0;
+                for (int kb = k0; kb < k1; ++kb) {
+                    if (!mbar_wait(&bar->acc_empty[acc], aph ^ 1u, w, kSiteMmaAccEmpty) ||
+                        !mbar_wait(&bar->full[s], ph, w, kSiteMmaFull))
+                        break;
+                    tc_fence_after();
+                    const uint32_t sa = smem_u32(smem + s * F::kStage), sb = sa + F::kTiles * kBoxBytes;
+#pragma unroll
+                    for (int h = 0; h < F::kTiles; ++h)
+#pragma unroll
+                        for (int k = 0; k < 4; ++k)
+                            mma_f8(tmem + acc * F::kAcc + h * T, sdesc_sw128(sa + h * kBoxBytes + 32 * k), sdesc_sw128(sb + 32 * k),
+                                   idesc, k > 0);
+                    mma_commit(&bar->empty[s]);
+                    mma_commit(&bar->acc_full[acc]);
+                    if (++s == F::kStages) {
+                        s = 0;
+                        ph ^= 1u;
+                    }
+                    if (++acc == F::kBufs) {
+                        acc = 0;
+                        aph ^= 1u;
+                    }
+                }
+            }
+            mma_commit(&bar->drain);
+            mbar_wait_drain(&bar->drain, 0, 200000000ull, a.status);
+        }
+    } else {
+        const int quad = warp & 3, e = warp - 2, c0 = (e >> 2) * F::kCols;
+        const int n = n0 + quad * 32 + lane;
+        const uint32_t lanes = (uint32_t)(quad * 32) << 16;
+        float *mine = scales + e * 2 * F::kTiles * F::kCols;     // two buffers of this warp's products of scales
+        constexpr int kPer = (F::kCols + 31) / 32;               // of them a lane
+        const float *sx[kPer];
+#pragma unroll
+        for (int i = 0; i < kPer; ++i) {
+            const int c = 32 * i + lane, m = m0 + c0 + c;
+            sx[i] = (c < F::kCols && m < a.M) ? a.sx + (int64_t)m * a.nkb : nullptr;
+        }
+        const float *sw0 = a.sw + (int64_t)tile * a.nkb, *sw1 = GU ? sw0 + (int64_t)(a.N / 128) * a.nkb : sw0;
+        uint64_t sum[F::kTiles][F::kCols / 2];
+#pragma unroll
+        for (int h = 0; h < F::kTiles; ++h)
+#pragma unroll
+            for (int i = 0; i < F::kCols / 2; ++i) sum[h][i] = 0;
+        float x[kPer], w0 = 0.0f, w1 = 0.0f;
+        const auto fetch = [&](int kb) {
+#pragma unroll
+            for (int i = 0; i < kPer; ++i) x[i] = sx[i] ? __ldg(sx[i] + kb) : 0.0f;
+            w0 = __ldg(sw0 + kb);
+            if (GU) w1 = __ldg(sw1 + kb);
+        };
+        fetch(k0);
+        uint32_t acc = 0, aph = 0;
+        bool ok = true;
+        for (int kb = k0; kb < k1; ++kb) {
+            float *f = mine + (kb & 1) * F::kTiles * F::kCols;
+#pragma unroll
+            for (int i = 0; i < kPer; ++i) {
+                if (32 * i + lane < F::kCols) {
+                    f[32 * i + lane] = x[i] * w0;
+                    if (GU) f[F::kCols + 32 * i + lane] = x[i] * w1;
+                }
+            }
+            __syncwarp();
+            if (kb + 1 < k1) fetch(kb + 1);
+            if (!mbar_wait(&bar->acc_full[acc], aph, w, kSiteEpiAccFull)) {
+                ok = false;
+                break;
+            }
+            tc_fence_after();
+            const uint32_t at = tmem + acc * F::kAcc + lanes + c0;
+            constexpr int kPiece = F::kCols < 32 ? 16 : 32, kPieces = F::kTiles * F::kCols / kPiece;
+            const auto load = [&](int j, uint32_t(&r)[kPiece]) {
+                const uint32_t from = at + j * kPiece / F::kCols * T + j * kPiece % F::kCols;
+                if constexpr (kPiece == 16) tmem_ld16(from, r);
+                else tmem_ld32(from, r);
+            };
+            uint32_t r[2][kPiece];
+            load(0, r[0]);
+            tmem_ready(r[0]);
+#pragma unroll
+            for (int j = 0; j < kPieces; ++j) {
+                if (j + 1 < kPieces) {
+                    load(j + 1, r[(j + 1) & 1]);
+                } else {
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&bar->acc_empty[acc]);
+                }
+                const int h = j * kPiece / F::kCols, c = j * kPiece % F::kCols;
+#pragma unroll
+                for (int i = 0; i < kPiece / 4; ++i) {
+                    const ulonglong2 p = *reinterpret_cast<const ulonglong2 *>(f + h * F::kCols + c + 4 * i);
+                    const uint32_t *d = r[j & 1] + 4 * i;
+                    uint64_t *o = &sum[h][(c + 4 * i) / 2];
+                    o[0] = fma_f2(p.x, pack_u2(d[0], d[1]), o[0]);
+                    o[1] = fma_f2(p.y, pack_u2(d[2], d[3]), o[1]);
+                }
+                if (j + 1 < kPieces) tmem_ready(r[(j + 1) & 1]);
+            }
+            if (++acc == F::kBufs) {
+                acc = 0;
+                aph ^= 1u;
+            }
+        }
+        if (ok && split == 1) {
+            if (n < a.N) {
+                const float b0 = a.bias ? bf16_at(a.bias + n) : 0.0f, b1 = GU && a.bias ? bf16_at(a.bias + a.N + n) : 0.0f;
+#pragma unroll
+                for (int i = 0; i < F::kCols; ++i) {
+                    if (m0 + c0 + i >= a.M) break;
+                    float v[2], u[2] = {0.0f, 0.0f};
+                    unpack_f2(sum[0][i / 2], v[0], v[1]);
+                    float y = v[i & 1] + b0;
+                    if (GU) {
+                        unpack_f2(sum[F::kTiles - 1][i / 2], u[0], u[1]);
+                        y = silu_mul_ieee(y, u[i & 1] + b1);
+                    }
+                    a.out[(int64_t)(m0 + c0 + i) * a.ldo + n] = __bfloat16_as_ushort(__float2bfloat16_rn(y));
+                }
+            }
+        } else if (ok) {
+            // every k-block's MMAs have ended, so the ring is free: this part's sums, [tile][row of x][lane]
+            float *part = reinterpret_cast<float *>(smem) + quad * 32 + lane;
+#pragma unroll
+            for (int h = 0; h < F::kTiles; ++h)
+#pragma unroll
+                for (int i = 0; i < F::kCols; ++i) {
+                    float v[2];
+                    unpack_f2(sum[h][i / 2], v[0], v[1]);
+                    part[(h * T + c0 + i) * 128] = v[i & 1];
+                }
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (split > 1) {
+        cluster_sync();
+        if (warp >= 2 && !bar->abort) {
+            const int i = threadIdx.x - 64, n = n0 + (i & 127);
+            const float b0 = a.bias && n < a.N ? bf16_at(a.bias + n) : 0.0f;
+            const float b1 = GU && a.bias && n < a.N ? bf16_at(a.bias + a.N + n) : 0.0f;
+            // this CTA's share of the rows of x
+            for (int c = rank + split * (i >> 7); c < T && m0 + c < a.M; c += split * (F::kEpi / 4)) {
+                float v = 0.0f, u = 0.0f;
+                const uint32_t at = base + (uint32_t)(smem - smem_raw) + (uint32_t)((c * 128 + (i & 127)) * 4);
+                for (int q = 0; q < split; ++q) {
+                    v += ld_cluster(at, q);
+                    if (GU) u += ld_cluster(at + T * 512, q);
+                }
+                v += b0;
+                if (GU) v = silu_mul_ieee(v, u + b1);
+                if (n < a.N) a.out[(int64_t)(m0 + c) * a.ldo + n] = __bfloat16_as_ushort(__float2bfloat16_rn(v));
+            }
+        }
+        cluster_sync();
+    }
+    pdl_launch_dependents();
+    if (warp == 1) {
+        tc_fence_after();
+        tmem_dealloc(tmem, F::kTmem);
+    }
+}
+
+// ------------------------------------------------------------ launches
+
+int maps(CUtensorMap &tx, CUtensorMap &tw, const void *qx, const void *qw, int64_t M, int64_t wrows, int64_t K, uint32_t xrows) {
+    const int rc = internal_make_tmap(&tx, CU_TENSOR_MAP_DATA_TYPE_UINT8, qx, (uint64_t)K, (uint64_t)M, (uint64_t)K, 128, xrows,
+                                      CU_TENSOR_MAP_SWIZZLE_128B);
+    return rc ? rc : internal_make_tmap(&tw, CU_TENSOR_MAP_DATA_TYPE_UINT8, qw, (uint64_t)K, (uint64_t)wrows, (uint64_t)K, 128, 128,
+                                        CU_TENSOR_MAP_SWIZZLE_128B);
+}
+
+template <bool GU>
+int launch_wide(const void *qx, const void *qw, int64_t K, BlockArgs a, int sms, cudaStream_t st) {
+    static SmemOptIn opt;
+    static std::atomic<int> most{0};
+    auto kern = wide_kernel<GU>;
+    cudaError_t e = opt.set(reinterpret_cast<const void *>(kern), kWideSmem);
+    if (e != cudaSuccess) return internal_cuda_error(e, "block linear smem attribute");
+    int pairs = most.load(std::memory_order_relaxed);
+    if (pairs == 0) {
+        // pairs that the device holds at once, whatever this call's SM budget
+        cudaLaunchConfig_t cfg = {};
+        cudaLaunchAttribute attr[1];
+        attr[0].id = cudaLaunchAttributeClusterDimension;
+        attr[0].val.clusterDim.x = 2;
+        attr[0].val.clusterDim.y = 1;
+        attr[0].val.clusterDim.z = 1;
+        int dev = 0, all = sms;
+        if (cudaGetDevice(&dev) == cudaSuccess) cudaDeviceGetAttribute(&all, cudaDevAttrMultiProcessorCount, dev);
+        cfg.gridDim = dim3((unsigned)(all & ~1), 1, 1);
+        cfg.blockDim = dim3(kWideThreads, 1, 1);
+        cfg.dynamicSmemBytes = kWideSmem;
+        cfg.attrs = attr;
+        cfg.numAttrs = 1;
+        if (cudaOccupancyMaxActiveClusters(&pairs, kern, &cfg) != cudaSuccess || pairs < 1) pairs = std::max(1, all / 2);
+        most.store(pairs, std::memory_order_relaxed);
+    }
+    pairs = std::max(1, std::min(pairs, sms / 2));
+    const int num_m = (a.M + 255) / 256, num_n = GU ? a.N / 128 : (a.N + 255) / 256;
+    // bands whose rows of x take up to 24 MB, so that they stay in L2 while the weight passes; of even size
+    const int64_t per = 256 * K, fit = std::max<int64_t>(1, ((int64_t)24 << 20) / per);
+    const int bands = (int)((num_m + fit - 1) / fit);
+    a.band = (num_m + bands - 1) / bands;
+    CUtensorMap tx, tw;
+    const int rc = maps(tx, tw, qx, qw, a.M, (GU ? 2 : 1) * (int64_t)a.N, K, 128);
+    if (rc) return rc;
+    const int tiles = num_m * num_n;
+    e = launch_kernel(kern, dim3((unsigned)(2 * std::min(tiles, pairs))), dim3(kWideThreads), kWideSmem, st, 2, true, tx, tw, a);
+    return e == cudaSuccess ? CLEF_OK : internal_cuda_error(e, "block linear launch");
+}
+
+template <int T, bool GU>
+int launch_few(const void *qx, const void *qw, int64_t K, const BlockArgs &a, cudaStream_t st) {
+    using F = Few<T, GU>;
+    static SmemOptIn opt;
+    auto kern = few_kernel<T, GU>;
+    cudaError_t e = opt.set(reinterpret_cast<const void *>(kern), F::kSmem);
+    if (e != cudaSuccess) return internal_cuda_error(e, "block linear smem attribute");
+    CUtensorMap tx, tw;
+    const int rc = maps(tx, tw, qx, qw, a.M, (GU ? 2 : 1) * (int64_t)a.N, K, T);
+    if (rc) return rc;
+    const dim3 grid((unsigned)((a.N + 127) / 128 * a.split), (unsigned)((a.M + T - 1) / T));
+    e = launch_kernel(kern, grid, dim3(F::kThreads), F::kSmem, st, a.split, true, tx, tw, a);
+    return e == cudaSuccess ? CLEF_OK : internal_cuda_error(e, "block linear launch");
+}
+
+int block_call(bool gu, const void *qx, const float *sx, const void *qw, const float *sw, const void *bias, int64_t M,
+               int64_t N, int64_t K, void *out, int64_t ldo, void *stream) {
+    constexpr int64_t kMax = (int64_t)1 << 30;
+    if (M < 0 || M > kMax) return kv_fail("M out of range");
+    if (N <= 0 || N > kMax / 2 || N % (gu ? 128 : 8) != 0)
+        return kv_fail(gu ? "N must be positive and a multiple of 128" : "N must be positive and a multiple of 8");
+    if (K <= 0 || K > 65536 || K % 16 != 0) return kv_fail("K must be in (0, 65536] and a multiple of 16");
+    if (ldo < N || ldo % 8 != 0) return kv_fail("output row pitch must be >= N and a multiple of 8");
+    if (M == 0) return CLEF_OK;
+    if (!qx || !qw || !out || !sx || !sw) return kv_fail("null pointer");
+    if (kv_misaligned(qx, 16) || kv_misaligned(qw, 16) || kv_misaligned(out, 16) || kv_misaligned(bias, 16))
+        return kv_fail("operands, bias and output must be 16-byte aligned");
+    if (kv_misaligned(sx, 4) || kv_misaligned(sw, 4)) return kv_fail("scales must be 4-byte aligned");
+    const int64_t tiles_n = (N + 127) / 128;
+    if ((M + 255) / 256 * (gu ? tiles_n : (N + 255) / 256) > 0x7FFFFFFF) return kv_fail("output too large");
+    int sms = 0;
+    unsigned int *status = nullptr;
+    const int rc = internal_device(&sms, &status);
+    if (rc) return rc;
+    sms = internal_launch_sms(sms);
+    BlockArgs a;
+    a.M = (int)M;
+    a.N = (int)N;
+    a.nkb = (int)((K + 127) / 128);
+    a.sx = sx;
+    a.sw = sw;
+    a.bias = static_cast<const uint16_t *>(bias);
+    a.out = static_cast<uint16_t *>(out);
+    a.ldo = ldo;
+    a.v32 = !kv_misaligned(out, 32) && ldo % 16 == 0;
+    a.band = a.split = 1;
+    a.status = status;
+    a.limit_ns = internal_wait_limit(&a.force_timeout);
+    const cudaStream_t st = static_cast<cudaStream_t>(stream);
+    if (M > 128) return gu ? launch_wide<true>(qx, qw, K, a, sms, st) : launch_wide<false>(qx, qw, K, a, sms, st);
+    // CTAs that share a tile: as many as SMs are left, each with four k-blocks or more
+    const int64_t share = std::min<int64_t>({kMaxSplit, sms / tiles_n, a.nkb / 4});
+    a.split = (int)std::max<int64_t>(1, share);
+    if (gu) return M <= 16 ? launch_few<16, true>(qx, qw, K, a, st) : M <= 32 ? launch_few<32, true>(qx, qw, K, a, st)
+                 : M <= 64 ? launch_few<64, true>(qx, qw, K, a, st) : launch_few<128, true>(qx, qw, K, a, st);
+    return M <= 16 ? launch_few<16, false>(qx, qw, K, a, st) : M <= 32 ? launch_few<32, false>(qx, qw, K, a, st)
+         : M <= 64 ? launch_few<64, false>(qx, qw, K, a, st) : launch_few<128, false>(qx, qw, K, a, st);
+}
+
+}  // namespace
+
+}  // namespace clef
+
+using namespace clef;
+
+extern "C" int clef_fp8_block_linear(const void *qx, const float *sx, const void *qw, const float *sw, const void *bias,
+                                     int64_t M, int64_t N, int64_t K, void *y, int64_t ldy, void *stream) {
+    return block_call(false, qx, sx, qw, sw, bias, M, N, K, y, ldy, stream);
+}
+
+extern "C" int clef_fp8_block_gateup_swiglu(const void *qx, const float *sx, const void *qw_gu, const float *sw_gu,
+                                            const void *bias_gu, int64_t M, int64_t N, int64_t K, void *h, int64_t ldh,
+                                            void *stream) {
+    return block_call(true, qx, sx, qw_gu, sw_gu, bias_gu, M, N, K, h, ldh, stream);
+}

@@ -566,6 +566,53 @@ PyObject *quant_fp8_block(PyObject *, Args a, Py_ssize_t n) {   // x, rows, q, s
     END_HANDLE_TH_ERRORS
 }
 
+// e4m3 codes [rows][K] and their scales, one for each `per` rows and 128 columns.
+struct Blocks {
+    void *codes;
+    float *scales;
+    int64_t rows, K;
+};
+
+Blocks blocks(PyObject *qo, const char *qname, PyObject *so, const char *sname, int64_t per, int device) {
+    const Tensor &q = dense(tensor(qo, qname), qname);
+    const ScalarType t = q.scalar_type();
+    CHECK(t == ScalarType::Byte || t == ScalarType::Float8_e4m3fn, qname, " has dtype ", t, ", expected uint8 or float8_e4m3fn");
+    CHECK(device < 0 || q.get_device() == device, qname, " is on device ", (int)q.get_device(), ", other tensors on ", device);
+    CHECK(q.dim() == 2, qname, " must be 2-D");
+    const int64_t rows = q.size(0), K = q.size(1), groups = (rows + per - 1) / per, count = blocks_of(K);
+    const Tensor &s = dense(on(so, sname, ScalarType::Float, (int)q.get_device()), sname);
+    CHECK(s.dim() == 2 && s.size(0) == groups && s.size(1) == count, sname, " has shape ", s.sizes(), ", expected [", groups, ", ", count, "]");
+    return {q.data_ptr(), (float *)s.data_ptr(), rows, K};
+}
+
+PyObject *fp8_block(PyObject *, Args a, Py_ssize_t n) {   // qx, sx, qw, sw, bias, out, stream, gate and up
+    ARGS(8);
+    const int gu = PyObject_IsTrue(a[7]);
+    if (gu < 0) throw python_error();
+    const Blocks x = blocks(a[0], "qx", a[1], "sx", 1, -1);
+    const int dev = THPVariable_Unpack(a[0]).get_device();
+    const Blocks w = blocks(a[2], "qw", a[3], "sw", 128, dev);
+    CHECK(x.K == w.K, "qx and qw disagree on K");
+    CHECK(!gu || w.rows % 2 == 0, "packed gate/up weights need an even row count (gate rows, then up rows)");
+    const int64_t N = gu ? w.rows / 2 : w.rows;
+    void *bias = nullptr;
+    if (a[4] != Py_None) {
+        const Tensor &b = dense(on(a[4], "bias", ScalarType::BFloat16, dev), "bias");
+        CHECK(b.numel() == w.rows, "bias has ", b.numel(), " values for ", w.rows, " weight rows");
+        bias = b.data_ptr();
+    }
+    const Stream s = stream_of(a[6], dev);
+    Result out(a[5]);
+    if (!out.passed) out.own = fresh({x.rows, N}, ScalarType::BFloat16, s);
+    const Matrix y = matrix(out.passed ? on(a[5], "output", ScalarType::BFloat16, dev) : out.own, "output", x.rows, N);
+    if (gu)
+        CLEF_CALL(clef_fp8_block_gateup_swiglu, x.codes, x.scales, w.codes, w.scales, bias, x.rows, N, x.K, y.at, y.ld, s.at);
+    else
+        CLEF_CALL(clef_fp8_block_linear, x.codes, x.scales, w.codes, w.scales, bias, x.rows, N, x.K, y.at, y.ld, s.at);
+    return out.object();
+    END_HANDLE_TH_ERRORS
+}
+
 PyObject *rotary(PyObject *, Args a, Py_ssize_t n) {   // x, pos, turns, gain, interleaved, out, stream
     ARGS(7);
     const Tensor &x = on(a[0], "x", ScalarType::BFloat16);
@@ -610,7 +657,7 @@ PyObject *set_error(PyObject *, PyObject *type) {
 PyMethodDef methods[] = {METHOD(quant_w4),   METHOD(w4_linear),  METHOD(kv_append),     METHOD(kv_gather),
                          METHOD(kv_attention), METHOD(kv_reserve), METHOD(kv_fork),     METHOD(kv_free),
                          METHOD(kv_compact), METHOD(kv_copy_pages), METHOD(rms_norm), METHOD(rms_norm_quant),
-                         METHOD(quant_fp8_block), METHOD(rotary), {"set_error", set_error, METH_O, nullptr},
+                         METHOD(quant_fp8_block), METHOD(fp8_block), METHOD(rotary), {"set_error", set_error, METH_O, nullptr},
                          {nullptr, nullptr, 0, nullptr}};
 
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "clef_decode", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
