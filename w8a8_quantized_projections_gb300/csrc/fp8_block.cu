@@ -47,7 +47,6 @@ struct BlockArgs {
     const uint16_t *bias;     // of the weight's rows, or null
     uint16_t *out;
     int64_t ldo;
-    int v32;                  // every row of the output starts on a 32-byte boundary
     int band;                 // wide: tiles of rows a band
     int split;                // few: CTAs that share a tile's K
     unsigned int *status;
@@ -74,6 +73,14 @@ __device__ __forceinline__ uint64_t fma_f2(uint64_t a, uint64_t b, uint64_t c) {
     return d;
 }
 
+// One lane of a whole warp.  The MMA issuers run with all lanes and elect one for each k-block's MMAs: what they
+// count then stays in uniform registers, which the MMAs take their operands from.
+__device__ __forceinline__ bool elect_one() {
+    uint32_t p;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
+    return p != 0;
+}
+
 // Waits for this thread's TMEM loads; the registers are operands, so that no use of them moves before it.
 __device__ __forceinline__ void tmem_ready(uint32_t (&r)[32]) {
     asm volatile("tcgen05.wait::ld.sync.aligned;"
@@ -93,19 +100,37 @@ __device__ __forceinline__ void tmem_ready(uint32_t (&r)[16]) {
 
 __device__ __forceinline__ float bf16_at(const uint16_t *p) { return __uint_as_float((uint32_t)__ldg(p) << 16); }
 
+// Copies of tiles from shared memory, and the waits for them.
+__device__ __forceinline__ void tma_store_2d(const CUtensorMap *m, const void *src, int32_t c0, int32_t c1) {
+    asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.bulk_group [%0, {%2, %3}], [%1];"
+                 ::"l"(reinterpret_cast<uint64_t>(m)), "r"(smem_u32(src)), "r"(c0), "r"(c1) : "memory");
+}
+__device__ __forceinline__ void bulk_commit() { asm volatile("cp.async.bulk.commit_group;" ::: "memory"); }
+__device__ __forceinline__ void bulk_wait_read_all() { asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory"); }
+__device__ __forceinline__ void bulk_wait_all() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
+
 // ------------------------------------------------------------ many rows
 
 constexpr int kBoxBytes = 128 * 128;         // 128 rows of a k-block
 constexpr int kWideStage = 2 * kBoxBytes;    // rows of x, then of the weight
-constexpr int kWideStages = 7;
+constexpr int kMaxWideStages = 6;
 constexpr int kWideEpi = 8;                  // warps that read TMEM back
+constexpr int kParts = kWideEpi / 4, kSums = 256 / kParts;    // of a row, and columns that each holds
 constexpr int kWideThreads = 128 + 32 * kWideEpi;
-constexpr int kWideSmem = kWideStages * kWideStage + 1024 + 512;
-static_assert(kWideSmem <= 232448, "shared memory");
+constexpr int kOutBox = 32 * 128;            // 32 rows of 64 columns of the output, bf16
+template <bool GU>
+struct Wide {
+    static constexpr int kBoxes = GU ? 1 : 2;                    // of 64 columns of the output a warp
+    static constexpr int kOut = kWideEpi * kBoxes * kOutBox;
+    static constexpr int kStages = GU ? 6 : 5;
+    static constexpr int kSmem = kStages * kWideStage + kOut + 1024 + 512;
+    static_assert(kSmem <= 232448, "shared memory");
+};
 
 struct WideBars {
-    uint64_t full[kWideStages], empty[kWideStages];
-    uint64_t acc_full[2], acc_empty[2];
+    uint64_t full[kMaxWideStages];
+    uint64_t done[kMaxWideStages];      // a k-block's MMAs: its stage is free, its sums are complete
+    uint64_t acc_empty[2];
     uint64_t drain, never;
     uint32_t tmem;
     int abort;
@@ -124,11 +149,14 @@ __device__ __forceinline__ WideTile wide_tile(int t, int num_m, int num_n, int b
 
 template <bool GU>
 __global__ void __launch_bounds__(kWideThreads, 1)
-wide_kernel(const __grid_constant__ CUtensorMap tmx, const __grid_constant__ CUtensorMap tmw, const BlockArgs a) {
+wide_kernel(const __grid_constant__ CUtensorMap tmx, const __grid_constant__ CUtensorMap tmw,
+            const __grid_constant__ CUtensorMap tmo, const BlockArgs a) {
+    using W = Wide<GU>;
+    constexpr int kWideStages = W::kStages;
     extern __shared__ uint8_t smem_raw[];
     const uint32_t base = smem_u32(smem_raw);
     uint8_t *smem = smem_raw + (((base + 1023u) & ~1023u) - base);
-    WideBars *bar = reinterpret_cast<WideBars *>(smem + kWideStages * kWideStage);
+    WideBars *bar = reinterpret_cast<WideBars *>(smem + kWideStages * kWideStage + W::kOut);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const uint32_t rank = cluster_rank();
     constexpr int kCols = GU ? 128 : 256;     // columns of the output a tile
@@ -136,12 +164,9 @@ wide_kernel(const __grid_constant__ CUtensorMap tmx, const __grid_constant__ CUt
     if (threadIdx.x == 0) {
         for (int s = 0; s < kWideStages; ++s) {
             mbar_init(&bar->full[s], 1);
-            mbar_init(&bar->empty[s], 1);
+            mbar_init(&bar->done[s], 1);
         }
-        for (int s = 0; s < 2; ++s) {
-            mbar_init(&bar->acc_full[s], 1);
-            mbar_init(&bar->acc_empty[s], 2 * kWideEpi);
-        }
+        for (int s = 0; s < 2; ++s) mbar_init(&bar->acc_empty[s], 2 * kWideEpi);
         mbar_init(&bar->drain, 1);
         mbar_init(&bar->never, 1);
         bar->abort = 0;
@@ -178,7 +203,7 @@ wide_kernel(const __grid_constant__ CUtensorMap tmx, const __grid_constant__ CUt
                 const int row = o.mb * 256 + (int)rank * 128;
                 const int wrow = GU ? (rank ? a.N : 0) + o.nb * 128 : o.nb * 256 + (int)rank * 128;
                 for (int kb = 0; kb < nkb; ++kb) {
-                    if (!mbar_wait_cl(&bar->empty[s], ph ^ 1u, w, kSiteTmaEmpty)) {
+                    if (!mbar_wait(&bar->done[s], ph ^ 1u, w, kSiteTmaEmpty)) {
                         ok = false;
                         break;
                     }
@@ -199,136 +224,162 @@ wide_kernel(const __grid_constant__ CUtensorMap tmx, const __grid_constant__ CUt
             if (rank == 0)
                 for (int i = 0; i < kWideStages; ++i)
                     if (filled >> i & 1u) mbar_wait_drain(&bar->full[i], last >> i & 1u, 200000000ull, a.status);
-        } else if (warp == 1 && lane == 0 && rank == 0) {
+        } else if (warp == 1 && rank == 0) {
             constexpr uint32_t idesc = idesc_f32acc(0, 0, 256, 256);
             if (a.force_timeout == 1 || (a.force_timeout >= 2 && a.force_timeout - 2 == slot)) {
                 mbar_wait(&bar->never, 0, w, kSiteMmaFull);
             } else {
                 uint32_t s = 0, ph = 0, acc = 0, aph = 0;
-                bool ok = true;
-                for (int t = slot; t < tiles && ok; t += slots)
-                    for (int kb = 0; kb < nkb; ++kb) {
-                        if (!mbar_wait_cl(&bar->acc_empty[acc], aph ^ 1u, w, kSiteMmaAccEmpty) ||
-                            !mbar_wait_cl(&bar->full[s], ph, w, kSiteMmaFull)) {
-                            ok = false;
-                            break;
-                        }
-                        tc_fence_after();
-                        const uint32_t sa = smem_u32(smem + s * kWideStage), sb = sa + kBoxBytes;
+                const int64_t steps = (int64_t)((tiles - 1 - slot) / slots + 1) * nkb;
+                for (int64_t i = 0; i < steps; ++i) {
+                    if (!mbar_wait(&bar->acc_empty[acc], aph ^ 1u, w, kSiteMmaAccEmpty) ||
+                        !mbar_wait(&bar->full[s], ph, w, kSiteMmaFull))
+                        break;
+                    tc_fence_after();
+                    const uint32_t sa = smem_u32(smem + s * kWideStage), d = tmem + acc * 256;
+                    const uint64_t da = sdesc_sw128(sa), db = sdesc_sw128(sa + kBoxBytes);
+                    if (elect_one()) {
 #pragma unroll
-                        for (int k = 0; k < 4; ++k)
-                            mma2_f8(tmem + acc * 256, sdesc_sw128(sa + 32 * k), sdesc_sw128(sb + 32 * k), idesc, k > 0);
-                        mma2_commit_both(&bar->empty[s]);
-                        mma2_commit_both(&bar->acc_full[acc]);
-                        if (++s == kWideStages) {
-                            s = 0;
-                            ph ^= 1u;
-                        }
-                        if (++acc == 2) {
-                            acc = 0;
-                            aph ^= 1u;
-                        }
+                        for (int k = 0; k < 4; ++k) mma2_f8(d, da + 2 * k, db + 2 * k, idesc, k > 0);
+                        mma2_commit_both(&bar->done[s]);
                     }
+                    __syncwarp();
+                    if (++s == kWideStages) {
+                        s = 0;
+                        ph ^= 1u;
+                    }
+                    acc ^= 1u;
+                    if (!acc) aph ^= 1u;
+                }
             }
-            mma2_commit_local(&bar->drain);
+            if (elect_one()) mma2_commit_local(&bar->drain);
+            __syncwarp();
             mbar_wait_drain(&bar->drain, 0, 200000000ull, a.status);
         }
     } else {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 224;");
-        const int quad = warp & 3, half = (warp - 4) >> 2;
+        const int quad = warp & 3, part = (warp - 4) >> 2;
         const uint32_t lanes = (uint32_t)(quad * 32) << 16;
-        // TMEM columns of this warp's four pieces of 32: a half of the tile, or of its gate and of its up columns
-        const auto piece = [&](int j) { return GU ? (j >> 1) * 128 + half * 64 + (j & 1) * 32 : half * 128 + 32 * j; };
-        uint32_t acc = 0, aph = 0;
+        // TMEM column of this warp's piece j of 32: consecutive ones of the tile, or first gate's, then up's
+        constexpr int kPieces = kSums / 32;
+        const auto piece = [&](int j) {
+            return GU ? (j / (kPieces / 2)) * 128 + part * (kSums / 2) + (j % (kPieces / 2)) * 32 : part * kSums + 32 * j;
+        };
+        uint8_t *box = smem + kWideStages * kWideStage + (warp - 4) * W::kBoxes * kOutBox;
+        uint32_t acc = 0, s = 0, ph = 0;
         bool ok = true;
-        for (int t = slot; t < tiles && ok; t += slots) {
+        int row = 0, n0 = 0;
+        const float *sx, *sw0, *sw1;
+        float x, w0, w1;
+        // where a tile's rows, columns and scales are, and its first scales
+        const auto enter = [&](int t) {
             const WideTile o = wide_tile(t, num_m, num_n, a.band);
-            const int row = o.mb * 256 + (int)rank * 128 + quad * 32 + lane;
-            const float *sx = a.sx + (int64_t)min(row, a.M - 1) * nkb;
-            const int b0 = GU ? o.nb : min(2 * o.nb + half, (a.N - 1) / 128);
-            const float *sw0 = a.sw + (int64_t)b0 * nkb, *sw1 = GU ? sw0 + (int64_t)(a.N / 128) * nkb : sw0;
-            uint64_t sum[64];
+            row = o.mb * 256 + (int)rank * 128 + quad * 32;
+            n0 = o.nb * kCols + part * (kCols / kParts);
+            sx = a.sx + (int64_t)min(row + lane, a.M - 1) * nkb;
+            sw0 = a.sw + (int64_t)(GU ? o.nb : min(n0 / 128, (a.N - 1) / 128)) * nkb;
+            sw1 = GU ? sw0 + (int64_t)(a.N / 128) * nkb : sw0;
+            x = __ldg(sx);
+            w0 = __ldg(sw0);
+            w1 = GU ? __ldg(sw1) : 0.0f;
+        };
+        if (slot < tiles) enter(slot);
+        for (int t = slot; t < tiles && ok; t += slots) {
+            uint64_t sum[kSums / 2];
 #pragma unroll
-            for (int i = 0; i < 64; ++i) sum[i] = 0;
-            float x = __ldg(sx), w0 = __ldg(sw0), w1 = GU ? __ldg(sw1) : 0.0f;
+            for (int i = 0; i < kSums / 2; ++i) sum[i] = 0;
             for (int kb = 0; kb < nkb; ++kb) {
                 const float f0 = x * w0, f1 = GU ? x * w1 : f0;
                 const int next = min(kb + 1, nkb - 1);      // its scales are on their way meanwhile
                 x = __ldg(sx + next);
                 w0 = __ldg(sw0 + next);
                 if (GU) w1 = __ldg(sw1 + next);
-                if (!mbar_wait_cl(&bar->acc_full[acc], aph, w, kSiteEpiAccFull)) {
+                if (!mbar_wait(&bar->done[s], ph, w, kSiteEpiAccFull)) {
                     ok = false;
                     break;
                 }
                 tc_fence_after();
                 const uint32_t at = tmem + acc * 256 + lanes;
-                uint32_t r[2][32];
-                tmem_ld32(at + piece(0), r[0]);
-                tmem_ready(r[0]);
+                constexpr int kAtOnce = kPieces / 2;
+                uint32_t r[kAtOnce][32];
 #pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    if (j < 3) tmem_ld32(at + piece(j + 1), r[(j + 1) & 1]);
-                    const float f = (GU && j >= 2) ? f1 : f0;
-                    const uint64_t ff = pack_f2(f, f);
+                for (int h = 0; h < 2; ++h) {
 #pragma unroll
-                    for (int i = 0; i < 16; ++i)
-                        sum[16 * j + i] = fma_f2(ff, pack_u2(r[j & 1][2 * i], r[j & 1][2 * i + 1]), sum[16 * j + i]);
-                    if (j < 3) tmem_ready(r[(j + 1) & 1]);
-                    if (j == 2) {
-                        // the last piece is in registers: the buffer goes back.  (Relaxed: the values read are
-                        // held, nothing else passes between the two.)
+                    for (int q = 0; q < kAtOnce; ++q) tmem_ld32(at + piece(kAtOnce * h + q), r[q]);
+#pragma unroll
+                    for (int q = 0; q < kAtOnce; ++q) tmem_ready(r[q]);
+                    if (h == 1) {
+                        // the last pieces are in registers: the buffer goes back.  (Relaxed: the values read
+                        // are held, nothing else passes between the two.)
                         tc_fence_before();
                         __syncwarp();
                         if (lane == 0) arrive_cluster_relaxed(leader_addr(&bar->acc_empty[acc]));
                     }
-                }
-                if (++acc == 2) {
-                    acc = 0;
-                    aph ^= 1u;
-                }
-            }
-            uint16_t *out = a.out + (int64_t)row * a.ldo;
+                    const float f = (GU && h) ? f1 : f0;
+                    const uint64_t ff = pack_f2(f, f);
 #pragma unroll
-            for (int j = 0; j < (GU ? 4 : 8); ++j) {     // sixteen columns each
-                if (!ok || row >= a.M) break;
-                const int n = o.nb * kCols + half * (kCols / 2) + 16 * j;
-                uint32_t p[8];
+                    for (int q = 0; q < kAtOnce; ++q)
 #pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    float v0, v1;
-                    unpack_f2(sum[8 * j + i], v0, v1);
-                    if (a.bias && n + 2 * i < a.N) {
-                        const uint32_t b = *reinterpret_cast<const uint32_t *>(a.bias + n + 2 * i);
-                        v0 += __uint_as_float(b << 16);
-                        v1 += __uint_as_float(b & 0xFFFF0000u);
-                    }
-                    if (GU) {
-                        float u0, u1;
-                        unpack_f2(sum[32 + 8 * j + i], u0, u1);
-                        if (a.bias) {
-                            const uint32_t b = *reinterpret_cast<const uint32_t *>(a.bias + a.N + n + 2 * i);
-                            u0 += __uint_as_float(b << 16);
-                            u1 += __uint_as_float(b & 0xFFFF0000u);
+                        for (int i = 0; i < 16; ++i) {
+                            uint64_t &o2 = sum[16 * (kAtOnce * h + q) + i];
+                            o2 = fma_f2(ff, pack_u2(r[q][2 * i], r[q][2 * i + 1]), o2);
                         }
-                        v0 = silu_mul_ieee(v0, u0);
-                        v1 = silu_mul_ieee(v1, u1);
-                    }
-                    p[i] = pack_bf16x2(v0, v1);
                 }
-                if (n >= a.N) continue;
-                if (a.v32 && n + 16 <= a.N) {
-                    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};"
-                                 :: "l"(out + n), "r"(p[0]), "r"(p[1]), "r"(p[2]), "r"(p[3]), "r"(p[4]), "r"(p[5]),
-                                    "r"(p[6]), "r"(p[7])
-                                 : "memory");
-                } else {
-                    *reinterpret_cast<uint4 *>(out + n) = make_uint4(p[0], p[1], p[2], p[3]);
-                    if (n + 8 < a.N) *reinterpret_cast<uint4 *>(out + n + 8) = make_uint4(p[4], p[5], p[6], p[7]);
+                acc ^= 1u;
+                if (++s == kWideStages) {
+                    s = 0;
+                    ph ^= 1u;
                 }
             }
+            if (!ok) break;
+            const int trow = row, tn = n0;
+            if (t + slots < tiles) enter(t + slots);
+            if (a.bias) {
+#pragma unroll
+                for (int c = 0; c < kSums; c += 2) {
+                    const int n = tn + (GU ? c % (kSums / 2) : c);
+                    if (n < a.N) {
+                        const uint32_t bb = __ldg(reinterpret_cast<const uint32_t *>(a.bias + (GU && c >= kSums / 2 ? a.N : 0) + n));
+                        float v0, v1;
+                        unpack_f2(sum[c / 2], v0, v1);
+                        sum[c / 2] = pack_f2(v0 + __uint_as_float(bb << 16), v1 + __uint_as_float(bb & 0xFFFF0000u));
+                    }
+                }
+            }
+            // through shared memory, 64 columns a box: 16-byte units swizzled as the copy expects them
+            if (lane == 0) bulk_wait_read_all();
             __syncwarp();
+#pragma unroll
+            for (int b = 0; b < W::kBoxes; ++b)
+#pragma unroll
+                for (int q = 0; q < 8; ++q) {
+                    uint32_t p[4];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        float v0, v1;
+                        const int c = 64 * b + 8 * q + 2 * i;
+                        unpack_f2(sum[c / 2], v0, v1);
+                        if (GU) {
+                            float u0, u1;
+                            unpack_f2(sum[kSums / 4 + c / 2], u0, u1);
+                            v0 = silu_mul_fast(v0, u0);
+                            v1 = silu_mul_fast(v1, u1);
+                        }
+                        p[i] = pack_bf16x2(v0, v1);
+                    }
+                    *reinterpret_cast<uint4 *>(box + b * kOutBox + lane * 128 + ((q ^ (lane & 7)) << 4)) =
+                        make_uint4(p[0], p[1], p[2], p[3]);
+                }
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0 && trow < a.M) {
+#pragma unroll
+                for (int b = 0; b < W::kBoxes; ++b)
+                    if (tn + 64 * b < a.N) tma_store_2d(&tmo, box + b * kOutBox, tn + 64 * b, trow);
+                bulk_commit();
+            }
         }
+        if (lane == 0) bulk_wait_all();     // the copies have read the boxes before the CTA ends
     }
     pdl_launch_dependents();
     tc_fence_before();
@@ -347,16 +398,21 @@ wide_kernel(const __grid_constant__ CUtensorMap tmx, const __grid_constant__ CUt
 
 // ------------------------------------------------------------ few rows
 
-constexpr int kMaxStages = 12, kMaxSplit = 8;
+constexpr int kMaxStages = 12, kMaxSplit = 8, kMaxBufs = 8;
 
 template <int T, bool GU>
 struct Few {
-    static constexpr int kEpi = T >= 64 ? 8 : 4;               // warps that read TMEM back
-    static constexpr int kCols = T / (kEpi / 4);               // rows of x a warp holds
+    // The warps that read TMEM back: a k-block takes four (of 32 weight rows each), or eight that share the rows
+    // of x where one thread cannot hold them all.  For fewer rows a k-block's copy arrives in less time than
+    // one group of warps takes for it, so that `kSets` groups take k-blocks in turn.
+    static constexpr int kHalves = T == 128 ? 2 : 1;
+    static constexpr int kSets = T <= 32 ? 4 : T == 64 ? 2 : 1;
+    static constexpr int kEpi = 4 * kHalves * kSets;
+    static constexpr int kCols = T / kHalves;                  // rows of x a warp holds
     static constexpr int kTiles = GU ? 2 : 1;                  // weight tiles: gate, up
     static constexpr int kStage = kTiles * kBoxBytes + T * 128;
     static constexpr int kAcc = kTiles * T;                    // TMEM columns of a buffer
-    static constexpr int kBufs = 512 / kAcc >= 4 ? 4 : 2;
+    static constexpr int kBufs = 512 / kAcc >= kMaxBufs ? kMaxBufs : 512 / kAcc;
     static constexpr int kTmem = kBufs * kAcc;
     static constexpr int kScales = kEpi * 2 * kTiles * kCols;  // floats
     static constexpr int kRest = 1024 + 512 + kScales * 4;
@@ -365,25 +421,28 @@ struct Few {
     static constexpr int kSmem = kStages * kStage + kRest;
     static constexpr int kThreads = 64 + 32 * kEpi;
     static_assert(kTmem >= 32 && kTmem <= 512 && (kTmem & (kTmem - 1)) == 0, "TMEM columns");
-    static_assert(kStages >= 3, "stages");
-    static_assert(kTiles * T * 128 * 4 <= kStages * kStage, "the parts of a split K fit in the ring");
+    static_assert(kStages >= 3 && kBufs >= 2 && kBufs % kSets == 0, "stages, buffers");
+    static_assert(kSets * kTiles * T * 512 <= kStages * kStage, "the sums of the groups fit in the ring");
 };
 
 struct FewBars {
     uint64_t full[kMaxStages], empty[kMaxStages];
-    uint64_t acc_full[4], acc_empty[4];
+    uint64_t acc_full[kMaxBufs], acc_empty[kMaxBufs];
     uint64_t drain, never;
     uint32_t tmem;
     int abort;
 };
 static_assert(sizeof(FewBars) <= 512, "barrier block");
 
-__device__ __forceinline__ float ld_cluster(uint32_t local, int rank) {
-    uint32_t at;
+__device__ __forceinline__ float ld_cluster(uint32_t at) {
     float v;
-    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"(local), "r"(rank));
     asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(at) : "memory");
     return v;
+}
+__device__ __forceinline__ uint32_t cluster_addr(uint32_t local, int rank) {
+    uint32_t at;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"(local), "r"(rank));
+    return at;
 }
 
 template <int T, bool GU>
@@ -404,7 +463,7 @@ few_kernel(const __grid_constant__ CUtensorMap tmx, const __grid_constant__ CUte
         }
         for (int s = 0; s < F::kBufs; ++s) {
             mbar_init(&bar->acc_full[s], 1);
-            mbar_init(&bar->acc_empty[s], F::kEpi);
+            mbar_init(&bar->acc_empty[s], 4 * F::kHalves);
         }
         mbar_init(&bar->drain, 1);
         mbar_init(&bar->never, 1);
@@ -425,8 +484,7 @@ few_kernel(const __grid_constant__ CUtensorMap tmx, const __grid_constant__ CUte
     const uint32_t tmem = bar->tmem;
     const int split = a.split, rank = split > 1 ? (int)cluster_rank() : 0, tile = (int)blockIdx.x / split;
     const int n0 = tile * 128, m0 = (int)blockIdx.y * T;
-    // (k-blocks times CTAs stay far below 2^31: K is at most 65,536)
-    const int k0 = rank * a.nkb / split, k1 = (rank + 1) * a.nkb / split;
+    const int k0 = rank * a.nkb / split, k1 = (rank + 1) * a.nkb / split;      // (at most 8 times 512)
     const WaitCtx w{a.limit_ns, &bar->abort, a.status};
 
     if (warp == 0) {
@@ -450,42 +508,44 @@ few_kernel(const __grid_constant__ CUtensorMap tmx, const __grid_constant__ CUte
                 if (filled >> i & 1u) mbar_wait_drain(&bar->full[i], last >> i & 1u, 200000000ull, a.status);
         }
     } else if (warp == 1) {
-        if (lane == 0) {
-            constexpr uint32_t idesc = idesc_f32acc(0, 0, 128, T);
-            if (a.force_timeout == 1 || (a.force_timeout >= 2 && a.force_timeout - 2 == (int)blockIdx.x)) {
-                mbar_wait(&bar->never, 0, w, kSiteMmaFull);
-            } else {
-                uint32_t s = 0, ph = 0, acc = 0, aph = 0;
-                for (int kb = k0; kb < k1; ++kb) {
-                    if (!mbar_wait(&bar->acc_empty[acc], aph ^ 1u, w, kSiteMmaAccEmpty) ||
-                        !mbar_wait(&bar->full[s], ph, w, kSiteMmaFull))
-                        break;
-                    tc_fence_after();
-                    const uint32_t sa = smem_u32(smem + s * F::kStage), sb = sa + F::kTiles * kBoxBytes;
+        constexpr uint32_t idesc = idesc_f32acc(0, 0, 128, T);
+        if (a.force_timeout == 1 || (a.force_timeout >= 2 && a.force_timeout - 2 == (int)blockIdx.x)) {
+            mbar_wait(&bar->never, 0, w, kSiteMmaFull);
+        } else {
+            uint32_t s = 0, ph = 0, acc = 0, aph = 0;
+            for (int kb = k0; kb < k1; ++kb) {
+                if (!mbar_wait(&bar->acc_empty[acc], aph ^ 1u, w, kSiteMmaAccEmpty) ||
+                    !mbar_wait(&bar->full[s], ph, w, kSiteMmaFull))
+                    break;
+                tc_fence_after();
+                const uint32_t sa = smem_u32(smem + s * F::kStage);
+                const uint64_t da = sdesc_sw128(sa), db = sdesc_sw128(sa + F::kTiles * kBoxBytes);
+                const uint32_t d = tmem + acc * F::kAcc;
+                if (elect_one()) {
 #pragma unroll
-                    for (int h = 0; h < F::kTiles; ++h)
+                    for (int k = 0; k < 4; ++k)
 #pragma unroll
-                        for (int k = 0; k < 4; ++k)
-                            mma_f8(tmem + acc * F::kAcc + h * T, sdesc_sw128(sa + h * kBoxBytes + 32 * k), sdesc_sw128(sb + 32 * k),
-                                   idesc, k > 0);
-                    mma_commit(&bar->empty[s]);
+                        for (int h = 0; h < F::kTiles; ++h)
+                            mma_f8(d + h * T, da + 2 * k + h * (kBoxBytes >> 4), db + 2 * k, idesc, k > 0);
                     mma_commit(&bar->acc_full[acc]);
-                    if (++s == F::kStages) {
-                        s = 0;
-                        ph ^= 1u;
-                    }
-                    if (++acc == F::kBufs) {
-                        acc = 0;
-                        aph ^= 1u;
-                    }
+                    mma_commit(&bar->empty[s]);
+                }
+                __syncwarp();
+                if (++s == F::kStages) {
+                    s = 0;
+                    ph ^= 1u;
+                }
+                if (++acc == F::kBufs) {
+                    acc = 0;
+                    aph ^= 1u;
                 }
             }
-            mma_commit(&bar->drain);
-            mbar_wait_drain(&bar->drain, 0, 200000000ull, a.status);
         }
+        if (elect_one()) mma_commit(&bar->drain);
+        __syncwarp();
+        mbar_wait_drain(&bar->drain, 0, 200000000ull, a.status);
     } else {
-        const int quad = warp & 3, e = warp - 2, c0 = (e >> 2) * F::kCols;
-        const int n = n0 + quad * 32 + lane;
+        const int quad = warp & 3, e = warp - 2, set = (e >> 2) / F::kHalves, c0 = (e >> 2) % F::kHalves * F::kCols;
         const uint32_t lanes = (uint32_t)(quad * 32) << 16;
         float *mine = scales + e * 2 * F::kTiles * F::kCols;     // two buffers of this warp's products of scales
         constexpr int kPer = (F::kCols + 31) / 32;               // of them a lane
@@ -508,11 +568,12 @@ few_kernel(const __grid_constant__ CUtensorMap tmx, const __grid_constant__ CUte
             w0 = __ldg(sw0 + kb);
             if (GU) w1 = __ldg(sw1 + kb);
         };
-        fetch(k0);
-        uint32_t acc = 0, aph = 0;
+        if (k0 + set < k1) fetch(k0 + set);
+        uint32_t acc = set, aph = 0, flip = 0;
         bool ok = true;
-        for (int kb = k0; kb < k1; ++kb) {
-            float *f = mine + (kb & 1) * F::kTiles * F::kCols;
+        for (int kb = k0 + set; kb < k1; kb += F::kSets) {
+            float *f = mine + flip * F::kTiles * F::kCols;
+            flip ^= 1u;
 #pragma unroll
             for (int i = 0; i < kPer; ++i) {
                 if (32 * i + lane < F::kCols) {
@@ -521,7 +582,7 @@ few_kernel(const __grid_constant__ CUtensorMap tmx, const __grid_constant__ CUte
                 }
             }
             __syncwarp();
-            if (kb + 1 < k1) fetch(kb + 1);
+            if (kb + F::kSets < k1) fetch(kb + F::kSets);
             if (!mbar_wait(&bar->acc_full[acc], aph, w, kSiteEpiAccFull)) {
                 ok = false;
                 break;
@@ -557,34 +618,22 @@ few_kernel(const __grid_constant__ CUtensorMap tmx, const __grid_constant__ CUte
                 }
                 if (j + 1 < kPieces) tmem_ready(r[(j + 1) & 1]);
             }
-            if (++acc == F::kBufs) {
-                acc = 0;
+            acc += F::kSets;
+            if (acc >= F::kBufs) {
+                acc -= F::kBufs;
                 aph ^= 1u;
             }
         }
-        if (ok && split == 1) {
-            if (n < a.N) {
-                const float b0 = a.bias ? bf16_at(a.bias + n) : 0.0f, b1 = GU && a.bias ? bf16_at(a.bias + a.N + n) : 0.0f;
-#pragma unroll
-                for (int i = 0; i < F::kCols; ++i) {
-                    if (m0 + c0 + i >= a.M) break;
-                    float v[2], u[2] = {0.0f, 0.0f};
-                    unpack_f2(sum[0][i / 2], v[0], v[1]);
-                    float y = v[i & 1] + b0;
-                    if (GU) {
-                        unpack_f2(sum[F::kTiles - 1][i / 2], u[0], u[1]);
-                        y = silu_mul_ieee(y, u[i & 1] + b1);
-                    }
-                    a.out[(int64_t)(m0 + c0 + i) * a.ldo + n] = __bfloat16_as_ushort(__float2bfloat16_rn(y));
-                }
-            }
-        } else if (ok) {
-            // every k-block's MMAs have ended, so the ring is free: this part's sums, [tile][row of x][lane]
-            float *part = reinterpret_cast<float *>(smem) + quad * 32 + lane;
+        // The ring is free once every group has seen its last k-block complete; then each leaves its sums there,
+        // [group][gate, up][row of x][weight row].
+        asm volatile("bar.sync 1, %0;" ::"n"(32 * F::kEpi) : "memory");
+        if (ok) {
+            float *part = reinterpret_cast<float *>(smem) + set * F::kTiles * T * 128 + quad * 32 + lane;
 #pragma unroll
             for (int h = 0; h < F::kTiles; ++h)
 #pragma unroll
                 for (int i = 0; i < F::kCols; ++i) {
+                    if (m0 + c0 + i >= a.M) break;
                     float v[2];
                     unpack_f2(sum[h][i / 2], v[0], v[1]);
                     part[(h * T + c0 + i) * 128] = v[i & 1];
@@ -593,27 +642,29 @@ few_kernel(const __grid_constant__ CUtensorMap tmx, const __grid_constant__ CUte
     }
     tc_fence_before();
     __syncthreads();
-    if (split > 1) {
-        cluster_sync();
-        if (warp >= 2 && !bar->abort) {
-            const int i = threadIdx.x - 64, n = n0 + (i & 127);
-            const float b0 = a.bias && n < a.N ? bf16_at(a.bias + n) : 0.0f;
-            const float b1 = GU && a.bias && n < a.N ? bf16_at(a.bias + a.N + n) : 0.0f;
-            // this CTA's share of the rows of x
-            for (int c = rank + split * (i >> 7); c < T && m0 + c < a.M; c += split * (F::kEpi / 4)) {
-                float v = 0.0f, u = 0.0f;
-                const uint32_t at = base + (uint32_t)(smem - smem_raw) + (uint32_t)((c * 128 + (i & 127)) * 4);
-                for (int q = 0; q < split; ++q) {
-                    v += ld_cluster(at, q);
-                    if (GU) u += ld_cluster(at + T * 512, q);
+    if (split > 1) cluster_sync();
+    if (warp >= 2 && !bar->abort) {
+        // this CTA's share of the rows of x: the sums of the cluster's CTAs and their groups, always in this order
+        const int i = threadIdx.x - 64, n = n0 + (i & 127);
+        const float b0 = a.bias && n < a.N ? bf16_at(a.bias + n) : 0.0f;
+        const float b1 = GU && a.bias && n < a.N ? bf16_at(a.bias + a.N + n) : 0.0f;
+        for (int c = rank + split * (i >> 7); c < T && m0 + c < a.M; c += split * (F::kEpi / 4)) {
+            float v = 0.0f, u = 0.0f;
+            const uint32_t local = base + (uint32_t)(smem - smem_raw) + (uint32_t)((c * 128 + (i & 127)) * 4);
+            for (int q = 0; q < split; ++q) {
+                const uint32_t at = split > 1 ? cluster_addr(local, q) : local;
+#pragma unroll
+                for (int g = 0; g < F::kSets; ++g) {
+                    v += ld_cluster(at + g * F::kTiles * T * 512);
+                    if (GU) u += ld_cluster(at + (g * F::kTiles + 1) * T * 512);
                 }
-                v += b0;
-                if (GU) v = silu_mul_ieee(v, u + b1);
-                if (n < a.N) a.out[(int64_t)(m0 + c) * a.ldo + n] = __bfloat16_as_ushort(__float2bfloat16_rn(v));
             }
+            v += b0;
+            if (GU) v = silu_mul_fast(v, u + b1);
+            if (n < a.N) a.out[(int64_t)(m0 + c) * a.ldo + n] = __bfloat16_as_ushort(__float2bfloat16_rn(v));
         }
-        cluster_sync();
     }
+    if (split > 1) cluster_sync();
     pdl_launch_dependents();
     if (warp == 1) {
         tc_fence_after();
@@ -632,6 +683,7 @@ int maps(CUtensorMap &tx, CUtensorMap &tw, const void *qx, const void *qw, int64
 
 template <bool GU>
 int launch_wide(const void *qx, const void *qw, int64_t K, BlockArgs a, int sms, cudaStream_t st) {
+    constexpr int kWideSmem = Wide<GU>::kSmem;
     static SmemOptIn opt;
     static std::atomic<int> most{0};
     auto kern = wide_kernel<GU>;
@@ -665,8 +717,12 @@ int launch_wide(const void *qx, const void *qw, int64_t K, BlockArgs a, int sms,
     CUtensorMap tx, tw;
     const int rc = maps(tx, tw, qx, qw, a.M, (GU ? 2 : 1) * (int64_t)a.N, K, 128);
     if (rc) return rc;
+    CUtensorMap to;
+    const int rco = internal_make_tmap(&to, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, a.out, (uint64_t)a.N, (uint64_t)a.M, (uint64_t)a.ldo * 2,
+                                       64, 32, CU_TENSOR_MAP_SWIZZLE_128B);
+    if (rco) return rco;
     const int tiles = num_m * num_n;
-    e = launch_kernel(kern, dim3((unsigned)(2 * std::min(tiles, pairs))), dim3(kWideThreads), kWideSmem, st, 2, true, tx, tw, a);
+    e = launch_kernel(kern, dim3((unsigned)(2 * std::min(tiles, pairs))), dim3(kWideThreads), kWideSmem, st, 2, true, tx, tw, to, a);
     return e == cudaSuccess ? CLEF_OK : internal_cuda_error(e, "block linear launch");
 }
 
@@ -714,7 +770,6 @@ int block_call(bool gu, const void *qx, const float *sx, const void *qw, const f
     a.bias = static_cast<const uint16_t *>(bias);
     a.out = static_cast<uint16_t *>(out);
     a.ldo = ldo;
-    a.v32 = !kv_misaligned(out, 32) && ldo % 16 == 0;
     a.band = a.split = 1;
     a.status = status;
     a.limit_ns = internal_wait_limit(&a.force_timeout);

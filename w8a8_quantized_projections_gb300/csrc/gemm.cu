@@ -288,16 +288,6 @@ __device__ __forceinline__ float bf16_round(float x) { return __bfloat162float(_
 __device__ __forceinline__ float bf16_lo(uint32_t w) { return __uint_as_float(w << 16); }
 __device__ __forceinline__ float bf16_hi(uint32_t w) { return __uint_as_float(w & 0xFFFF0000u); }
 
-// The same with the hardware exp2 and reciprocal approximations (a few fp32 ulps; beside
-// silu_mul_ieee's, the bf16 results of both stay within one ulp of the correctly rounded value).
-// Denominators above 2^126 (g below about -87) are scaled by 2^-64 with the
-// numerator, exactly, to keep the fast quotient in its accurate range.
-__device__ __forceinline__ float silu_mul_fast(float g, float u) {
-    const float d = __fadd_rn(1.0f, __expf(-g));
-    const float sc = d > 0x1p126f ? 0x1p-64f : 1.0f;
-    return __fmul_rn(__fdividef(g * sc, d * sc), u);
-}
-
 // Epilogue value of one accumulator: ((acc * sa) * sb) + bias, each rounded
 // (no bias: no add, so a -0 product stays -0).
 __device__ __forceinline__ float scale_bias(float acc, float sa, float sb, float bias, bool has_bias) {
