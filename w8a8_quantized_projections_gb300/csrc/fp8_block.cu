@@ -49,6 +49,7 @@ struct BlockArgs {
     int64_t ldo;
     int band;                 // wide: tiles of rows a band
     int split;                // few: CTAs that share a tile's K
+    int tiles_m;              // few: tiles of rows
     unsigned int *status;
     uint64_t limit_ns;
     int force_timeout;
@@ -73,12 +74,24 @@ __device__ __forceinline__ uint64_t fma_f2(uint64_t a, uint64_t b, uint64_t c) {
     return d;
 }
 
-// One lane of a whole warp.  The MMA issuers run with all lanes and elect one for each k-block's MMAs: what they
-// count then stays in uniform registers, which the MMAs take their operands from.
+// One lane of a whole warp.  The warps that issue copies and MMAs run with all lanes and elect one for each k-block:
+// what they count then stays in uniform registers, which those instructions take their operands from.
 __device__ __forceinline__ bool elect_one() {
     uint32_t p;
     asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
     return p != 0;
+}
+
+// Whether the phase has completed, without waiting for it.  The MMA issuers ask for the next k-block's barriers before
+// they issue a k-block's MMAs: a wait takes some 60 clocks even where there is nothing to wait for.
+__device__ __forceinline__ bool mbar_done(uint64_t *bar, uint32_t parity) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}\n"
+        : "=r"(ok) : "r"(smem_u32(bar)), "r"(parity) : "memory");
+    return ok != 0;
 }
 
 // Waits for this thread's TMEM loads; the registers are operands, so that no use of them moves before it.
@@ -195,7 +208,7 @@ wide_kernel(const __grid_constant__ CUtensorMap tmx, const __grid_constant__ CUt
     // 4 x 32 x 56 + 8 x 32 x 224 registers of the 384 x 168 launched
     if (warp < 4) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
-        if (warp == 0 && lane == 0) {
+        if (warp == 0) {
             uint32_t s = 0, ph = 0, filled = 0, last = 0;
             bool ok = true;
             for (int t = slot; t < tiles && ok; t += slots) {
@@ -209,9 +222,12 @@ wide_kernel(const __grid_constant__ CUtensorMap tmx, const __grid_constant__ CUt
                     }
                     uint8_t *st = smem + s * kWideStage;
                     const uint32_t full = leader_addr(&bar->full[s]);
-                    if (rank == 0) mbar_arrive_expect_tx(&bar->full[s], 2 * kWideStage);
-                    tma_load_2d_pair(st, &tmx, kb * 128, row, full);
-                    tma_load_2d_pair(st + kBoxBytes, &tmw, kb * 128, wrow, full);
+                    if (elect_one()) {
+                        if (rank == 0) mbar_arrive_expect_tx(&bar->full[s], 2 * kWideStage);
+                        tma_load_2d_pair(st, &tmx, kb * 128, row, full);
+                        tma_load_2d_pair(st + kBoxBytes, &tmw, kb * 128, wrow, full);
+                    }
+                    __syncwarp();
                     filled |= 1u << s;
                     last = (last & ~(1u << s)) | ph << s;
                     if (++s == kWideStages) {
@@ -231,25 +247,28 @@ wide_kernel(const __grid_constant__ CUtensorMap tmx, const __grid_constant__ CUt
             } else {
                 uint32_t s = 0, ph = 0, acc = 0, aph = 0;
                 const int64_t steps = (int64_t)((tiles - 1 - slot) / slots + 1) * nkb;
+                bool ready = false;
                 for (int64_t i = 0; i < steps; ++i) {
-                    if (!mbar_wait(&bar->acc_empty[acc], aph ^ 1u, w, kSiteMmaAccEmpty) ||
-                        !mbar_wait(&bar->full[s], ph, w, kSiteMmaFull))
+                    if (!ready && (!mbar_wait(&bar->acc_empty[acc], aph ^ 1u, w, kSiteMmaAccEmpty) ||
+                                   !mbar_wait(&bar->full[s], ph, w, kSiteMmaFull)))
                         break;
                     tc_fence_after();
-                    const uint32_t sa = smem_u32(smem + s * kWideStage), d = tmem + acc * 256;
+                    const uint32_t sa = smem_u32(smem + s * kWideStage), d = tmem + acc * 256, s0 = s;
                     const uint64_t da = sdesc_sw128(sa), db = sdesc_sw128(sa + kBoxBytes);
-                    if (elect_one()) {
-#pragma unroll
-                        for (int k = 0; k < 4; ++k) mma2_f8(d, da + 2 * k, db + 2 * k, idesc, k > 0);
-                        mma2_commit_both(&bar->done[s]);
-                    }
-                    __syncwarp();
                     if (++s == kWideStages) {
                         s = 0;
                         ph ^= 1u;
                     }
                     acc ^= 1u;
                     if (!acc) aph ^= 1u;
+                    const bool e0 = mbar_done(&bar->acc_empty[acc], aph ^ 1u), e1 = mbar_done(&bar->full[s], ph);
+                    if (elect_one()) {
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) mma2_f8(d, da + 2 * k, db + 2 * k, idesc, k > 0);
+                        mma2_commit_both(&bar->done[s0]);
+                    }
+                    __syncwarp();
+                    ready = e0 && e1;
                 }
             }
             if (elect_one()) mma2_commit_local(&bar->drain);
@@ -406,17 +425,18 @@ struct Few {
     // of x where one thread cannot hold them all.  For fewer rows a k-block's copy arrives in less time than
     // one group of warps takes for it, so that `kSets` groups take k-blocks in turn.
     static constexpr int kHalves = T == 128 ? 2 : 1;
-    static constexpr int kSets = T <= 32 ? 4 : T == 64 ? 2 : 1;
+    static constexpr int kSets = T <= 32 || (T == 64 && !GU) ? 2 : 1;
+    static constexpr int kPerSm = T <= 32 && !GU ? 2 : 1;      // CTAs an SM
     static constexpr int kEpi = 4 * kHalves * kSets;
     static constexpr int kCols = T / kHalves;                  // rows of x a warp holds
     static constexpr int kTiles = GU ? 2 : 1;                  // weight tiles: gate, up
     static constexpr int kStage = kTiles * kBoxBytes + T * 128;
     static constexpr int kAcc = kTiles * T;                    // TMEM columns of a buffer
-    static constexpr int kBufs = 512 / kAcc >= kMaxBufs ? kMaxBufs : 512 / kAcc;
+    static constexpr int kBufs = 512 / kPerSm / kAcc >= kMaxBufs ? kMaxBufs : 512 / kPerSm / kAcc;
     static constexpr int kTmem = kBufs * kAcc;
     static constexpr int kScales = kEpi * 2 * kTiles * kCols;  // floats
     static constexpr int kRest = 1024 + 512 + kScales * 4;
-    static constexpr int kFit = (232448 - kRest) / kStage;
+    static constexpr int kFit = ((kPerSm == 2 ? 115712 : 232448) - kRest) / kStage;
     static constexpr int kStages = kFit > kMaxStages ? kMaxStages : kFit;
     static constexpr int kSmem = kStages * kStage + kRest;
     static constexpr int kThreads = 64 + 32 * kEpi;
@@ -446,7 +466,7 @@ __device__ __forceinline__ uint32_t cluster_addr(uint32_t local, int rank) {
 }
 
 template <int T, bool GU>
-__global__ void __launch_bounds__(Few<T, GU>::kThreads, 1)
+__global__ void __launch_bounds__(Few<T, GU>::kThreads, Few<T, GU>::kPerSm)
 few_kernel(const __grid_constant__ CUtensorMap tmx, const __grid_constant__ CUtensorMap tmw, const BlockArgs a) {
     using F = Few<T, GU>;
     extern __shared__ uint8_t smem_raw[];
@@ -482,55 +502,48 @@ few_kernel(const __grid_constant__ CUtensorMap tmx, const __grid_constant__ CUte
     pdl_wait();
 
     const uint32_t tmem = bar->tmem;
-    const int split = a.split, rank = split > 1 ? (int)cluster_rank() : 0, tile = (int)blockIdx.x / split;
-    const int n0 = tile * 128, m0 = (int)blockIdx.y * T;
+    // tiles of one part of the weight side by side, so that it is read from memory once
+    const int split = a.split, rank = split > 1 ? (int)cluster_rank() : 0, both = (int)blockIdx.x / split;
+    const int tile = both / a.tiles_m, n0 = tile * 128, m0 = (both - tile * a.tiles_m) * T;
     const int k0 = rank * a.nkb / split, k1 = (rank + 1) * a.nkb / split;      // (at most 8 times 512)
     const WaitCtx w{a.limit_ns, &bar->abort, a.status};
 
     if (warp == 0) {
-        if (lane == 0) {
-            uint32_t s = 0, ph = 0, filled = 0, last = 0;
-            for (int kb = k0; kb < k1; ++kb) {
-                if (!mbar_wait(&bar->empty[s], ph ^ 1u, w, kSiteTmaEmpty)) break;
-                uint8_t *st = smem + s * F::kStage;
+        uint32_t s = 0, ph = 0, filled = 0, last = 0;
+        for (int kb = k0; kb < k1; ++kb) {
+            if (!mbar_wait(&bar->empty[s], ph ^ 1u, w, kSiteTmaEmpty)) break;
+            uint8_t *st = smem + s * F::kStage;
+            if (elect_one()) {
                 mbar_arrive_expect_tx(&bar->full[s], F::kStage);
                 tma_load_2d(st, &tmw, kb * 128, n0, &bar->full[s]);
                 if (GU) tma_load_2d(st + kBoxBytes, &tmw, kb * 128, a.N + n0, &bar->full[s]);
                 tma_load_2d(st + F::kTiles * kBoxBytes, &tmx, kb * 128, m0, &bar->full[s]);
-                filled |= 1u << s;
-                last = (last & ~(1u << s)) | ph << s;
-                if (++s == F::kStages) {
-                    s = 0;
-                    ph ^= 1u;
-                }
             }
-            for (int i = 0; i < F::kStages; ++i)
-                if (filled >> i & 1u) mbar_wait_drain(&bar->full[i], last >> i & 1u, 200000000ull, a.status);
+            __syncwarp();
+            filled |= 1u << s;
+            last = (last & ~(1u << s)) | ph << s;
+            if (++s == F::kStages) {
+                s = 0;
+                ph ^= 1u;
+            }
         }
+        for (int i = 0; i < F::kStages; ++i)
+            if (filled >> i & 1u) mbar_wait_drain(&bar->full[i], last >> i & 1u, 200000000ull, a.status);
     } else if (warp == 1) {
         constexpr uint32_t idesc = idesc_f32acc(0, 0, 128, T);
         if (a.force_timeout == 1 || (a.force_timeout >= 2 && a.force_timeout - 2 == (int)blockIdx.x)) {
             mbar_wait(&bar->never, 0, w, kSiteMmaFull);
         } else {
             uint32_t s = 0, ph = 0, acc = 0, aph = 0;
+            bool ready = false;
             for (int kb = k0; kb < k1; ++kb) {
-                if (!mbar_wait(&bar->acc_empty[acc], aph ^ 1u, w, kSiteMmaAccEmpty) ||
-                    !mbar_wait(&bar->full[s], ph, w, kSiteMmaFull))
+                if (!ready && (!mbar_wait(&bar->acc_empty[acc], aph ^ 1u, w, kSiteMmaAccEmpty) ||
+                               !mbar_wait(&bar->full[s], ph, w, kSiteMmaFull)))
                     break;
                 tc_fence_after();
                 const uint32_t sa = smem_u32(smem + s * F::kStage);
                 const uint64_t da = sdesc_sw128(sa), db = sdesc_sw128(sa + F::kTiles * kBoxBytes);
-                const uint32_t d = tmem + acc * F::kAcc;
-                if (elect_one()) {
-#pragma unroll
-                    for (int k = 0; k < 4; ++k)
-#pragma unroll
-                        for (int h = 0; h < F::kTiles; ++h)
-                            mma_f8(d + h * T, da + 2 * k + h * (kBoxBytes >> 4), db + 2 * k, idesc, k > 0);
-                    mma_commit(&bar->acc_full[acc]);
-                    mma_commit(&bar->empty[s]);
-                }
-                __syncwarp();
+                const uint32_t d = tmem + acc * F::kAcc, s0 = s, acc0 = acc;
                 if (++s == F::kStages) {
                     s = 0;
                     ph ^= 1u;
@@ -539,6 +552,18 @@ few_kernel(const __grid_constant__ CUtensorMap tmx, const __grid_constant__ CUte
                     acc = 0;
                     aph ^= 1u;
                 }
+                const bool e0 = mbar_done(&bar->acc_empty[acc], aph ^ 1u), e1 = mbar_done(&bar->full[s], ph);
+                if (elect_one()) {
+#pragma unroll
+                    for (int k = 0; k < 4; ++k)
+#pragma unroll
+                        for (int h = 0; h < F::kTiles; ++h)
+                            mma_f8(d + h * T, da + 2 * k + h * (kBoxBytes >> 4), db + 2 * k, idesc, k > 0);
+                    mma_commit(&bar->acc_full[acc0]);
+                    mma_commit(&bar->empty[s0]);
+                }
+                __syncwarp();
+                ready = e0 && e1;
             }
         }
         if (elect_one()) mma_commit(&bar->drain);
@@ -726,8 +751,58 @@ int launch_wide(const void *qx, const void *qw, int64_t K, BlockArgs a, int sms,
     return e == cudaSuccess ? CLEF_OK : internal_cuda_error(e, "block linear launch");
 }
 
+// Clusters of `split` CTAs that the device holds at once where an SM holds one CTA: how many fit into its groups of
+// SMs (asked once for each size).
+int clusters_at_once(int split) {
+    using F = Few<64, false>;
+    static SmemOptIn opt;
+    static std::atomic<int> known[kMaxSplit + 1];
+    int n = known[split].load(std::memory_order_relaxed);
+    if (n == 0) {
+        cudaLaunchConfig_t cfg = {};
+        cudaLaunchAttribute attr[1];
+        attr[0].id = cudaLaunchAttributeClusterDimension;
+        attr[0].val.clusterDim.x = (unsigned)split;
+        attr[0].val.clusterDim.y = 1;
+        attr[0].val.clusterDim.z = 1;
+        cfg.gridDim = dim3((unsigned)(split * 1024), 1, 1);
+        cfg.blockDim = dim3(F::kThreads, 1, 1);
+        cfg.dynamicSmemBytes = F::kSmem;
+        cfg.attrs = attr;
+        cfg.numAttrs = 1;
+        auto kern = few_kernel<64, false>;
+        if (opt.set(reinterpret_cast<const void *>(kern), F::kSmem) != cudaSuccess ||
+            cudaOccupancyMaxActiveClusters(&n, kern, &cfg) != cudaSuccess || n < 1)
+            n = 1;
+        known[split].store(n, std::memory_order_relaxed);
+    }
+    return n;
+}
+
+struct FewPlan {
+    int rows, split;      // rows of x a tile, CTAs that share a tile
+    double us;            // what the call is expected to take
+};
+
+// A call with tiles of T rows.  CTAs that share a tile's K: as many as run at once, each with four k-blocks or more.
+// Expected time: 4 us for launch, first copies and end, which grow with the sums that meet at the end; then
+// k-blocks at what one takes a CTA while the weight comes out of L2, or the weight's bytes at 6 TB/s.
 template <int T, bool GU>
-int launch_few(const void *qx, const void *qw, int64_t K, const BlockArgs &a, cudaStream_t st) {
+FewPlan plan_few(const BlockArgs &a, int sms, int all_sms) {
+    using F = Few<T, GU>;
+    const int64_t tiles = (int64_t)((a.N + 127) / 128) * ((a.M + T - 1) / T), slots = (int64_t)F::kPerSm * sms;
+    FewPlan p{T, 1, 0.0};
+    for (int n = 2; n <= kMaxSplit && 4 * n <= a.nkb; ++n)
+        if (tiles * n <= slots && tiles <= (int64_t)F::kPerSm * clusters_at_once(n) * sms / all_sms) p.split = n;
+    const double step = GU ? (T == 16 ? 0.30 : T == 32 ? 0.40 : 0.60) : (T == 16 ? 0.24 : T == 32 ? 0.31 : T == 64 ? 0.29 : 0.44);
+    const double steps = (double)((tiles * p.split + slots - 1) / slots) * ((a.nkb + p.split - 1) / p.split);
+    const double bytes = (double)F::kTiles * ((a.N + 127) / 128) * a.nkb * kBoxBytes;
+    p.us = 4.0 + 0.04 * F::kTiles * std::min(T, a.M) + std::max(steps * step, bytes / 6.0e6);
+    return p;
+}
+
+template <int T, bool GU>
+int launch_few(const void *qx, const void *qw, int64_t K, BlockArgs a, int split, cudaStream_t st) {
     using F = Few<T, GU>;
     static SmemOptIn opt;
     auto kern = few_kernel<T, GU>;
@@ -736,9 +811,38 @@ int launch_few(const void *qx, const void *qw, int64_t K, const BlockArgs &a, cu
     CUtensorMap tx, tw;
     const int rc = maps(tx, tw, qx, qw, a.M, (GU ? 2 : 1) * (int64_t)a.N, K, T);
     if (rc) return rc;
-    const dim3 grid((unsigned)((a.N + 127) / 128 * a.split), (unsigned)((a.M + T - 1) / T));
-    e = launch_kernel(kern, grid, dim3(F::kThreads), F::kSmem, st, a.split, true, tx, tw, a);
+    a.split = split;
+    a.tiles_m = (a.M + T - 1) / T;
+    const int64_t grid = (int64_t)((a.N + 127) / 128) * a.tiles_m * split;   // (far below 2^31: split is 1 past a few hundred tiles)
+    e = launch_kernel(kern, dim3((unsigned)grid), dim3(F::kThreads), F::kSmem, st, split, true, tx, tw, a);
     return e == cudaSuccess ? CLEF_OK : internal_cuda_error(e, "block linear launch");
+}
+
+// The kernel for a call: the one expected to take least.  (Both sides measured at 2048 x 2048, 1024 x 5120, 6144 x 5120,
+// 5120 x 17408 and 34816 x 5120, and at 2048 and 17408 gate/up columns, for 1 .. 512 rows.)
+template <bool GU>
+int launch_block(const void *qx, const void *qw, int64_t K, const BlockArgs &a, int sms, int all_sms, cudaStream_t st) {
+    // many rows: rounds of tiles, each k-block 0.38 us, or the weight's bytes at 4.5 TB/s
+    const int64_t pairs = std::max(1, sms / 2), tiles = (int64_t)((a.M + 255) / 256) * (GU ? a.N / 128 : (a.N + 255) / 256);
+    const double weight = (GU ? 2.0 : 1.0) * a.N * (double)K;
+    FewPlan best{0, 1, 4.0 + std::max((double)((tiles + pairs - 1) / pairs) * a.nkb * 0.38, weight / 4.5e6)};
+    if (a.M <= 512) {
+        for (const FewPlan &p : {plan_few<16, GU>(a, sms, all_sms), plan_few<32, GU>(a, sms, all_sms), plan_few<64, GU>(a, sms, all_sms)})
+            if (p.us < best.us) best = p;
+        if constexpr (!GU) {
+            const FewPlan p = plan_few<128, GU>(a, sms, all_sms);
+            if (p.us < best.us) best = p;
+        }
+    }
+    switch (best.rows) {
+        case 16: return launch_few<16, GU>(qx, qw, K, a, best.split, st);
+        case 32: return launch_few<32, GU>(qx, qw, K, a, best.split, st);
+        case 64: return launch_few<64, GU>(qx, qw, K, a, best.split, st);
+        case 128:
+            if constexpr (!GU) return launch_few<128, GU>(qx, qw, K, a, best.split, st);
+            [[fallthrough]];
+        default: return launch_wide<GU>(qx, qw, K, a, sms, st);
+    }
 }
 
 int block_call(bool gu, const void *qx, const float *sx, const void *qw, const float *sw, const void *bias, int64_t M,
@@ -760,6 +864,7 @@ int block_call(bool gu, const void *qx, const float *sx, const void *qw, const f
     unsigned int *status = nullptr;
     const int rc = internal_device(&sms, &status);
     if (rc) return rc;
+    const int all_sms = sms;
     sms = internal_launch_sms(sms);
     BlockArgs a;
     a.M = (int)M;
@@ -770,18 +875,11 @@ int block_call(bool gu, const void *qx, const float *sx, const void *qw, const f
     a.bias = static_cast<const uint16_t *>(bias);
     a.out = static_cast<uint16_t *>(out);
     a.ldo = ldo;
-    a.band = a.split = 1;
+    a.band = a.split = a.tiles_m = 1;
     a.status = status;
     a.limit_ns = internal_wait_limit(&a.force_timeout);
     const cudaStream_t st = static_cast<cudaStream_t>(stream);
-    if (M > 128) return gu ? launch_wide<true>(qx, qw, K, a, sms, st) : launch_wide<false>(qx, qw, K, a, sms, st);
-    // CTAs that share a tile: as many as SMs are left, each with four k-blocks or more
-    const int64_t share = std::min<int64_t>({kMaxSplit, sms / tiles_n, a.nkb / 4});
-    a.split = (int)std::max<int64_t>(1, share);
-    if (gu) return M <= 16 ? launch_few<16, true>(qx, qw, K, a, st) : M <= 32 ? launch_few<32, true>(qx, qw, K, a, st)
-                 : M <= 64 ? launch_few<64, true>(qx, qw, K, a, st) : launch_few<128, true>(qx, qw, K, a, st);
-    return M <= 16 ? launch_few<16, false>(qx, qw, K, a, st) : M <= 32 ? launch_few<32, false>(qx, qw, K, a, st)
-         : M <= 64 ? launch_few<64, false>(qx, qw, K, a, st) : launch_few<128, false>(qx, qw, K, a, st);
+    return gu ? launch_block<true>(qx, qw, K, a, sms, all_sms, st) : launch_block<false>(qx, qw, K, a, sms, all_sms, st);
 }
 
 }  // namespace
