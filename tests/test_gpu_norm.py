@@ -220,3 +220,31 @@ def test_refusals():
         with pytest.raises(clef.ClefError) as e:
             call()
         assert e.value.status == 1
+
+
+@pytest.mark.parametrize("mode", MODES)
+@pytest.mark.parametrize("k", [576, 1024, 5120, 8256, 16384, 16400])
+def test_many_rows_have_the_bits_of_one(mode, k):
+    """Calls whose CTAs keep rows ahead in shared memory, against calls of a row."""
+    if mode.endswith("h128") and k % 128:
+        k = k // 128 * 128
+    m = 1300
+    x, w, r = values((m, k), 30), weight(k, 31), values((m, k), 32)
+    x[700] = (x[700].float() * 2.0 ** 70).to(torch.bfloat16)
+    x[701] = 0
+    r[701] = 0
+    x[1299] = (x[1299].float() * 2.0 ** 100).to(torch.bfloat16)
+    total, y = torch.empty_like(r), torch.empty_like(x)
+    q, s = clef.rms_norm_quant(x, w, mode, residual=r, residual_out=total, y=y)
+    assert torch.equal(total, (x.float() + r.float()).to(torch.bfloat16))
+    assert torch.equal(clef.rms_norm(x, w, residual=r, residual_out=torch.empty_like(r)), y)
+    for i in (0, 1, 151, 152, 455, 456, 700, 701, 702, 1298, 1299):
+        yi = torch.empty_like(x[i:i + 1])
+        qi, si = clef.rms_norm_quant(x[i:i + 1], w, mode, residual=r[i:i + 1].clone(), y=yi)
+        assert torch.equal(qi[0], q[i]) and torch.equal(si[0], s[i]) and torch.equal(yi[0], y[i]), i
+    keep = [i for i in range(0, m, 13) if i not in (700, 1299)]
+    check_quant(q[keep], s[keep], mode, norm(x[keep], w, 1e-6, r[keep]), norm_rel(k))
+    plain = clef.rms_norm_quant(x, w, mode)                                     # without a residual
+    qi, si = clef.rms_norm_quant(x[9:10], w, mode)
+    assert torch.equal(qi[0], plain[0][9]) and torch.equal(si[0], plain[1][9])
+    assert clef.poll_status() == 0
