@@ -4,8 +4,8 @@
 // neighbours (2 i, 2 i + 1) -- become gain (a cos t - b sin t, b cos t + a sin t),
 // t the position times the frequency of pair i; the rest of the head stays.
 //
-// Bound by HBM: 2 bytes in and 2 out an element.  A thread owns eight pairs (four
-// where they are neighbours) of a token for all heads of its slice, so that it
+// Bound by HBM: 2 bytes in and 2 out an element.  A thread owns up to eight pairs
+// (four where they are neighbours) of a token for all heads of its slice, so that it
 // finds their cosines and sines once.  A frequency is a number of turns a position
 // in units of 2^-64, kept modulo one turn: the product with a position is exact
 // modulo one turn in 64-bit integers, so that an angle is as exact at position
@@ -34,9 +34,7 @@ struct RotaryArgs {
     const int64_t *turns;
     int64_t ldx, ldx_head, ldo, ldo_head, tokens;
     int heads, slice;      // heads of the call, and of a row of CTAs
-    int pairs;             // pairs of a head
-    int units, tail;       // pieces of a token: of pairs, and of values that only move (none in place)
-    int rot;
+    int rot, tail;         // rotated values of a head, and those that only move (none in place)
     float gain;
 };
 
@@ -69,83 +67,103 @@ __device__ __forceinline__ uint32_t turn(uint32_t w, float c, float s) {
     return pack2(fmaf(a, c, -(b * s)), fmaf(b, c, a * s));
 }
 
-// Pieces of 16 bytes: two of a head's halves, or one of neighbouring pairs.
-template <bool kNeighbours>
+// V values (8, 4, 2 or 1), as words.
+template <int V>
+struct Piece {
+    uint32_t w[V == 1 ? 1 : V / 2];
+
+    __device__ __forceinline__ void load(const uint16_t *p) {
+        if constexpr (V == 8) {
+            const uint4 v = *reinterpret_cast<const uint4 *>(p);
+            w[0] = v.x; w[1] = v.y; w[2] = v.z; w[3] = v.w;
+        } else if constexpr (V == 4) {
+            const uint2 v = *reinterpret_cast<const uint2 *>(p);
+            w[0] = v.x; w[1] = v.y;
+        } else if constexpr (V == 2) {
+            w[0] = *reinterpret_cast<const uint32_t *>(p);
+        } else {
+            w[0] = *p;
+        }
+    }
+    __device__ __forceinline__ void store(uint16_t *p) const {
+        if constexpr (V == 8) *reinterpret_cast<uint4 *>(p) = make_uint4(w[0], w[1], w[2], w[3]);
+        else if constexpr (V == 4) *reinterpret_cast<uint2 *>(p) = make_uint2(w[0], w[1]);
+        else if constexpr (V == 2) *reinterpret_cast<uint32_t *>(p) = w[0];
+        else *p = (uint16_t)w[0];
+    }
+};
+
+// Neighbouring pairs: a thread owns a piece of V values.  Otherwise two pieces: the first and the second values of V
+// pairs, or two of those that only move.  Threads that rotate and threads that move share their loop, as a
+// warp holds both.  Heads are taken kAhead at a time: their loads are on their way together.
+template <int V, bool kNeighbours>
 __global__ void __launch_bounds__(256) rotary_kernel(const RotaryArgs a) {
-    const int per = a.units + a.tail;
+    constexpr int kPieces = kNeighbours ? 1 : 2, kPairs = kNeighbours ? V / 2 : V, kAhead = 4;
+    const int units = a.rot / (kPieces * V), moved = (a.tail / V + kPieces - 1) / kPieces, per = units + moved;
     const int64_t i = blockIdx.x * (int64_t)256 + threadIdx.x;
     const int64_t token = i / per;
     pdl_wait();
     if (token < a.tokens) {
-        const int u = (int)(i - token * per);
+        const int u = (int)(i - token * per), t = u - units;
+        const bool turns = t < 0;
+        // where its pieces start (a second one that there is not: the first once more)
+        const int p0 = turns ? V * u : a.rot + V * t;
+        const int p1 = turns ? p0 + a.rot / 2 : V * (t + moved) < a.tail ? p0 + V * moved : p0;
         const int h0 = blockIdx.y * a.slice, h1 = min(a.heads, h0 + a.slice);
-        const uint16_t *x = a.x + token * a.ldx;
-        uint16_t *out = a.out + token * a.ldo;
-        if (u >= a.units) {
-            const int at = a.rot + 8 * (u - a.units);
-#pragma unroll 4
-            for (int h = h0; h < h1; ++h)
-                *reinterpret_cast<uint4 *>(out + h * a.ldo_head + at) = *reinterpret_cast<const uint4 *>(x + h * a.ldx_head + at);
-        } else if (kNeighbours) {
+        float c[kPairs], s[kPairs];
+        if (turns) {
             const int32_t pos = a.pos[token];
-            float c[4], s[4];
 #pragma unroll
-            for (int k = 0; k < 4; ++k) angle(a, pos, 4 * u + k, c[k], s[k]);
-#pragma unroll 4
-            for (int h = h0; h < h1; ++h) {
-                uint4 w = *reinterpret_cast<const uint4 *>(x + h * a.ldx_head + 8 * u);
-                w = make_uint4(turn(w.x, c[0], s[0]), turn(w.y, c[1], s[1]), turn(w.z, c[2], s[2]), turn(w.w, c[3], s[3]));
-                *reinterpret_cast<uint4 *>(out + h * a.ldo_head + 8 * u) = w;
-            }
-        } else {
-            const int32_t pos = a.pos[token];
-            float c[8], s[8];
+            for (int k = 0; k < kPairs; ++k) angle(a, pos, kPairs * u + k, c[k], s[k]);
+        }
+        const uint16_t *x = a.x + token * a.ldx + h0 * a.ldx_head;
+        uint16_t *out = a.out + token * a.ldo + h0 * a.ldo_head;
+        for (int h = h0; h < h1; h += kAhead, x += kAhead * a.ldx_head, out += kAhead * a.ldo_head) {
+            Piece<V> p[kAhead][kPieces];
 #pragma unroll
-            for (int k = 0; k < 8; ++k) angle(a, pos, 8 * u + k, c[k], s[k]);
-#pragma unroll 4
-            for (int h = h0; h < h1; ++h) {
-                const uint16_t *from = x + h * a.ldx_head + 8 * u;
-                uint16_t *to = out + h * a.ldo_head + 8 * u;
-                uint4 p = *reinterpret_cast<const uint4 *>(from), q = *reinterpret_cast<const uint4 *>(from + a.pairs);
-                turn(p.x, q.x, c, s);
-                turn(p.y, q.y, c + 2, s + 2);
-                turn(p.z, q.z, c + 4, s + 4);
-                turn(p.w, q.w, c + 6, s + 6);
-                *reinterpret_cast<uint4 *>(to) = p;
-                *reinterpret_cast<uint4 *>(to + a.pairs) = q;
-            }
+            for (int k = 0; k < kAhead; ++k)
+                if (h + k < h1) {
+                    p[k][0].load(x + k * a.ldx_head + p0);
+                    if (!kNeighbours) p[k][kPieces - 1].load(x + k * a.ldx_head + p1);
+                }
+#pragma unroll
+            for (int k = 0; k < kAhead; ++k)
+                if (h + k < h1) {
+                    if (turns) {
+                        if constexpr (kNeighbours) {
+#pragma unroll
+                            for (int j = 0; j < kPairs; ++j) p[k][0].w[j] = turn(p[k][0].w[j], c[j], s[j]);
+                        } else if constexpr (V == 1) {
+                            const uint32_t w = turn(p[k][0].w[0] | p[k][1].w[0] << 16, c[0], s[0]);
+                            p[k][0].w[0] = w & 0xFFFFu;
+                            p[k][1].w[0] = w >> 16;
+                        } else {
+#pragma unroll
+                            for (int j = 0; j < V / 2; ++j) turn(p[k][0].w[j], p[k][1].w[j], c + 2 * j, s + 2 * j);
+                        }
+                    }
+                    p[k][0].store(out + k * a.ldo_head + p0);
+                    if (!kNeighbours) p[k][kPieces - 1].store(out + k * a.ldo_head + p1);
+                }
         }
     }
     pdl_launch_dependents();
 }
 
-// Pieces of one pair or one value, for heads whose rotated part does not end between pieces of 16 bytes.
-__global__ void __launch_bounds__(256) rotary_single_kernel(const RotaryArgs a, int interleaved) {
-    const int per = a.units + a.tail;
-    const int64_t i = blockIdx.x * (int64_t)256 + threadIdx.x;
-    const int64_t token = i / per;
-    pdl_wait();
-    if (token < a.tokens) {
-        const int u = (int)(i - token * per);
-        const int h0 = blockIdx.y * a.slice, h1 = min(a.heads, h0 + a.slice);
-        const uint16_t *x = a.x + token * a.ldx;
-        uint16_t *out = a.out + token * a.ldo;
-        if (u >= a.units) {
-            const int at = a.rot + u - a.units;
-            for (int h = h0; h < h1; ++h) out[h * a.ldo_head + at] = x[h * a.ldx_head + at];
-        } else {
-            float c, s;
-            angle(a, a.pos[token], u, c, s);
-            const int first = interleaved ? 2 * u : u, second = interleaved ? 2 * u + 1 : u + a.pairs;
-#pragma unroll 4
-            for (int h = h0; h < h1; ++h) {
-                const uint32_t w = turn(x[h * a.ldx_head + first] | (uint32_t)x[h * a.ldx_head + second] << 16, c, s);
-                out[h * a.ldo_head + first] = (uint16_t)w;
-                out[h * a.ldo_head + second] = (uint16_t)(w >> 16);
-            }
-        }
-    }
-    pdl_launch_dependents();
+template <int V, bool kNeighbours>
+int launch_rotary(RotaryArgs a, int sms, cudaStream_t st) {
+    constexpr int kPieces = kNeighbours ? 1 : 2;
+    const int per = a.rot / (kPieces * V) + (a.tail / V + kPieces - 1) / kPieces;
+    const int64_t blocks = (a.tokens * per + 255) / 256;      // under 2^30 * 1024 / 256
+    if (blocks > 0x7FFFFFFF) return kv_fail("too many tokens");
+    // heads of a row of CTAs: all of them where the tokens alone give every SM its 2,048 threads, fewer otherwise
+    const int64_t want = (int64_t)sms * 8;
+    int rows = (int)(blocks >= want ? 1 : (want + blocks - 1) / blocks);
+    if (rows > a.heads) rows = a.heads;
+    a.slice = (a.heads + rows - 1) / rows;
+    rows = (a.heads + a.slice - 1) / a.slice;
+    const cudaError_t e = launch_kernel(rotary_kernel<V, kNeighbours>, dim3((unsigned)blocks, (unsigned)rows), dim3(256), 0, st, 1, true, a);
+    return e == cudaSuccess ? CLEF_OK : internal_cuda_error(e, "rotary launch");
 }
 
 }  // namespace
@@ -185,26 +203,15 @@ extern "C" int clef_rotary(const void *x, int64_t ldx, int64_t ldx_head, int64_t
     a.ldo_head = ldo_head;
     a.tokens = tokens;
     a.heads = heads;
-    a.pairs = rot / 2;
+    a.slice = heads;
     a.rot = rot;
+    a.tail = in_place ? 0 : dim - rot;
     a.gain = gain;
-    const int width = interleaved ? 8 : 16;       // values of a piece of pairs
-    const bool whole = rot % width == 0;
-    a.units = whole ? rot / width : rot / 2;
-    a.tail = in_place ? 0 : whole ? (dim - rot) / 8 : dim - rot;
-    const int64_t blocks = (tokens * (a.units + a.tail) + 255) / 256;   // under 2^30 * 1024 / 256
-    if (blocks > 0x7FFFFFFF) return kv_fail("too many tokens");
-    // heads of a row of CTAs: all of them where the tokens alone give every SM its 2,048 threads, fewer otherwise
-    const int64_t want = (int64_t)internal_launch_sms(sms) * 8;
-    int rows = (int)(blocks >= want ? 1 : (want + blocks - 1) / blocks);
-    if (rows > heads) rows = heads;
-    a.slice = (heads + rows - 1) / rows;
-    rows = (heads + a.slice - 1) / a.slice;
-    const dim3 grid((unsigned)blocks, (unsigned)rows);
+    sms = internal_launch_sms(sms);
     const cudaStream_t st = static_cast<cudaStream_t>(stream);
-    cudaError_t e;
-    if (!whole) e = launch_kernel(rotary_single_kernel, grid, dim3(256), 0, st, 1, true, a, interleaved ? 1 : 0);
-    else if (interleaved) e = launch_kernel(rotary_kernel<true>, grid, dim3(256), 0, st, 1, true, a);
-    else e = launch_kernel(rotary_kernel<false>, grid, dim3(256), 0, st, 1, true, a);
-    return e == cudaSuccess ? CLEF_OK : internal_cuda_error(e, "rotary launch");
+    // the widest pieces that the rotated part is whole ones of
+    if (interleaved) return rot % 8 == 0 ? launch_rotary<8, true>(a, sms, st) : rot % 4 == 0 ? launch_rotary<4, true>(a, sms, st)
+                                                                              : launch_rotary<2, true>(a, sms, st);
+    return rot % 16 == 0 ? launch_rotary<8, false>(a, sms, st) : rot % 8 == 0 ? launch_rotary<4, false>(a, sms, st)
+         : rot % 4 == 0 ? launch_rotary<2, false>(a, sms, st) : launch_rotary<1, false>(a, sms, st);
 }
