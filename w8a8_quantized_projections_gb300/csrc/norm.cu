@@ -503,28 +503,41 @@ __global__ void __launch_bounds__(512) norm_staged_kernel(const __grid_constant_
 
 // ------------------------------------------------------------ blocks of 128
 
-// Codes of x in blocks of one row by 128: eight lanes a block.
+// Codes of x in blocks of one row by 128: four lanes a block, two pieces each.
 __global__ void __launch_bounds__(256) quant_rows_kernel(const uint16_t *__restrict__ x, int64_t ldx, int K, int blocks,
-                                                         int64_t total, uint8_t *__restrict__ q, float *__restrict__ scale) {
+                                                         int64_t total, bool q32, uint8_t *__restrict__ q,
+                                                         float *__restrict__ scale) {
     pdl_wait();
-    for (int64_t i0 = blockIdx.x * (int64_t)32; i0 < total; i0 += (int64_t)gridDim.x * 32) {
-        const int64_t i = i0 + threadIdx.x / kLanes;      // block of the matrix
+    for (int64_t i0 = blockIdx.x * (int64_t)64; i0 < total; i0 += (int64_t)gridDim.x * 64) {
+        const int64_t i = i0 + threadIdx.x / 4;      // block of the matrix
         const int64_t m = i / blocks;
-        const int b = (int)(i - m * blocks), e = b * 128 + (int)(threadIdx.x % kLanes) * kE;
-        const bool in = i < total && e < K;
-        uint64_t v[8];
+        const int b = (int)(i - m * blocks), e = b * 128 + (int)(threadIdx.x % 4) * 2 * kE;
+        uint64_t v[2][8];
         float amax = 0.0f;
-        if (in) {
-            uint32_t p[8];
-            load16(x + m * ldx + e, p);
 #pragma unroll
-            for (int k = 0; k < 8; ++k) v[k] = f2(lo(p[k]), hi(p[k]));
-            amax = absmax16(v, 0.0f);
+        for (int c = 0; c < 2; ++c) {
+            if (i < total && e + c * kE < K) {
+                uint32_t p[8];
+                load16(x + m * ldx + e + c * kE, p);
+#pragma unroll
+                for (int k = 0; k < 8; ++k) v[c][k] = f2(lo(p[k]), hi(p[k]));
+                amax = absmax16(v[c], amax);
+            }
         }
 #pragma unroll
-        for (int s = 1; s < kLanes; s <<= 1) amax = fmaxf(amax, __shfl_xor_sync(kAll, amax, s));
-        if (in) {
-            *reinterpret_cast<uint4 *>(q + m * K + e) = codes16<false>(v, code_factor(amax, 448.0f));
+        for (int s = 1; s < 4; s <<= 1) amax = fmaxf(amax, __shfl_xor_sync(kAll, amax, s));
+        if (i < total && e < K) {
+            const float r = code_factor(amax, 448.0f);
+            const uint4 a = codes16<false>(v[0], r);
+            uint8_t *o = q + m * K + e;
+            if (q32) {      // (K is a multiple of 32 then)
+                const uint4 c = codes16<false>(v[1], r);
+                asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};"
+                             :: "l"(o), "r"(a.x), "r"(a.y), "r"(a.z), "r"(a.w), "r"(c.x), "r"(c.y), "r"(c.z), "r"(c.w) : "memory");
+            } else {
+                *reinterpret_cast<uint4 *>(o) = a;
+                if (e + kE < K) *reinterpret_cast<uint4 *>(o + kE) = codes16<false>(v[1], r);
+            }
             if (e % 128 == 0) scale[i] = __fdiv_rn(amax, 448.0f);
         }
     }
@@ -745,9 +758,10 @@ extern "C" int clef_quant_fp8_block(const void *x, int64_t M, int64_t K, int64_t
     cudaError_t e;
     if (rows == 1) {
         const int64_t total = M * blocks, most = (int64_t)internal_launch_sms(sms) * 64;
-        const int64_t grid = (total + 31) / 32;
+        const int64_t grid = (total + 63) / 64;
+        const bool q32 = !kv_misaligned(q, 32) && K % 32 == 0;
         e = launch_kernel(quant_rows_kernel, dim3((unsigned)(grid < most ? grid : most)), dim3(256), 0, st, 1, true,
-                          static_cast<const uint16_t *>(x), ldx, (int)K, blocks, total, static_cast<uint8_t *>(q), scale);
+                          static_cast<const uint16_t *>(x), ldx, (int)K, blocks, total, q32, static_cast<uint8_t *>(q), scale);
     } else {
         const int64_t grid = (M + 127) / 128 * blocks;   // (under 2^31 / 128 * 512)
         if (grid > 0x7FFFFFFF) return kv_fail("too many blocks");
