@@ -9,8 +9,13 @@ ways is read once and forked, its pages shared.  Everything that a step needs
 kernels only and can be captured in a CUDA graph (``capture``), which also
 takes the host's cost per call out of short steps.
 
-RMS normalisation, the rotation of queries and keys by their position and the
-residual adds are torch's elementwise operations here; they are not part of the library.
+There, RMS normalisation, the rotation of queries and keys by their position and the
+residual adds are torch's elementwise operations.  With ``linears="fp8_block"`` they are the
+library's too, and one copy of each weight serves prompts and answers: e4m3 codes with a scale
+for each block of 128, whose linears take one row or many.  A layer then is a norm that adds
+the residual and leaves codes, the packed projection, the rotation in place, the cache and its
+attention, and the same again for the MLP: no launch between them but the quantizers of the
+o and down projections' inputs.
 
     PYTHONPATH=. python examples/decoder.py        # random weights: a prompt, three answers of 40 tokens
 """
@@ -20,8 +25,10 @@ from typing import Dict, List, Sequence
 
 import torch
 
-from w8a8_quantized_projections_gb300 import (kv_append, kv_attention, kv_compact, kv_fork, kv_free, kv_reserve, poll_status,
-                                              quant_act, quant_w4, swiglu_bf16, w4_linear, w8a8_gateup_swiglu, w8a8_linear)
+from w8a8_quantized_projections_gb300 import (fp8_block_gateup_swiglu, fp8_block_linear, kv_append, kv_attention, kv_compact,
+                                              kv_fork, kv_free, kv_reserve, poll_status, quant_act, quant_fp8_block, quant_w4,
+                                              rms_norm_quant, rotary, rotary_turns, swiglu_bf16, w4_linear,
+                                              w8a8_gateup_swiglu, w8a8_linear)
 
 NAMES = ("qkv", "o", "gateup", "down")
 
@@ -29,20 +36,30 @@ NAMES = ("qkv", "o", "gateup", "down")
 class Decoder:
     def __init__(self, layers: List[Dict[str, torch.Tensor]], q_heads: int, kv_heads: int, dim: int, sequences: int,
                  pages: int, width: int, page: int = 64, kind: str = "int8", group: int = 128, theta: float = 10000.0,
-                 eps: float = 1e-6):
+                 eps: float = 1e-6, linears: str = "int8_w4"):
         """layers: for each layer bf16 weights "qkv" [(q_heads + 2 kv_heads) dim][hidden],
         "o" [hidden][q_heads dim], "gateup" [2 F][hidden], "down" [hidden][F] and the
         norms' "norm_attn" and "norm_mlp" [hidden];
         sequences: how many there can be; pages: pages of the pool, each `page`
         tokens of every layer; width: pages a sequence can have;
-        kind: "int8" or "e4m3" cache codes; group: weights that share a scale."""
+        kind: "int8" or "e4m3" cache codes; group: weights that share a scale (4 bits);
+        linears: "int8_w4", INT8 for prompts and 4 bits for answers, or "fp8_block", e4m3 in
+        blocks for both (F a multiple of 128)."""
         if kind not in ("int8", "e4m3"):
             raise ValueError(f"kind {kind!r}: int8 or e4m3")
+        if linears not in ("int8_w4", "fp8_block"):
+            raise ValueError(f"linears {linears!r}: int8_w4 or fp8_block")
         device = layers[0]["qkv"].device
         self.q_heads, self.kv_heads, self.dim, self.page, self.eps = q_heads, kv_heads, dim, page, eps
-        self.norms = [(w["norm_attn"].float(), w["norm_mlp"].float()) for w in layers]
-        self.w8 = [{n: quant_act(w[n], "int8_h128") for n in NAMES} for w in layers]
-        self.w4 = [{n: quant_w4(w[n], group) for n in NAMES} for w in layers]
+        self.blocks = linears == "fp8_block"
+        if self.blocks:
+            self.norms = [(w["norm_attn"], w["norm_mlp"]) for w in layers]
+            self.fp8 = [{n: quant_fp8_block(w[n], 128) for n in NAMES} for w in layers]
+            self.turns = rotary_turns(dim, theta, device=device)
+        else:
+            self.norms = [(w["norm_attn"].float(), w["norm_mlp"].float()) for w in layers]
+            self.w8 = [{n: quant_act(w[n], "int8_h128") for n in NAMES} for w in layers]
+            self.w4 = [{n: quant_w4(w[n], group) for n in NAMES} for w in layers]
         code = torch.int8 if kind == "int8" else torch.float8_e4m3fn
         self.codes = torch.zeros((2 * len(layers), pages, kv_heads, page, dim), dtype=torch.uint8, device=device).view(code)
         self.scales = torch.zeros((2 * len(layers), pages, kv_heads), dtype=torch.float32, device=device)
@@ -127,6 +144,8 @@ class Decoder:
         return self.table.index_select(0, seqs), self.lens.index_select(0, seqs), self.rows[-1:]
 
     def _run(self, x, at, table, lens, placed, start, project):
+        if self.blocks:
+            return self._run_blocks(x, at.to(torch.int32), table, lens, placed, start)
         hq, hk, d = self.q_heads, self.kv_heads, self.dim
         angle = at.to(torch.float32)[:, None] * self.freq
         cos, sin = angle.cos()[:, None], angle.sin()[:, None]
@@ -139,6 +158,26 @@ class Decoder:
             x = x + project(i, "o", o.view(-1, hq * d))
             x = x + project(i, "down", project(i, "gateup", self._norm(x, norm_mlp)))
         return x
+
+    def _run_blocks(self, x, at, table, lens, placed, start):
+        hq, hk, d = self.q_heads, self.kv_heads, self.dim
+        x, delta = x.clone(), None                       # the residual stream, and what is added to it next
+
+        def normed(w):
+            return rms_norm_quant(x, w, "fp8_b128", self.eps) if delta is None else \
+                rms_norm_quant(delta, w, "fp8_b128", self.eps, residual=x)
+
+        for i, (norm_attn, norm_mlp) in enumerate(self.norms):
+            codes, scales, w = self.codes[2 * i : 2 * i + 2], self.scales[2 * i : 2 * i + 2], self.fp8[i]
+            qkv = fp8_block_linear(*normed(norm_attn), *w["qkv"]).view(-1, hq + 2 * hk, d)
+            qk = qkv[:, : hq + hk]
+            rotary(qk, at, self.turns, out=qk)
+            kv_append(qk[:, hq:], qkv[:, hq + hk :], codes, scales, table, lens, placed)
+            o = kv_attention(qk[:, :hq], codes, scales, table, lens, start)
+            delta = fp8_block_linear(*quant_fp8_block(o.view(-1, hq * d)), *w["o"])
+            h = fp8_block_gateup_swiglu(*normed(norm_mlp), *w["gateup"])
+            delta = fp8_block_linear(*quant_fp8_block(h), *w["down"])
+        return x + delta
 
     def _many_rows(self, i, name, a):
         q, s = quant_act(a, "int8_h128")

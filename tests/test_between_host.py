@@ -98,3 +98,22 @@ def test_scaled_turns():
 def test_turns_refusals(kw):
     with pytest.raises(ValueError):
         clef.rotary_turns(**kw, device="cpu")
+
+
+# ---------------------------------------------------------------- block linears
+
+LIN = dict(qx=P, sx=P, qw=P, sw=P, bias=Z, M=4, N=256, K=512, y=P, ldy=256)
+
+
+@pytest.mark.parametrize("name", ["clef_fp8_block_linear", "clef_fp8_block_gateup_swiglu"])
+@pytest.mark.parametrize("bad", [dict(qx=Z), dict(qx=ODD), dict(sx=Z), dict(sx=C.c_void_p(0x10002)), dict(qw=ODD), dict(sw=Z),
+                                 dict(sw=C.c_void_p(0x10001)), dict(bias=ODD), dict(M=-1), dict(M=2 ** 31), dict(N=0), dict(N=4, ldy=8),
+                                 dict(N=2 ** 30), dict(K=0), dict(K=40), dict(K=65552), dict(y=Z), dict(y=ODD), dict(ldy=248), dict(ldy=260)])
+def test_block_linear_refusals(name, bad):
+    assert getattr(clef.library(), name)(*(LIN | bad).values(), Z) == 1
+
+
+def test_gateup_needs_whole_blocks():
+    L = clef.library()
+    assert L.clef_fp8_block_gateup_swiglu(*(LIN | dict(N=136, ldy=136)).values(), Z) == 1
+    assert L.clef_fp8_block_linear(*(LIN | dict(M=0, qx=Z, sx=Z, y=Z)).values(), Z) == 0
