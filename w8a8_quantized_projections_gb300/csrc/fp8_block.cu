@@ -502,194 +502,204 @@ few_kernel(const __grid_constant__ CUtensorMap tmx, const __grid_constant__ CUte
     pdl_wait();
 
     const uint32_t tmem = bar->tmem;
-    // tiles of one part of the weight side by side, so that it is read from memory once
-    const int split = a.split, rank = split > 1 ? (int)cluster_rank() : 0, both = (int)blockIdx.x / split;
-    const int tile = both / a.tiles_m, n0 = tile * 128, m0 = (both - tile * a.tiles_m) * T;
+    const int split = a.split, rank = split > 1 ? (int)cluster_rank() : 0;
     const int k0 = rank * a.nkb / split, k1 = (rank + 1) * a.nkb / split;      // (at most 8 times 512)
+    const int tiles = (a.N + 127) / 128 * a.tiles_m, clusters = (int)gridDim.x / split;
     const WaitCtx w{a.limit_ns, &bar->abort, a.status};
+    // Under a budget of SMs a cluster takes one tile after another; otherwise there is a cluster for each.  The
+    // rings go on where they are: s, ph of the stages, and `done` k-blocks of the TMEM buffers before this tile.
+    uint32_t s = 0, ph = 0, done = 0, filled = 0, last = 0;
 
-    if (warp == 0) {
-        uint32_t s = 0, ph = 0, filled = 0, last = 0;
-        for (int kb = k0; kb < k1; ++kb) {
-            if (!mbar_wait(&bar->empty[s], ph ^ 1u, w, kSiteTmaEmpty)) break;
-            uint8_t *st = smem + s * F::kStage;
-            if (elect_one()) {
-                mbar_arrive_expect_tx(&bar->full[s], F::kStage);
-                tma_load_2d(st, &tmw, kb * 128, n0, &bar->full[s]);
-                if (GU) tma_load_2d(st + kBoxBytes, &tmw, kb * 128, a.N + n0, &bar->full[s]);
-                tma_load_2d(st + F::kTiles * kBoxBytes, &tmx, kb * 128, m0, &bar->full[s]);
-            }
-            __syncwarp();
-            filled |= 1u << s;
-            last = (last & ~(1u << s)) | ph << s;
-            if (++s == F::kStages) {
-                s = 0;
-                ph ^= 1u;
-            }
-        }
-        for (int i = 0; i < F::kStages; ++i)
-            if (filled >> i & 1u) mbar_wait_drain(&bar->full[i], last >> i & 1u, 200000000ull, a.status);
-    } else if (warp == 1) {
-        constexpr uint32_t idesc = idesc_f32acc(0, 0, 128, T);
-        if (a.force_timeout == 1 || (a.force_timeout >= 2 && a.force_timeout - 2 == (int)blockIdx.x)) {
-            mbar_wait(&bar->never, 0, w, kSiteMmaFull);
-        } else {
-            uint32_t s = 0, ph = 0, acc = 0, aph = 0;
-            bool ready = false;
+    for (int both = (int)blockIdx.x / split; both < tiles; both += clusters, done += (uint32_t)(k1 - k0)) {
+        // tiles of one part of the weight side by side, so that it is read from memory once
+        const int tile = both / a.tiles_m, n0 = tile * 128, m0 = (both - tile * a.tiles_m) * T;
+        if (warp == 0) {
             for (int kb = k0; kb < k1; ++kb) {
-                if (!ready && (!mbar_wait(&bar->acc_empty[acc], aph ^ 1u, w, kSiteMmaAccEmpty) ||
-                               !mbar_wait(&bar->full[s], ph, w, kSiteMmaFull)))
-                    break;
-                tc_fence_after();
-                const uint32_t sa = smem_u32(smem + s * F::kStage);
-                const uint64_t da = sdesc_sw128(sa), db = sdesc_sw128(sa + F::kTiles * kBoxBytes);
-                const uint32_t d = tmem + acc * F::kAcc, s0 = s, acc0 = acc;
+                if (!mbar_wait(&bar->empty[s], ph ^ 1u, w, kSiteTmaEmpty)) break;
+                uint8_t *st = smem + s * F::kStage;
+                if (elect_one()) {
+                    mbar_arrive_expect_tx(&bar->full[s], F::kStage);
+                    tma_load_2d(st, &tmw, kb * 128, n0, &bar->full[s]);
+                    if (GU) tma_load_2d(st + kBoxBytes, &tmw, kb * 128, a.N + n0, &bar->full[s]);
+                    tma_load_2d(st + F::kTiles * kBoxBytes, &tmx, kb * 128, m0, &bar->full[s]);
+                }
+                __syncwarp();
+                filled |= 1u << s;
+                last = (last & ~(1u << s)) | ph << s;
                 if (++s == F::kStages) {
                     s = 0;
                     ph ^= 1u;
                 }
-                if (++acc == F::kBufs) {
-                    acc = 0;
-                    aph ^= 1u;
-                }
-                const bool e0 = mbar_done(&bar->acc_empty[acc], aph ^ 1u), e1 = mbar_done(&bar->full[s], ph);
-                if (elect_one()) {
-#pragma unroll
-                    for (int k = 0; k < 4; ++k)
-#pragma unroll
-                        for (int h = 0; h < F::kTiles; ++h)
-                            mma_f8(d + h * T, da + 2 * k + h * (kBoxBytes >> 4), db + 2 * k, idesc, k > 0);
-                    mma_commit(&bar->acc_full[acc0]);
-                    mma_commit(&bar->empty[s0]);
-                }
-                __syncwarp();
-                ready = e0 && e1;
             }
-        }
-        if (elect_one()) mma_commit(&bar->drain);
-        __syncwarp();
-        mbar_wait_drain(&bar->drain, 0, 200000000ull, a.status);
-    } else {
-        const int quad = warp & 3, e = warp - 2, set = (e >> 2) / F::kHalves, c0 = (e >> 2) % F::kHalves * F::kCols;
-        const uint32_t lanes = (uint32_t)(quad * 32) << 16;
-        float *mine = scales + e * 2 * F::kTiles * F::kCols;     // two buffers of this warp's products of scales
-        constexpr int kPer = (F::kCols + 31) / 32;               // of them a lane
-        const float *sx[kPer];
+        } else if (warp == 1) {
+            constexpr uint32_t idesc = idesc_f32acc(0, 0, 128, T);
+            if (a.force_timeout == 1 || (a.force_timeout >= 2 && a.force_timeout - 2 == (int)blockIdx.x)) {
+                mbar_wait(&bar->never, 0, w, kSiteMmaFull);
+            } else {
+                bool ready = false;
+                for (uint32_t g = done; g != done + (uint32_t)(k1 - k0); ++g) {
+                    const uint32_t acc = g % F::kBufs, s0 = s;
+                    if (!ready && (!mbar_wait(&bar->acc_empty[acc], (g / F::kBufs & 1u) ^ 1u, w, kSiteMmaAccEmpty) ||
+                                   !mbar_wait(&bar->full[s], ph, w, kSiteMmaFull)))
+                        break;
+                    tc_fence_after();
+                    const uint32_t sa = smem_u32(smem + s * F::kStage), d = tmem + acc * F::kAcc;
+                    const uint64_t da = sdesc_sw128(sa), db = sdesc_sw128(sa + F::kTiles * kBoxBytes);
+                    if (++s == F::kStages) {
+                        s = 0;
+                        ph ^= 1u;
+                    }
+                    const bool e0 = mbar_done(&bar->acc_empty[(g + 1) % F::kBufs], ((g + 1) / F::kBufs & 1u) ^ 1u);
+                    const bool e1 = mbar_done(&bar->full[s], ph);
+                    if (elect_one()) {
 #pragma unroll
-        for (int i = 0; i < kPer; ++i) {
-            const int c = 32 * i + lane, m = m0 + c0 + c;
-            sx[i] = (c < F::kCols && m < a.M) ? a.sx + (int64_t)m * a.nkb : nullptr;
-        }
-        const float *sw0 = a.sw + (int64_t)tile * a.nkb, *sw1 = GU ? sw0 + (int64_t)(a.N / 128) * a.nkb : sw0;
-        uint64_t sum[F::kTiles][F::kCols / 2];
+                        for (int k = 0; k < 4; ++k)
 #pragma unroll
-        for (int h = 0; h < F::kTiles; ++h)
-#pragma unroll
-            for (int i = 0; i < F::kCols / 2; ++i) sum[h][i] = 0;
-        float x[kPer], w0 = 0.0f, w1 = 0.0f;
-        const auto fetch = [&](int kb) {
-#pragma unroll
-            for (int i = 0; i < kPer; ++i) x[i] = sx[i] ? __ldg(sx[i] + kb) : 0.0f;
-            w0 = __ldg(sw0 + kb);
-            if (GU) w1 = __ldg(sw1 + kb);
-        };
-        if (k0 + set < k1) fetch(k0 + set);
-        uint32_t acc = set, aph = 0, flip = 0;
-        bool ok = true;
-        for (int kb = k0 + set; kb < k1; kb += F::kSets) {
-            float *f = mine + flip * F::kTiles * F::kCols;
-            flip ^= 1u;
+                            for (int h = 0; h < F::kTiles; ++h)
+                                mma_f8(d + h * T, da + 2 * k + h * (kBoxBytes >> 4), db + 2 * k, idesc, k > 0);
+                        mma_commit(&bar->acc_full[acc]);
+                        mma_commit(&bar->empty[s0]);
+                    }
+                    __syncwarp();
+                    ready = e0 && e1;
+                }
+            }
+        } else {
+            const int quad = warp & 3, e = warp - 2, set = (e >> 2) / F::kHalves, c0 = (e >> 2) % F::kHalves * F::kCols;
+            const uint32_t lanes = (uint32_t)(quad * 32) << 16;
+            float *mine = scales + e * 2 * F::kTiles * F::kCols;     // two buffers of this warp's products of scales
+            constexpr int kPer = (F::kCols + 31) / 32;               // of them a lane
+            const float *sx[kPer];
 #pragma unroll
             for (int i = 0; i < kPer; ++i) {
-                if (32 * i + lane < F::kCols) {
-                    f[32 * i + lane] = x[i] * w0;
-                    if (GU) f[F::kCols + 32 * i + lane] = x[i] * w1;
-                }
+                const int c = 32 * i + lane, m = m0 + c0 + c;
+                sx[i] = (c < F::kCols && m < a.M) ? a.sx + (int64_t)m * a.nkb : nullptr;
             }
-            __syncwarp();
-            if (kb + F::kSets < k1) fetch(kb + F::kSets);
-            if (!mbar_wait(&bar->acc_full[acc], aph, w, kSiteEpiAccFull)) {
-                ok = false;
-                break;
-            }
-            tc_fence_after();
-            const uint32_t at = tmem + acc * F::kAcc + lanes + c0;
-            constexpr int kPiece = F::kCols < 32 ? 16 : 32, kPieces = F::kTiles * F::kCols / kPiece;
-            const auto load = [&](int j, uint32_t(&r)[kPiece]) {
-                const uint32_t from = at + j * kPiece / F::kCols * T + j * kPiece % F::kCols;
-                if constexpr (kPiece == 16) tmem_ld16(from, r);
-                else tmem_ld32(from, r);
-            };
-            uint32_t r[2][kPiece];
-            load(0, r[0]);
-            tmem_ready(r[0]);
-#pragma unroll
-            for (int j = 0; j < kPieces; ++j) {
-                if (j + 1 < kPieces) {
-                    load(j + 1, r[(j + 1) & 1]);
-                } else {
-                    tc_fence_before();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(&bar->acc_empty[acc]);
-                }
-                const int h = j * kPiece / F::kCols, c = j * kPiece % F::kCols;
-#pragma unroll
-                for (int i = 0; i < kPiece / 4; ++i) {
-                    const ulonglong2 p = *reinterpret_cast<const ulonglong2 *>(f + h * F::kCols + c + 4 * i);
-                    const uint32_t *d = r[j & 1] + 4 * i;
-                    uint64_t *o = &sum[h][(c + 4 * i) / 2];
-                    o[0] = fma_f2(p.x, pack_u2(d[0], d[1]), o[0]);
-                    o[1] = fma_f2(p.y, pack_u2(d[2], d[3]), o[1]);
-                }
-                if (j + 1 < kPieces) tmem_ready(r[(j + 1) & 1]);
-            }
-            acc += F::kSets;
-            if (acc >= F::kBufs) {
-                acc -= F::kBufs;
-                aph ^= 1u;
-            }
-        }
-        // The ring is free once every group has seen its last k-block complete; then each leaves its sums there,
-        // [group][gate, up][row of x][weight row].
-        asm volatile("bar.sync 1, %0;" ::"n"(32 * F::kEpi) : "memory");
-        if (ok) {
-            float *part = reinterpret_cast<float *>(smem) + set * F::kTiles * T * 128 + quad * 32 + lane;
+            const float *sw0 = a.sw + (int64_t)tile * a.nkb, *sw1 = GU ? sw0 + (int64_t)(a.N / 128) * a.nkb : sw0;
+            uint64_t sum[F::kTiles][F::kCols / 2];
 #pragma unroll
             for (int h = 0; h < F::kTiles; ++h)
 #pragma unroll
-                for (int i = 0; i < F::kCols; ++i) {
-                    if (m0 + c0 + i >= a.M) break;
-                    float v[2];
-                    unpack_f2(sum[h][i / 2], v[0], v[1]);
-                    part[(h * T + c0 + i) * 128] = v[i & 1];
-                }
-        }
-    }
-    tc_fence_before();
-    __syncthreads();
-    if (split > 1) cluster_sync();
-    if (warp >= 2 && !bar->abort) {
-        // this CTA's share of the rows of x: the sums of the cluster's CTAs and their groups, always in this order
-        const int i = threadIdx.x - 64, n = n0 + (i & 127);
-        const float b0 = a.bias && n < a.N ? bf16_at(a.bias + n) : 0.0f;
-        const float b1 = GU && a.bias && n < a.N ? bf16_at(a.bias + a.N + n) : 0.0f;
-        for (int c = rank + split * (i >> 7); c < T && m0 + c < a.M; c += split * (F::kEpi / 4)) {
-            float v = 0.0f, u = 0.0f;
-            const uint32_t local = base + (uint32_t)(smem - smem_raw) + (uint32_t)((c * 128 + (i & 127)) * 4);
-            for (int q = 0; q < split; ++q) {
-                const uint32_t at = split > 1 ? cluster_addr(local, q) : local;
+                for (int i = 0; i < F::kCols / 2; ++i) sum[h][i] = 0;
+            float x[kPer], w0 = 0.0f, w1 = 0.0f;
+            const auto fetch = [&](int kb) {
 #pragma unroll
-                for (int g = 0; g < F::kSets; ++g) {
-                    v += ld_cluster(at + g * F::kTiles * T * 512);
-                    if (GU) u += ld_cluster(at + (g * F::kTiles + 1) * T * 512);
+                for (int i = 0; i < kPer; ++i) x[i] = sx[i] ? __ldg(sx[i] + kb) : 0.0f;
+                w0 = __ldg(sw0 + kb);
+                if (GU) w1 = __ldg(sw1 + kb);
+            };
+            if (k0 + set < k1) fetch(k0 + set);
+            uint32_t flip = 0;
+            bool ok = true;
+            for (int kb = k0 + set; kb < k1; kb += F::kSets) {
+                const uint32_t g = done + (uint32_t)(kb - k0), acc = g % F::kBufs;
+                float *f = mine + flip * F::kTiles * F::kCols;
+                flip ^= 1u;
+#pragma unroll
+                for (int i = 0; i < kPer; ++i) {
+                    if (32 * i + lane < F::kCols) {
+                        f[32 * i + lane] = x[i] * w0;
+                        if (GU) f[F::kCols + 32 * i + lane] = x[i] * w1;
+                    }
+                }
+                __syncwarp();
+                if (kb + F::kSets < k1) fetch(kb + F::kSets);
+                if (!mbar_wait(&bar->acc_full[acc], g / F::kBufs & 1u, w, kSiteEpiAccFull)) {
+                    ok = false;
+                    break;
+                }
+                tc_fence_after();
+                const uint32_t at = tmem + acc * F::kAcc + lanes + c0;
+                constexpr int kPiece = F::kCols < 32 ? 16 : 32, kPieces = F::kTiles * F::kCols / kPiece;
+                const auto load = [&](int j, uint32_t(&r)[kPiece]) {
+                    const uint32_t from = at + j * kPiece / F::kCols * T + j * kPiece % F::kCols;
+                    if constexpr (kPiece == 16) tmem_ld16(from, r);
+                    else tmem_ld32(from, r);
+                };
+                uint32_t r[2][kPiece];
+                load(0, r[0]);
+                tmem_ready(r[0]);
+#pragma unroll
+                for (int j = 0; j < kPieces; ++j) {
+                    if (j + 1 < kPieces) {
+                        load(j + 1, r[(j + 1) & 1]);
+                    } else {
+                        tc_fence_before();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(&bar->acc_empty[acc]);
+                    }
+                    const int h = j * kPiece / F::kCols, c = j * kPiece % F::kCols;
+#pragma unroll
+                    for (int i = 0; i < kPiece / 4; ++i) {
+                        const ulonglong2 p = *reinterpret_cast<const ulonglong2 *>(f + h * F::kCols + c + 4 * i);
+                        const uint32_t *d = r[j & 1] + 4 * i;
+                        uint64_t *o = &sum[h][(c + 4 * i) / 2];
+                        o[0] = fma_f2(p.x, pack_u2(d[0], d[1]), o[0]);
+                        o[1] = fma_f2(p.y, pack_u2(d[2], d[3]), o[1]);
+                    }
+                    if (j + 1 < kPieces) tmem_ready(r[(j + 1) & 1]);
                 }
             }
-            v += b0;
-            if (GU) v = silu_mul_fast(v, u + b1);
-            if (n < a.N) a.out[(int64_t)(m0 + c) * a.ldo + n] = __bfloat16_as_ushort(__float2bfloat16_rn(v));
+            // The ring is free once every group has seen its last k-block complete; then each leaves its sums
+            // there, [group][gate, up][row of x][weight row].
+            asm volatile("bar.sync 1, %0;" ::"n"(32 * F::kEpi) : "memory");
+            if (ok) {
+                float *part = reinterpret_cast<float *>(smem) + set * F::kTiles * T * 128 + quad * 32 + lane;
+#pragma unroll
+                for (int h = 0; h < F::kTiles; ++h)
+#pragma unroll
+                    for (int i = 0; i < F::kCols; ++i) {
+                        if (m0 + c0 + i >= a.M) break;
+                        float v[2];
+                        unpack_f2(sum[h][i / 2], v[0], v[1]);
+                        part[(h * T + c0 + i) * 128] = v[i & 1];
+                    }
+            }
         }
+        tc_fence_before();
+        __syncthreads();
+        if (split > 1) cluster_sync();
+        const bool failed = bar->abort != 0;
+        if (warp >= 2 && !failed) {
+            // this CTA's share of the rows of x: the sums of the cluster's CTAs and their groups, always in this order
+            const int i = threadIdx.x - 64, n = n0 + (i & 127);
+            const float b0 = a.bias && n < a.N ? bf16_at(a.bias + n) : 0.0f;
+            const float b1 = GU && a.bias && n < a.N ? bf16_at(a.bias + a.N + n) : 0.0f;
+            for (int c = rank + split * (i >> 7); c < T && m0 + c < a.M; c += split * (F::kEpi / 4)) {
+                float v = 0.0f, u = 0.0f;
+                const uint32_t local = base + (uint32_t)(smem - smem_raw) + (uint32_t)((c * 128 + (i & 127)) * 4);
+                for (int q = 0; q < split; ++q) {
+                    const uint32_t at = split > 1 ? cluster_addr(local, q) : local;
+#pragma unroll
+                    for (int g = 0; g < F::kSets; ++g) {
+                        v += ld_cluster(at + g * F::kTiles * T * 512);
+                        if (GU) u += ld_cluster(at + (g * F::kTiles + 1) * T * 512);
+                    }
+                }
+                v += b0;
+                if (GU) v = silu_mul_fast(v, u + b1);
+                if (n < a.N) a.out[(int64_t)(m0 + c) * a.ldo + n] = __bfloat16_as_ushort(__float2bfloat16_rn(v));
+            }
+        }
+        __syncwarp();
+        if (both + clusters < tiles) fence_proxy_async_smem();     // the sums, before the next tile's copies over them
+        if (split > 1) cluster_sync();
+        else if (both + clusters < tiles) __syncthreads();
+        tc_fence_after();
     }
-    if (split > 1) cluster_sync();
+    // Copies and MMAs have ended before the CTA does: each has been waited for, but where a wait ran out.
+    if (bar->abort) {
+        if (warp == 0) {
+            for (int i = 0; i < F::kStages; ++i)
+                if (filled >> i & 1u) mbar_wait_drain(&bar->full[i], last >> i & 1u, 200000000ull, a.status);
+        } else if (warp == 1) {
+            if (elect_one()) mma_commit(&bar->drain);
+            __syncwarp();
+            mbar_wait_drain(&bar->drain, 0, 200000000ull, a.status);
+        }
+        tc_fence_before();
+        __syncthreads();
+    }
     pdl_launch_dependents();
     if (warp == 1) {
         tc_fence_after();
@@ -788,12 +798,12 @@ struct FewPlan {
 // Expected time: 4 us for launch, first copies and end, which grow with the sums that meet at the end; then
 // k-blocks at what one takes a CTA while the weight comes out of L2, or the weight's bytes at 6 TB/s.
 template <int T, bool GU>
-FewPlan plan_few(const BlockArgs &a, int sms, int all_sms) {
+FewPlan plan_few(const BlockArgs &a, int sms) {
     using F = Few<T, GU>;
     const int64_t tiles = (int64_t)((a.N + 127) / 128) * ((a.M + T - 1) / T), slots = (int64_t)F::kPerSm * sms;
     FewPlan p{T, 1, 0.0};
     for (int n = 2; n <= kMaxSplit && 4 * n <= a.nkb; ++n)
-        if (tiles * n <= slots && tiles <= (int64_t)F::kPerSm * clusters_at_once(n) * sms / all_sms) p.split = n;
+        if (tiles * n <= slots && tiles <= (int64_t)F::kPerSm * clusters_at_once(n)) p.split = n;
     const double step = GU ? (T == 16 ? 0.30 : T == 32 ? 0.40 : 0.60) : (T == 16 ? 0.24 : T == 32 ? 0.31 : T == 64 ? 0.29 : 0.44);
     const double steps = (double)((tiles * p.split + slots - 1) / slots) * ((a.nkb + p.split - 1) / p.split);
     const double bytes = (double)F::kTiles * ((a.N + 127) / 128) * a.nkb * kBoxBytes;
@@ -802,7 +812,7 @@ FewPlan plan_few(const BlockArgs &a, int sms, int all_sms) {
 }
 
 template <int T, bool GU>
-int launch_few(const void *qx, const void *qw, int64_t K, BlockArgs a, int split, cudaStream_t st) {
+int launch_few(const void *qx, const void *qw, int64_t K, BlockArgs a, int split, int sms, int all_sms, cudaStream_t st) {
     using F = Few<T, GU>;
     static SmemOptIn opt;
     auto kern = few_kernel<T, GU>;
@@ -813,33 +823,36 @@ int launch_few(const void *qx, const void *qw, int64_t K, BlockArgs a, int split
     if (rc) return rc;
     a.split = split;
     a.tiles_m = (a.M + T - 1) / T;
-    const int64_t grid = (int64_t)((a.N + 127) / 128) * a.tiles_m * split;   // (far below 2^31: split is 1 past a few hundred tiles)
+    int64_t clusters = (int64_t)((a.N + 127) / 128) * a.tiles_m;             // (N is under 2^29, and tiles_m at most 32)
+    if (sms < all_sms) clusters = std::min<int64_t>(clusters, std::max(1, sms / split));   // a budget of SMs
+    const int64_t grid = clusters * split;
     e = launch_kernel(kern, dim3((unsigned)grid), dim3(F::kThreads), F::kSmem, st, split, true, tx, tw, a);
     return e == cudaSuccess ? CLEF_OK : internal_cuda_error(e, "block linear launch");
 }
 
-// The kernel for a call: the one expected to take least.  (Both sides measured at 2048 x 2048, 1024 x 5120, 6144 x 5120,
+// The kernel for a call: the one expected to take least on the whole device, so that a budget of SMs changes no
+// sum's order.  (Both sides measured at 2048 x 2048, 1024 x 5120, 6144 x 5120,
 // 5120 x 17408 and 34816 x 5120, and at 2048 and 17408 gate/up columns, for 1 .. 512 rows.)
 template <bool GU>
 int launch_block(const void *qx, const void *qw, int64_t K, const BlockArgs &a, int sms, int all_sms, cudaStream_t st) {
     // many rows: rounds of tiles, each k-block 0.38 us, or the weight's bytes at 4.5 TB/s
-    const int64_t pairs = std::max(1, sms / 2), tiles = (int64_t)((a.M + 255) / 256) * (GU ? a.N / 128 : (a.N + 255) / 256);
+    const int64_t pairs = std::max(1, all_sms / 2), tiles = (int64_t)((a.M + 255) / 256) * (GU ? a.N / 128 : (a.N + 255) / 256);
     const double weight = (GU ? 2.0 : 1.0) * a.N * (double)K;
     FewPlan best{0, 1, 4.0 + std::max((double)((tiles + pairs - 1) / pairs) * a.nkb * 0.38, weight / 4.5e6)};
     if (a.M <= 512) {
-        for (const FewPlan &p : {plan_few<16, GU>(a, sms, all_sms), plan_few<32, GU>(a, sms, all_sms), plan_few<64, GU>(a, sms, all_sms)})
+        for (const FewPlan &p : {plan_few<16, GU>(a, all_sms), plan_few<32, GU>(a, all_sms), plan_few<64, GU>(a, all_sms)})
             if (p.us < best.us) best = p;
         if constexpr (!GU) {
-            const FewPlan p = plan_few<128, GU>(a, sms, all_sms);
+            const FewPlan p = plan_few<128, GU>(a, all_sms);
             if (p.us < best.us) best = p;
         }
     }
     switch (best.rows) {
-        case 16: return launch_few<16, GU>(qx, qw, K, a, best.split, st);
-        case 32: return launch_few<32, GU>(qx, qw, K, a, best.split, st);
-        case 64: return launch_few<64, GU>(qx, qw, K, a, best.split, st);
+        case 16: return launch_few<16, GU>(qx, qw, K, a, best.split, sms, all_sms, st);
+        case 32: return launch_few<32, GU>(qx, qw, K, a, best.split, sms, all_sms, st);
+        case 64: return launch_few<64, GU>(qx, qw, K, a, best.split, sms, all_sms, st);
         case 128:
-            if constexpr (!GU) return launch_few<128, GU>(qx, qw, K, a, best.split, st);
+            if constexpr (!GU) return launch_few<128, GU>(qx, qw, K, a, best.split, sms, all_sms, st);
             [[fallthrough]];
         default: return launch_wide<GU>(qx, qw, K, a, sms, st);
     }

@@ -449,6 +449,9 @@ PyObject *kv_copy_pages(PyObject *, Args a, Py_ssize_t n) {   // codes, scales, 
 
 // ------------------------------------------------------------ between the projections
 
+// (These make the tensors' device the current one for the call.)
+using Guard = c10::cuda::CUDAGuard;
+
 double real(PyObject *o) {
     const double v = PyFloat_AsDouble(o);
     if (v == -1.0 && PyErr_Occurred()) throw python_error();
@@ -498,6 +501,7 @@ NormCall norm_args(PyObject *xo, PyObject *wo, PyObject *eps, PyObject *ro, PyOb
 PyObject *rms_norm(PyObject *, Args a, Py_ssize_t n) {   // x, w, eps, residual, residual_out, y, stream
     ARGS(7);
     const NormCall c = norm_args(a[0], a[1], a[2], a[3], a[4]);
+    const Guard guard((c10::DeviceIndex)c.dev);
     const Stream s = stream_of(a[6], c.dev);
     Result out(a[5]);
     if (!out.passed) out.own = fresh({c.M, c.K}, ScalarType::BFloat16, s);
@@ -531,6 +535,7 @@ PyObject *rms_norm_quant(PyObject *, Args a, Py_ssize_t n) {
     ARGS(10);
     const int64_t mode = integer(a[2]);
     const NormCall c = norm_args(a[0], a[1], a[3], a[4], a[5]);
+    const Guard guard((c10::DeviceIndex)c.dev);
     const Stream s = stream_of(a[9], c.dev);
     const bool is_int8 = mode == CLEF_ACT_INT8_H128, blocked = mode == CLEF_ACT_FP8_E4M3_B128;
     Matrix y{};
@@ -554,6 +559,7 @@ PyObject *quant_fp8_block(PyObject *, Args a, Py_ssize_t n) {   // x, rows, q, s
     const int dev = x.get_device();
     const int64_t ldx = pitch(x, "x"), M = x.size(0), K = x.size(1), rows = integer(a[1]);
     CHECK(rows == 1 || rows == 128, "rows must be 1 or 128");
+    const Guard guard((c10::DeviceIndex)dev);
     const Stream s = stream_of(a[4], dev);
     const int64_t groups = (M + rows - 1) / rows, blocks = blocks_of(K);
     Result q(a[2]), scale(a[3]);
@@ -601,6 +607,7 @@ PyObject *fp8_block(PyObject *, Args a, Py_ssize_t n) {   // qx, sx, qw, sw, bia
         CHECK(b.numel() == w.rows, "bias has ", b.numel(), " values for ", w.rows, " weight rows");
         bias = b.data_ptr();
     }
+    const Guard guard((c10::DeviceIndex)dev);
     const Stream s = stream_of(a[6], dev);
     Result out(a[5]);
     if (!out.passed) out.own = fresh({x.rows, N}, ScalarType::BFloat16, s);
@@ -627,6 +634,7 @@ PyObject *rotary(PyObject *, Args a, Py_ssize_t n) {   // x, pos, turns, gain, i
     const double gain = real(a[3]);
     const int interleaved = PyObject_IsTrue(a[4]);
     if (interleaved < 0) throw python_error();
+    const Guard guard((c10::DeviceIndex)dev);
     const Stream s = stream_of(a[6], dev);
     Result out(a[5]);
     Rows o;
