@@ -8,7 +8,8 @@
  * row x column scales, the bias and, for packed gate/up weights, the SwiGLU
  * product, and the runtime LoRA add.  For answering token by token it adds
  * linears over 4-bit weights, a paged 8-bit cache of keys and values, and the
- * attention that reads it.  Every step runs in hand-written CUDA kernels on
+ * attention that reads it; between the projections norms whose results are
+ * already codes, rotary positions, and linears over e4m3 codes in blocks of 128.  Every step runs in hand-written CUDA kernels on
  * the caller's stream.
  *
  * Conventions shared by every entry point:
@@ -557,14 +558,15 @@ int clef_kv_copy_pages(void *codes, int64_t plane_bytes, float *scales, int64_t 
  *
  * clef_fp8_block_linear -- the linear over such codes: with b the blocks of 128 of K,
  *   y[m][n] = bf16(sum_b sx[m][b] sw[n / 128][b] sum_{k in b} qx[m][k] qw[n][k] + bias[n])
- * with fp32 sums: a block's in the tensor core's order, the blocks' in an order that
- * follows the sizes M, N and K of the call.  sx: fp32 [M][ceil(K / 128)]; sw: fp32
+ * with fp32 sums: a block's in the tensor core's order, the blocks' in one that follows
+ * M, N and K of the call (so a row's bits may differ between calls of other M, never
+ * between calls of one size).  sx: fp32 [M][ceil(K / 128)]; sw: fp32
  * [ceil(N / 128)][ceil(K / 128)]; both 4-byte aligned.  Other arguments and
  * requirements as clef_fp8_linear.
  *
  * clef_fp8_block_gateup_swiglu -- h = bf16(g / (1 + exp(-g)) * u) of the unrounded
  * values g, u of rows n and N + n of the packed weight [2N][K]; N % 128 == 0, so that
- * no block of scales holds rows of both.  silu as in clef_fp8_gateup_swiglu.
+ * no block of scales holds rows of both.  silu as in clef_swiglu_bf16.
  *
  * clef_rotary -- rotation of heads by the positions of their tokens.  Pair i of
  * rot / 2 is the values (i, i + rot / 2) of a head, or (2 i, 2 i + 1) where
@@ -671,7 +673,9 @@ void clef_set_pdl(int on);
 
 /*
  * clef_set_sm_budget -- how many SMs the library's compute launches issued
- * afterwards may fill (GEMMs, LoRA launches, quantizers): sms, rounded down
+ * afterwards may fill (GEMMs, LoRA launches, quantizers, norms that keep rows
+ * ahead; a block linear of few rows takes one cluster of up to eight CTAs at
+ * least): sms, rounded down
  * to an even count, or every SM of the device for sms == 0 or sms at least
  * the device's count.  Results are the same bytes under any budget (the
  * tile order and every split follow the shapes, not the SM count; only the

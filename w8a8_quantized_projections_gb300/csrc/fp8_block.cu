@@ -13,17 +13,27 @@
 //  wide  many rows.  A cluster of two CTAs (cta_group::2) owns a tile of 256
 //        rows by 256 columns (128 gate and the 128 matching up columns); each CTA
 //        stages its 128 rows and half of the weight rows of a k-block (32 KB) in
-//        a ring of seven stages.  A TMEM lane is a row of x, so a thread's scale is its
-//        row's times one of the weight's, the same for its 128 columns.  Reading
-//        back is 128 x 256 fp32 a k-block and CTA, 256 clocks of TMEM and 128 of
-//        packed fp32 multiply-adds on each of the SM's four parts, beside 512 of
-//        the tensor core.  Persistent over tiles, in bands of rows that stay in L2.
-//  few   few rows, bound by the weight's bytes; operands change places.  A CTA
-//        owns 128 rows of the weight (TMEM lanes) and up to 128 rows of x
-//        (columns), so that the weight streams once through a ring of
-//        about 200 KB a SM; K is cut among the CTAs of a cluster where the
-//        weight's tiles alone leave SMs without work, and their sums meet
-//        through distributed shared memory, added in K order.
+//        a ring.  A TMEM lane is a row of x, so a thread's scale is its row's times
+//        one of the weight's, the same for its 128 columns.  Persistent over tiles, in
+//        bands of rows that stay in L2; a tile leaves through shared memory and TMA.
+//        24,032 x 5,120 x 6,144: 484 us, 3,120 TFLOP/s; 1,502 x 5,120 x 17,408 gate/up 203
+//        us.  MMAs alone, without reading back, take 432 us of the first (operands'
+//        shared-memory traffic: 64 KB a k-block and SM); the rest is a tile's end
+//        (about 3,000 clocks of 30,000, two k-blocks of which are hidden) and the way from
+//        an MMA's end over both CTAs' reading back to the MMA that reuses the buffer
+//        (about 1,300 clocks, 1,000 of them hidden).  What was tried: sixteen warps
+//        that read back (8% slower: the fixed part of a k-block, some 80 instructions, counts
+//        for each), halves of a buffer with MMAs of 128 columns (45% slower: A is
+//        read twice from shared memory), scales by 16-byte loads (no gain).
+//  few   up to 512 rows, bound by the weight's bytes; operands change places.  A CTA
+//        owns 128 rows of the weight (TMEM lanes) and 16 to 128 rows of x
+//        (columns), so that the weight streams through rings of about 200 KB a SM; K
+//        is cut among the CTAs of a cluster where the weight's tiles alone leave SMs
+//        without work, and their sums meet through distributed shared memory, always
+//        in the same order.  1 x 5,120 x 17,408 gate/up: 30.5 us (178 MB, 5.8 TB/s); 13 x
+//        17,408 x 5,120: 19.4 us (89 MB; 2.5 us are a launch's, the bytes alone take 14 at
+//        the 6.4 TB/s of a long call).  Copies of later k-blocks into L2 ahead of the
+//        ring: 20% slower; MMAs of two k-blocks side by side: no gain.
 #include <algorithm>
 #include <atomic>
 #include <cstdint>

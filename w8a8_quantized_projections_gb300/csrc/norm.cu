@@ -7,7 +7,9 @@
 //
 // Bound by HBM: 2 bytes an element in for x, 2 in and 2 out for the residual, 1
 // out for a code (2 for a bf16 result), so the row is read once and stays in
-// registers.  g is a factor of the whole row, and the rotation is linear: the
+// registers (or, many rows at a time, in shared memory until it is coded).  24,032 x
+// 5,120 with a residual: codes in blocks 145 us (88% of the copy rate), rotated INT8
+// 130 us (98%), bf16 153 us (95%); a row of 5,120: 2 us, its launch.  g is a factor of the whole row, and the rotation is linear: the
 // absmax of v = h w (rotated) is found beside the sum of squares, in one
 // reduction over the row; the codes are rne(v * top / absmax(v)), in which g
 // cancels, and the scale is absmax(v) g / top.  Scales of blocks of 128 need no
@@ -503,7 +505,8 @@ __global__ void __launch_bounds__(512) norm_staged_kernel(const __grid_constant_
 
 // ------------------------------------------------------------ blocks of 128
 
-// Codes of x in blocks of one row by 128: four lanes a block, two pieces each.
+// Codes of x in blocks of one row by 128: four lanes a block, two pieces each.  24,032 x 5,120: 61 us, 89% of the copy
+// rate (eight lanes of a piece: 65 us); 1,502 x 17,408: 15 us.
 __global__ void __launch_bounds__(256) quant_rows_kernel(const uint16_t *__restrict__ x, int64_t ldx, int K, int blocks,
                                                          int64_t total, bool q32, uint8_t *__restrict__ q,
                                                          float *__restrict__ scale) {
@@ -544,7 +547,7 @@ __global__ void __launch_bounds__(256) quant_rows_kernel(const uint16_t *__restr
     pdl_launch_dependents();
 }
 
-// Codes of w in blocks of 128 rows by 128: a CTA a block, 64 values a thread, kept as bf16.
+// Codes of w in blocks of 128 rows by 128: a CTA a block, 64 values a thread, kept as bf16.  5,120 x 17,408: 49 us, 81%.
 __global__ void __launch_bounds__(256) quant_tiles_kernel(const uint16_t *__restrict__ w, int64_t ldw, int64_t M, int K,
                                                           int blocks, uint8_t *__restrict__ q, float *__restrict__ scale) {
     __shared__ float part[8];
@@ -707,6 +710,8 @@ int norm_call(const void *x, int64_t ldx, const void *residual, int64_t ldr, con
     a.blocks = (int)((K + 127) / 128);
     a.eps = eps;
     a.y32 = !kv_misaligned(y, 32) && ldy % 16 == 0;
+    // (Residuals of rotated modes are written in halves of sectors: 24,032 x 5,120 INT8 130 us, 145 in whole ones.  The
+    // others are the other way round: codes in blocks 145 and 156 us, and rotated rows of 16,384 77 and 81 us.)
     a.r32 = !kv_misaligned(residual_out, 32) && ldro % 16 == 0 &&
             !((mode == kNormI8H || mode == kNormF8H) && K <= 8192);
     a.q32 = !kv_misaligned(q, 32) && K % 32 == 0;
