@@ -223,7 +223,7 @@ def test_refusals():
 
 
 @pytest.mark.parametrize("mode", MODES)
-@pytest.mark.parametrize("k", [576, 1024, 5120, 8256, 16384, 16400])
+@pytest.mark.parametrize("k", [528, 576, 1024, 5120, 5136, 8256, 16384, 16400, 17408, 17424, 32768])
 def test_many_rows_have_the_bits_of_one(mode, k):
     """Calls whose CTAs keep rows ahead in shared memory, against calls of a row."""
     if mode.endswith("h128") and k % 128:

@@ -25,7 +25,7 @@
 //        that read back (8% slower: the fixed part of a k-block, some 80 instructions, counts
 //        for each), halves of a buffer with MMAs of 128 columns (45% slower: A is
 //        read twice from shared memory), scales by 16-byte loads (no gain).
-//  few   up to 512 rows, bound by the weight's bytes; operands change places.  A CTA
+//  few   few rows, bound by the weight's bytes; operands change places.  A CTA
 //        owns 128 rows of the weight (TMEM lanes) and 16 to 128 rows of x
 //        (columns), so that the weight streams through rings of about 200 KB a SM; K
 //        is cut among the CTAs of a cluster where the weight's tiles alone leave SMs
@@ -833,7 +833,7 @@ int launch_few(const void *qx, const void *qw, int64_t K, BlockArgs a, int split
     if (rc) return rc;
     a.split = split;
     a.tiles_m = (a.M + T - 1) / T;
-    int64_t clusters = (int64_t)((a.N + 127) / 128) * a.tiles_m;             // (N is under 2^29, and tiles_m at most 32)
+    int64_t clusters = (int64_t)((a.N + 127) / 128) * a.tiles_m;             // (N is under 2^29, and tiles_m at most 256)
     if (sms < all_sms) clusters = std::min<int64_t>(clusters, std::max(1, sms / split));   // a budget of SMs
     const int64_t grid = clusters * split;
     e = launch_kernel(kern, dim3((unsigned)grid), dim3(F::kThreads), F::kSmem, st, split, true, tx, tw, a);
@@ -842,14 +842,14 @@ int launch_few(const void *qx, const void *qw, int64_t K, BlockArgs a, int split
 
 // The kernel for a call: the one expected to take least on the whole device, so that a budget of SMs changes no
 // sum's order.  (Both sides measured at 2048 x 2048, 1024 x 5120, 6144 x 5120,
-// 5120 x 17408 and 34816 x 5120, and at 2048 and 17408 gate/up columns, for 1 .. 512 rows.)
+// 5120 x 17408 and 34816 x 5120, and at 2048 and 17408 gate/up columns, and narrow ones, for 1 .. 4,096 rows.)
 template <bool GU>
 int launch_block(const void *qx, const void *qw, int64_t K, const BlockArgs &a, int sms, int all_sms, cudaStream_t st) {
     // many rows: rounds of tiles, each k-block 0.38 us, or the weight's bytes at 4.5 TB/s
     const int64_t pairs = std::max(1, all_sms / 2), tiles = (int64_t)((a.M + 255) / 256) * (GU ? a.N / 128 : (a.N + 255) / 256);
     const double weight = (GU ? 2.0 : 1.0) * a.N * (double)K;
     FewPlan best{0, 1, 4.0 + std::max((double)((tiles + pairs - 1) / pairs) * a.nkb * 0.38, weight / 4.5e6)};
-    if (a.M <= 512) {
+    if (a.M <= 4096) {
         for (const FewPlan &p : {plan_few<16, GU>(a, all_sms), plan_few<32, GU>(a, all_sms), plan_few<64, GU>(a, all_sms)})
             if (p.us < best.us) best = p;
         if constexpr (!GU) {

@@ -360,8 +360,9 @@ __global__ void __launch_bounds__(G ? 128 : 512) norm_kernel(const NormArgs a) {
 
 // Many rows: CTAs that stay, each with a ring of rows of x and the residual in shared memory, filled by copies several
 // rows ahead, so that HBM is read while earlier rows are reduced and written.  A row is lines of 128 bytes with
-// the 128-byte swizzle: unit u of 16 bytes of line l lies at unit u ^ (l & 7).  A thread owns half a line (C =
-// 2), or a line (C = 4); the operations and their order are norm_kernel's.
+// the 128-byte swizzle: unit u of 16 bytes of line l lies at unit u ^ (l & 7).  (Rows of other lengths are copied as
+// they are; their reads meet in the banks.)  A thread owns half a line (C = 2), or a line (C = 4); the operations
+// and their order are norm_kernel's.
 constexpr int kMaxRing = 8;
 
 __device__ __forceinline__ void tma_lines(void *dst, const CUtensorMap *m, int line, int64_t row, uint64_t *bar) {
@@ -376,9 +377,14 @@ __device__ __forceinline__ void tma_row(uint8_t *dst, const CUtensorMap *m, int 
     if (lines > 256) tma_lines(dst + lines / 2 * 128, m, lines / 2, row, bar);
 }
 
+__device__ __forceinline__ void bulk_row(void *dst, const void *src, uint32_t bytes, uint64_t *bar) {
+    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];"
+                 ::"r"(smem_u32(dst)), "l"(src), "r"(bytes), "r"(smem_u32(bar)) : "memory");
+}
+
 template <int MODE, int C>
 __global__ void __launch_bounds__(512) norm_staged_kernel(const __grid_constant__ CUtensorMap tmx, const __grid_constant__ CUtensorMap tmr,
-                                                          const __grid_constant__ CUtensorMap tmw, const NormArgs a, int ring, uint32_t slot_bytes, unsigned int *status,
+                                                          const __grid_constant__ CUtensorMap tmw, const NormArgs a, bool lines, int ring, uint32_t slot_bytes, unsigned int *status,
                                                           uint64_t limit_ns) {
     constexpr bool kRotate = MODE == kNormI8H || MODE == kNormF8H;
     constexpr bool kRowMax = MODE != kNormBf16 && MODE != kNormF8B;
@@ -392,7 +398,6 @@ __global__ void __launch_bounds__(512) norm_staged_kernel(const __grid_constant_
     const uint32_t row_bytes = (uint32_t)a.K * 2u, r_at = (row_bytes + 1023u) & ~1023u;
     uint8_t *weights = smem_raw + (((base + 1023u) & ~1023u) - base), *rows = weights + r_at;
     const int e = tid * C * kE;
-    const bool in = e < a.K;
     if (tid == 0) {
         for (int s = 0; s < ring; ++s) mbar_init(&full[s], 1);
         mbar_init(&w_full, 1);
@@ -409,20 +414,26 @@ __global__ void __launch_bounds__(512) norm_staged_kernel(const __grid_constant_
     const auto fill = [&](int slot, int64_t m) {
         uint8_t *dst = rows + (uint32_t)slot * slot_bytes;
         mbar_arrive_expect_tx(&full[slot], a.r ? 2u * row_bytes : row_bytes);
-        tma_row(dst, &tmx, a.K / 64, m, &full[slot]);
-        if (a.r) tma_row(dst + r_at, &tmr, a.K / 64, m, &full[slot]);
+        if (lines) {
+            tma_row(dst, &tmx, a.K / 64, m, &full[slot]);
+            if (a.r) tma_row(dst + r_at, &tmr, a.K / 64, m, &full[slot]);
+        } else {
+            bulk_row(dst, a.x + m * a.ldx, row_bytes, &full[slot]);
+            if (a.r) bulk_row(dst + r_at, a.r + m * a.ldr, row_bytes, &full[slot]);
+        }
     };
     const int64_t first = blockIdx.x, step = gridDim.x;
     if (tid == 0) {
         mbar_arrive_expect_tx(&w_full, row_bytes);
-        tma_row(weights, &tmw, a.K / 64, 0, &w_full);
+        if (lines) tma_row(weights, &tmw, a.K / 64, 0, &w_full);
+        else bulk_row(weights, a.w, row_bytes, &w_full);
     }
     if (tid == 0)
         for (int s = 0; s < ring && first + s * step < a.M; ++s) fill(s, first + s * step);
     const uint32_t line = (uint32_t)tid / (4 / C), unit = (uint32_t)tid % (4 / C) * 4u;
     uint32_t off[2 * C];
 #pragma unroll
-    for (int j = 0; j < 2 * C; ++j) off[j] = line * 128u + (((unit + j) ^ (line & 7u)) << 4);
+    for (int j = 0; j < 2 * C; ++j) off[j] = line * 128u + (((unit + j) ^ (lines ? line & 7u : 0u)) << 4);
     const auto piece = [&](const uint8_t *p, int c, uint32_t(&o)[8]) {
         const uint4 x = *reinterpret_cast<const uint4 *>(p + off[2 * c]), y = *reinterpret_cast<const uint4 *>(p + off[2 * c + 1]);
         o[0] = x.x; o[1] = x.y; o[2] = x.z; o[3] = x.w;
@@ -443,7 +454,7 @@ __global__ void __launch_bounds__(512) norm_staged_kernel(const __grid_constant_
 #pragma unroll
             for (int c = 0; c < C; ++c) {
                 total[c] = 0.0f;
-                if (in) {
+                if (e + c * kE < a.K) {
                     uint32_t xp[8], rp[8], wp[8], sum[8];
                     piece(at, c, xp);
                     if (a.r) piece(at + r_at, c, rp);
@@ -477,9 +488,9 @@ __global__ void __launch_bounds__(512) norm_staged_kernel(const __grid_constant_
         if constexpr (MODE != kNormBf16) leave_codes<MODE, C>(a, m, e, true, v, g, amax);
         if (MODE == kNormBf16 || a.y) {
             if constexpr (kRotate) take(false);      // the values before their rotation once more: the row is still there
-            if (in)
 #pragma unroll
-                for (int c = 0; c < C; ++c) leave_y(a, m, e + c * kE, v + 8 * c, g);
+            for (int c = 0; c < C; ++c)
+                if (e + c * kE < a.K) leave_y(a, m, e + c * kE, v + 8 * c, g);
         }
         if (kRotate && a.y) __syncthreads();
         // past the last barrier every thread has read the row
@@ -606,18 +617,21 @@ int launch_staged(const NormArgs &a, const NormEnv &env, int threads, cudaStream
     auto kern = norm_staged_kernel<MODE, C>;
     cudaError_t e = opt.set(reinterpret_cast<const void *>(kern), kMost);
     if (e != cudaSuccess) return internal_cuda_error(e, "norm smem attribute");
-    const uint64_t dims[3] = {64, (uint64_t)(a.K / 64), (uint64_t)a.M};
-    const uint32_t box[3] = {64, (uint32_t)(a.K / 64 > 256 ? a.K / 128 : a.K / 64), 1};
-    CUtensorMap tx, tr;
-    const uint64_t sx[2] = {128, (uint64_t)a.ldx * 2}, sr[2] = {128, (uint64_t)a.ldr * 2};
-    int rc = internal_make_tmap_nd(&tx, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, a.x, dims, sx, box, CU_TENSOR_MAP_SWIZZLE_128B);
-    if (rc) return rc;
-    tr = tx;
-    if (a.r && (rc = internal_make_tmap_nd(&tr, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, a.r, dims, sr, box, CU_TENSOR_MAP_SWIZZLE_128B)))
-        return rc;
-    CUtensorMap tw;
-    const uint64_t one[3] = {64, (uint64_t)(a.K / 64), 1}, sw[2] = {128, (uint64_t)a.K * 2};
-    if ((rc = internal_make_tmap_nd(&tw, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, a.w, one, sw, box, CU_TENSOR_MAP_SWIZZLE_128B))) return rc;
+    // rows of whole lines, up to 256 of them, or twice a multiple of eight
+    const bool lines = a.K % 64 == 0 && (a.K <= 256 * 64 || a.K % 1024 == 0);
+    CUtensorMap tx = {}, tr = {}, tw = {};
+    if (lines) {
+        const uint64_t dims[3] = {64, (uint64_t)(a.K / 64), (uint64_t)a.M}, one[3] = {64, (uint64_t)(a.K / 64), 1};
+        const uint32_t box[3] = {64, (uint32_t)(a.K / 64 > 256 ? a.K / 128 : a.K / 64), 1};
+        const auto map = [&](CUtensorMap &m, const void *at, const uint64_t *d, int64_t ld) {
+            const uint64_t strides[2] = {128, (uint64_t)ld * 2};
+            return internal_make_tmap_nd(&m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, at, d, strides, box, CU_TENSOR_MAP_SWIZZLE_128B);
+        };
+        int rc = map(tx, a.x, dims, a.ldx);
+        if (!rc) rc = map(tw, a.w, one, a.K);
+        if (!rc && a.r) rc = map(tr, a.r, dims, a.ldr);
+        if (rc) return rc;
+    }
     // CTAs that registers and threads let an SM hold (asked once for each number of warps)
     static std::atomic<int> known[17];
     int most = known[threads / 32].load(std::memory_order_relaxed);
@@ -633,7 +647,7 @@ int launch_staged(const NormArgs &a, const NormEnv &env, int threads, cudaStream
     ring = std::min((kMost / per_sm - 2048 - row) / slot, kMaxRing);
     const int64_t ctas = (int64_t)per_sm * env.sms;
     e = launch_kernel(kern, dim3((unsigned)(a.M < ctas ? a.M : ctas)), dim3((unsigned)threads), (size_t)(row + ring * slot + 1024), st, 1, true,
-                      tx, tr, tw, a, ring, (uint32_t)slot, env.status, env.limit_ns);
+                      tx, tr, tw, a, lines, ring, (uint32_t)slot, env.status, env.limit_ns);
     return e == cudaSuccess ? CLEF_OK : internal_cuda_error(e, "norm launch");
 }
 
@@ -652,12 +666,14 @@ int launch_norm(const NormArgs &a, const NormEnv &env, cudaStream_t st) {
     if (chunks <= 8) e = lanes(norm_kernel<MODE, 1, 8>, 8);
     else if (chunks <= 16) e = lanes(norm_kernel<MODE, 1, 16>, 16);
     else if (chunks <= 32) e = lanes(norm_kernel<MODE, 1, 32>, 32);
+    // (a warp a row up to 1,024: 100,000 rows to fp8 114 us, 129 staged; rotated rows 150 and 110, rows of 2,048 worse)
+    else if (chunks <= 64 && MODE != kNormI8H && MODE != kNormF8H) e = lanes(norm_kernel<MODE, 2, 32>, 32);
     else {
-        // Rows enough that CTAs pay which keep some ahead.  (Bf16 results of short rows are written as fast as one CTA
-        // a row comes and goes: 24,032 x 5,120 153 us, 160 staged; 1,502 x 5,120 12.7 and 11.7.)
-        const bool many = a.M >= 8 * (int64_t)env.sms && !(MODE == kNormBf16 && chunks <= 512 && a.M >= 32 * (int64_t)env.sms);
-        if (many && chunks <= 1024 && a.K % 64 == 0) return launch_staged<MODE, 2>(a, env, (chunks + 63) / 64 * 32, st);
-        if (many && a.K % 1024 == 0) return launch_staged<MODE, 4>(a, env, (chunks + 127) / 128 * 32, st);
+        // Rows enough that CTAs pay which keep some ahead.  (Beside a residual, bf16 results of shorter rows leave a little
+        // faster where a CTA a row comes and goes: 24,032 x 5,120 152 us, 159 staged; 5,136 the other way round.)
+        const bool many = a.M >= 8 * (int64_t)env.sms && !(MODE == kNormBf16 && a.r && a.K <= 5120 && a.M >= 32 * (int64_t)env.sms);
+        if (many && chunks <= 1024) return launch_staged<MODE, 2>(a, env, (chunks + 63) / 64 * 32, st);
+        if (many) return launch_staged<MODE, 4>(a, env, (chunks + 127) / 128 * 32, st);
         e = chunks <= 512 ? cta(norm_kernel<MODE, 1, 0>, 1) : chunks <= 1024 ? cta(norm_kernel<MODE, 2, 0>, 2) : cta(norm_kernel<MODE, 4, 0>, 4);
     }
     return e == cudaSuccess ? CLEF_OK : internal_cuda_error(e, "norm launch");
