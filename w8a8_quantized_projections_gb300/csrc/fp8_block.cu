@@ -259,8 +259,9 @@ wide_kernel(const __grid_constant__ CUtensorMap tmx, const __grid_constant__ CUt
                 const int64_t steps = (int64_t)((tiles - 1 - slot) / slots + 1) * nkb;
                 bool ready = false;
                 for (int64_t i = 0; i < steps; ++i) {
-                    if (!ready && (!mbar_wait(&bar->acc_empty[acc], aph ^ 1u, w, kSiteMmaAccEmpty) ||
-                                   !mbar_wait(&bar->full[s], ph, w, kSiteMmaFull)))
+                    // (the buffer comes back last)
+                    if (!ready && (!mbar_wait(&bar->full[s], ph, w, kSiteMmaFull) ||
+                                   !mbar_wait(&bar->acc_empty[acc], aph ^ 1u, w, kSiteMmaAccEmpty)))
                         break;
                     tc_fence_after();
                     const uint32_t sa = smem_u32(smem + s * kWideStage), d = tmem + acc * 256, s0 = s;
@@ -549,8 +550,8 @@ few_kernel(const __grid_constant__ CUtensorMap tmx, const __grid_constant__ CUte
                 bool ready = false;
                 for (uint32_t g = done; g != done + (uint32_t)(k1 - k0); ++g) {
                     const uint32_t acc = g % F::kBufs, s0 = s;
-                    if (!ready && (!mbar_wait(&bar->acc_empty[acc], (g / F::kBufs & 1u) ^ 1u, w, kSiteMmaAccEmpty) ||
-                                   !mbar_wait(&bar->full[s], ph, w, kSiteMmaFull)))
+                    if (!ready && (!mbar_wait(&bar->full[s], ph, w, kSiteMmaFull) ||
+                                   !mbar_wait(&bar->acc_empty[acc], (g / F::kBufs & 1u) ^ 1u, w, kSiteMmaAccEmpty)))
                         break;
                     tc_fence_after();
                     const uint32_t sa = smem_u32(smem + s * F::kStage), d = tmem + acc * F::kAcc;
