@@ -560,7 +560,7 @@ int clef_kv_copy_pages(void *codes, int64_t plane_bytes, float *scales, int64_t 
  *   y[m][n] = bf16(sum_b sx[m][b] sw[n / 128][b] sum_{k in b} qx[m][k] qw[n][k] + bias[n])
  * with fp32 sums: a block's in the tensor core's order, the blocks' in one that follows
  * M, N and K of the call (so a row's bits may differ between calls of other M, never
- * between calls of one size).  sx: fp32 [M][ceil(K / 128)]; sw: fp32
+ * between calls of one size).  A product sx sw is fp32 too.  sx: fp32 [M][ceil(K / 128)]; sw: fp32
  * [ceil(N / 128)][ceil(K / 128)]; both 4-byte aligned.  Other arguments and
  * requirements as clef_fp8_linear.
  *

@@ -390,7 +390,7 @@ __device__ __forceinline__ void bulk_row(void *dst, const void *src, uint32_t by
 template <int MODE, int C>
 __global__ void __launch_bounds__(512) norm_staged_kernel(const __grid_constant__ CUtensorMap tmx, const __grid_constant__ CUtensorMap tmr,
                                                           const __grid_constant__ CUtensorMap tmw, const NormArgs a, bool lines, int ring, uint32_t slot_bytes, unsigned int *status,
-                                                          uint64_t limit_ns) {
+                                                          uint64_t limit_ns, int force_timeout) {
     constexpr bool kRotate = MODE == kNormI8H || MODE == kNormF8H;
     constexpr bool kRowMax = MODE != kNormBf16 && MODE != kNormF8B;
     extern __shared__ uint8_t smem_raw[];
@@ -449,6 +449,8 @@ __global__ void __launch_bounds__(512) norm_staged_kernel(const __grid_constant_
     uint32_t phase = 0, which = 0;
     int64_t m = first;
     mbar_wait(&w_full, 0, w, kSiteQuantFull);
+    // test knob: a wait for what nothing signals
+    if (force_timeout == 1 || force_timeout - 2 == (int)blockIdx.x) mbar_wait(&w_full, 1, w, kSiteQuantFull);
     for (; m < a.M; m += step) {
         mbar_wait(&full[slot], phase, w, kSiteQuantFull);
         const uint8_t *at = rows + (uint32_t)slot * slot_bytes;
@@ -606,6 +608,7 @@ struct NormEnv {
     int sms;
     unsigned int *status;
     uint64_t limit_ns;
+    int force_timeout;
 };
 
 // The staged kernel's launch: CTAs an SM for 1,024 threads, with the rows that 220 KB hold.
@@ -646,7 +649,7 @@ int launch_staged(const NormArgs &a, const NormEnv &env, int threads, cudaStream
     ring = std::min((kMost / per_sm - 2048 - row) / slot, kMaxRing);
     const int64_t ctas = (int64_t)per_sm * env.sms;
     e = launch_kernel(kern, dim3((unsigned)(a.M < ctas ? a.M : ctas)), dim3((unsigned)threads), (size_t)(row + ring * slot + 1024), st, 1, true,
-                      tx, tr, tw, a, lines, ring, (uint32_t)slot, env.status, env.limit_ns);
+                      tx, tr, tw, a, lines, ring, (uint32_t)slot, env.status, env.limit_ns, env.force_timeout);
     return e == cudaSuccess ? CLEF_OK : internal_cuda_error(e, "norm launch");
 }
 
@@ -704,10 +707,9 @@ int norm_call(const void *x, int64_t ldx, const void *residual, int64_t ldr, con
     const int rc = internal_device(&sms, &status);
     if (rc) return rc;
     NormEnv env;
-    int force = 0;
     env.sms = internal_launch_sms(sms);
     env.status = status;
-    env.limit_ns = internal_wait_limit(&force);
+    env.limit_ns = internal_wait_limit(&env.force_timeout);
     NormArgs a;
     a.x = static_cast<const uint16_t *>(x);
     a.r = static_cast<const uint16_t *>(residual);

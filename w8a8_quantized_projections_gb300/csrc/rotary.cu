@@ -6,7 +6,7 @@
 //
 // Bound by HBM: 2 bytes in and 2 out an element.  A thread owns up to eight pairs
 // (four where they are neighbours) of a token for all heads of its slice, so that it
-// finds their cosines and sines once (24,032 x 56 x 128: 108 us, 94% of the copy rate;
+// finds their cosines and sines once (24,032 x 56 x 128: 106 us, 96% of the copy rate;
 // a quarter of 28 heads of 256: 107 us; three tokens: 1.7 us, a launch).  A frequency is a number of turns a position
 // in units of 2^-64, kept modulo one turn: the product with a position is exact
 // modulo one turn in 64-bit integers, so that an angle is as exact at position
