@@ -235,6 +235,17 @@ def test_linears_at_once_and_waits_that_run_out(m, gateup):
     assert torch.equal(y[1:m - 1], want[0][1:m - 1]) and y[0].isnan().all()
 
 
+@pytest.mark.parametrize("m", [16, 300, 4200])
+def test_gates_of_every_size(m):
+    """Gates from -100 to 100: past the largest e^-g of fp32 and back."""
+    one = torch.tensor([0x38], dtype=torch.uint8, device="cuda")               # 1.0
+    qx, qw = torch.zeros((m, 128), dtype=torch.uint8, device="cuda"), torch.zeros((256, 128), dtype=torch.uint8, device="cuda")
+    qx[:, 0], qw[:, 0] = one, one
+    args = (qx, torch.linspace(-100, 100, m, device="cuda")[:, None].contiguous(), qw,
+            torch.tensor([[1.0], [2.0 ** -16]], device="cuda"), None)
+    check_gateup(clef.fp8_block_gateup_swiglu(*args), args)
+
+
 # ---------------------------------------------------------------- rotary positions
 
 @pytest.mark.parametrize("interleaved", [False, True])

@@ -16,7 +16,7 @@
 //        a ring.  A TMEM lane is a row of x, so a thread's scale is its row's times
 //        one of the weight's, the same for its 128 columns.  Persistent over tiles, in
 //        bands of rows that stay in L2; a tile leaves through shared memory and TMA.
-//        24,032 x 5,120 x 6,144: 484 us, 3,120 TFLOP/s; 1,502 x 5,120 x 17,408 gate/up 203
+//        24,032 x 5,120 x 6,144: 484 us, 3,120 TFLOP/s; 1,502 x 5,120 x 17,408 gate/up 196
 //        us.  MMAs alone, without reading back, take 432 us of the first (operands'
 //        shared-memory traffic: 64 KB a k-block and SM); the rest is a tile's end
 //        (about 3,000 clocks of 30,000, two k-blocks of which are hidden) and the way from
@@ -30,8 +30,8 @@
 //        (columns), so that the weight streams through rings of about 200 KB a SM; K
 //        is cut among the CTAs of a cluster where the weight's tiles alone leave SMs
 //        without work, and their sums meet through distributed shared memory, always
-//        in the same order.  1 x 5,120 x 17,408 gate/up: 30.5 us (178 MB, 5.8 TB/s); 13 x
-//        17,408 x 5,120: 19.4 us (89 MB; 2.5 us are a launch's, the bytes alone take 14 at
+//        in the same order.  1 x 5,120 x 17,408 gate/up: 28.9 us (178 MB, 6.2 TB/s); 13 x
+//        17,408 x 5,120: 19.1 us (89 MB; 2.5 us are a launch's, the bytes alone take 14 at
 //        the 6.4 TB/s of a long call).  Copies of later k-blocks into L2 ahead of the
 //        ring: 20% slower; MMAs of two k-blocks side by side: no gain.
 #include <algorithm>
@@ -82,6 +82,32 @@ __device__ __forceinline__ uint64_t fma_f2(uint64_t a, uint64_t b, uint64_t c) {
     uint64_t d;
     asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
     return d;
+}
+
+__device__ __forceinline__ uint64_t mul_f2(uint64_t a, uint64_t b) {
+    uint64_t d;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
+}
+__device__ __forceinline__ uint64_t add_f2(uint64_t a, uint64_t b) {
+    uint64_t d;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
+}
+
+// g / (1 + e^-g) u of two values, as (g / 4) u / (1/4 + 2^(-g log2 e - 2)): the divisor is below 2^126, where the
+// reciprocal underflows, for every e^-g that fp32 holds, so that none has to be looked at and scaled
+// (1,502 x 5,120 x 17,408: 200 to 196 us; 188 without a silu, whose exponentials and reciprocals are what a tile waits for).
+__device__ __forceinline__ uint64_t silu_mul2(uint64_t g, uint64_t u) {
+    constexpr float kLog2E = 1.44269504088896341f;
+    float a, b;
+    unpack_f2(fma_f2(g, pack_f2(-kLog2E, -kLog2E), pack_f2(-2.0f, -2.0f)), a, b);
+    asm("ex2.approx.ftz.f32 %0, %0;" : "+f"(a));
+    asm("ex2.approx.ftz.f32 %0, %0;" : "+f"(b));
+    unpack_f2(add_f2(pack_f2(a, b), pack_f2(0.25f, 0.25f)), a, b);
+    asm("rcp.approx.ftz.f32 %0, %0;" : "+f"(a));
+    asm("rcp.approx.ftz.f32 %0, %0;" : "+f"(b));
+    return mul_f2(mul_f2(mul_f2(g, pack_f2(0.25f, 0.25f)), pack_f2(a, b)), u);
 }
 
 // One lane of a whole warp.  The warps that issue copies and MMAs run with all lanes and elect one for each k-block:
@@ -388,13 +414,7 @@ wide_kernel(const __grid_constant__ CUtensorMap tmx, const __grid_constant__ CUt
                     for (int i = 0; i < 4; ++i) {
                         float v0, v1;
                         const int c = 64 * b + 8 * q + 2 * i;
-                        unpack_f2(sum[c / 2], v0, v1);
-                        if (GU) {
-                            float u0, u1;
-                            unpack_f2(sum[kSums / 4 + c / 2], u0, u1);
-                            v0 = silu_mul_fast(v0, u0);
-                            v1 = silu_mul_fast(v1, u1);
-                        }
+                        unpack_f2(GU ? silu_mul2(sum[c / 2], sum[(GU ? kSums / 4 : 0) + c / 2]) : sum[c / 2], v0, v1);
                         p[i] = pack_bf16x2(v0, v1);
                     }
                     *reinterpret_cast<uint4 *>(box + b * kOutBox + lane * 128 + ((q ^ (lane & 7)) << 4)) =
