@@ -556,8 +556,8 @@ __global__ void __launch_bounds__(256) quant_rows_kernel(const uint16_t *__restr
     pdl_launch_dependents();
 }
 
-// Codes of w in blocks of 128 rows by 128: a CTA a block, two pieces of a row a thread, kept as bf16.  5,120 x 17,408: 46 us, 86% of the
-// copy rate (256 threads of four pieces 48 us).
+// Codes of w in blocks of 128 rows by 128: a CTA a block, two pieces of a row a thread, kept as bf16.  5,120 x 17,408: 44 us, 90% of the
+// copy rate (256 threads of four pieces: 48.8 us where this took 45.7).
 __global__ void __launch_bounds__(512, 3) quant_tiles_kernel(const uint16_t *__restrict__ w, int64_t ldw, int64_t M, int K,
                                                              int blocks, bool q32, uint8_t *__restrict__ q, float *__restrict__ scale) {
     __shared__ float part[16];
