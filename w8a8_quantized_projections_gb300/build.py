@@ -89,7 +89,7 @@ def _link_extension(obj: str) -> None:
     """Against libclef.so beside it and the torch libraries that the process has loaded."""
     tmp = EXT + f".{os.getpid()}.tmp"
     _run("link of clef_decode.so", ["g++", "-shared", "-o", tmp, obj, "-L", BUILD, "-l:libclef.so", "-Wl,-rpath,$ORIGIN",
-                                    "-L", os.path.join(_torch_dir(), "lib"), "-ltorch_python", "-ltorch", "-ltorch_cpu",
+                                    "-L", os.path.join(_torch_dir(), "lib"), "-ltorch_python", "-ltorch", "-ltorch_cpu", "-ltorch_cuda",
                                     "-lc10_cuda", "-lc10"])
     os.replace(tmp, EXT)
     tmp = KEY + f".{os.getpid()}.tmp"

@@ -20,7 +20,7 @@
 #include <cmath>
 
 #include <ATen/core/Tensor.h>
-#include <ATen/ops/empty.h>
+#include <ATen/cuda/EmptyTensor.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/Exceptions.h>
@@ -194,11 +194,13 @@ c10::cuda::CUDAStream external(const Stream &s) {
 
 // Torch's allocator hands memory out again in the order of the stream that was
 // current at its allocation, so a given stream is made the current one for it.
+// (From the allocator's own entry: by way of the dispatcher a call with two new
+// results takes 4.6 us of the host, so 4.2, of which 2.2 are the launch.)
 Tensor fresh(at::IntArrayRef shape, ScalarType type, const Stream &s) {
-    const auto options = at::TensorOptions().dtype(type).device(c10::kCUDA, (c10::DeviceIndex)s.device);
-    if (!s.given) return at::empty(shape, options);
+    const c10::Device device(c10::kCUDA, (c10::DeviceIndex)s.device);
+    if (!s.given) return Tensor(at::detail::empty_cuda(shape, type, device, std::nullopt));
     c10::cuda::CUDAStreamGuard guard(external(s));
-    return at::empty(shape, options);
+    return Tensor(at::detail::empty_cuda(shape, type, device, std::nullopt));
 }
 
 // A result that the caller passed, or a new one.
