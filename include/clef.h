@@ -674,8 +674,7 @@ void clef_set_pdl(int on);
 /*
  * clef_set_sm_budget -- how many SMs the library's compute launches issued
  * afterwards may fill (GEMMs, LoRA launches, quantizers, norms that keep rows
- * ahead; a block linear of few rows takes one cluster of up to eight CTAs at
- * least): sms, rounded down
+ * ahead; a block linear takes one cluster of up to eight CTAs at least): sms, rounded down
  * to an even count, or every SM of the device for sms == 0 or sms at least
  * the device's count.  Results are the same bytes under any budget (the
  * tile order and every split follow the shapes, not the SM count; only the

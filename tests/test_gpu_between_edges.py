@@ -209,6 +209,45 @@ def test_gateup_of_many_rows(m, n, k):
     assert (out[:, :8] == 7.0).all() and (out[:, n + 8:] == 7.0).all() and clef.poll_status() == 0
 
 
+# (few tiles of 256 rows: two or four pairs of CTAs share one)
+@pytest.mark.parametrize("gateup,m,n,k", [(False, 600, 2040, 5136), (False, 1000, 512, 4112), (False, 2049, 264, 2064), (False, 4200, 8, 8208),
+                                          (True, 600, 1024, 5136), (True, 2100, 128, 5136), (True, 1281, 640, 2064)])
+def test_tiles_shared_by_pairs(gateup, m, n, k):
+    f, check_one = (clef.fp8_block_gateup_swiglu, check_gateup) if gateup else (clef.fp8_block_linear, check_linear)
+    for with_bias in (False, True):
+        args = inputs(m, n, k, 74, with_bias=with_bias, gateup=gateup)
+        out = torch.full((m, n + 24), 7.0, dtype=torch.bfloat16, device="cuda")
+        y = f(*args, out[:, 8:n + 8])
+        check_one(y, args)
+        assert (out[:, :8] == 7.0).all() and (out[:, n + 8:] == 7.0).all()
+        for sms in (0, 2, 20, 100):
+            clef.set_sm_budget(sms)
+            try:
+                assert torch.equal(f(*args), y)
+            finally:
+                clef.set_sm_budget(0)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = [f(*args) for _ in range(3)]
+    for _ in range(2):
+        for g in got:
+            g.zero_()
+        graph.replay()
+        assert all(torch.equal(g, y) for g in got)
+    assert clef.poll_status() == 0
+    eventually()
+    try:
+        f(*args)
+        assert clef.poll_status() == 4
+        clef.set_sm_budget(20)
+        f(*args)
+        assert clef.poll_status() == 4
+    finally:
+        clef.set_sm_budget(0)
+        restore()
+    assert torch.equal(f(*args), y) and clef.poll_status() == 0
+
+
 @pytest.mark.parametrize("gateup", [False, True])
 @pytest.mark.parametrize("m", [2, 40, 4100])
 def test_linears_at_once_and_waits_that_run_out(m, gateup):

@@ -25,6 +25,10 @@
 //        that read back (8% slower: the fixed part of a k-block, some 80 instructions, counts
 //        for each), halves of a buffer with MMAs of 128 columns (45% slower: A is
 //        read twice from shared memory), scales by 16-byte loads (no gain).
+//        Where tiles are few, two or four pairs share one, each with a part of K; each takes
+//        a part of its columns to the end with the sums that the others write into its shared
+//        memory (1,502 x 5,120 x 1,024: 20.5 to 16.5 us, 1,024 x 17,408 x 2,048: 54 to 35; sums that
+//        each leaves in its own memory for the others to read: 1 us slower).
 //  few   few rows, bound by the weight's bytes; operands change places.  A CTA
 //        owns 128 rows of the weight (TMEM lanes) and 16 to 128 rows of x
 //        (columns), so that the weight streams through rings of about 200 KB a SM; K
@@ -59,6 +63,7 @@ struct BlockArgs {
     int64_t ldo;
     int band;                 // wide: tiles of rows a band
     int split;                // few: CTAs that share a tile's K
+    bool whole;               // wide: the output's rows start on 32 bytes
     int tiles_m;              // few: tiles of rows
     unsigned int *status;
     uint64_t limit_ns;
@@ -158,6 +163,21 @@ __device__ __forceinline__ void bulk_commit() { asm volatile("cp.async.bulk.comm
 __device__ __forceinline__ void bulk_wait_read_all() { asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory"); }
 __device__ __forceinline__ void bulk_wait_all() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
 
+// An address in the same shared memory of another CTA of the cluster.
+__device__ __forceinline__ uint32_t cluster_addr(uint32_t local, int rank) {
+    uint32_t at;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"(local), "r"(rank));
+    return at;
+}
+__device__ __forceinline__ float ld_cluster(uint32_t at) {
+    float v;
+    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(at) : "memory");
+    return v;
+}
+__device__ __forceinline__ void st_cluster(uint32_t at, uint64_t a, uint64_t b) {
+    asm volatile("st.shared::cluster.v2.b64 [%0], {%1, %2};" ::"r"(at), "l"(a), "l"(b) : "memory");
+}
+
 // ------------------------------------------------------------ many rows
 
 constexpr int kBoxBytes = 128 * 128;         // 128 rows of a k-block
@@ -167,11 +187,13 @@ constexpr int kWideEpi = 8;                  // warps that read TMEM back
 constexpr int kParts = kWideEpi / 4, kSums = 256 / kParts;    // of a row, and columns that each holds
 constexpr int kWideThreads = 128 + 32 * kWideEpi;
 constexpr int kOutBox = 32 * 128;            // 32 rows of 64 columns of the output, bf16
-template <bool GU>
+template <bool GU, int S>
 struct Wide {
     static constexpr int kBoxes = GU ? 1 : 2;                    // of 64 columns of the output a warp
-    static constexpr int kOut = kWideEpi * kBoxes * kOutBox;
-    static constexpr int kStages = GU ? 6 : 5;
+    static constexpr int kMine = kSums / S;                      // sums of a thread that it brings to their end
+    // what leaves through shared memory, or the other pairs' sums
+    static constexpr int kOut = S == 1 ? kWideEpi * kBoxes * kOutBox : (S - 1) * kWideEpi * 32 * kMine * 4;
+    static constexpr int kStages = S == 1 ? (GU ? 6 : 5) : S == 2 ? 5 : 4;
     static constexpr int kSmem = kStages * kWideStage + kOut + 1024 + 512;
     static_assert(kSmem <= 232448, "shared memory");
 };
@@ -196,18 +218,28 @@ __device__ __forceinline__ WideTile wide_tile(int t, int num_m, int num_n, int b
     return {m0 + i % rows, i / rows};
 }
 
-template <bool GU>
+// As mma2_commit_both, for the pair of CTAs from rank `first` on of a larger cluster.
+__device__ __forceinline__ void commit_pair(uint64_t *bar, uint32_t first) {
+    asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;"
+                 ::"r"(smem_u32(bar)), "h"((uint16_t)(3u << first)) : "memory");
+}
+
+// S > 1: a cluster is S pairs that share a tile, each with a part of K.  A pair takes a part of the columns to their end: the
+// others leave their sums of these in its shared memory, and it adds them to its own, always in the same order.
+template <bool GU, int S>
 __global__ void __launch_bounds__(kWideThreads, 1)
 wide_kernel(const __grid_constant__ CUtensorMap tmx, const __grid_constant__ CUtensorMap tmw,
             const __grid_constant__ CUtensorMap tmo, const BlockArgs a) {
-    using W = Wide<GU>;
+    using W = Wide<GU, S>;
+    constexpr bool SPLIT = S > 1;
     constexpr int kWideStages = W::kStages;
     extern __shared__ uint8_t smem_raw[];
     const uint32_t base = smem_u32(smem_raw);
     uint8_t *smem = smem_raw + (((base + 1023u) & ~1023u) - base);
     WideBars *bar = reinterpret_cast<WideBars *>(smem + kWideStages * kWideStage + W::kOut);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const uint32_t rank = cluster_rank();
+    const uint32_t place = cluster_rank(), rank = SPLIT ? place & 1u : place, first = SPLIT ? place & ~1u : 0u;
+    const auto leader = [&](const void *p) { return SPLIT ? cluster_addr(smem_u32(p), (int)first) : leader_addr(p); };
     constexpr int kCols = GU ? 128 : 256;     // columns of the output a tile
 
     if (threadIdx.x == 0) {
@@ -236,9 +268,16 @@ wide_kernel(const __grid_constant__ CUtensorMap tmx, const __grid_constant__ CUt
 
     const uint32_t own_tmem = bar->tmem;
     uint32_t tmem;
-    asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(tmem) : "r"(leader_addr(&bar->tmem)));
-    const int slot = blockIdx.x >> 1, slots = gridDim.x >> 1;
+    asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(tmem) : "r"(leader(&bar->tmem)));
+    const int slot = (int)blockIdx.x / (2 * S), slots = (int)gridDim.x / (2 * S);
     const int num_m = (a.M + 255) / 256, num_n = (a.N + kCols - 1) / kCols, tiles = num_m * num_n, nkb = a.nkb;
+    const int share = (int)(place >> 1), k0 = SPLIT ? share * nkb / S : 0, k1 = SPLIT ? (share + 1) * nkb / S : nkb;
+    // Where a tile's sums meet: all warps come by twice, before they are read and, where another tile's follow, after.
+    const auto meet = [&](int t) {
+        __syncwarp();
+        cluster_sync();
+        if (t + slots < tiles) cluster_sync();
+    };
     const WaitCtx w{a.limit_ns, &bar->abort, a.status};
 
     // 4 x 32 x 56 + 8 x 32 x 224 registers of the 384 x 168 launched
@@ -247,17 +286,17 @@ wide_kernel(const __grid_constant__ CUtensorMap tmx, const __grid_constant__ CUt
         if (warp == 0) {
             uint32_t s = 0, ph = 0, filled = 0, last = 0;
             bool ok = true;
-            for (int t = slot; t < tiles && ok; t += slots) {
+            for (int t = slot; t < tiles && (SPLIT || ok); t += slots) {
                 const WideTile o = wide_tile(t, num_m, num_n, a.band);
                 const int row = o.mb * 256 + (int)rank * 128;
                 const int wrow = GU ? (rank ? a.N : 0) + o.nb * 128 : o.nb * 256 + (int)rank * 128;
-                for (int kb = 0; kb < nkb; ++kb) {
+                for (int kb = k0; kb < k1 && (!SPLIT || ok); ++kb) {
                     if (!mbar_wait(&bar->done[s], ph ^ 1u, w, kSiteTmaEmpty)) {
                         ok = false;
                         break;
                     }
                     uint8_t *st = smem + s * kWideStage;
-                    const uint32_t full = leader_addr(&bar->full[s]);
+                    const uint32_t full = leader(&bar->full[s]);
                     if (elect_one()) {
                         if (rank == 0) mbar_arrive_expect_tx(&bar->full[s], 2 * kWideStage);
                         tma_load_2d_pair(st, &tmx, kb * 128, row, full);
@@ -271,6 +310,7 @@ wide_kernel(const __grid_constant__ CUtensorMap tmx, const __grid_constant__ CUt
                         ph ^= 1u;
                     }
                 }
+                if (SPLIT) meet(t);
             }
             // every copy of the pair has landed (they are counted on the leader's barriers) before a CTA ends
             if (rank == 0)
@@ -278,39 +318,47 @@ wide_kernel(const __grid_constant__ CUtensorMap tmx, const __grid_constant__ CUt
                     if (filled >> i & 1u) mbar_wait_drain(&bar->full[i], last >> i & 1u, 200000000ull, a.status);
         } else if (warp == 1 && rank == 0) {
             constexpr uint32_t idesc = idesc_f32acc(0, 0, 256, 256);
-            if (a.force_timeout == 1 || (a.force_timeout >= 2 && a.force_timeout - 2 == slot)) {
-                mbar_wait(&bar->never, 0, w, kSiteMmaFull);
-            } else {
+            const bool forced = a.force_timeout == 1 || (a.force_timeout >= 2 && a.force_timeout - 2 == slot);
+            if (forced) mbar_wait(&bar->never, 0, w, kSiteMmaFull);
+            if (SPLIT || !forced) {
                 uint32_t s = 0, ph = 0, acc = 0, aph = 0;
-                const int64_t steps = (int64_t)((tiles - 1 - slot) / slots + 1) * nkb;
-                bool ready = false;
-                for (int64_t i = 0; i < steps; ++i) {
-                    // (the buffer comes back last)
-                    if (!ready && (!mbar_wait(&bar->full[s], ph, w, kSiteMmaFull) ||
-                                   !mbar_wait(&bar->acc_empty[acc], aph ^ 1u, w, kSiteMmaAccEmpty)))
-                        break;
-                    tc_fence_after();
-                    const uint32_t sa = smem_u32(smem + s * kWideStage), d = tmem + acc * 256, s0 = s;
-                    const uint64_t da = sdesc_sw128(sa), db = sdesc_sw128(sa + kBoxBytes);
-                    if (++s == kWideStages) {
-                        s = 0;
-                        ph ^= 1u;
-                    }
-                    acc ^= 1u;
-                    if (!acc) aph ^= 1u;
-                    const bool e0 = mbar_done(&bar->acc_empty[acc], aph ^ 1u), e1 = mbar_done(&bar->full[s], ph);
-                    if (elect_one()) {
+                const int64_t steps = SPLIT ? k1 - k0 : (int64_t)((tiles - 1 - slot) / slots + 1) * nkb;
+                bool ready = false, ok = !forced;
+                for (int t = slot; t < (SPLIT ? tiles : slot + 1); t += SPLIT ? slots : 1) {
+                    for (int64_t i = 0; i < steps && (!SPLIT || ok); ++i) {
+                        // (the buffer comes back last)
+                        if (!ready && (!mbar_wait(&bar->full[s], ph, w, kSiteMmaFull) ||
+                                       !mbar_wait(&bar->acc_empty[acc], aph ^ 1u, w, kSiteMmaAccEmpty))) {
+                            ok = false;
+                            break;
+                        }
+                        tc_fence_after();
+                        const uint32_t sa = smem_u32(smem + s * kWideStage), d = tmem + acc * 256, s0 = s;
+                        const uint64_t da = sdesc_sw128(sa), db = sdesc_sw128(sa + kBoxBytes);
+                        if (++s == kWideStages) {
+                            s = 0;
+                            ph ^= 1u;
+                        }
+                        acc ^= 1u;
+                        if (!acc) aph ^= 1u;
+                        const bool e0 = mbar_done(&bar->acc_empty[acc], aph ^ 1u), e1 = mbar_done(&bar->full[s], ph);
+                        if (elect_one()) {
 #pragma unroll
-                        for (int k = 0; k < 4; ++k) mma2_f8(d, da + 2 * k, db + 2 * k, idesc, k > 0);
-                        mma2_commit_both(&bar->done[s0]);
+                            for (int k = 0; k < 4; ++k) mma2_f8(d, da + 2 * k, db + 2 * k, idesc, k > 0);
+                            if (SPLIT) commit_pair(&bar->done[s0], first);
+                            else mma2_commit_both(&bar->done[s0]);
+                        }
+                        __syncwarp();
+                        ready = e0 && e1;
                     }
-                    __syncwarp();
-                    ready = e0 && e1;
+                    if (SPLIT) meet(t);
                 }
             }
             if (elect_one()) mma2_commit_local(&bar->drain);
             __syncwarp();
             mbar_wait_drain(&bar->drain, 0, 200000000ull, a.status);
+        } else if (SPLIT) {
+            for (int t = slot; t < tiles; t += slots) meet(t);
         }
     } else {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 224;");
@@ -321,7 +369,7 @@ wide_kernel(const __grid_constant__ CUtensorMap tmx, const __grid_constant__ CUt
         const auto piece = [&](int j) {
             return GU ? (j / (kPieces / 2)) * 128 + part * (kSums / 2) + (j % (kPieces / 2)) * 32 : part * kSums + 32 * j;
         };
-        uint8_t *box = smem + kWideStages * kWideStage + (warp - 4) * W::kBoxes * kOutBox;
+        uint8_t *box0 = smem + kWideStages * kWideStage, *box = box0 + (warp - 4) * W::kBoxes * kOutBox;
         uint32_t acc = 0, s = 0, ph = 0;
         bool ok = true;
         int row = 0, n0 = 0;
@@ -335,18 +383,18 @@ wide_kernel(const __grid_constant__ CUtensorMap tmx, const __grid_constant__ CUt
             sx = a.sx + (int64_t)min(row + lane, a.M - 1) * nkb;
             sw0 = a.sw + (int64_t)(GU ? o.nb : min(n0 / 128, (a.N - 1) / 128)) * nkb;
             sw1 = GU ? sw0 + (int64_t)(a.N / 128) * nkb : sw0;
-            x = __ldg(sx);
-            w0 = __ldg(sw0);
-            w1 = GU ? __ldg(sw1) : 0.0f;
+            x = __ldg(sx + k0);
+            w0 = __ldg(sw0 + k0);
+            w1 = GU ? __ldg(sw1 + k0) : 0.0f;
         };
         if (slot < tiles) enter(slot);
-        for (int t = slot; t < tiles && ok; t += slots) {
+        for (int t = slot; t < tiles && (SPLIT || ok); t += slots) {
             uint64_t sum[kSums / 2];
 #pragma unroll
             for (int i = 0; i < kSums / 2; ++i) sum[i] = 0;
-            for (int kb = 0; kb < nkb; ++kb) {
+            for (int kb = k0; kb < k1 && (!SPLIT || ok); ++kb) {
                 const float f0 = x * w0, f1 = GU ? x * w1 : f0;
-                const int next = min(kb + 1, nkb - 1);      // its scales are on their way meanwhile
+                const int next = min(kb + 1, k1 - 1);      // its scales are on their way meanwhile
                 x = __ldg(sx + next);
                 w0 = __ldg(sw0 + next);
                 if (GU) w1 = __ldg(sw1 + next);
@@ -369,7 +417,7 @@ wide_kernel(const __grid_constant__ CUtensorMap tmx, const __grid_constant__ CUt
                         // are held, nothing else passes between the two.)
                         tc_fence_before();
                         __syncwarp();
-                        if (lane == 0) arrive_cluster_relaxed(leader_addr(&bar->acc_empty[acc]));
+                        if (lane == 0) arrive_cluster_relaxed(leader(&bar->acc_empty[acc]));
                     }
                     const float f = (GU && h) ? f1 : f0;
                     const uint64_t ff = pack_f2(f, f);
@@ -386,6 +434,82 @@ wide_kernel(const __grid_constant__ CUtensorMap tmx, const __grid_constant__ CUt
                     s = 0;
                     ph ^= 1u;
                 }
+            }
+            if constexpr (SPLIT) {
+                constexpr int kMine = W::kMine, kUnits = kMine / 4, kCount = GU ? kMine / 2 : kMine;
+                // unit u of four columns of pair j's: consecutive ones, or first gate's, then up's
+                const auto unit = [&](int j, int u) {
+                    return GU ? (u / (kUnits / 2)) * (kSums / 2) + j * (kMine / 2) + u % (kUnits / 2) * 4 : j * kMine + 4 * u;
+                };
+                const int share = (int)(cluster_rank() >> 1), rank = (int)(cluster_rank() & 1u);   // (read again: no registers to spare)
+                const uint32_t in = smem_u32(box0) + (uint32_t)((warp - 4) * kUnits * 512 + lane * 16);
+#pragma unroll
+                for (int j = 0; j < S; ++j)
+                    if (j != share && ok) {
+                        const uint32_t to = cluster_addr(in + (uint32_t)((share - (share > j)) * kWideEpi * kUnits * 512), 2 * j + (int)rank);
+#pragma unroll
+                        for (int u = 0; u < kUnits; ++u) st_cluster(to + u * 512, sum[unit(j, u) / 2], sum[unit(j, u) / 2 + 1]);
+                    }
+                __syncwarp();
+                cluster_sync();
+                // (the sums stay in their registers: a copy of this for each pair)
+#pragma unroll
+                for (int j = 0; j < S; ++j) {
+                    if (j != share || bar->abort) continue;
+#pragma unroll
+                    for (int q = 0; q < S - 1; ++q)
+#pragma unroll
+                        for (int u = 0; u < kUnits; ++u) {
+                            uint64_t v0, v1;
+                            asm volatile("ld.shared.v2.b64 {%0, %1}, [%2];" : "=l"(v0), "=l"(v1) : "r"(in + (q * kWideEpi * kUnits + u) * 512) : "memory");
+                            uint64_t &o0 = sum[unit(j, u) / 2], &o1 = sum[unit(j, u) / 2 + 1];
+                            o0 = add_f2(o0, v0);
+                            o1 = add_f2(o1, v1);
+                        }
+                    const int m = row + lane, n = n0 + j * kCount;
+                    // the sums of two columns from c on: consecutive ones, or of the gate and, kSums / 2 on, of up
+                    const auto at = [&](int c) -> uint64_t & { return sum[(j * kCount + c) / 2]; };
+                    if (a.bias) {
+#pragma unroll
+                        for (int c = 0; c < kCount; c += 2)
+                            if (n + c < a.N) {
+                                const uint32_t *b = reinterpret_cast<const uint32_t *>(a.bias + n + c);
+                                uint32_t bb = __ldg(b);
+                                at(c) = add_f2(at(c), pack_f2(__uint_as_float(bb << 16), __uint_as_float(bb & 0xFFFF0000u)));
+                                if (GU) {
+                                    bb = __ldg(b + a.N / 2);
+                                    at(c + kSums / 2) = add_f2(at(c + kSums / 2), pack_f2(__uint_as_float(bb << 16), __uint_as_float(bb & 0xFFFF0000u)));
+                                }
+                            }
+                    }
+                    if (m < a.M) {
+                        uint16_t *y = a.out + (int64_t)m * a.ldo + n;
+#pragma unroll
+                        for (int c = 0; c < kCount; c += 16) {
+                            uint32_t p[8];
+#pragma unroll
+                            for (int i = 0; i < 8; ++i) {
+                                float v0, v1;
+                                unpack_f2(GU ? silu_mul2(at(c + 2 * i), at((GU ? kSums / 2 : 0) + c + 2 * i)) : at(c + 2 * i), v0, v1);
+                                p[i] = pack_bf16x2(v0, v1);
+                            }
+                            if (a.whole && n + c + 16 <= a.N) {
+                                asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};"
+                                             ::"l"(y + c), "r"(p[0]), "r"(p[1]), "r"(p[2]), "r"(p[3]), "r"(p[4]), "r"(p[5]), "r"(p[6]), "r"(p[7])
+                                             : "memory");
+                            } else {
+                                if (n + c < a.N) *reinterpret_cast<uint4 *>(y + c) = make_uint4(p[0], p[1], p[2], p[3]);
+                                if (n + c + 8 < a.N) *reinterpret_cast<uint4 *>(y + c + 8) = make_uint4(p[4], p[5], p[6], p[7]);
+                            }
+                        }
+                    }
+                }
+                if (t + slots < tiles) {
+                    enter(t + slots);
+                    __syncwarp();
+                    cluster_sync();
+                }
+                continue;
             }
             if (!ok) break;
             const int trow = row, tn = n0;
@@ -484,17 +608,6 @@ struct FewBars {
     int abort;
 };
 static_assert(sizeof(FewBars) <= 512, "barrier block");
-
-__device__ __forceinline__ float ld_cluster(uint32_t at) {
-    float v;
-    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(at) : "memory");
-    return v;
-}
-__device__ __forceinline__ uint32_t cluster_addr(uint32_t local, int rank) {
-    uint32_t at;
-    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"(local), "r"(rank));
-    return at;
-}
 
 template <int T, bool GU>
 __global__ void __launch_bounds__(Few<T, GU>::kThreads, Few<T, GU>::kPerSm)
@@ -747,51 +860,6 @@ int maps(CUtensorMap &tx, CUtensorMap &tw, const void *qx, const void *qw, int64
                                         CU_TENSOR_MAP_SWIZZLE_128B);
 }
 
-template <bool GU>
-int launch_wide(const void *qx, const void *qw, int64_t K, BlockArgs a, int sms, cudaStream_t st) {
-    constexpr int kWideSmem = Wide<GU>::kSmem;
-    static SmemOptIn opt;
-    static std::atomic<int> most{0};
-    auto kern = wide_kernel<GU>;
-    cudaError_t e = opt.set(reinterpret_cast<const void *>(kern), kWideSmem);
-    if (e != cudaSuccess) return internal_cuda_error(e, "block linear smem attribute");
-    int pairs = most.load(std::memory_order_relaxed);
-    if (pairs == 0) {
-        // pairs that the device holds at once, whatever this call's SM budget
-        cudaLaunchConfig_t cfg = {};
-        cudaLaunchAttribute attr[1];
-        attr[0].id = cudaLaunchAttributeClusterDimension;
-        attr[0].val.clusterDim.x = 2;
-        attr[0].val.clusterDim.y = 1;
-        attr[0].val.clusterDim.z = 1;
-        int dev = 0, all = sms;
-        if (cudaGetDevice(&dev) == cudaSuccess) cudaDeviceGetAttribute(&all, cudaDevAttrMultiProcessorCount, dev);
-        cfg.gridDim = dim3((unsigned)(all & ~1), 1, 1);
-        cfg.blockDim = dim3(kWideThreads, 1, 1);
-        cfg.dynamicSmemBytes = kWideSmem;
-        cfg.attrs = attr;
-        cfg.numAttrs = 1;
-        if (cudaOccupancyMaxActiveClusters(&pairs, kern, &cfg) != cudaSuccess || pairs < 1) pairs = std::max(1, all / 2);
-        most.store(pairs, std::memory_order_relaxed);
-    }
-    pairs = std::max(1, std::min(pairs, sms / 2));
-    const int num_m = (a.M + 255) / 256, num_n = GU ? a.N / 128 : (a.N + 255) / 256;
-    // bands whose rows of x take up to 24 MB, so that they stay in L2 while the weight passes; of even size
-    const int64_t per = 256 * K, fit = std::max<int64_t>(1, ((int64_t)24 << 20) / per);
-    const int bands = (int)((num_m + fit - 1) / fit);
-    a.band = (num_m + bands - 1) / bands;
-    CUtensorMap tx, tw;
-    const int rc = maps(tx, tw, qx, qw, a.M, (GU ? 2 : 1) * (int64_t)a.N, K, 128);
-    if (rc) return rc;
-    CUtensorMap to;
-    const int rco = internal_make_tmap(&to, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, a.out, (uint64_t)a.N, (uint64_t)a.M, (uint64_t)a.ldo * 2,
-                                       64, 32, CU_TENSOR_MAP_SWIZZLE_128B);
-    if (rco) return rco;
-    const int tiles = num_m * num_n;
-    e = launch_kernel(kern, dim3((unsigned)(2 * std::min(tiles, pairs))), dim3(kWideThreads), kWideSmem, st, 2, true, tx, tw, to, a);
-    return e == cudaSuccess ? CLEF_OK : internal_cuda_error(e, "block linear launch");
-}
-
 // Clusters of `split` CTAs that the device holds at once where an SM holds one CTA: how many fit into its groups of
 // SMs (asked once for each size).
 int clusters_at_once(int split) {
@@ -818,6 +886,34 @@ int clusters_at_once(int split) {
         known[split].store(n, std::memory_order_relaxed);
     }
     return n;
+}
+
+template <bool GU, int S>
+int launch_wide(const void *qx, const void *qw, int64_t K, BlockArgs a, int sms, cudaStream_t st) {
+    constexpr int kWideSmem = Wide<GU, S>::kSmem;
+    static SmemOptIn opt;
+    auto kern = wide_kernel<GU, S>;
+    cudaError_t e = opt.set(reinterpret_cast<const void *>(kern), kWideSmem);
+    if (e != cudaSuccess) return internal_cuda_error(e, "block linear smem attribute");
+    // clusters that the device holds at once, or this call's SM budget
+    const int clusters = std::max(1, std::min(clusters_at_once(2 * S), sms / (2 * S)));
+    const int num_m = (a.M + 255) / 256, num_n = GU ? a.N / 128 : (a.N + 255) / 256;
+    // bands whose rows of x take up to 24 MB, so that they stay in L2 while the weight passes; of even size
+    const int64_t per = 256 * K, fit = std::max<int64_t>(1, ((int64_t)24 << 20) / per);
+    const int bands = (int)((num_m + fit - 1) / fit);
+    a.band = (num_m + bands - 1) / bands;
+    a.whole = !kv_misaligned(a.out, 32) && a.ldo % 16 == 0;
+    CUtensorMap tx, tw;
+    const int rc = maps(tx, tw, qx, qw, a.M, (GU ? 2 : 1) * (int64_t)a.N, K, 128);
+    if (rc) return rc;
+    CUtensorMap to;
+    const int rco = internal_make_tmap(&to, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, a.out, (uint64_t)a.N, (uint64_t)a.M, (uint64_t)a.ldo * 2,
+                                       64, 32, CU_TENSOR_MAP_SWIZZLE_128B);
+    if (rco) return rco;
+    const int tiles = num_m * num_n;
+    e = launch_kernel(kern, dim3((unsigned)(2 * S * std::min(tiles, clusters))), dim3(kWideThreads), kWideSmem, st, 2 * S, true,
+                      tx, tw, to, a);
+    return e == cudaSuccess ? CLEF_OK : internal_cuda_error(e, "block linear launch");
 }
 
 struct FewPlan {
@@ -870,6 +966,13 @@ int launch_block(const void *qx, const void *qw, int64_t K, const BlockArgs &a, 
     const int64_t pairs = std::max(1, all_sms / 2), tiles = (int64_t)((a.M + 255) / 256) * (GU ? a.N / 128 : (a.N + 255) / 256);
     const double weight = (GU ? 2.0 : 1.0) * a.N * (double)K;
     FewPlan best{0, 1, 4.0 + std::max((double)((tiles + pairs - 1) / pairs) * a.nkb * 0.38, weight / 4.5e6)};
+    // pairs that share a tile's K: clusters that run at once, each pair with four k-blocks or more.  (768 x 5,120 x 1,024
+    // 18.4 us by one pair, 13.7 by two, 12.6 by four; 1,024 x 2,048 x 1,024 10.0, 9.4 and 10.1; 768 x 1,536 x 768 8.5
+    // and 8.7.)
+    for (int n = 2; n <= 4 && 4 * n <= a.nkb && tiles * n <= pairs && tiles <= clusters_at_once(2 * n); n *= 2) {
+        const double us = (n == 2 ? 6.7 : 9.5) + std::max((a.nkb + n - 1) / n * 0.38, weight / 4.5e6);
+        if (us < best.us) best = {0, n, us};
+    }
     if (a.M <= 4096) {
         for (const FewPlan &p : {plan_few<16, GU>(a, all_sms), plan_few<32, GU>(a, all_sms), plan_few<64, GU>(a, all_sms)})
             if (p.us < best.us) best = p;
@@ -885,7 +988,10 @@ int launch_block(const void *qx, const void *qw, int64_t K, const BlockArgs &a, 
         case 128:
             if constexpr (!GU) return launch_few<128, GU>(qx, qw, K, a, best.split, sms, all_sms, st);
             [[fallthrough]];
-        default: return launch_wide<GU>(qx, qw, K, a, sms, st);
+        default:
+            return best.split == 4 ? launch_wide<GU, 4>(qx, qw, K, a, sms, st)
+                 : best.split == 2 ? launch_wide<GU, 2>(qx, qw, K, a, sms, st)
+                                   : launch_wide<GU, 1>(qx, qw, K, a, sms, st);
     }
 }
 
@@ -920,6 +1026,7 @@ int block_call(bool gu, const void *qx, const float *sx, const void *qw, const f
     a.out = static_cast<uint16_t *>(out);
     a.ldo = ldo;
     a.band = a.split = a.tiles_m = 1;
+    a.whole = false;
     a.status = status;
     a.limit_ns = internal_wait_limit(&a.force_timeout);
     const cudaStream_t st = static_cast<cudaStream_t>(stream);
