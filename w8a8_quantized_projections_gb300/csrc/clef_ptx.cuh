@@ -111,6 +111,14 @@ __device__ __forceinline__ bool mbar_wait(uint64_t *bar, uint32_t parity, const 
     }
 }
 
+// mbar_wait for a whole warp: the same answer in every lane, so that the warp
+// stays together for the aligned instructions that follow.  (Each lane polls the
+// barrier, the clock and the abort flag for itself: where a wait runs out, some
+// may see the phase complete and others give up.)
+__device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t parity, const WaitCtx &w, unsigned int site) {
+    return __all_sync(0xFFFFFFFFu, mbar_wait(bar, parity, w, site));
+}
+
 // ---------------------------------------------------------------- TMA
 
 __device__ __forceinline__ void tma_prefetch_desc(const CUtensorMap *m) {

@@ -115,6 +115,19 @@ __device__ __forceinline__ uint64_t silu_mul2(uint64_t g, uint64_t u) {
     return mul_f2(mul_f2(mul_f2(g, pack_f2(0.25f, 0.25f)), pack_f2(a, b)), u);
 }
 
+constexpr unsigned kWarp = 0xFFFFFFFFu;
+
+// Waits of a whole warp.  Each lane polls for itself, so that where a wait runs out some lanes may see the phase complete
+// and others give up; the instructions around (elect.sync, TMEM loads, cluster barriers) want them together.  So no lane
+// leaves a loop on its own answer: it keeps it (`ok`, false from then on), the elected lane issues while its own holds,
+// sums of the others go on and are not used, and a tile's end votes.  (24,032 x 5,120 x 6,144 and 1,502 x 5,120 x 17,408
+// gate/up within 0.5% of lanes that leave, few rows 0.1 us slower; a vote beside each wait costs 2-3% of both.)
+
+// mbar_wait for lanes that stay: once a wait of this CTA has run out no further one is sat through.
+__device__ __forceinline__ bool stay_wait(uint64_t *bar, uint32_t parity, const WaitCtx &w, unsigned int site) {
+    return mbar_try_wait(smem_u32(bar), parity) || (!*w.abort && mbar_wait(bar, parity, w, site));
+}
+
 // One lane of a whole warp.  The warps that issue copies and MMAs run with all lanes and elect one for each k-block:
 // what they count then stays in uniform registers, which those instructions take their operands from.
 __device__ __forceinline__ bool elect_one() {
@@ -290,27 +303,27 @@ wide_kernel(const __grid_constant__ CUtensorMap tmx, const __grid_constant__ CUt
                 const WideTile o = wide_tile(t, num_m, num_n, a.band);
                 const int row = o.mb * 256 + (int)rank * 128;
                 const int wrow = GU ? (rank ? a.N : 0) + o.nb * 128 : o.nb * 256 + (int)rank * 128;
-                for (int kb = k0; kb < k1 && (!SPLIT || ok); ++kb) {
-                    if (!mbar_wait(&bar->done[s], ph ^ 1u, w, kSiteTmaEmpty)) {
-                        ok = false;
-                        break;
-                    }
+                for (int kb = k0; kb < k1; ++kb) {
+                    ok = ok && mbar_wait(&bar->done[s], ph ^ 1u, w, kSiteTmaEmpty);
                     uint8_t *st = smem + s * kWideStage;
                     const uint32_t full = leader(&bar->full[s]);
-                    if (elect_one()) {
+                    if (elect_one() && ok) {
                         if (rank == 0) mbar_arrive_expect_tx(&bar->full[s], 2 * kWideStage);
                         tma_load_2d_pair(st, &tmx, kb * 128, row, full);
                         tma_load_2d_pair(st + kBoxBytes, &tmw, kb * 128, wrow, full);
                     }
                     __syncwarp();
-                    filled |= 1u << s;
-                    last = (last & ~(1u << s)) | ph << s;
+                    if (ok) {
+                        filled |= 1u << s;
+                        last = (last & ~(1u << s)) | ph << s;
+                    }
                     if (++s == kWideStages) {
                         s = 0;
                         ph ^= 1u;
                     }
                 }
                 if (SPLIT) meet(t);
+                else ok = __all_sync(kWarp, ok);
             }
             // every copy of the pair has landed (they are counted on the leader's barriers) before a CTA ends
             if (rank == 0)
@@ -319,19 +332,16 @@ wide_kernel(const __grid_constant__ CUtensorMap tmx, const __grid_constant__ CUt
         } else if (warp == 1 && rank == 0) {
             constexpr uint32_t idesc = idesc_f32acc(0, 0, 256, 256);
             const bool forced = a.force_timeout == 1 || (a.force_timeout >= 2 && a.force_timeout - 2 == slot);
-            if (forced) mbar_wait(&bar->never, 0, w, kSiteMmaFull);
+            if (forced) warp_wait(&bar->never, 0, w, kSiteMmaFull);
             if (SPLIT || !forced) {
                 uint32_t s = 0, ph = 0, acc = 0, aph = 0;
                 const int64_t steps = SPLIT ? k1 - k0 : (int64_t)((tiles - 1 - slot) / slots + 1) * nkb;
                 bool ready = false, ok = !forced;
                 for (int t = slot; t < (SPLIT ? tiles : slot + 1); t += SPLIT ? slots : 1) {
-                    for (int64_t i = 0; i < steps && (!SPLIT || ok); ++i) {
+                    for (int64_t i = 0; i < steps; ++i) {
                         // (the buffer comes back last)
-                        if (!ready && (!mbar_wait(&bar->full[s], ph, w, kSiteMmaFull) ||
-                                       !mbar_wait(&bar->acc_empty[acc], aph ^ 1u, w, kSiteMmaAccEmpty))) {
-                            ok = false;
-                            break;
-                        }
+                        ok = ok && (ready || (mbar_wait(&bar->full[s], ph, w, kSiteMmaFull) &&
+                                              mbar_wait(&bar->acc_empty[acc], aph ^ 1u, w, kSiteMmaAccEmpty)));
                         tc_fence_after();
                         const uint32_t sa = smem_u32(smem + s * kWideStage), d = tmem + acc * 256, s0 = s;
                         const uint64_t da = sdesc_sw128(sa), db = sdesc_sw128(sa + kBoxBytes);
@@ -342,7 +352,7 @@ wide_kernel(const __grid_constant__ CUtensorMap tmx, const __grid_constant__ CUt
                         acc ^= 1u;
                         if (!acc) aph ^= 1u;
                         const bool e0 = mbar_done(&bar->acc_empty[acc], aph ^ 1u), e1 = mbar_done(&bar->full[s], ph);
-                        if (elect_one()) {
+                        if (elect_one() && ok) {
 #pragma unroll
                             for (int k = 0; k < 4; ++k) mma2_f8(d, da + 2 * k, db + 2 * k, idesc, k > 0);
                             if (SPLIT) commit_pair(&bar->done[s0], first);
@@ -392,16 +402,13 @@ wide_kernel(const __grid_constant__ CUtensorMap tmx, const __grid_constant__ CUt
             uint64_t sum[kSums / 2];
 #pragma unroll
             for (int i = 0; i < kSums / 2; ++i) sum[i] = 0;
-            for (int kb = k0; kb < k1 && (!SPLIT || ok); ++kb) {
+            for (int kb = k0; kb < k1; ++kb) {
                 const float f0 = x * w0, f1 = GU ? x * w1 : f0;
                 const int next = min(kb + 1, k1 - 1);      // its scales are on their way meanwhile
                 x = __ldg(sx + next);
                 w0 = __ldg(sw0 + next);
                 if (GU) w1 = __ldg(sw1 + next);
-                if (!mbar_wait(&bar->done[s], ph, w, kSiteEpiAccFull)) {
-                    ok = false;
-                    break;
-                }
+                if (!stay_wait(&bar->done[s], ph, w, kSiteEpiAccFull)) ok = false;
                 tc_fence_after();
                 const uint32_t at = tmem + acc * 256 + lanes;
                 constexpr int kAtOnce = kPieces / 2;
@@ -417,7 +424,7 @@ wide_kernel(const __grid_constant__ CUtensorMap tmx, const __grid_constant__ CUt
                         // are held, nothing else passes between the two.)
                         tc_fence_before();
                         __syncwarp();
-                        if (lane == 0) arrive_cluster_relaxed(leader(&bar->acc_empty[acc]));
+                        if (lane == 0 && ok) arrive_cluster_relaxed(leader(&bar->acc_empty[acc]));
                     }
                     const float f = (GU && h) ? f1 : f0;
                     const uint64_t ff = pack_f2(f, f);
@@ -511,7 +518,7 @@ wide_kernel(const __grid_constant__ CUtensorMap tmx, const __grid_constant__ CUt
                 }
                 continue;
             }
-            if (!ok) break;
+            if (!(ok = __all_sync(kWarp, ok))) break;
             const int trow = row, tn = n0;
             if (t + slots < tiles) enter(t + slots);
             if (a.bias) {
@@ -555,6 +562,7 @@ wide_kernel(const __grid_constant__ CUtensorMap tmx, const __grid_constant__ CUt
         }
         if (lane == 0) bulk_wait_all();     // the copies have read the boxes before the CTA ends
     }
+    __syncwarp();
     pdl_launch_dependents();
     tc_fence_before();
     __syncthreads();
@@ -653,23 +661,26 @@ few_kernel(const __grid_constant__ CUtensorMap tmx, const __grid_constant__ CUte
     // Under a budget of SMs a cluster takes one tile after another; otherwise there is a cluster for each.  The
     // rings go on where they are: s, ph of the stages, and `done` k-blocks of the TMEM buffers before this tile.
     uint32_t s = 0, ph = 0, done = 0, filled = 0, last = 0;
+    bool ok = true;
 
     for (int both = (int)blockIdx.x / split; both < tiles; both += clusters, done += (uint32_t)(k1 - k0)) {
         // tiles of one part of the weight side by side, so that it is read from memory once
         const int tile = both / a.tiles_m, n0 = tile * 128, m0 = (both - tile * a.tiles_m) * T;
         if (warp == 0) {
             for (int kb = k0; kb < k1; ++kb) {
-                if (!mbar_wait(&bar->empty[s], ph ^ 1u, w, kSiteTmaEmpty)) break;
+                ok = ok && mbar_wait(&bar->empty[s], ph ^ 1u, w, kSiteTmaEmpty);
                 uint8_t *st = smem + s * F::kStage;
-                if (elect_one()) {
+                if (elect_one() && ok) {
                     mbar_arrive_expect_tx(&bar->full[s], F::kStage);
                     tma_load_2d(st, &tmw, kb * 128, n0, &bar->full[s]);
                     if (GU) tma_load_2d(st + kBoxBytes, &tmw, kb * 128, a.N + n0, &bar->full[s]);
                     tma_load_2d(st + F::kTiles * kBoxBytes, &tmx, kb * 128, m0, &bar->full[s]);
                 }
                 __syncwarp();
-                filled |= 1u << s;
-                last = (last & ~(1u << s)) | ph << s;
+                if (ok) {
+                    filled |= 1u << s;
+                    last = (last & ~(1u << s)) | ph << s;
+                }
                 if (++s == F::kStages) {
                     s = 0;
                     ph ^= 1u;
@@ -678,14 +689,13 @@ few_kernel(const __grid_constant__ CUtensorMap tmx, const __grid_constant__ CUte
         } else if (warp == 1) {
             constexpr uint32_t idesc = idesc_f32acc(0, 0, 128, T);
             if (a.force_timeout == 1 || (a.force_timeout >= 2 && a.force_timeout - 2 == (int)blockIdx.x)) {
-                mbar_wait(&bar->never, 0, w, kSiteMmaFull);
+                warp_wait(&bar->never, 0, w, kSiteMmaFull);
             } else {
                 bool ready = false;
                 for (uint32_t g = done; g != done + (uint32_t)(k1 - k0); ++g) {
                     const uint32_t acc = g % F::kBufs, s0 = s;
-                    if (!ready && (!mbar_wait(&bar->full[s], ph, w, kSiteMmaFull) ||
-                                   !mbar_wait(&bar->acc_empty[acc], (g / F::kBufs & 1u) ^ 1u, w, kSiteMmaAccEmpty)))
-                        break;
+                    ok = ok && (ready || (mbar_wait(&bar->full[s], ph, w, kSiteMmaFull) &&
+                                          mbar_wait(&bar->acc_empty[acc], (g / F::kBufs & 1u) ^ 1u, w, kSiteMmaAccEmpty)));
                     tc_fence_after();
                     const uint32_t sa = smem_u32(smem + s * F::kStage), d = tmem + acc * F::kAcc;
                     const uint64_t da = sdesc_sw128(sa), db = sdesc_sw128(sa + F::kTiles * kBoxBytes);
@@ -695,7 +705,7 @@ few_kernel(const __grid_constant__ CUtensorMap tmx, const __grid_constant__ CUte
                     }
                     const bool e0 = mbar_done(&bar->acc_empty[(g + 1) % F::kBufs], ((g + 1) / F::kBufs & 1u) ^ 1u);
                     const bool e1 = mbar_done(&bar->full[s], ph);
-                    if (elect_one()) {
+                    if (elect_one() && ok) {
 #pragma unroll
                         for (int k = 0; k < 4; ++k)
 #pragma unroll
@@ -734,7 +744,6 @@ few_kernel(const __grid_constant__ CUtensorMap tmx, const __grid_constant__ CUte
             };
             if (k0 + set < k1) fetch(k0 + set);
             uint32_t flip = 0;
-            bool ok = true;
             for (int kb = k0 + set; kb < k1; kb += F::kSets) {
                 const uint32_t g = done + (uint32_t)(kb - k0), acc = g % F::kBufs;
                 float *f = mine + flip * F::kTiles * F::kCols;
@@ -748,10 +757,7 @@ few_kernel(const __grid_constant__ CUtensorMap tmx, const __grid_constant__ CUte
                 }
                 __syncwarp();
                 if (kb + F::kSets < k1) fetch(kb + F::kSets);
-                if (!mbar_wait(&bar->acc_full[acc], g / F::kBufs & 1u, w, kSiteEpiAccFull)) {
-                    ok = false;
-                    break;
-                }
+                if (!stay_wait(&bar->acc_full[acc], g / F::kBufs & 1u, w, kSiteEpiAccFull)) ok = false;
                 tc_fence_after();
                 const uint32_t at = tmem + acc * F::kAcc + lanes + c0;
                 constexpr int kPiece = F::kCols < 32 ? 16 : 32, kPieces = F::kTiles * F::kCols / kPiece;
@@ -770,7 +776,7 @@ few_kernel(const __grid_constant__ CUtensorMap tmx, const __grid_constant__ CUte
                     } else {
                         tc_fence_before();
                         __syncwarp();
-                        if (lane == 0) mbar_arrive(&bar->acc_empty[acc]);
+                        if (lane == 0 && ok) mbar_arrive(&bar->acc_empty[acc]);
                     }
                     const int h = j * kPiece / F::kCols, c = j * kPiece % F::kCols;
 #pragma unroll
@@ -841,6 +847,7 @@ few_kernel(const __grid_constant__ CUtensorMap tmx, const __grid_constant__ CUte
             __syncwarp();
             mbar_wait_drain(&bar->drain, 0, 200000000ull, a.status);
         }
+        __syncwarp();
         tc_fence_before();
         __syncthreads();
     }

@@ -984,12 +984,6 @@ __device__ __forceinline__ uint64_t pair_of(float x) {
     return r;
 }
 
-// mbar_wait for a whole warp: the same answer in every lane, so that the warp
-// stays together for the aligned instructions that follow.
-__device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t parity, const WaitCtx &w, unsigned int site) {
-    return __all_sync(0xFFFFFFFFu, mbar_wait(bar, parity, w, site));
-}
-
 struct TileBars {
     uint64_t q_full[2], k_full[2], k_empty[2], v_full[4], v_empty[4], s_full[2], p_half[2], p_full[2], o_done[2];
     uint64_t raw_full[2][4], raw_empty[2][4];      // of keys and of values
