@@ -77,6 +77,18 @@ def test_warps_of_the_block_linears_agree():
     assert text.count("ok = __all_sync(kWarp, ok)") == 2 and len(re.findall(r"elect_one\(\) && ok", text)) == 4
 
 
+def test_warps_of_the_gemms_agree():
+    """Converters and epilogue; copies and MMAs are issued by functions that one lane runs."""
+    text = code("gemm.cu")
+    converter = text[text.index("static __device__ void converter("):text.index("static __device__ void forwarder(")]
+    epilogue = text[text.index("static __device__ void epilogue_tiles("):text.index("__global__")]
+    assert unvoted(converter) == [] and unvoted(epilogue) == []
+    assert len(re.findall(r"__all_sync|\bwarp_wait\(|\bwarp_pair\(", converter + epilogue)) >= 11
+    assert re.search(r"bool warp_pair\([^{]*\{\s*return __all_sync\(0xFFFFFFFFu, wait_pair\(", text)
+    for role in ("G::producer(", "G::mma_issuer(", "G::forwarder("):
+        assert re.search(r"if \(lane == 0[^{]*\{[^{}]*$", text[:text.index(role)]), role
+
+
 def test_the_shared_helper_votes():
     helper = code("clef_ptx.cuh").split("bool warp_wait(")[1].split("}")[0]
     assert "__all_sync(0xFFFFFFFFu, mbar_wait(" in helper

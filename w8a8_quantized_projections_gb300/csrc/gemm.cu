@@ -473,6 +473,11 @@ struct Gemm {
                                                      unsigned int site) {
         return PAIR ? mbar_wait_cl(bar, parity, c.w, site) : mbar_wait(bar, parity, c.w, site);
     }
+    // The same for a whole warp, with one answer for all its lanes (as warp_wait).
+    static __device__ __forceinline__ bool warp_pair(uint64_t *bar, uint32_t parity, const Ctx &c,
+                                                     unsigned int site) {
+        return __all_sync(0xFFFFFFFFu, wait_pair(bar, parity, c, site));
+    }
 
     // Row of the weight operand that this CTA's B stage starts with.
     static __device__ __forceinline__ int b_row(const Ctx &c, const GemmArgs &a, int nb, int half) {
@@ -666,7 +671,10 @@ struct Gemm {
         int ktile = 0;     // and its tile's index in this CTA's tile sequence
         while (C::kLoraFused && kin >= per) { kin -= per; ++ktile; }
         for (int kidx = group; kidx < total; kidx += kG) {
-            if (!mbar_wait(&c.bar->raw_full[rs], rph, c.w, kSiteConvRaw)) return;
+            // (a warp's lanes go on, or give up, together)
+            if (!__all_sync(0xFFFFFFFFu, mbar_wait(&c.bar->raw_full[rs], rph, c.w, kSiteConvRaw) &&
+                                             wait_pair(&c.bar->empty[cs], cph ^ 1u, c, kSiteConvEmpty)))
+                return;
             if (C::kLoraFused && kin >= c.nkb) {
                 // a LoRA k-block: every warp of the group waits for the slot to be
                 // free, as for an INT8 k-block (each warp's successive waits on the
@@ -675,7 +683,6 @@ struct Gemm {
                 // copies the tile's t rows and B-factor rows (bf16, 64 of K,
                 // already in the MMA's swizzled layout) into it by TMA, waits for
                 // them to land, and arrives for the whole group
-                if (!wait_pair(&c.bar->empty[cs], cph ^ 1u, c, kSiteConvEmpty)) return;
                 bool ok = true;
                 if (ctid == 0) ok = lora_copy(c, a, cs, rs, ktile, kin);
                 __syncwarp();
@@ -688,7 +695,6 @@ struct Gemm {
                 while (kin >= per) { kin -= per; ++ktile; }
                 continue;
             }
-            if (!wait_pair(&c.bar->empty[cs], cph ^ 1u, c, kSiteConvEmpty)) return;
             const uint32_t src = raw_base + rs * C::kRawStage + src0;
             const uint32_t dst = stage_base + cs * C::kStage;
             constexpr int kBatch = kPer >= 4 ? 4 : kPer;  // loads in flight per thread
@@ -1307,7 +1313,7 @@ struct Gemm {
 #pragma unroll
                 for (int i = 0; i < C::kColsPerThread; ++i) tot[i] = 0;
                 for (int kb0 = sg.kb0; kb0 < sg.kb1; kb0 += c.chunk) {
-                    if (!wait_pair(&c.bar->acc_full[acc], aph, c, kSiteEpiAccFull)) return;
+                    if (!warp_pair(&c.bar->acc_full[acc], aph, c, kSiteEpiAccFull)) return;
                     tc_fence_after();
                     const uint32_t tbase = c.tmem + acc * BN + lane_off;
 #pragma unroll
@@ -1325,7 +1331,7 @@ struct Gemm {
                 // once the last piece to arrive has added the others)
                 if constexpr (C::kLoraFused) {
                     if (lora_kblocks(c, sg) > 0) {
-                        if (!wait_pair(&c.bar->acc_full[acc], aph, c, kSiteEpiAccFull)) return;
+                        if (!warp_pair(&c.bar->acc_full[acc], aph, c, kSiteEpiAccFull)) return;
                         tc_fence_after();
                         finish_row_lora(c, a, row, row_ok, nb, half, tot, c.tmem + acc * BN + lane_off, acc, lane);
                         if (++acc == (uint32_t)C::kAccBufs) { acc = 0; aph ^= 1u; }
@@ -1356,9 +1362,9 @@ struct Gemm {
                         ++yloads;
                     }
                 }
-                if (!wait_pair(&c.bar->acc_full[acc], aph, c, kSiteEpiAccFull)) return;
+                if (!warp_pair(&c.bar->acc_full[acc], aph, c, kSiteEpiAccFull)) return;
                 tc_fence_after();
-                if (!mbar_wait(&c.bar->ybar[b], (uint32_t)(yiter / C::kYBufs) & 1u, c.w, kSiteEpiAccFull)) return;
+                if (!warp_wait(&c.bar->ybar[b], (uint32_t)(yiter / C::kYBufs) & 1u, c.w, kSiteEpiAccFull)) return;
                 const uint32_t tbase = c.tmem + acc * BN + lane_off;
                 uint32_t vg[32], vu[32];
                 tmem_ld32(tbase + chunk_col(0, half), vg);
@@ -1370,9 +1376,10 @@ struct Gemm {
                 fence_proxy_async_smem();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&c.bar->epi_done);
-                if (e == 0 && lane == 0) {
-                    if (!mbar_wait(&c.bar->epi_done, (uint32_t)yiter & 1u, c.w, kSiteEpiAccFull)) return;
-                    h_tile_store(c, a, t, b);
+                if (e == 0) {
+                    // (the whole warp waits: it goes on, or gives up, together)
+                    if (!warp_wait(&c.bar->epi_done, (uint32_t)yiter & 1u, c.w, kSiteEpiAccFull)) return;
+                    if (lane == 0) h_tile_store(c, a, t, b);
                 }
                 ++yiter;
             } else if constexpr (EPI == kEpiAddBF16) {
@@ -1396,9 +1403,9 @@ struct Gemm {
                         ++yloads;
                     }
                 }
-                if (!wait_pair(&c.bar->acc_full[acc], aph, c, kSiteEpiAccFull)) return;
+                if (!warp_pair(&c.bar->acc_full[acc], aph, c, kSiteEpiAccFull)) return;
                 tc_fence_after();
-                if (!mbar_wait(&c.bar->ybar[b], (uint32_t)(yiter / C::kYBufs) & 1u, c.w, kSiteEpiAccFull)) return;
+                if (!warp_wait(&c.bar->ybar[b], (uint32_t)(yiter / C::kYBufs) & 1u, c.w, kSiteEpiAccFull)) return;
                 const uint32_t tbase = c.tmem + acc * BN + lane_off;
 #pragma unroll
                 for (int j = 0; j < C::kChunks32; ++j) {
@@ -1414,9 +1421,10 @@ struct Gemm {
                 fence_proxy_async_smem();   // the tile's smem writes, before the TMA store reads them
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&c.bar->epi_done);
-                if (e == 0 && lane == 0) {
-                    if (!mbar_wait(&c.bar->epi_done, (uint32_t)yiter & 1u, c.w, kSiteEpiAccFull)) return;
-                    y_tile_store(c, a, t, b);
+                if (e == 0) {
+                    // (the whole warp waits: it goes on, or gives up, together)
+                    if (!warp_wait(&c.bar->epi_done, (uint32_t)yiter & 1u, c.w, kSiteEpiAccFull)) return;
+                    if (lane == 0) y_tile_store(c, a, t, b);
                 }
                 ++yiter;
             } else if constexpr (C::kKSplit) {
@@ -1426,7 +1434,7 @@ struct Gemm {
                 // piece arriving last sums them all in K order
                 uint32_t v[C::kColsPerThread];
                 for (int kb0 = sg.kb0; kb0 < sg.kb1; kb0 += c.chunk) {
-                    if (!wait_pair(&c.bar->acc_full[acc], aph, c, kSiteEpiAccFull)) return;
+                    if (!warp_pair(&c.bar->acc_full[acc], aph, c, kSiteEpiAccFull)) return;
                     tc_fence_after();
                     const uint32_t tbase = c.tmem + acc * BN + lane_off;
                     if (kb0 == sg.kb0) {
@@ -1455,7 +1463,7 @@ struct Gemm {
                 }
                 if (whole) finish_row(a, row, row_ok, nb, half, v);
             } else {
-                if (!wait_pair(&c.bar->acc_full[acc], aph, c, kSiteEpiAccFull)) return;
+                if (!warp_pair(&c.bar->acc_full[acc], aph, c, kSiteEpiAccFull)) return;
                 tc_fence_after();
                 const uint32_t tbase = c.tmem + acc * BN + lane_off;
                 uint32_t v[C::kColsPerThread];
