@@ -5,6 +5,7 @@ import torch
 
 import w8a8_quantized_projections_gb300 as clef
 from test_gpu_fp8_block import inputs
+from test_gpu_norm import values, weight
 
 pytestmark = pytest.mark.gpu
 
@@ -77,3 +78,28 @@ def test_one_cluster_that_takes_tile_after_tile(m, n, k, only):
     assert torch.equal(clef.fp8_block_linear(*args), want) and clef.poll_status() == 0
     clef.set_sm_budget(0)
     assert torch.equal(clef.fp8_block_linear(*args), want) and clef.poll_status() == 0
+
+
+# ---------------------------------------------------------------- rows kept ahead
+
+@pytest.mark.parametrize("mode", ["int8_h128", "fp8_b128"])
+@pytest.mark.parametrize("k", [1152, 5120])
+@pytest.mark.parametrize("cta", [0, 5, 151])
+def test_one_cta_of_a_norm_that_keeps_rows(cta, k, mode, only):
+    """A CTA takes every so many-th row: those it left are as they were, the others right."""
+    m = 1300
+    x, w, r = values((m, k), 93), weight(k, 94), values((m, k), 95)
+    want = clef.rms_norm_quant(x, w, mode, residual=r, residual_out=torch.empty_like(r))
+    q, s = torch.full_like(want[0], 77), torch.full_like(want[1], -1.0)
+    assert clef.poll_status() == 0
+    only(cta)
+    clef.rms_norm_quant(x, w, mode, residual=r, residual_out=torch.empty_like(r), q=q, scale=s)
+    assert clef.poll_status() == 4
+    left = [i for i in range(m) if not torch.equal(s[i], want[1][i])]
+    step = left[1] - left[0] if len(left) > 1 else m
+    assert left == list(range(cta, m, step)) and step >= 152
+    rest = [i for i in range(m) if i not in left]
+    assert torch.equal(q[rest], want[0][rest]) and (q[left] == 77).all() and (s[left] == -1.0).all()
+    finish()
+    got = clef.rms_norm_quant(x, w, mode, residual=r, residual_out=torch.empty_like(r), q=q, scale=s)
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1]) and clef.poll_status() == 0

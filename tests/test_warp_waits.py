@@ -9,6 +9,8 @@ which no lane leaves."""
 import os
 import re
 
+import pytest
+
 CSRC = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))),
                     "w8a8_quantized_projections_gb300", "csrc")
 
@@ -87,6 +89,15 @@ def test_warps_of_the_gemms_agree():
     assert re.search(r"bool warp_pair\([^{]*\{\s*return __all_sync\(0xFFFFFFFFu, wait_pair\(", text)
     for role in ("G::producer(", "G::mma_issuer(", "G::forwarder("):
         assert re.search(r"if \(lane == 0[^{]*\{[^{}]*$", text[:text.index(role)]), role
+
+
+@pytest.mark.parametrize("name", ["norm.cu", "quant_act.cu"])
+def test_warps_that_keep_rows_leave_together(name):
+    """They go on after a wait that ran out, as far as the row's barrier, and leave on the flag of the CTA, which another
+    warp may be setting while they read it: by vote, as reductions over the warp follow."""
+    text = code(name)
+    assert re.findall(r"if \([^;{]*abort_flag[^;{]*\) break;", text) == re.findall(r"if \(__any_sync\([^,]*, abort_flag\)\) break;", text) != []
+    assert not re.search(r"(if|while) \([^;{)]*mbar_wait\(", text)
 
 
 def test_the_shared_helper_votes():

@@ -491,7 +491,7 @@ __global__ void __launch_bounds__(512) norm_staged_kernel(const __grid_constant_
             if (ss <= kFltMax) break;
             unit = 0x1p-80f;
         }
-        if (abort_flag) break;
+        if (__any_sync(kAll, abort_flag)) break;     // (another warp may be setting it: a warp's lanes leave together)
         if constexpr (MODE != kNormBf16) leave_codes<MODE, C>(a, m, e, true, v, g, amax);
         if (MODE == kNormBf16 || a.y) {
             if constexpr (kRotate) take(false);      // the values before their rotation once more: the row is still there

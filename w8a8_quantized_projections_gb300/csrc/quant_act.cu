@@ -469,7 +469,7 @@ quant_staged_kernel(const __grid_constant__ CUtensorMap tmx, int M, int K, int n
         amax = warp_max_nonneg(amax);
         if (lane == 0) red[it & 1][warp] = amax;
         __syncthreads();
-        if (abort_flag) break;
+        if (__any_sync(0xFFFFFFFFu, abort_flag)) break;   // (another warp may be setting it: a warp's lanes leave together)
         if (tid == 0) {
             const int mn = m + nslot * (int)gridDim.x;
             if (mn < M) {
