@@ -65,6 +65,35 @@ private:
     std::atomic<uint64_t> done_{0};
 };
 
+// Answers that a device is asked for once for each key (how many CTAs or clusters of a kernel it holds), positive ones.
+// A question that fails is asked again by the next call, and leaves no error behind.
+template <int kKeys>
+class AskedOnce {
+public:
+    template <typename Ask>
+    cudaError_t get(int key, int *answer, Ask ask) {
+        int dev = 0;
+        cudaError_t e = cudaGetDevice(&dev);
+        if (e != cudaSuccess) return e;
+        const bool kept = dev < kDevices;
+        *answer = kept ? known_[dev][key].load(std::memory_order_relaxed) : 0;
+        if (*answer > 0) return cudaSuccess;
+        e = ask(answer);
+        if (e == cudaSuccess && *answer < 1) e = cudaErrorInvalidConfiguration;
+        if (e != cudaSuccess) {
+            *answer = 0;
+            (void)cudaGetLastError();
+            return e;
+        }
+        if (kept) known_[dev][key].store(*answer, std::memory_order_relaxed);
+        return cudaSuccess;
+    }
+
+private:
+    static constexpr int kDevices = 64;
+    std::atomic<int> known_[kDevices][kKeys] = {};
+};
+
 enum ActMode : int { kActInt8H128 = 0, kActFp8 = 1, kActFp8H128 = 2 };
 
 // What the quantizer launch needs from the device set-up.  staging: 0 =

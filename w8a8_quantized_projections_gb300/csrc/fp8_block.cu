@@ -39,7 +39,6 @@
 //        the 6.4 TB/s of a long call).  Copies of later k-blocks into L2 ahead of the
 //        ring: 20% slower; MMAs of two k-blocks side by side: no gain.
 #include <algorithm>
-#include <atomic>
 #include <cstdint>
 #include <cuda.h>
 #include <cuda_bf16.h>
@@ -867,14 +866,17 @@ int maps(CUtensorMap &tx, CUtensorMap &tw, const void *qx, const void *qw, int64
                                         CU_TENSOR_MAP_SWIZZLE_128B);
 }
 
-// Clusters of `split` CTAs that the device holds at once where an SM holds one CTA: how many fit into its groups of
-// SMs (asked once for each size).
-int clusters_at_once(int split) {
+// Clusters of `split` CTAs that a device of `all_sms` SMs holds at once where an SM holds one CTA: how many fit into its
+// groups of SMs.  (Where it cannot be asked: as if any SMs could form one.)
+int clusters_at_once(int split, int all_sms) {
     using F = Few<64, false>;
     static SmemOptIn opt;
-    static std::atomic<int> known[kMaxSplit + 1];
-    int n = known[split].load(std::memory_order_relaxed);
-    if (n == 0) {
+    static AskedOnce<kMaxSplit + 1> known;
+    int n = 0;
+    const cudaError_t e = known.get(split, &n, [&](int *most) {
+        auto kern = few_kernel<64, false>;
+        const cudaError_t set = opt.set(reinterpret_cast<const void *>(kern), F::kSmem);
+        if (set != cudaSuccess) return set;
         cudaLaunchConfig_t cfg = {};
         cudaLaunchAttribute attr[1];
         attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -886,24 +888,20 @@ int clusters_at_once(int split) {
         cfg.dynamicSmemBytes = F::kSmem;
         cfg.attrs = attr;
         cfg.numAttrs = 1;
-        auto kern = few_kernel<64, false>;
-        if (opt.set(reinterpret_cast<const void *>(kern), F::kSmem) != cudaSuccess ||
-            cudaOccupancyMaxActiveClusters(&n, kern, &cfg) != cudaSuccess || n < 1)
-            n = 1;
-        known[split].store(n, std::memory_order_relaxed);
-    }
-    return n;
+        return cudaOccupancyMaxActiveClusters(most, kern, &cfg);
+    });
+    return e == cudaSuccess ? n : std::max(1, all_sms / split);
 }
 
 template <bool GU, int S>
-int launch_wide(const void *qx, const void *qw, int64_t K, BlockArgs a, int sms, cudaStream_t st) {
+int launch_wide(const void *qx, const void *qw, int64_t K, BlockArgs a, int sms, int all_sms, cudaStream_t st) {
     constexpr int kWideSmem = Wide<GU, S>::kSmem;
     static SmemOptIn opt;
     auto kern = wide_kernel<GU, S>;
     cudaError_t e = opt.set(reinterpret_cast<const void *>(kern), kWideSmem);
     if (e != cudaSuccess) return internal_cuda_error(e, "block linear smem attribute");
     // clusters that the device holds at once, or this call's SM budget
-    const int clusters = std::max(1, std::min(clusters_at_once(2 * S), sms / (2 * S)));
+    const int clusters = std::max(1, std::min(clusters_at_once(2 * S, all_sms), sms / (2 * S)));
     const int num_m = (a.M + 255) / 256, num_n = GU ? a.N / 128 : (a.N + 255) / 256;
     // bands whose rows of x take up to 24 MB, so that they stay in L2 while the weight passes; of even size
     const int64_t per = 256 * K, fit = std::max<int64_t>(1, ((int64_t)24 << 20) / per);
@@ -937,7 +935,7 @@ FewPlan plan_few(const BlockArgs &a, int sms) {
     const int64_t tiles = (int64_t)((a.N + 127) / 128) * ((a.M + T - 1) / T), slots = (int64_t)F::kPerSm * sms;
     FewPlan p{T, 1, 0.0};
     for (int n = 2; n <= kMaxSplit && 4 * n <= a.nkb; ++n)
-        if (tiles * n <= slots && tiles <= (int64_t)F::kPerSm * clusters_at_once(n)) p.split = n;
+        if (tiles * n <= slots && tiles <= (int64_t)F::kPerSm * clusters_at_once(n, sms)) p.split = n;
     const double step = GU ? (T == 16 ? 0.30 : T == 32 ? 0.40 : 0.60) : (T == 16 ? 0.24 : T == 32 ? 0.31 : T == 64 ? 0.29 : 0.44);
     const double steps = (double)((tiles * p.split + slots - 1) / slots) * ((a.nkb + p.split - 1) / p.split);
     const double bytes = (double)F::kTiles * ((a.N + 127) / 128) * a.nkb * kBoxBytes;
@@ -976,7 +974,7 @@ int launch_block(const void *qx, const void *qw, int64_t K, const BlockArgs &a, 
     // pairs that share a tile's K: clusters that run at once, each pair with four k-blocks or more.  (768 x 5,120 x 1,024
     // 18.4 us by one pair, 13.7 by two, 12.6 by four; 1,024 x 2,048 x 1,024 10.0, 9.4 and 10.1; 768 x 1,536 x 768 8.5
     // and 8.7.)
-    for (int n = 2; n <= 4 && 4 * n <= a.nkb && tiles * n <= pairs && tiles <= clusters_at_once(2 * n); n *= 2) {
+    for (int n = 2; n <= 4 && 4 * n <= a.nkb && tiles * n <= pairs && tiles <= clusters_at_once(2 * n, all_sms); n *= 2) {
         const double us = (n == 2 ? 6.7 : 9.5) + std::max((a.nkb + n - 1) / n * 0.38, weight / 4.5e6);
         if (us < best.us) best = {0, n, us};
     }
@@ -996,9 +994,9 @@ int launch_block(const void *qx, const void *qw, int64_t K, const BlockArgs &a, 
             if constexpr (!GU) return launch_few<128, GU>(qx, qw, K, a, best.split, sms, all_sms, st);
             [[fallthrough]];
         default:
-            return best.split == 4 ? launch_wide<GU, 4>(qx, qw, K, a, sms, st)
-                 : best.split == 2 ? launch_wide<GU, 2>(qx, qw, K, a, sms, st)
-                                   : launch_wide<GU, 1>(qx, qw, K, a, sms, st);
+            return best.split == 4 ? launch_wide<GU, 4>(qx, qw, K, a, sms, all_sms, st)
+                 : best.split == 2 ? launch_wide<GU, 2>(qx, qw, K, a, sms, all_sms, st)
+                                   : launch_wide<GU, 1>(qx, qw, K, a, sms, all_sms, st);
     }
 }
 

@@ -21,7 +21,6 @@
 // out by the sum, which is then infinite; the row is read again and summed in
 // units of 2^80.
 #include <algorithm>
-#include <atomic>
 #include <cstdint>
 #include <cuda.h>
 #include <cuda_bf16.h>
@@ -634,14 +633,11 @@ int launch_staged(const NormArgs &a, const NormEnv &env, int threads, cudaStream
         if (!rc && a.r) rc = map(tr, a.r, dims, a.ldr);
         if (rc) return rc;
     }
-    // CTAs that registers and threads let an SM hold (asked once for each number of warps)
-    static std::atomic<int> known[17];
-    int most = known[threads / 32].load(std::memory_order_relaxed);
-    if (most == 0) {
-        e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&most, kern, threads, 0);
-        if (e != cudaSuccess || most < 1) return internal_cuda_error(e, "norm occupancy");
-        known[threads / 32].store(most, std::memory_order_relaxed);
-    }
+    // CTAs that registers and threads let an SM hold, for each number of warps
+    static AskedOnce<17> known;
+    int most = 0;
+    e = known.get(threads / 32, &most, [&](int *n) { return cudaOccupancyMaxActiveBlocksPerMultiprocessor(n, kern, threads, 0); });
+    if (e != cudaSuccess) return internal_cuda_error(e, "norm occupancy");
     const int row = (a.K * 2 + 1023) / 1024 * 1024, slot = row * (a.r ? 2 : 1);
     int per_sm = std::min(most, 16), ring = 0;
     for (;  per_sm > 1; --per_sm)
