@@ -535,7 +535,8 @@ int clef_kv_copy_pages(void *codes, int64_t plane_bytes, float *scales, int64_t 
  *   residual_out = bf16(h),  y = bf16(h w / sqrt(mean(h^2) + eps)),
  * from the fp32 sum h, before its rounding.  x, residual, residual_out, y: bf16
  * [M][K] with pitches ldx, ldr, ldro, ldy; w: bf16 [K].  residual_out may be the
- * residual, and y may be x.  A row's bits depend on the row and w alone.
+ * residual, and y may be x, with the same pitch; they are disjoint from it and from
+ * each other otherwise.  A row's bits depend on the row and w alone.
  *
  * clef_rms_norm_quant -- the same with 8-bit codes of the unrounded result v = h w
  * / sqrt(mean(h^2) + eps) as the linears take them: modes CLEF_ACT_INT8_H128,

@@ -26,7 +26,8 @@ def _ext():
 
 def rms_norm(x, w, eps: float = 1e-6, residual=None, residual_out=None, y=None, stream=None):
     """bf16(h w / sqrt(mean(h^2) + eps)) of the rows of h = x + residual (bf16 [M][K]; x alone
-    without one).  bf16(h) goes to residual_out, or to residual itself where it is not given."""
+    without one).  bf16(h) goes to residual_out, or to residual itself where it is not given.
+    y may be x itself."""
     return _ext().rms_norm(x, w, eps, residual, residual_out, y, stream)
 
 

@@ -698,6 +698,9 @@ int norm_call(const void *x, int64_t ldx, const void *residual, int64_t ldr, con
         kv_misaligned(y, 16) || kv_misaligned(q, 16))
         return kv_fail("tensors must be 16-byte aligned");
     if (kv_misaligned(scale, 4)) return kv_fail("scale not 4-byte aligned");
+    // (with another pitch a row's result would land on rows not read yet)
+    if (M > 1 && ((y == x && ldy != ldx) || (residual && residual_out == residual && ldro != ldr)))
+        return kv_fail("in place, the pitches must agree");
     int sms = 0;
     unsigned int *status = nullptr;
     const int rc = internal_device(&sms, &status);
