@@ -407,9 +407,11 @@ __global__ void __launch_bounds__(512) norm_staged_kernel(const __grid_constant_
         mbar_init(&w_full, 1);
         abort_flag = 0;
         fence_barrier_init();
-        tma_prefetch_desc(&tmx);
-        tma_prefetch_desc(&tmr);
-        tma_prefetch_desc(&tmw);
+        if (lines) {      // (the maps that are made)
+            tma_prefetch_desc(&tmx);
+            tma_prefetch_desc(&tmw);
+            if (a.r) tma_prefetch_desc(&tmr);
+        }
     }
     __syncthreads();
     pdl_wait();
