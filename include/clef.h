@@ -535,8 +535,8 @@ int clef_kv_copy_pages(void *codes, int64_t plane_bytes, float *scales, int64_t 
  *   residual_out = bf16(h),  y = bf16(h w / sqrt(mean(h^2) + eps)),
  * from the fp32 sum h, before its rounding.  x, residual, residual_out, y: bf16
  * [M][K] with pitches ldx, ldr, ldro, ldy; w: bf16 [K].  residual_out may be the
- * residual, and y may be x, with the same pitch; they are disjoint from it and from
- * each other otherwise.  A row's bits depend on the row and w alone.
+ * residual, and y may be x, with the same pitch; otherwise the outputs are disjoint from
+ * the inputs and from each other.  A row's bits depend on the row and w alone.
  *
  * clef_rms_norm_quant -- the same with 8-bit codes of the unrounded result v = h w
  * / sqrt(mean(h^2) + eps) as the linears take them: modes CLEF_ACT_INT8_H128,
@@ -581,8 +581,8 @@ int clef_kv_copy_pages(void *codes, int64_t plane_bytes, float *scales, int64_t 
  * otherwise.  pos: int32 [tokens].
  * Requirements: dim % 8 == 0, dim <= 1024, rot even, 2 <= rot <= dim, heads <= 1024,
  * pitches >= dim and multiples of 8; x and out 16-byte, turns 8-byte, pos 4-byte
- * aligned.  rot a multiple of 16 (8 where interleaved) takes 16-byte accesses,
- * another one single values.
+ * aligned.  Accesses are of 16, 8, 4 or 2 bytes where rot is a multiple of 16, 8, 4 or
+ * 2; where interleaved, of 16, 8 or 4 where it is one of 8, 4 or 2.
  */
 int clef_rms_norm(const void *x, int64_t ldx, const void *residual, int64_t ldr, const void *w, int64_t M, int64_t K,
                   float eps, void *residual_out, int64_t ldro, void *y, int64_t ldy, void *stream);

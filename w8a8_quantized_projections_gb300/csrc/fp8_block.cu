@@ -16,9 +16,10 @@
 //        a ring.  A TMEM lane is a row of x, so a thread's scale is its row's times
 //        one of the weight's, the same for its 128 columns.  Persistent over tiles, in
 //        bands of rows that stay in L2; a tile leaves through shared memory and TMA.
-//        24,032 x 5,120 x 6,144: 484 us, 3,120 TFLOP/s; 1,502 x 5,120 x 17,408 gate/up 196
-//        us.  MMAs alone, without reading back, take 432 us of the first (operands'
-//        shared-memory traffic: 64 KB a k-block and SM); the rest is a tile's end
+//        24,032 x 5,120 x 6,144: 496 us, 3,050 TFLOP/s, ten calls in a row (557 for a second, under
+//        the power cap); 1,502 x 5,120 x 17,408 gate/up 200 us (215).  MMAs that are not read back take
+//        406 and 154 us (462 and 173; operands' shared-memory traffic: 64 KB a k-block and SM), the
+//        per-row linears of gemm.cu 430 and 170 (486 and 185); the rest is a tile's end
 //        (about 3,000 clocks of 30,000, two k-blocks of which are hidden) and the way from
 //        an MMA's end over both CTAs' reading back to the MMA that reuses the buffer
 //        (about 1,300 clocks, 1,000 of them hidden).  What was tried: sixteen warps
@@ -101,7 +102,8 @@ __device__ __forceinline__ uint64_t add_f2(uint64_t a, uint64_t b) {
 
 // g / (1 + e^-g) u of two values, as (g / 4) u / (1/4 + 2^(-g log2 e - 2)): the divisor is below 2^126, where the
 // reciprocal underflows, for every e^-g that fp32 holds, so that none has to be looked at and scaled
-// (1,502 x 5,120 x 17,408: 200 to 196 us; 188 without a silu, whose exponentials and reciprocals are what a tile waits for).
+// (1,502 x 5,120 x 17,408, ten calls in a row: 4 us of 200; 8 more without a silu, whose exponentials and reciprocals are what a tile
+// waits for).
 __device__ __forceinline__ uint64_t silu_mul2(uint64_t g, uint64_t u) {
     constexpr float kLog2E = 1.44269504088896341f;
     float a, b;
@@ -963,8 +965,11 @@ int launch_few(const void *qx, const void *qw, int64_t K, BlockArgs a, int split
 }
 
 // The kernel for a call: the one expected to take least on the whole device, so that a budget of SMs changes no
-// sum's order.  (Both sides measured at 2048 x 2048, 1024 x 5120, 6144 x 5120,
-// 5120 x 17408 and 34816 x 5120, and at 2048 and 17408 gate/up columns, and narrow ones, for 1 .. 4,096 rows.)
+// sum's order.  (Every kernel measured at 2048 x 2048, 1024 x 5120, 6144 x 5120,
+// 5120 x 17408 and 34816 x 5120, and at 2048 and 17408 gate/up columns, and narrow ones, for 1 .. 4,096 rows, weights out of
+// memory: in 149 of 162 calls the one taken is the fastest or within 6% of it.  The others: 17 to 64 rows by 6144, 34816 or
+// 2 x 17408 columns, 8-19%, where tiles of 16 rows are taken and 32, or pairs, are faster; 100 rows by 34816 x 5120, 37%,
+// pairs again; 200 and 256 rows by 2048 x 2048 and 1,502 and 2,048 by 256 x 2048, 12-18%, 32 rows a tile taken, 16 faster.)
 template <bool GU>
 int launch_block(const void *qx, const void *qw, int64_t K, const BlockArgs &a, int sms, int all_sms, cudaStream_t st) {
     // many rows: rounds of tiles, each k-block 0.38 us, or the weight's bytes at 4.5 TB/s

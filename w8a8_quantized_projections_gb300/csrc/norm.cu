@@ -8,8 +8,8 @@
 // Bound by HBM: 2 bytes an element in for x, 2 in and 2 out for the residual, 1
 // out for a code (2 for a bf16 result), so the row is read once and stays in
 // registers (or, many rows at a time, in shared memory until it is coded).  24,032 x
-// 5,120 with a residual: codes in blocks 145 us (88% of the copy rate), rotated INT8
-// 130 us (98%), bf16 153 us (95%); a row of 5,120: 2 us, its launch.  g is a factor of the whole row, and the rotation is linear: the
+// 5,120 with a residual: codes in blocks 143 us (89% of the copy rate), e4m3 with a scale a row 141 (90%), rotated INT8
+// 128 us (99%), rotated e4m3 129, bf16 150 us (97%); a row of 5,120: 2 us, its launch.  g is a factor of the whole row, and the rotation is linear: the
 // absmax of v = h w (rotated) is found beside the sum of squares, in one
 // reduction over the row; the codes are rne(v * top / absmax(v)), in which g
 // cancels, and the scale is absmax(v) g / top.  Scales of blocks of 128 need no
@@ -669,8 +669,10 @@ int launch_norm(const NormArgs &a, const NormEnv &env, cudaStream_t st) {
     // (a warp a row up to 1,024: 100,000 rows to fp8 114 us, 129 staged; rotated rows 150 and 110, rows of 2,048 worse)
     else if (chunks <= 64 && MODE != kNormI8H && MODE != kNormF8H) e = lanes(norm_kernel<MODE, 2, 32>, 32);
     else {
-        // Rows enough that CTAs pay which keep some ahead.  (Beside a residual, bf16 results of shorter rows leave a little
-        // faster where a CTA a row comes and goes: 24,032 x 5,120 152 us, 159 staged; 5,136 the other way round.)
+        // Rows enough that CTAs pay which keep some ahead.  (Beside a residual, bf16 results of rows up to 5,120 leave faster
+        // where a CTA a row comes and goes: its 64 registers a thread let an SM hold 32 warps, three CTAs of the ten that
+        // 5,120 takes, two of eleven.  24,032 rows of 2,048: 57 us, 66 staged; 4,608: 139 and 142; 5,120: 150 and 157; 5,136: 200 and
+        // 152; 6,144: 208 and 191; 8,192: 258 and 253; 16,384: 633 and 507.)
         const bool many = a.M >= 8 * (int64_t)env.sms && !(MODE == kNormBf16 && a.r && a.K <= 5120 && a.M >= 32 * (int64_t)env.sms);
         if (many && chunks <= 1024) return launch_staged<MODE, 2>(a, env, (chunks + 63) / 64 * 32, st);
         if (many) return launch_staged<MODE, 4>(a, env, (chunks + 127) / 128 * 32, st);
@@ -728,8 +730,10 @@ int norm_call(const void *x, int64_t ldx, const void *residual, int64_t ldr, con
     a.blocks = (int)((K + 127) / 128);
     a.eps = eps;
     a.y32 = !kv_misaligned(y, 32) && ldy % 16 == 0;
-    // (Residuals of rotated modes are written in halves of sectors: 24,032 x 5,120 INT8 130 us, 145 in whole ones.  The
-    // others are the other way round: codes in blocks 145 and 156 us, and rotated rows of 16,384 77 and 81 us.)
+    // (Residuals of rotated modes are written in halves of sectors up to 8,192, where an SM holds two of the CTAs that keep
+    // rows ahead or more -- 16 warps of 104 registers a thread --, and in whole ones beyond, where it holds one.  24,032 rows, INT8,
+    // halves and whole: 2,048 55 and 57 us, 4,096 106 and 116, 5,120 128 and 151, 8,192 203 and 216, 9,216 326 and 313,
+    // 12,288 355 and 327, 16,384 433 and 410.  The other modes take whole ones: codes in blocks of 5,120 145 us, 156 in halves.)
     a.r32 = !kv_misaligned(residual_out, 32) && ldro % 16 == 0 &&
             !((mode == kNormI8H || mode == kNormF8H) && K <= 8192);
     a.q32 = !kv_misaligned(q, 32) && K % 32 == 0;
