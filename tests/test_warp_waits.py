@@ -37,6 +37,9 @@ def voted(text, pos):
 def stays(text, pos):
     """Whether the wait at pos only goes into the kept flag `ok`."""
     before = re.split(r"[;{}]", text[:pos])[-1]
+    if re.match(r"\s*bool ok = ", before):       # of one turn of the loop: voted on before the turn can end
+        way = text[pos:text.index("return", pos)]
+        return re.search(r"if \(!__all_sync\(0xFFFFFFFFu, ok\)\) $", way) is not None and not re.search(r"\b(break|continue)\b", way)
     return re.match(r"\s*ok = ok && ", before) is not None or \
         re.fullmatch(r"\s*if \(!", before) is not None and re.match(r"[^;{]*\) ok = false;", text[pos:]) is not None
 
@@ -60,6 +63,8 @@ def test_the_scan_finds_what_it_looks_for():
     assert unvoted("if (!warp_wait(&b, 0, w, 1)) break;") == []
     assert unvoted("ok = ok && (ready || (mbar_wait(&b, 0, w, 1) && mbar_wait(&d, 0, w, 1)));") == []
     assert unvoted("if (!stay_wait(&b, 0, w, 1)) ok = false;") == []
+    assert unvoted("bool ok = mbar_wait(&b, 0, w, 1); x(); if (!__all_sync(0xFFFFFFFFu, ok)) return;") == []
+    assert unvoted("bool ok = mbar_wait(&b, 0, w, 1); if (!ok) return; if (!__all_sync(0xFFFFFFFFu, ok)) return;") == ["mbar_wait(&b"]
     assert unvoted("if (!stay_wait(&b, 0, w, 1)) { ok = false; break; }") == ["stay_wait(&b"]
     assert lone_exits("if (!ok) break; if (!(ok = __all_sync(kWarp, ok))) break; for (;i < n && ok;) x();") == ["if (!ok) break;", "i < n && ok;"]
 
